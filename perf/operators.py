@@ -28,29 +28,29 @@ E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
 def listed():
     return [
         # one step of speculative decoding: 64 requests append 8 tokens each (latency)
-        {"name": "write, decode 64x8", "op": "write", "fmt": "e4m3", "type": "bf16", "heads": 2, "B": 64, "q_lo": 8, "q_hi": 8, "ctx": 4096, "lens": 1},
+        {"name": "write decode 64x8", "op": "write", "fmt": "e4m3", "type": "bf16", "heads": 2, "B": 64, "q_lo": 8, "q_hi": 8, "ctx": 4096, "lens": 1},
         # a large prefill batch: 8 chunks of about 8k tokens, 8 KV heads (bandwidth)
-        {"name": "write, prefill 8 x 8k", "op": "write", "fmt": "e4m3", "type": "bf16", "heads": 8, "B": 8, "q_lo": 7001, "q_hi": 8192, "ctx": 9000, "lens": 2},
+        {"name": "write prefill 8 x 8k", "op": "write", "fmt": "e4m3", "type": "bf16", "heads": 8, "B": 8, "q_lo": 7001, "q_hi": 8192, "ctx": 9000, "lens": 2},
         # ragged chunked prefill into NVFP4 pages, and the chunk read back as the attention sees it
         {"name": "write nvfp4 and read back", "op": "write", "fmt": "nvfp4", "type": "fp16", "heads": 2, "B": 8, "q_lo": 128, "q_hi": 4096, "ctx": 32768, "lens": 3},
         # a whole 1M-token context read back in bf16
-        {"name": "read, 1M tokens", "op": "read", "fmt": "e4m3", "type": "bf16", "heads": 2, "B": 1, "q_lo": 1048576, "q_hi": 1048576, "ctx": 1048576, "lens": 4},
+        {"name": "read 1M tokens", "op": "read", "fmt": "e4m3", "type": "bf16", "heads": 2, "B": 1, "q_lo": 1048576, "q_hi": 1048576, "ctx": 1048576, "lens": 4},
         # parts of 16 NVFP4 requests from odd positions, in fp32
-        {"name": "read nvfp4, 16 parts", "op": "read", "fmt": "nvfp4", "type": "fp32", "heads": 2, "B": 16, "q_lo": 300, "q_hi": 9001, "ctx": 32768, "lens": 5},
+        {"name": "read nvfp4 16 parts", "op": "read", "fmt": "nvfp4", "type": "fp32", "heads": 2, "B": 16, "q_lo": 300, "q_hi": 9001, "ctx": 32768, "lens": 5},
         # plain decode of 16 requests behind one 32k-token system prompt
-        {"name": "attend, 16x1 over 32k", "op": "attend", "hq": 16, "heads": 2, "B": 16, "q_lo": 1, "q_hi": 1, "prefix": 256, "own_lo": 1, "own_hi": 500, "lens": 6},
+        {"name": "attend 16x1 over 32k", "op": "attend", "hq": 16, "heads": 2, "B": 16, "q_lo": 1, "q_hi": 1, "prefix": 256, "own_lo": 1, "own_hi": 500, "lens": 6},
         # speculative verify of 64 requests behind a 128k-token shared document
-        {"name": "attend, 64x8 over 128k", "op": "attend", "hq": 16, "heads": 2, "B": 64, "q_lo": 8, "q_hi": 8, "prefix": 1024, "own_lo": 8, "own_hi": 2000, "lens": 7},
+        {"name": "attend 64x8 over 128k", "op": "attend", "hq": 16, "heads": 2, "B": 64, "q_lo": 8, "q_hi": 8, "prefix": 1024, "own_lo": 8, "own_hi": 2000, "lens": 7},
         # nothing shared: 16 requests of up to 128k tokens of their own
-        {"name": "attend, 16x8 own 128k", "op": "attend", "hq": 16, "heads": 2, "B": 16, "q_lo": 8, "q_hi": 8, "prefix": 0, "own_lo": 32768, "own_hi": 131072, "lens": 8},
+        {"name": "attend 16x8 own 128k", "op": "attend", "hq": 16, "heads": 2, "B": 16, "q_lo": 8, "q_hi": 8, "prefix": 0, "own_lo": 32768, "own_hi": 131072, "lens": 8},
         # ragged chunks of new prompts behind an 8k-token shared prefix, groups of 3 query heads
-        {"name": "attend, 5 chunks over 8k", "op": "attend", "hq": 12, "heads": 4, "B": 5, "q_lo": 1, "q_hi": 700, "prefix": 65, "own_lo": 700, "own_hi": 1500, "lens": 9},
+        {"name": "attend 5 chunks over 8k", "op": "attend", "hq": 12, "heads": 4, "B": 5, "q_lo": 1, "q_hi": 700, "prefix": 65, "own_lo": 700, "own_hi": 1500, "lens": 9},
         # one request, three drafts, a small vocabulary (latency)
-        {"name": "verify, 1x3 of 32k", "op": "verify", "type": "fp32", "B": 1, "k": 3, "V": 32000},
+        {"name": "verify 1x3 of 32k", "op": "verify", "type": "fp32", "B": 1, "k": 3, "V": 32000},
         # 64 requests, seven drafts, a large odd vocabulary
-        {"name": "verify, 64x7 of 200k", "op": "verify", "type": "fp32", "B": 64, "k": 7, "V": 200003},
+        {"name": "verify 64x7 of 200k", "op": "verify", "type": "fp32", "B": 64, "k": 7, "V": 200003},
         # the same step decided greedily on bf16 logits
-        {"name": "greedy, 64x7 of 131k", "op": "greedy", "type": "bf16", "B": 64, "k": 7, "V": 131072},
+        {"name": "greedy 64x7 of 131k", "op": "greedy", "type": "bf16", "B": 64, "k": 7, "V": 131072},
     ]
 
 
