@@ -13,6 +13,9 @@ Calls (same names as the C ABI, without the ``msa_`` prefix where noted):
   msa_combine   merge split partials by log-sum-exp
   msa_prefill_nvfp4, msa_decode_nvfp4   the same over NVFP4 K/V pages
   msa_nvfp4_to_e4m3   NVFP4 pages -> the E4M3 pages those calls read
+  msa_kv_write, msa_kv_read (and _nvfp4)   new K/V tokens into the pages, and
+                cached tokens back out of them
+  msa_verify, msa_verify_greedy   which drafted tokens stand, and the next one
 """
 from __future__ import annotations
 
@@ -30,6 +33,7 @@ TOPK = 16
 
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
+DTYPE_F16 = 2
 
 STATUS_BAD_PAGE_ID = 1 << 0
 STATUS_BAD_BLOCK = 1 << 1
@@ -73,6 +77,10 @@ def load():
     P, i64, f32, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_int
     SZ = ctypes.POINTER(ctypes.c_size_t)
     PL = ctypes.POINTER(MsaPlanStruct)
+    _WRITE = ([P, i64, i64, P, i64, i64, i32, P, i64, f32, f32, P, i64, P, P,
+               i64, i64, i64, P, P], i32)
+    _READ = ([P, i64, f32, f32, P, i64, P, P, i64, i64, i64, P, i64, i64, P,
+              i64, i64, i32, P, P], i32)
     sigs = {
         "msa_version": ([], i32),
         "msa_status_string": ([i32], ctypes.c_char_p),
@@ -105,6 +113,14 @@ def load():
                                ctypes.c_size_t, P, P, P], i32),
         "msa_prefill_attention_bf16q": ([P, P, i64, f32, f32, f32, f32, P, i64,
                                          PL, P, ctypes.c_size_t, P], i32),
+        "msa_kv_write": _WRITE,
+        "msa_kv_write_nvfp4": _WRITE,
+        "msa_kv_read": _READ,
+        "msa_kv_read_nvfp4": _READ,
+        "msa_verify": ([P, i64, i64, P, i64, i64, i32, P, P, P, i64, i64, i64,
+                        P, P, P], i32),
+        "msa_verify_greedy": ([P, i64, i64, i32, P, P, i64, i64, i64, P, P, P],
+                              i32),
         "msa_test_set_wait_limit_ns": ([ctypes.c_uint64], i32),
         "msa_read_status": ([PL, ctypes.POINTER(ctypes.c_uint32)], i32),
         "msa_read_counters": ([PL, ctypes.POINTER(ctypes.c_int64),
@@ -583,3 +599,7 @@ def run_workload(w, stream=None):
                                w.softmax_scale, w.block_table, plan,
                                stream=stream)
     return out, lse, plan
+
+
+from .serve import (msa_kv_read, msa_kv_read_nvfp4, msa_kv_write,  # noqa: E402,F401
+                    msa_kv_write_nvfp4, msa_verify, msa_verify_greedy)

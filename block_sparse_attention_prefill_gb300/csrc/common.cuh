@@ -121,6 +121,49 @@ cudaError_t launch_decode_seqlens(const int32_t* seq_lens, int64_t B,
 cudaError_t launch_nvfp4_to_e4m3(const uint8_t* kv4, int64_t page_heads,
                                  uint8_t* kv8, cudaStream_t stream);
 
+// Cache writes and reads (kv_cache.cu).  k and v are [T][Hkv][128] with
+// strides in elements; pool is either page format.
+struct KvCacheArgs {
+  void* k;
+  void* v;
+  int64_t k_token, k_head, v_token, v_head;
+  int dtype;             // MSA_DTYPE_*
+  uint8_t* pool;
+  int64_t num_pages;
+  float k_scale, v_scale;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  const int32_t* cu;     // [B + 1] the call's tokens by request
+  const int32_t* cu_k;   // [B + 1] write: sequence lengths
+  const int32_t* starts; // [B] read: first position of each request, or NULL
+  int B;
+  int64_t T;
+  int Hkv;
+  uint32_t* status;      // MSA_STATUS_* bits are set here, or NULL
+  bool fp4, write;
+};
+cudaError_t launch_kv_cache(const KvCacheArgs& a, cudaStream_t stream);
+
+// Draft verification (verify.cu).  Row (b, i) of target is at b * t_req +
+// i * t_row elements, of draft_probs at b * d_req + i * d_row.
+struct VerifyArgs {
+  const void* target;
+  int64_t t_req, t_row;
+  const void* draft;     // NULL: each draft was certain
+  int64_t d_req, d_row;
+  int dtype;
+  const int32_t* tokens_in;  // [B][n - 1]
+  const float* u;        // [B][n]
+  const int32_t* counts; // [B] drafts of each request, or NULL: n - 1
+  int64_t B;
+  int n;
+  int64_t V;
+  int32_t* tokens;       // [B][n]
+  int32_t* accepted;     // [B]
+};
+cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream);
+cudaError_t launch_verify_greedy(const VerifyArgs& a, cudaStream_t stream);
+
 int num_sms();
 
 // Programmatic dependent launch.  A kernel launched with launch_pdl may

@@ -288,6 +288,105 @@ int prefill_impl(const uint8_t* q, const uint8_t* kv, int64_t num_pages,
   return prefill_combine_impl(plan, ws, ws_bytes, out, lse, stream);
 }
 
+// k and v of a cache write or read: 16-byte aligned rows of 128 values with
+// token and head strides (in elements) that keep them aligned.
+int check_rows(const void* p, int64_t token, int64_t head, int64_t T, int64_t Hkv, int64_t es) {
+  if (!p) return MSA_ERR_NULL;
+  if (token < 0 || head < 0) return MSA_ERR_SHAPE;
+  if (!aligned(p, 16) || (T > 1 && token * es % 16) || (Hkv > 1 && head * es % 16))
+    return MSA_ERR_ALIGN;
+  return MSA_OK;
+}
+
+int kv_cache_impl(KvCacheArgs a, int64_t B, int64_t Hkv, const void* lens, cudaStream_t st) {
+  if (a.dtype != MSA_DTYPE_F32 && a.dtype != MSA_DTYPE_BF16 && a.dtype != MSA_DTYPE_F16)
+    return MSA_ERR_UNSUPPORTED;
+  if (B < 0 || B >= kI32Max / 2 || a.T < 0 || a.T >= kI32Max || Hkv < 1 || Hkv > 127 ||
+      a.num_pages < 0 || a.num_pages >= kI32Max || a.bt_stride < 0 || a.bt_stride > (1 << 24))
+    return MSA_ERR_SHAPE;
+  if (!(a.k_scale > 0.f) || !(a.v_scale > 0.f) || !std::isfinite(a.k_scale) ||
+      !std::isfinite(a.v_scale))
+    return MSA_ERR_SHAPE;
+  if (B == 0 || a.T == 0) return MSA_OK;
+  if (!a.pool || !a.block_table || !a.cu || (a.write && !lens)) return MSA_ERR_NULL;
+  const int64_t es = a.dtype == MSA_DTYPE_F32 ? 4 : 2;
+  int rc = check_rows(a.k, a.k_token, a.k_head, a.T, Hkv, es);
+  if (rc) return rc;
+  rc = check_rows(a.v, a.v_token, a.v_head, a.T, Hkv, es);
+  if (rc) return rc;
+  if (!aligned(a.pool, 16) || !aligned(a.block_table, 4) || !aligned(a.cu, 4) ||
+      !aligned(a.cu_k, 4) || !aligned(a.starts, 4) || !aligned(a.status, 4))
+    return MSA_ERR_ALIGN;
+  a.B = (int)B;
+  a.Hkv = (int)Hkv;
+  return cuda_rc(launch_kv_cache(a, st));
+}
+
+int kv_write_impl(const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
+                  int64_t v_head, int dtype, uint8_t* pool, int64_t num_pages, float k_scale,
+                  float v_scale, const int32_t* block_table, int64_t bt_stride,
+                  const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t T, int64_t Hkv,
+                  uint32_t* status, void* stream, bool fp4) {
+  KvCacheArgs a = {};
+  a.k = const_cast<void*>(k);
+  a.v = const_cast<void*>(v);
+  a.k_token = k_token, a.k_head = k_head, a.v_token = v_token, a.v_head = v_head;
+  a.dtype = dtype;
+  a.pool = pool;
+  a.num_pages = num_pages;
+  a.k_scale = k_scale, a.v_scale = v_scale;
+  a.block_table = block_table;
+  a.bt_stride = bt_stride;
+  a.cu = cu_q;
+  a.cu_k = cu_k;
+  a.T = T;
+  a.status = status;
+  a.fp4 = fp4;
+  a.write = true;
+  return kv_cache_impl(a, B, Hkv, cu_k, static_cast<cudaStream_t>(stream));
+}
+
+int kv_read_impl(const uint8_t* pool, int64_t num_pages, float k_scale, float v_scale,
+                 const int32_t* block_table, int64_t bt_stride, const int32_t* cu,
+                 const int32_t* starts, int64_t B, int64_t T, int64_t Hkv, void* k,
+                 int64_t k_token, int64_t k_head, void* v, int64_t v_token, int64_t v_head,
+                 int dtype, uint32_t* status, void* stream, bool fp4) {
+  KvCacheArgs a = {};
+  a.k = k;
+  a.v = v;
+  a.k_token = k_token, a.k_head = k_head, a.v_token = v_token, a.v_head = v_head;
+  a.dtype = dtype;
+  a.pool = const_cast<uint8_t*>(pool);
+  a.num_pages = num_pages;
+  a.k_scale = k_scale, a.v_scale = v_scale;
+  a.block_table = block_table;
+  a.bt_stride = bt_stride;
+  a.cu = cu;
+  a.starts = starts;
+  a.T = T;
+  a.status = status;
+  a.fp4 = fp4;
+  a.write = false;
+  return kv_cache_impl(a, B, Hkv, nullptr, static_cast<cudaStream_t>(stream));
+}
+
+int verify_impl(const VerifyArgs& a, bool greedy, cudaStream_t st) {
+  if (a.dtype != MSA_DTYPE_F32 && a.dtype != MSA_DTYPE_BF16 && a.dtype != MSA_DTYPE_F16)
+    return MSA_ERR_UNSUPPORTED;
+  if (a.B < 0 || a.B > kI32Max / 64 || a.n < 1 || a.n > MSA_VERIFY_MAX_TOKENS || a.V < 1 ||
+      a.V >= MSA_VERIFY_MAX_VOCAB || a.t_req < 0 || a.t_row < 0 || a.d_req < 0 || a.d_row < 0)
+    return MSA_ERR_SHAPE;
+  if (a.B == 0) return MSA_OK;
+  if (!a.target || !a.tokens || !a.accepted || (a.n > 1 && !a.tokens_in) || (!greedy && !a.u))
+    return MSA_ERR_NULL;
+  const size_t es = a.dtype == MSA_DTYPE_F32 ? 4 : 2;
+  if (!aligned(a.target, es) || !aligned(a.draft, es) || !aligned(a.tokens_in, 4) ||
+      !aligned(a.u, 4) || !aligned(a.counts, 4) || !aligned(a.tokens, 4) ||
+      !aligned(a.accepted, 4))
+    return MSA_ERR_ALIGN;
+  return cuda_rc(greedy ? launch_verify_greedy(a, st) : launch_verify(a, st));
+}
+
 struct DecodeLayout {
   int64_t R;
   size_t cu_bytes, plan_bytes, prefill_bytes, total;
@@ -528,6 +627,68 @@ int msa_combine(const void* part_o, int part_dtype, const float* part_lse,
   return cuda_rc(launch_combine(part_o, part_dtype, part_lse, rows,
                                 splits, out, lse_out,
                                 static_cast<cudaStream_t>(stream)));
+}
+
+int msa_kv_write(const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
+                 int64_t v_head, int dtype, uint8_t* kv, int64_t num_pages, float k_scale,
+                 float v_scale, const int32_t* block_table, int64_t bt_stride,
+                 const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int64_t B, int64_t T,
+                 int64_t Hkv, uint32_t* status, void* stream) {
+  return kv_write_impl(k, k_token, k_head, v, v_token, v_head, dtype, kv, num_pages, k_scale,
+                       v_scale, block_table, bt_stride, cu_seqlens_q, cu_seqlens_k, B, T, Hkv,
+                       status, stream, false);
+}
+
+int msa_kv_write_nvfp4(const void* k, int64_t k_token, int64_t k_head, const void* v,
+                       int64_t v_token, int64_t v_head, int dtype, uint8_t* kv4,
+                       int64_t num_pages, float k_scale, float v_scale,
+                       const int32_t* block_table, int64_t bt_stride,
+                       const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int64_t B,
+                       int64_t T, int64_t Hkv, uint32_t* status, void* stream) {
+  return kv_write_impl(k, k_token, k_head, v, v_token, v_head, dtype, kv4, num_pages, k_scale,
+                       v_scale, block_table, bt_stride, cu_seqlens_q, cu_seqlens_k, B, T, Hkv,
+                       status, stream, true);
+}
+
+int msa_kv_read(const uint8_t* kv, int64_t num_pages, float k_scale, float v_scale,
+                const int32_t* block_table, int64_t bt_stride, const int32_t* cu_tokens,
+                const int32_t* starts, int64_t B, int64_t T, int64_t Hkv, void* k,
+                int64_t k_token, int64_t k_head, void* v, int64_t v_token, int64_t v_head,
+                int dtype, uint32_t* status, void* stream) {
+  return kv_read_impl(kv, num_pages, k_scale, v_scale, block_table, bt_stride, cu_tokens, starts,
+                      B, T, Hkv, k, k_token, k_head, v, v_token, v_head, dtype, status, stream,
+                      false);
+}
+
+int msa_kv_read_nvfp4(const uint8_t* kv4, int64_t num_pages, float k_scale, float v_scale,
+                      const int32_t* block_table, int64_t bt_stride, const int32_t* cu_tokens,
+                      const int32_t* starts, int64_t B, int64_t T, int64_t Hkv, void* k,
+                      int64_t k_token, int64_t k_head, void* v, int64_t v_token, int64_t v_head,
+                      int dtype, uint32_t* status, void* stream) {
+  return kv_read_impl(kv4, num_pages, k_scale, v_scale, block_table, bt_stride, cu_tokens, starts,
+                      B, T, Hkv, k, k_token, k_head, v, v_token, v_head, dtype, status, stream,
+                      true);
+}
+
+int msa_verify(const void* target_probs, int64_t target_req, int64_t target_row,
+               const void* draft_probs, int64_t draft_req, int64_t draft_row, int dtype,
+               const int32_t* draft_tokens, const float* uniforms, const int32_t* num_drafts,
+               int64_t B, int64_t n, int64_t V, int32_t* tokens, int32_t* accepted,
+               void* stream) {
+  if (n < 1 || n > MSA_VERIFY_MAX_TOKENS) return MSA_ERR_SHAPE;
+  VerifyArgs a = {target_probs, target_req, target_row, n > 1 ? draft_probs : nullptr, draft_req,
+                  draft_row, dtype, draft_tokens, uniforms, num_drafts, B, (int)n, V, tokens,
+                  accepted};
+  return verify_impl(a, false, static_cast<cudaStream_t>(stream));
+}
+
+int msa_verify_greedy(const void* target, int64_t target_req, int64_t target_row, int dtype,
+                      const int32_t* draft_tokens, const int32_t* num_drafts, int64_t B,
+                      int64_t n, int64_t V, int32_t* tokens, int32_t* accepted, void* stream) {
+  if (n < 1 || n > MSA_VERIFY_MAX_TOKENS) return MSA_ERR_SHAPE;
+  VerifyArgs a = {target, target_req, target_row, nullptr, 0, 0, dtype, draft_tokens, nullptr,
+                  num_drafts, B, (int)n, V, tokens, accepted};
+  return verify_impl(a, true, static_cast<cudaStream_t>(stream));
 }
 
 int msa_decode_workspace_bytes(int64_t B, int64_t n, int64_t Hq, int64_t Hkv,

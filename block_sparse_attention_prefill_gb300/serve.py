@@ -1,0 +1,266 @@
+"""What a server calls around the block-sparse attention: cache writes and
+reads, dense attention behind a shared prefix, draft verification.
+
+Argument marshalling only, as in the package's ``__init__`` (whose public
+names these are); ``include/msa.h`` has each call's meaning.  These calls
+check every shape, type, stride and device here, because the library sees
+only pointers; tensors have to be on the current device.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import (DTYPE_BF16, DTYPE_F16, DTYPE_F32, HEAD_DIM, MsaError, NVFP4_SLOT_BYTES, PAGE_SIZE,
+               load, status_string)
+
+_TYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
+_WORD = (torch.int32, torch.uint32)
+
+
+def _fail(what, *args):
+    raise MsaError(what % args)
+
+
+def _check(rc, what):
+    if rc:
+        raise MsaError("%s: %s (code %d)" % (what, status_string(rc), rc))
+
+
+def _tensor(t, name, dtypes, shape=None, contiguous=True):
+    """Type and shape (None: any size in its place) of a required tensor."""
+    if t is None:
+        _fail("%s is required", name)
+    if t.dtype not in dtypes:
+        _fail("%s has dtype %s, expected one of %s", name, t.dtype, dtypes)
+    if shape is not None:
+        have = t.shape
+        if len(have) != len(shape) or any(w is not None and w != h for w, h in zip(shape, have)):
+            _fail("%s must be [%s], got %s", name,
+                  ", ".join("any" if w is None else str(w) for w in shape), tuple(have))
+    if contiguous and not t.is_contiguous():
+        _fail("%s must be contiguous", name)
+
+
+def _place(first, *others):
+    """The device that all given tensors share, which must be the current one."""
+    if not first.is_cuda:
+        _fail("tensors must be CUDA tensors")
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            _fail("tensors are on different devices: %s and %s", dev, t.device)
+    if dev.index != torch.cuda.current_device():
+        _fail("tensors are on %s, the current device is cuda:%d", dev, torch.cuda.current_device())
+    return dev
+
+
+def _handle(stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _new(shape, dtype, dev, handle):
+    """A tensor for use on the stream `handle`, whichever stream is current."""
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    if handle != torch._C._cuda_getCurrentRawStream(dev.index):
+        t.record_stream(torch.cuda.ExternalStream(handle, device=dev))
+    return t
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _pool(kv, fp4):
+    """(num_pages, Hkv) of a page pool."""
+    if fp4:
+        _tensor(kv, "kv4", (torch.uint8,), (None, None, 2, NVFP4_SLOT_BYTES))
+    else:
+        _tensor(kv, "kv", _E4M3, (None, None, PAGE_SIZE, 2 * HEAD_DIM))
+    return kv.shape[0], kv.shape[1]
+
+
+def _rows(t, name, T, Hkv):
+    """Strides of K or V rows [T, Hkv, 128] whose 128 values are contiguous."""
+    _tensor(t, name, _TYPES, (T, Hkv, HEAD_DIM), contiguous=False)
+    token, head, one = t.stride()
+    if one != 1:
+        _fail("%s must have its 128 values contiguous", name)
+    return token, head
+
+
+def _table(block_table, B):
+    _tensor(block_table, "block_table", _I32, (B, None))
+    return block_table.shape[1]
+
+
+def _requests(cu, name, B=None):
+    _tensor(cu, name, _I32, (None if B is None else B + 1,))
+    if cu.shape[0] < 1:
+        _fail("%s must have at least one element", name)
+    return cu.shape[0] - 1
+
+
+def _status(status):
+    if status is not None:
+        _tensor(status, "status", _WORD, (1,))
+
+
+def _write(name, fp4, k, v, kv, k_scale, v_scale, block_table, cu_q, cu_k, status, stream):
+    pages, Hkv = _pool(kv, fp4)
+    B = _requests(cu_q, "cu_seqlens_q")
+    _requests(cu_k, "cu_seqlens_k", B)
+    width = _table(block_table, B)
+    if k is None or v is None or k.dim() != 3:
+        _fail("k and v must be [T, Hkv, 128]")
+    T = k.shape[0]
+    ks, vs = _rows(k, "k", T, Hkv), _rows(v, "v", T, Hkv)
+    if k.dtype != v.dtype:
+        _fail("k and v have different dtypes: %s and %s", k.dtype, v.dtype)
+    _status(status)
+    dev = _place(kv, k, v, block_table, cu_q, cu_k, status)
+    _check(getattr(load(), name)(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+                                 _TYPES[k.dtype], kv.data_ptr(), pages, k_scale, v_scale,
+                                 block_table.data_ptr(), width, cu_q.data_ptr(), cu_k.data_ptr(),
+                                 B, T, Hkv, _ptr(status), _handle(stream, dev)), name)
+
+
+def msa_kv_write(k, v, kv, k_scale, v_scale, block_table, cu_seqlens_q, cu_seqlens_k,
+                 status=None, stream=None):
+    """Write new tokens into the E4M3 pool kv [num_pages, Hkv, 128, 256].
+    k, v [T, Hkv, 128] in fp32, bf16 or fp16 (any token and head strides that
+    keep rows on 16 bytes); they are the last q_len positions of each request,
+    as in msa_plan.  Rows behind cu_seqlens_q's last are left out.  status: an
+    int32 [1] tensor that MSA_STATUS_* bits are OR-ed into."""
+    _write("msa_kv_write", False, k, v, kv, k_scale, v_scale, block_table, cu_seqlens_q,
+           cu_seqlens_k, status, stream)
+
+
+def msa_kv_write_nvfp4(k, v, kv4, k_scale, v_scale, block_table, cu_seqlens_q, cu_seqlens_k,
+                       status=None, stream=None):
+    """msa_kv_write into an NVFP4 pool kv4 uint8 [num_pages, Hkv, 2, 9216];
+    k_scale / v_scale are the global scales (amax / 448 keeps every block
+    scale in range)."""
+    _write("msa_kv_write_nvfp4", True, k, v, kv4, k_scale, v_scale, block_table, cu_seqlens_q,
+           cu_seqlens_k, status, stream)
+
+
+def _read(name, fp4, kv, k_scale, v_scale, block_table, cu, T, starts, dtype, k, v, status,
+          stream):
+    pages, Hkv = _pool(kv, fp4)
+    B = _requests(cu, "cu_tokens")
+    width = _table(block_table, B)
+    if starts is not None:
+        _tensor(starts, "starts", _I32, (B,))
+    _status(status)
+    dev = _place(kv, block_table, cu, starts, k, v, status)
+    handle = _handle(stream, dev)
+    T = int(T)
+    if T < 0:
+        _fail("total_tokens must not be negative")
+    if (k is None) != (v is None):
+        _fail("give both of k and v, or neither")
+    if k is None:
+        if dtype not in _TYPES:
+            _fail("dtype must be one of %s", tuple(_TYPES))
+        k = _new((T, Hkv, HEAD_DIM), dtype, dev, handle)
+        v = _new((T, Hkv, HEAD_DIM), dtype, dev, handle)
+    ks, vs = _rows(k, "k", T, Hkv), _rows(v, "v", T, Hkv)
+    if k.dtype != v.dtype:
+        _fail("k and v have different dtypes: %s and %s", k.dtype, v.dtype)
+    if (T > 1 and 0 in (ks[0], vs[0])) or (Hkv > 1 and 0 in (ks[1], vs[1])):
+        _fail("rows of k and v must not overlap")
+    _check(getattr(load(), name)(kv.data_ptr(), pages, k_scale, v_scale, block_table.data_ptr(),
+                                 width, cu.data_ptr(), _ptr(starts), B, T, Hkv, k.data_ptr(),
+                                 ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _TYPES[k.dtype],
+                                 _ptr(status), handle), name)
+    return k, v
+
+
+def msa_kv_read(kv, k_scale, v_scale, block_table, cu_tokens, total_tokens, starts=None,
+                dtype=torch.bfloat16, k=None, v=None, status=None, stream=None):
+    """Read cached tokens back from an E4M3 pool, dequantised: request b's
+    positions starts[b] .. (0 without starts) become rows cu_tokens[b] ..
+    cu_tokens[b + 1] - 1 of k and v [total_tokens, Hkv, 128].  k and v may be
+    given (any of the three types, strided); rows behind cu_tokens' last, and
+    rows whose page is not valid, keep their contents.  Returns (k, v)."""
+    return _read("msa_kv_read", False, kv, k_scale, v_scale, block_table, cu_tokens,
+                 total_tokens, starts, dtype, k, v, status, stream)
+
+
+def msa_kv_read_nvfp4(kv4, k_scale, v_scale, block_table, cu_tokens, total_tokens, starts=None,
+                      dtype=torch.bfloat16, k=None, v=None, status=None, stream=None):
+    """msa_kv_read from an NVFP4 pool: E4M3(code x block scale) x the global
+    scale, what the NVFP4 attention reads."""
+    return _read("msa_kv_read_nvfp4", True, kv4, k_scale, v_scale, block_table, cu_tokens,
+                 total_tokens, starts, dtype, k, v, status, stream)
+
+
+def _verify(name, target, drafts, uniforms, draft_probs, counts, tokens, accepted, stream):
+    greedy = name == "msa_verify_greedy"
+    _tensor(target, "target", _TYPES, (None, None, None), contiguous=False)
+    B, n, V = target.shape
+    if n < 1:
+        _fail("target must have at least one row a request")
+    if target.stride(2) != 1 and V > 1:
+        _fail("target's rows must be contiguous")
+    _tensor(drafts, "draft_tokens", _I32, (B, n - 1))
+    if not greedy:
+        _tensor(uniforms, "uniforms", _F32, (B, n))
+    if draft_probs is not None:
+        _tensor(draft_probs, "draft_probs", (target.dtype,), (B, n - 1, V), contiguous=False)
+        if draft_probs.stride(2) != 1 and V > 1:
+            _fail("draft_probs' rows must be contiguous")
+    if counts is not None:
+        _tensor(counts, "num_drafts", _I32, (B,))
+    dev = _place(target, drafts, uniforms, draft_probs, counts, tokens, accepted)
+    handle = _handle(stream, dev)
+    if tokens is None:
+        tokens = _new((B, n), torch.int32, dev, handle)
+    else:
+        _tensor(tokens, "tokens", _I32, (B, n))
+    if accepted is None:
+        accepted = _new((B,), torch.int32, dev, handle)
+    else:
+        _tensor(accepted, "accepted", _I32, (B,))
+    t_req, t_row, _ = target.stride()
+    lib = load()
+    if greedy:
+        rc = lib.msa_verify_greedy(target.data_ptr(), t_req, t_row, _TYPES[target.dtype],
+                                   drafts.data_ptr(), _ptr(counts), B, n, V, tokens.data_ptr(),
+                                   accepted.data_ptr(), handle)
+    else:
+        d = draft_probs if draft_probs is not None and n > 1 else None
+        d_req, d_row = d.stride()[:2] if d is not None else (0, 0)
+        rc = lib.msa_verify(target.data_ptr(), t_req, t_row, _ptr(d), d_req, d_row,
+                            _TYPES[target.dtype], drafts.data_ptr(), uniforms.data_ptr(),
+                            _ptr(counts), B, n, V, tokens.data_ptr(), accepted.data_ptr(), handle)
+    _check(rc, name)
+    return tokens, accepted
+
+
+def msa_verify(target_probs, draft_tokens, uniforms, draft_probs=None, num_drafts=None,
+               tokens=None, accepted=None, stream=None):
+    """Which drafted tokens stand, and the token that follows them.
+    target_probs [B, n, V] and draft_probs [B, n - 1, V] in fp32, bf16 or fp16
+    (strided rows allowed; no draft_probs: the drafts were certain),
+    draft_tokens int32 [B, n - 1], uniforms fp32 [B, n] in [0, 1), num_drafts
+    int32 [B] or None for n - 1 each.  Returns (tokens int32 [B, n]: the
+    drafts that stand, the next token, -1; accepted int32 [B])."""
+    return _verify("msa_verify", target_probs, draft_tokens, uniforms, draft_probs, num_drafts,
+                   tokens, accepted, stream)
+
+
+def msa_verify_greedy(target, draft_tokens, num_drafts=None, tokens=None, accepted=None,
+                      stream=None):
+    """msa_verify with a draft standing where it is the first of the largest
+    values of its row of target [B, n, V] (logits or probabilities), and the
+    best token following.  Returns (tokens, accepted)."""
+    return _verify("msa_verify_greedy", target, draft_tokens, None, None, num_drafts, tokens,
+                   accepted, stream)

@@ -80,9 +80,10 @@ extern "C" {
 #define MSA_STATUS_TIMEOUT (1u << 4)      /* a bounded device wait expired   */
 #define MSA_STATUS_BAD_WORK (1u << 5)     /* inconsistent work item skipped  */
 
-/* element types of split partials (msa_combine) */
+/* element types (split partials of msa_combine: F32 or BF16) */
 #define MSA_DTYPE_F32 0
 #define MSA_DTYPE_BF16 1
+#define MSA_DTYPE_F16 2
 
 /*
  * NVFP4 K/V pages ([P2] Details / "Kernel capability": with an E4M3 query,
@@ -464,6 +465,120 @@ MSA_API int msa_decode_noalloc(const uint8_t *q, const uint8_t *kv,
                                const int32_t *seq_lens, int64_t B, int64_t n,
                                int64_t Hq, int64_t Hkv, int64_t max_seqlen_k,
                                uint16_t *out, float *lse, void *stream);
+
+/*
+ * Writing new tokens into the cache.  The T new tokens of a batch, in the
+ * order of cu_seqlens_q, are the LAST q_len_b positions of their requests,
+ * as in msa_plan; token t's K and V go to the page that its position has in
+ * block_table, quantised:
+ *   E4M3:  code = E4M3(x / scale), nearest even, saturating at 448
+ *   NVFP4: per 16 values s = E4M3(min(amax / (6 g), 448)) and code =
+ *          E2M1(x / (s g)), nearest even, saturating at 6; 0 where s g = 0.
+ *          NaN (which E2M1 lacks) is written as 0.
+ * with true divisions in fp32.  A chunk may end or begin inside a page: only
+ * the rows of its tokens are written.
+ *   k, v         [T][Hkv][128] in `dtype` (MSA_DTYPE_F32, _BF16 or _F16),
+ *                16-byte aligned; *_token and *_head are the strides in
+ *                elements of a token and a head (multiples of 16 bytes), so
+ *                that parts of a fused projection can be passed as they are
+ *   kv / kv4     the pool, as in msa_prefill / msa_prefill_nvfp4
+ *   k_scale, v_scale  per-tensor scales (NVFP4: the global scales g), finite
+ *                and > 0
+ *   block_table, bt_stride, cu_seqlens_q, cu_seqlens_k, B  as in msa_plan
+ *   T            rows of k and v; tokens at or behind cu_seqlens_q[B] (the
+ *                padding of a captured batch) are left out
+ *   status       device word that MSA_STATUS_* bits are OR-ed into, or NULL:
+ *                BAD_SEQLENS for a request with more new tokens than its
+ *                length or a position past its block_table row, BAD_BLOCK
+ *                for an entry that is not a page; such tokens are not written
+ * Pages written by one call belong to one request each: where two requests
+ * write the same row, it holds parts of either.  One kernel on `stream`.
+ */
+MSA_API int msa_kv_write(const void *k, int64_t k_token, int64_t k_head, const void *v,
+                 int64_t v_token, int64_t v_head, int dtype, uint8_t *kv, int64_t num_pages,
+                 float k_scale, float v_scale, const int32_t *block_table, int64_t bt_stride,
+                 const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int64_t B,
+                 int64_t T, int64_t Hkv, uint32_t *status, void *stream);
+MSA_API int msa_kv_write_nvfp4(const void *k, int64_t k_token, int64_t k_head, const void *v,
+                       int64_t v_token, int64_t v_head, int dtype, uint8_t *kv4,
+                       int64_t num_pages, float k_scale, float v_scale,
+                       const int32_t *block_table, int64_t bt_stride,
+                       const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int64_t B,
+                       int64_t T, int64_t Hkv, uint32_t *status, void *stream);
+
+/*
+ * Reading cached tokens back: request b's tokens at positions starts[b] ..
+ * starts[b] + len_b - 1, len_b = cu_tokens[b + 1] - cu_tokens[b], become rows
+ * cu_tokens[b] .. of k and v, dequantised as the attention reads them (E4M3:
+ * code x scale; NVFP4: E4M3(code x s) x g): the product in fp32, rounded to
+ * `dtype`.
+ *   cu_tokens    int32 [B + 1], prefix sums from 0
+ *   starts       int32 [B] first positions, or NULL for 0
+ *   T            rows of k and v; rows at or behind cu_tokens[B] keep their
+ *                contents, as do rows whose position or page is not valid
+ *                (status bits as in msa_kv_write)
+ *   k, v, strides, dtype  as in msa_kv_write; the rows must not overlap
+ * One kernel on `stream`.
+ */
+MSA_API int msa_kv_read(const uint8_t *kv, int64_t num_pages, float k_scale, float v_scale,
+                const int32_t *block_table, int64_t bt_stride, const int32_t *cu_tokens,
+                const int32_t *starts, int64_t B, int64_t T, int64_t Hkv, void *k,
+                int64_t k_token, int64_t k_head, void *v, int64_t v_token, int64_t v_head,
+                int dtype, uint32_t *status, void *stream);
+MSA_API int msa_kv_read_nvfp4(const uint8_t *kv4, int64_t num_pages, float k_scale,
+                      float v_scale, const int32_t *block_table, int64_t bt_stride,
+                      const int32_t *cu_tokens, const int32_t *starts, int64_t B, int64_t T,
+                      int64_t Hkv, void *k, int64_t k_token, int64_t k_head, void *v,
+                      int64_t v_token, int64_t v_head, int dtype, uint32_t *status,
+                      void *stream);
+
+/*
+ * Verification of drafted tokens, the step after a speculative-verify decode:
+ * which of a request's drafts stand, and the token that follows them.  With
+ * p_i the target's and q_i the draft model's probabilities at draft i and
+ * x_i the drafted token, draft i stands iff every draft before it does and
+ *     uniforms[b][i] * q_i(x_i) < p_i(x_i)      (taken in 64 bits: exact)
+ * (an x_i outside [0, V) or a NaN falls).  At the first draft that falls, the
+ * next token is drawn from max(p - q, 0); when all stand, from the row behind
+ * them.  It is the lowest v whose cumulated weight exceeds
+ * floor(uniforms[b][n - 1] * total); a weight is floor(2^44 * min(w, 1)) of
+ * w = p - q rounded to fp32, so sums are exact and the answer depends on the
+ * inputs alone.  Where the difference has no weight at all, the token is
+ * drawn from p, and is -1 where p has none either.
+ *   target_probs  [B][n][V] in `dtype`; row (b, i) at b * target_req + i *
+ *                 target_row elements
+ *   draft_probs   [B][n - 1][V] in `dtype`, likewise; NULL: the drafts were
+ *                 certain (q_i is 1 at x_i and 0 elsewhere)
+ *   draft_tokens  int32 [B][n - 1]
+ *   uniforms      fp32 [B][n] in [0, 1)
+ *   num_drafts    int32 [B], drafts of each request (clamped to 0 .. n - 1),
+ *                 or NULL for n - 1
+ *   tokens        int32 [B][n]: the drafts that stand, the next token, -1
+ *   accepted      int32 [B]: how many drafts stand
+ * 1 <= n <= MSA_VERIFY_MAX_TOKENS, 1 <= V < MSA_VERIFY_MAX_VOCAB.  The rows
+ * need no more alignment than their elements; 16-byte aligned rows are read
+ * fastest.  One kernel on `stream`.
+ */
+#define MSA_VERIFY_MAX_TOKENS 32
+#define MSA_VERIFY_MAX_VOCAB (1 << 19)
+MSA_API int msa_verify(const void *target_probs, int64_t target_req, int64_t target_row,
+               const void *draft_probs, int64_t draft_req, int64_t draft_row, int dtype,
+               const int32_t *draft_tokens, const float *uniforms, const int32_t *num_drafts,
+               int64_t B, int64_t n, int64_t V, int32_t *tokens, int32_t *accepted,
+               void *stream);
+
+/*
+ * Greedy verification: draft i stands iff every draft before it does and x_i
+ * is the target's best token at i, the lowest index of the row's largest
+ * value (NaN is never the best; -1 for a row of NaN).  The next token is the
+ * best of the first row whose draft falls, or of the row behind the drafts.
+ *   target  [B][n][V] in `dtype`: logits or probabilities, rows as above
+ * Everything else as in msa_verify.
+ */
+MSA_API int msa_verify_greedy(const void *target, int64_t target_req, int64_t target_row,
+                      int dtype, const int32_t *draft_tokens, const int32_t *num_drafts,
+                      int64_t B, int64_t n, int64_t V, int32_t *tokens, int32_t *accepted,
+                      void *stream);
 
 /*
  * For tests of the expiry path only: sets the wall-time limit, in

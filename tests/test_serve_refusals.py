@@ -1,0 +1,112 @@
+"""What the cache, attention and verification calls refuse, without a GPU:
+the binding's checks of shapes, types, strides and devices run before the
+library sees a pointer, and the library's own before anything is launched."""
+import ctypes
+
+import pytest
+import torch
+
+import block_sparse_attention_prefill_gb300 as msa
+
+
+def _err(fn, *args, **kw):
+    with pytest.raises(msa.MsaError) as e:
+        fn(*args, **kw)
+    return str(e.value)
+
+
+def _cache(T=6, H=2, B=2, pages=4):
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    return {"k": torch.zeros((T, H, 128)), "v": torch.zeros((T, H, 128)),
+            "kv": torch.zeros((pages, H, 128, 256), dtype=torch.uint8), "table": i32(B, 3), "cu_q": i32(B + 1), "cu_k": i32(B + 1)}
+
+
+def _write(c, fn=msa.msa_kv_write, **kw):
+    return _err(fn, c["k"], c["v"], c["kv"], 1.0, 1.0, c["table"], c["cu_q"], c["cu_k"], **kw)
+
+
+def test_write_refusals():
+    c = _cache()
+    assert "CUDA" in _write(c)
+    assert "[6, 2, 128]" in _write(dict(c, v=torch.zeros((6, 3, 128))))
+    assert "[6, 2, 128]" in _write(dict(c, v=torch.zeros((5, 2, 128))))
+    assert "different dtypes" in _write(dict(c, v=torch.zeros((6, 2, 128), dtype=torch.float16)))
+    assert "dtype" in _write(dict(c, k=c["k"].double()))
+    assert "contiguous" in _write(dict(c, k=torch.zeros((6, 2, 256))[..., ::2]))
+    assert "kv must be" in _write(dict(c, kv=c["kv"][:, :, :64]))
+    assert "kv must be contiguous" in _write(dict(c, kv=torch.zeros((4, 3, 128, 256), dtype=torch.uint8)[:, :2]))
+    assert "kv4 must be" in _write(c, msa.msa_kv_write_nvfp4)
+    assert "block_table must be" in _write(dict(c, table=c["table"][:1]))
+    assert "block_table must be" in _write(dict(c, table=c["table"][0]))
+    assert "block_table has dtype" in _write(dict(c, table=c["table"].long()))
+    assert "cu_seqlens_k must be" in _write(dict(c, cu_k=c["cu_k"][:2]))
+    assert "at least one" in _write(dict(c, cu_q=c["cu_q"][:0]))
+    assert "status" in _write(c, status=torch.zeros(2, dtype=torch.int32))
+    assert "k and v must be" in _write(dict(c, k=None))
+
+
+def test_read_refusals():
+    c = _cache()
+    run = lambda fn=msa.msa_kv_read, total=6, **kw: _err(fn, kw.pop("kv", c["kv"]), 1.0, 1.0, c["table"], c["cu_q"], total, **kw)  # noqa: E731
+    assert "CUDA" in run()
+    assert "starts must be" in run(starts=torch.zeros(3, dtype=torch.int32))
+    assert "kv has dtype" in run(kv=c["kv"].to(torch.int8))
+
+
+def test_verify_refusals():
+    t, d, x, u = torch.zeros((2, 4, 50)), torch.zeros((2, 3, 50)), torch.zeros((2, 3), dtype=torch.int32), torch.zeros((2, 4))
+    assert "CUDA" in _err(msa.msa_verify, t, x, u, d)
+    assert "CUDA" in _err(msa.msa_verify_greedy, t, x)
+    assert "target must be" in _err(msa.msa_verify, t[0], x, u, d)
+    assert "at least one row" in _err(msa.msa_verify_greedy, t[:, :0], x)
+    assert "rows must be contiguous" in _err(msa.msa_verify, t.transpose(1, 2), x, u, d)
+    assert "draft_tokens must be" in _err(msa.msa_verify, t, x[:, :2], u, d)
+    assert "draft_tokens has dtype" in _err(msa.msa_verify, t, x.long(), u, d)
+    assert "uniforms must be" in _err(msa.msa_verify, t, x, u[:, :3], d)
+    assert "uniforms has dtype" in _err(msa.msa_verify, t, x, u.double(), d)
+    assert "draft_probs must be" in _err(msa.msa_verify, t, x, u, t)
+    assert "draft_probs has dtype" in _err(msa.msa_verify, t, x, u, d.half())
+    assert "num_drafts must be" in _err(msa.msa_verify, t, x, u, d, torch.zeros(3, dtype=torch.int32))
+
+
+def test_library_refusals():
+    lib, P = msa.load(), ctypes.c_void_p
+    a = P(4096)  # never dereferenced: every call below ends on the host
+
+    def write(k=a, kt=256, kh=128, dtype=1, kv=a, pages=4, s=1.0, table=a, width=3, cu_q=a, cu_k=a, B=2, T=6, H=2, status=None, fn=lib.msa_kv_write):
+        return fn(k, kt, kh, a, 256, 128, dtype, kv, pages, s, 1.0, table, width, cu_q, cu_k, B, T, H, status, None)
+
+    for fn in (lib.msa_kv_write, lib.msa_kv_write_nvfp4):
+        assert write(B=0, fn=fn) == 0 and write(T=0, k=None, fn=fn) == 0
+        assert write(k=None, fn=fn) == 6 and write(kv=None, fn=fn) == 6 and write(table=None, fn=fn) == 6
+        assert write(cu_q=None, fn=fn) == 6 and write(cu_k=None, fn=fn) == 6
+        assert write(dtype=3, fn=fn) == 2
+        assert write(T=-1, fn=fn) == 1 and write(B=-1, fn=fn) == 1 and write(H=0, fn=fn) == 1 and write(H=128, fn=fn) == 1
+        assert write(T=2 ** 31, fn=fn) == 1 and write(pages=-1, fn=fn) == 1 and write(width=-1, fn=fn) == 1
+        for s in (0.0, -1.0, float("nan"), float("inf")):
+            assert write(s=s, fn=fn) == 1
+        assert write(kt=-256, fn=fn) == 1
+        assert write(kt=260, fn=fn) == 3 and write(kh=129, fn=fn) == 3 and write(k=P(4104), fn=fn) == 3
+        assert write(kv=P(4104), fn=fn) == 3 and write(cu_q=P(4098), fn=fn) == 3 and write(status=P(4098), fn=fn) == 3
+
+    def read(kv=a, cu=a, starts=None, k=a, dtype=0, T=6, s=1.0, fn=lib.msa_kv_read):
+        return fn(kv, 4, s, 1.0, a, 3, cu, starts, 2, T, 2, k, 256, 128, a, 256, 128, dtype, None, None)
+
+    for fn in (lib.msa_kv_read, lib.msa_kv_read_nvfp4):
+        assert read(kv=None, fn=fn) == 6 and read(cu=None, fn=fn) == 6 and read(k=None, fn=fn) == 6
+        assert read(dtype=9, fn=fn) == 2 and read(T=-1, fn=fn) == 1 and read(s=-1.0, fn=fn) == 1
+        assert read(starts=P(4097), fn=fn) == 3 and read(k=P(4100), fn=fn) == 3 and read(T=0, fn=fn) == 0
+
+    def verify(t=a, d=a, dtype=0, x=a, u=a, B=2, n=4, V=50, tokens=a, acc=a):
+        return lib.msa_verify(t, 200, 50, d, 150, 50, dtype, x, u, None, B, n, V, tokens, acc, None)
+
+    def greedy(t=a, dtype=0, x=a, B=2, n=4, V=50, tokens=a, acc=a):
+        return lib.msa_verify_greedy(t, 200, 50, dtype, x, None, B, n, V, tokens, acc, None)
+
+    for fn in (verify, greedy):
+        assert fn(B=0) == 0
+        assert fn(t=None) == 6 and fn(x=None) == 6 and fn(tokens=None) == 6 and fn(acc=None) == 6
+        assert fn(dtype=3) == 2
+        assert fn(n=0) == 1 and fn(n=33) == 1 and fn(V=0) == 1 and fn(V=2 ** 19) == 1 and fn(B=-1) == 1
+        assert fn(t=P(4098)) == 3 and fn(x=P(4097)) == 3 and fn(acc=P(4097)) == 3
+    assert verify(u=None) == 6 and verify(d=P(4097)) == 3 and verify(u=P(4097)) == 3
