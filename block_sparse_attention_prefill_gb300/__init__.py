@@ -15,6 +15,7 @@ Calls (same names as the C ABI, without the ``msa_`` prefix where noted):
   msa_nvfp4_to_e4m3   NVFP4 pages -> the E4M3 pages those calls read
   msa_kv_write, msa_kv_read (and _nvfp4)   new K/V tokens into the pages, and
                 cached tokens back out of them
+  msa_prefix_attention   dense attention behind pages that a batch shares
   msa_verify, msa_verify_greedy   which drafted tokens stand, and the next one
 """
 from __future__ import annotations
@@ -117,6 +118,11 @@ def load():
         "msa_kv_write_nvfp4": _WRITE,
         "msa_kv_read": _READ,
         "msa_kv_read_nvfp4": _READ,
+        "msa_prefix_attention_workspace_bytes": ([i64, i64, i64, i64, i64, i64,
+                                                  i64, SZ], i32),
+        "msa_prefix_attention": ([P, P, i64, f32, f32, f32, f32, P, i64, P, P,
+                                  i64, i64, i64, i64, i64, i64, i64, P,
+                                  ctypes.c_size_t, P, P, P, P], i32),
         "msa_verify": ([P, i64, i64, P, i64, i64, i32, P, P, P, i64, i64, i64,
                         P, P, P], i32),
         "msa_verify_greedy": ([P, i64, i64, i32, P, P, i64, i64, i64, P, P, P],
@@ -602,4 +608,5 @@ def run_workload(w, stream=None):
 
 
 from .serve import (msa_kv_read, msa_kv_read_nvfp4, msa_kv_write,  # noqa: E402,F401
-                    msa_kv_write_nvfp4, msa_verify, msa_verify_greedy)
+                    msa_kv_write_nvfp4, msa_prefix_attention,
+                    msa_verify, msa_verify_greedy, prefix_attention_workspace_bytes)

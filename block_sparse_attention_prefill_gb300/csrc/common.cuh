@@ -164,6 +164,27 @@ struct VerifyArgs {
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream);
 cudaError_t launch_verify_greedy(const VerifyArgs& a, cudaStream_t stream);
 
+// Dense attention behind a shared prefix (prefix_attention.cu).
+struct PrefixArgs {
+  const uint8_t* q;      // E4M3 [T][Hq][128]
+  const uint8_t* kv;     // E4M3 pool
+  int64_t num_pages;
+  float score_log2;      // q_scale * k_scale * softmax_scale * log2(e)
+  float v_scale;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int64_t B, T, Hq, Hkv, prefix_pages, max_q, max_k;
+  uint16_t* out;         // bf16 [T][Hq][128]
+  float* lse;            // [T][Hq] or NULL
+  uint32_t* status;      // or NULL
+};
+// Bytes of workspace, or 0 where the sizes are out of range.
+size_t prefix_workspace(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t prefix_pages,
+                        int64_t max_k);
+cudaError_t launch_prefix_attention(const PrefixArgs& a, void* ws, cudaStream_t stream);
+
 int num_sms();
 
 // Programmatic dependent launch.  A kernel launched with launch_pdl may

@@ -387,6 +387,18 @@ int verify_impl(const VerifyArgs& a, bool greedy, cudaStream_t st) {
   return cuda_rc(greedy ? launch_verify_greedy(a, st) : launch_verify(a, st));
 }
 
+// Host-side checks of the shared-prefix attention's sizes.
+int prefix_shape(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t prefix, int64_t max_q,
+                 int64_t max_k, size_t* bytes) {
+  if (B < 0 || T < 0 || Hq <= 0 || Hkv <= 0 || prefix < 0 || max_q < 0 || max_k < max_q ||
+      max_k > (1 << 30) || prefix * kPage > max_k || B >= kI32Max / 2)
+    return MSA_ERR_SHAPE;
+  if (Hq % Hkv != 0 || Hq / Hkv > kTileM || Hkv > 127) return MSA_ERR_UNSUPPORTED;
+  if (T >= kI32Max / kTopK || T * Hq >= kI32Max / kTopK) return MSA_ERR_SHAPE;
+  *bytes = prefix_workspace(B, T, Hq, Hkv, prefix, max_k);
+  return *bytes ? MSA_OK : MSA_ERR_SHAPE;
+}
+
 struct DecodeLayout {
   int64_t R;
   size_t cu_bytes, plan_bytes, prefill_bytes, total;
@@ -668,6 +680,58 @@ int msa_kv_read_nvfp4(const uint8_t* kv4, int64_t num_pages, float k_scale, floa
   return kv_read_impl(kv4, num_pages, k_scale, v_scale, block_table, bt_stride, cu_tokens, starts,
                       B, T, Hkv, k, k_token, k_head, v, v_token, v_head, dtype, status, stream,
                       true);
+}
+
+int msa_prefix_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv,
+                                         int64_t prefix_pages, int64_t max_seqlen_q,
+                                         int64_t max_seqlen_k, size_t* bytes) {
+  if (!bytes) return MSA_ERR_NULL;
+  return prefix_shape(B, T, Hq, Hkv, prefix_pages, max_seqlen_q, max_seqlen_k, bytes);
+}
+
+int msa_prefix_attention(const uint8_t* q, const uint8_t* kv, int64_t num_pages, float q_scale,
+                         float k_scale, float v_scale, float softmax_scale,
+                         const int32_t* block_table, int64_t bt_stride,
+                         const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int64_t B,
+                         int64_t T, int64_t Hq, int64_t Hkv, int64_t prefix_pages,
+                         int64_t max_seqlen_q, int64_t max_seqlen_k, void* workspace,
+                         size_t workspace_bytes, uint16_t* out, float* lse, uint32_t* status,
+                         void* stream) {
+  size_t need = 0;
+  int rc = prefix_shape(B, T, Hq, Hkv, prefix_pages, max_seqlen_q, max_seqlen_k, &need);
+  if (rc) return rc;
+  if (num_pages < 0 || num_pages * Hkv * kPage >= kI32Max ||
+      bt_stride < ceil_div(max_seqlen_k, kPage) || bt_stride > (1 << 24))
+    return MSA_ERR_SHAPE;
+  if (!(q_scale > 0.f) || !(k_scale > 0.f) || !(v_scale > 0.f) || !(softmax_scale > 0.f) ||
+      !std::isfinite(q_scale * k_scale * softmax_scale) || !std::isfinite(v_scale))
+    return MSA_ERR_SHAPE;
+  if (B == 0 || T == 0) return MSA_OK;
+  if (!q || !kv || !block_table || !cu_seqlens_q || !cu_seqlens_k || !out) return MSA_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(block_table, 4) ||
+      !aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4) || !aligned(out, 8) ||
+      !aligned(lse, 4) || !aligned(status, 4))
+    return MSA_ERR_ALIGN;
+  if (!workspace || workspace_bytes < need) return MSA_ERR_WORKSPACE;
+  if (!aligned(workspace, kAlign)) return MSA_ERR_ALIGN;
+  PrefixArgs a = {};
+  a.q = q;
+  a.kv = kv;
+  a.num_pages = num_pages;
+  a.score_log2 = (float)((double)q_scale * (double)k_scale * (double)softmax_scale *
+                         1.4426950408889634074);
+  a.v_scale = v_scale;
+  a.block_table = block_table;
+  a.bt_stride = bt_stride;
+  a.cu_q = cu_seqlens_q;
+  a.cu_k = cu_seqlens_k;
+  a.B = B, a.T = T, a.Hq = Hq, a.Hkv = Hkv;
+  a.prefix_pages = prefix_pages;
+  a.max_q = max_seqlen_q, a.max_k = max_seqlen_k;
+  a.out = out;
+  a.lse = lse;
+  a.status = status;
+  return cuda_rc(launch_prefix_attention(a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 int msa_verify(const void* target_probs, int64_t target_req, int64_t target_row,

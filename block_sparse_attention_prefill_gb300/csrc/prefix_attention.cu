@@ -1,0 +1,1017 @@
+// Dense causal attention over the paged E4M3 cache for a batch whose requests
+// share their first pages: the part over the shared pages is computed once
+// for all requests.  sm_103a: TMA, tcgen05, TMEM.
+//
+// With s_j = (q . k_j) c (c: the scales times log2 e) the kernel keeps, per
+// query row, a reference m near the running maximum, l = sum 2^(s_j - m) and
+// O = sum 2^(s_j - m) v_j over a range of pages; ranges are merged by their
+// l and m (combine kernel below).  QK is an E4M3 MMA, exact products with
+// fp32 sums; the probabilities are rounded to f16 (2^-12 of their value at
+// most) and V widened to f16 (exact), so that the bf16 output is limited by
+// its own rounding.
+//
+// Work.  Rows are (token, query head of one KV head).  A tile is up to 2 C
+// tokens, C = floor(128 / G), with a range of pages: the shared pages for
+// tiles over the whole batch's tokens (they lie before every query: no mask),
+// a request's own pages for tiles over its tokens.  Both are the same kind
+// of work.  A tile of more than C tokens is two 128-row halves that share
+// every page (pair); a smaller one has its pages dealt in turn to the two
+// streams, each with its own O (solo).  The tiles of all heads, laid end to
+// end and weighted by pages, are cut into one equal range per CTA, so no
+// CTA waits for a last wave and only tiles that a cut meets are split.
+//
+// Kernels: plan (one CTA: tiles and their place in the line), attend (one
+// persistent CTA per SM), combine.
+#include <cuda.h>
+
+#include <algorithm>
+#include <atomic>
+#include <climits>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "lookup.cuh"
+#include "partial.cuh"
+#include "ptx.cuh"
+
+namespace msa {
+namespace {
+
+// ------------------------------------------------------------------- tiles
+
+// Cost of a tile: its pages by kind, and its start and end (Q, epilogue).
+constexpr int kCostSolo = 2, kCostPair = 4, kCostTile = 4;
+constexpr int kMinShare = 8;  // least cost of a CTA's range
+
+// Behind every key (positions are below 2^30), with room for a tile's tokens.
+constexpr int kNoMask = INT_MAX - 1024;
+
+struct __align__(16) Tile {
+  int b;       // row of block_table
+  int tok0;    // first token
+  int ntok;    // tokens
+  int page0;   // first logical page
+  int npages;
+  int start;   // cost of the head's tiles before this one
+  int pos0;    // position of tok0, or kNoMask (the shared pages)
+  int seq;     // keys of the request (a page's keys behind it are not read)
+};
+struct PlanHead {
+  int ntiles, cost, shared_tiles;
+  int bad;  // lengths inconsistent: every output row becomes empty
+};
+
+__host__ __device__ inline int64_t max_tiles(int64_t B, int64_t T, int64_t C, int64_t prefix) {
+  const int64_t n = ceil_div(T, 2 * C);
+  return (prefix > 0 ? n : 0) + (T < n + B ? T : n + B);
+}
+
+__device__ __forceinline__ int tile_rate(int ntok, int C) { return ntok > C ? kCostPair : kCostSolo; }
+__device__ __forceinline__ int tile_cost(int ntok, int npages, int C) {
+  return npages * tile_rate(ntok, C) + kCostTile;
+}
+// Pages of a tile in front of cost y of its own.
+__device__ __forceinline__ int pages_before(int64_t y, int npages, int rate) {
+  if (y <= kCostTile) return 0;
+  const int64_t p = (y - kCostTile + rate - 1) / rate;
+  return p < npages ? (int)p : npages;
+}
+__device__ __forceinline__ int64_t share_of(int64_t total, int ctas) {
+  const int64_t s = (total + ctas - 1) / ctas;
+  return s > kMinShare ? s : kMinShare;
+}
+
+// Rows of the partials.  A tile's part at CTA i starts at row 256 i + (its
+// head's rows) + twice the tokens before it: parts in line order never
+// overlap, because a part has at most 256 rows (moving on by a CTA) and at
+// most twice its tile's rows (moving on by a tile).
+__device__ __forceinline__ int64_t part_row(int cta, int h, int tile, int shared_tiles, int tok0,
+                                            int T, int G) {
+  const int64_t rows = 2 * (int64_t)T * G;
+  const int64_t per_head = shared_tiles > 0 ? 2 * rows : rows;
+  return 256 * (int64_t)cta + h * per_head + (tile >= shared_tiles && shared_tiles > 0 ? rows : 0) +
+         2 * (int64_t)tok0 * G;
+}
+
+constexpr int kPlanThreads = 1024;
+
+__device__ __forceinline__ int block_excl_scan(int v, int* total) {
+  __shared__ int sums[33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += n;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    const int s = sums[lane];
+    int si = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, si, o);
+      if (lane >= o) si += n;
+    }
+    sums[lane] = si - s;
+    if (lane == 31) sums[32] = si;
+  }
+  __syncthreads();
+  const int r = sums[warp] + incl - v;
+  *total = sums[32];
+  __syncthreads();
+  return r;
+}
+
+struct PlanParams {
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int B, T, C, prefix;
+  int64_t max_q, max_k;
+  PlanHead* head;
+  Tile* tiles;
+  int32_t* req_tile;  // [B + 1] first suffix tile of each request
+  uint32_t* status;
+};
+
+// Lists the tiles of one head (every head has the same): first those over the
+// shared pages, then each request's own.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
+  __shared__ int s_bad, s_first;
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  if (tid == 0) s_bad = 0, s_first = INT_MAX;
+  __syncthreads();
+  const int T = p.cu_q[p.B];
+  bool bad = p.cu_q[0] != 0 || T < 0 || T > p.T;
+  int run = 0;  // tiles of the requests before this round's
+  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < p.B) {
+      const int64_t q = (int64_t)p.cu_q[b + 1] - p.cu_q[b];
+      const int64_t k = (int64_t)p.cu_k[b + 1] - p.cu_k[b];
+      if (q < 0 || k < q || q > p.max_q || k > p.max_k ||
+          (q > 0 && k - q < (int64_t)p.prefix * kPage))
+        bad = true;
+      else if (q > 0)
+        n = (int)((q + 2 * p.C - 1) / (2 * p.C)), atomicMin(&s_first, b);
+    }
+    int total;
+    const int before = block_excl_scan(n, &total);
+    if (b < p.B) p.req_tile[b] = run + before;
+    run += total;
+  }
+  if (bad) s_bad = 1;
+  if (tid == 0) p.req_tile[p.B] = run;
+  __syncthreads();  // also makes req_tile visible to this CTA
+  if (s_bad) {
+    if (tid == 0) {
+      *p.head = PlanHead{0, 0, 0, 1};
+      if (p.status) atomicOr(p.status, (unsigned)MSA_STATUS_BAD_SEQLENS);
+    }
+    return;
+  }
+  const int shared_tiles = p.prefix > 0 ? (T + 2 * p.C - 1) / (2 * p.C) : 0;
+  const int ntiles = shared_tiles + run;
+  int cost = 0;
+  for (int i0 = 0; i0 < ntiles; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    Tile t = {};
+    int c = 0;
+    if (i < ntiles) {
+      if (i < shared_tiles) {
+        t.b = s_first;
+        t.tok0 = i * 2 * p.C;
+        t.ntok = min(2 * p.C, T - t.tok0);
+        t.page0 = 0;
+        t.npages = p.prefix;
+        t.pos0 = kNoMask;
+        t.seq = p.prefix * kPage;
+      } else {
+        int lo = 0, hi = p.B - 1;  // the last request with req_tile[b] <= i
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) / 2;
+          if (p.req_tile[mid] <= i - shared_tiles) lo = mid; else hi = mid - 1;
+        }
+        const int q = p.cu_q[lo + 1] - p.cu_q[lo], k = p.cu_k[lo + 1] - p.cu_k[lo];
+        const int o = (i - shared_tiles - p.req_tile[lo]) * 2 * p.C;
+        t.b = lo;
+        t.tok0 = p.cu_q[lo] + o;
+        t.ntok = min(2 * p.C, q - o);
+        t.page0 = p.prefix;
+        t.pos0 = k - q + o;
+        t.npages = (t.pos0 + t.ntok - 1) / kPage + 1 - p.prefix;
+        t.seq = k;
+      }
+      c = tile_cost(t.ntok, t.npages, p.C);
+    }
+    int total;
+    t.start = cost + block_excl_scan(c, &total);
+    cost += total;
+    if (i < ntiles) p.tiles[i] = t;
+  }
+  if (tid == 0) *p.head = PlanHead{ntiles, cost, shared_tiles, 0};
+}
+
+// ------------------------------------------------------------------ attend
+
+constexpr int kThreads = 512;
+constexpr int kTileBytes = 128 * 128;       // an E4M3 tile of 128 x 128
+constexpr int kRaw = 3;                     // K and V pages in flight
+constexpr int kWide = 2;                    // V pages widened to f16
+constexpr int kOffQ = 0;
+constexpr int kOffK = kOffQ + 2 * kTileBytes;
+constexpr int kOffV = kOffK + kRaw * kTileBytes;
+constexpr int kOffW = kOffV + kRaw * kTileBytes;
+constexpr int kOffBars = kOffW + kWide * 2 * kTileBytes;
+struct Bars {
+  uint64_t q_full, q_free;
+  uint64_t k_full[kRaw], k_free[kRaw], v_full[kRaw], v_free[kRaw];
+  uint64_t w_full[kWide], w_free[kWide];
+  uint64_t s_full[2], p_full[2], pv_done[2], mma_done;
+  uint32_t tmem_base;
+  int abort;
+  int nan_seen;      // a NaN among the V codes of valid keys
+  int first_tile;
+  int nan_key[8][kD];  // per softmax warp
+};
+constexpr int kSmem = kOffBars + (int)sizeof(Bars) + 1024;
+static_assert(kSmem <= 232448, "shared memory of a CTA");
+constexpr int kTmemCols = 512;  // S of the two streams, then their O
+// 512 threads with 128 registers: control 64, softmax 2 x 192, widening 64
+constexpr int kRegsControl = 64, kRegsSoftmax = 192, kRegsWiden = 64;
+static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsWiden <= 512, "registers");
+// P is kept as 2^(s - m + 7): with m allowed to lag the maximum by 8 the
+// largest P is 2^15, in f16's range, and f16's subnormals begin 2^-21 below
+// the maximum instead of 2^-14
+constexpr float kLag = 8.f, kPShift = 7.f;
+
+struct AttendParams {
+  const PlanHead* head;
+  const Tile* tiles;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  const uint8_t* kv;
+  int num_pages;
+  int T, G, C, Hkv;
+  float score_log2;
+  float* part_o;    // rows of 128 fp32, normalised
+  float* part_lse;  // base-2 log-sum-exp of the row's part
+  uint32_t* status;
+  uint32_t wait_ns;
+};
+
+// One CTA's range of the line, tile by tile; each role walks it for itself.
+struct Walk {
+  const AttendParams& p;
+  int ntiles, shared_tiles;
+  int64_t cost, x, end, share;
+  int h, tile;
+  Tile t;
+  int p0, p1;        // pages of the tile in this range
+  __device__ Walk(const AttendParams& prm, const PlanHead& hd, int first_tile)
+      : p(prm), ntiles(hd.ntiles), shared_tiles(hd.shared_tiles), cost(hd.cost), tile(first_tile) {
+    const int64_t total = cost * p.Hkv;
+    share = share_of(total, gridDim.x);
+    x = min(total, blockIdx.x * share);
+    end = min(total, x + share);
+    h = cost > 0 ? (int)(x / cost) : 0;
+  }
+  // The next part with pages; false at the range's end.
+  __device__ __forceinline__ bool next() {
+    while (x < end) {
+      t = p.tiles[tile];
+      const int rate = tile_rate(t.ntok, p.C);
+      const int64_t t0 = h * cost + t.start;
+      const int64_t t1 = t0 + tile_cost(t.ntok, t.npages, p.C);
+      const int64_t e = min(end, t1);
+      p0 = pages_before(x - t0, t.npages, rate);
+      p1 = pages_before(e - t0, t.npages, rate);
+      cur_h = h;
+      cur_tile = tile;
+      x = e;
+      if (e == t1 && ++tile == ntiles) tile = 0, ++h;
+      if (p1 > p0) return true;
+    }
+    return false;
+  }
+  int cur_h, cur_tile;
+  __device__ __forceinline__ bool pair() const { return t.ntok > p.C; }
+  // pages that stream s handles of this part
+  __device__ __forceinline__ int stream_pages(int s) const {
+    return pair() ? p1 - p0 : (p1 - p0 + 1 - s) >> 1;
+  }
+  // the part's i-th page of stream s, counted from p0
+  __device__ __forceinline__ int stream_page(int s, int i) const { return pair() ? i : 2 * i + s; }
+};
+
+__device__ __forceinline__ void give_up(Bars* bars, uint32_t* status) {
+  *(volatile int*)&bars->abort = 1;
+  if (status) atomicOr(status, (unsigned)MSA_STATUS_TIMEOUT);
+}
+
+// A wait of a whole warp: all lanes poll (bounded_wait), all agree.
+__device__ __forceinline__ bool all_wait(Bars* bars, uint64_t* bar, uint32_t parity,
+                                         const AttendParams& p) {
+  const bool ok = bounded_wait(bar, parity, &bars->abort, p.wait_ns);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  if ((threadIdx.x & 31) == 0 && !*(volatile int*)&bars->abort) give_up(bars, p.status);
+  return false;
+}
+
+// Four E4M3 codes -> four f16 in two words (exact).
+__device__ __forceinline__ uint2 widen4(uint32_t c) {
+  const __half2_raw a =
+      __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xFFFFu), __NV_E4M3);
+  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> 16), __NV_E4M3);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+// 0x80 in each byte of w whose E4M3 code is NaN (0x7F or 0xFF).
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
+              const AttendParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars* bars = reinterpret_cast<Bars*>(smem + kOffBars);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const volatile int* abort = &bars->abort;
+
+  if (tid == 0) {
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_free, 1);
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(&bars->k_full[i], 1);
+      mbar_init(&bars->k_free[i], 1);
+      mbar_init(&bars->v_full[i], 1);
+      mbar_init(&bars->v_free[i], 4);
+    }
+    for (int i = 0; i < kWide; ++i) {
+      mbar_init(&bars->w_full[i], 4);
+      mbar_init(&bars->w_free[i], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->s_full[s], 1);
+      mbar_init(&bars->p_full[s], 4);
+      mbar_init(&bars->pv_done[s], 1);
+    }
+    mbar_init(&bars->mma_done, 1);
+    bars->abort = 0;
+    bars->nan_seen = 0;
+    bars->first_tile = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tmem_alloc(&bars->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_trigger();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  const PlanHead hd = *p.head;
+  // the tile that this CTA's range starts in
+  {
+    const int64_t total = (int64_t)hd.cost * p.Hkv;
+    const int64_t x = blockIdx.x * share_of(total, gridDim.x);
+    if (x < total) {
+      const int r = (int)(x % hd.cost);
+      for (int i = tid; i < hd.ntiles; i += kThreads)
+        if (p.tiles[i].start <= r && (i + 1 == hd.ntiles || p.tiles[i + 1].start > r))
+          bars->first_tile = i;
+    }
+  }
+  __syncthreads();
+  Walk walk(p, hd, bars->first_tile);
+
+  if (warp < 4) {
+    setmaxnreg_dec<kRegsControl>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      int g = 0, part = 0;  // pages and parts so far
+      int q_loads = 0;
+      bool ok = true;
+      while (ok && walk.next()) {
+        const Tile& t = walk.t;
+        if (lane == 0) {
+          if (part > 0) ok = bounded_wait(&bars->q_free, (part - 1) & 1, abort, p.wait_ns);
+          if (ok) {
+            const int boxes = walk.pair() ? 2 : 1;
+            mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(boxes * p.C * p.G * kD));
+            for (int s = 0; s < boxes; ++s)
+              tma_load_3d(smem + kOffQ + s * kTileBytes, &q_map, &bars->q_full, 0,
+                          walk.cur_h * p.G, t.tok0 + s * p.C);
+            ++q_loads;
+          }
+        }
+        ++part;
+        const int32_t* table = p.block_table + t.b * p.bt_stride + t.page0;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        for (int j0 = walk.p0; ok && j0 < walk.p1; j0 += 32) {
+          const int mine = j0 + lane < walk.p1 ? __ldg(table + j0 + lane) : 0;
+          const int n = min(32, walk.p1 - j0);
+          for (int j = 0; j < n; ++j, ++g) {
+            const int page = __shfl_sync(0xffffffffu, mine, j);
+            if (lane == 0) {
+              const int slot = g % kRaw;
+              const uint32_t ph = ((g / kRaw) - 1) & 1;
+              const bool there = page >= 0 && page < p.num_pages;
+              if (!there && p.status) atomicOr(p.status, (unsigned)MSA_STATUS_BAD_BLOCK);
+              const int y = there ? (page * p.Hkv + walk.cur_h) * kPage : 0;
+              if (g >= kRaw) ok = bounded_wait(&bars->k_free[slot], ph, abort, p.wait_ns);
+              if (ok) {
+                if (there) {
+                  mbar_arrive_expect_tx(&bars->k_full[slot], kTileBytes);
+                  tma_load_2d(smem + kOffK + slot * kTileBytes, &kv_map, &bars->k_full[slot], 0, y);
+                } else {
+                  mbar_arrive(&bars->k_full[slot]);
+                }
+                if (g >= kRaw) ok = bounded_wait(&bars->v_free[slot], ph, abort, p.wait_ns);
+                if (ok) {
+                  if (there) {
+                    mbar_arrive_expect_tx(&bars->v_full[slot], kTileBytes);
+                    tma_load_2d(smem + kOffV + slot * kTileBytes, &kv_map, &bars->v_full[slot], kD,
+                                y);
+                  } else {
+                    mbar_arrive(&bars->v_full[slot]);
+                  }
+                } else {
+                  // the K load of this page has no V load beside it: waited
+                  // for here, the drain below counts whole pages
+                  bounded_wait(&bars->k_full[slot], (g / kRaw) & 1, nullptr, kWaitLimitNs);
+                }
+              }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+          }
+        }
+      }
+      if (lane == 0) {
+        if (!ok && !*abort) give_up(bars, p.status);
+        // every copy lands before the CTA may end
+        for (int i = max(0, g - kRaw); i < g; ++i) {
+          bounded_wait(&bars->k_full[i % kRaw], (i / kRaw) & 1, nullptr, kWaitLimitNs);
+          bounded_wait(&bars->v_full[i % kRaw], (i / kRaw) & 1, nullptr, kWaitLimitNs);
+        }
+        if (q_loads > 0)
+          bounded_wait(&bars->q_full, (q_loads - 1) & 1, nullptr, kWaitLimitNs);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      if (lane == 0) {
+        // ------------------------------------------------------ MMA issuer
+        // Per stream QK(0) PV(0) QK(1) PV(1) ..., each as soon as what it
+        // needs is there; the streams are independent.  P overwrites its S,
+        // so QK(i + 1) waits until PV(i) has completed.
+        constexpr uint32_t kQk = idesc_e4m3_f32(128, 128, false);
+        constexpr uint32_t kPv = idesc_f16_f32(128, 128, true);
+        int g0 = 0, part = 0;
+        uint32_t done_s[2] = {0, 0};  // S tiles, PVs issued per stream
+        bool ok = true;
+        while (ok && walk.next()) {
+          const bool pair = walk.pair();
+          const int n[2] = {walk.stream_pages(0), walk.stream_pages(1)};
+          int qk[2] = {0, 0}, pv[2] = {0, 0};
+          bool have_q = false;
+          uint32_t idle = 0, since = 0;
+          while (pv[0] < n[0] || pv[1] < n[1]) {
+            bool moved = false;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              if (qk[s] == pv[s] && qk[s] < n[s]) {
+                const int g = g0 + walk.stream_page(s, qk[s]);
+                if ((have_q || (have_q = mbar_test(&bars->q_full, part & 1))) &&
+                    (done_s[s] == 0 || mbar_test(&bars->pv_done[s], (done_s[s] - 1) & 1)) &&
+                    mbar_test(&bars->k_full[g % kRaw], (g / kRaw) & 1)) {
+                  tc_fence_after();
+                  const uint32_t qa =
+                      smem_u32(smem + kOffQ + (pair ? s : 0) * kTileBytes);
+                  const uint32_t kb = smem_u32(smem + kOffK + (g % kRaw) * kTileBytes);
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk)
+                    mma_f8f6f4(tmem + s * 128, smem_desc_sw128(qa + kk * 32, 16, 1024),
+                               smem_desc_sw128(kb + kk * 32, 16, 1024), kQk, kk > 0);
+                  mma_commit(&bars->s_full[s]);
+                  ++qk[s];
+                  if (!pair || qk[s ^ 1] >= qk[s]) mma_commit(&bars->k_free[g % kRaw]);
+                  if (qk[0] == n[0] && qk[1] == n[1]) mma_commit(&bars->q_free);
+                  moved = true;
+                }
+              } else if (pv[s] < qk[s]) {
+                const int g = g0 + walk.stream_page(s, pv[s]);
+                if (mbar_test(&bars->p_full[s], done_s[s] & 1) &&
+                    mbar_test(&bars->w_full[g % kWide], (g / kWide) & 1)) {
+                  tc_fence_after();
+                  const uint32_t vb = smem_u32(smem + kOffW + (g % kWide) * 2 * kTileBytes);
+#pragma unroll
+                  for (int kk = 0; kk < 8; ++kk)
+                    mma_f16_ts(tmem + 256 + s * 128, tmem + s * 128 + kk * 8,
+                               smem_desc_sw128(vb + kk * 16 * 128, kTileBytes, 1024), kPv,
+                               pv[s] > 0 || kk > 0);
+                  mma_commit(&bars->pv_done[s]);
+                  ++pv[s];
+                  ++done_s[s];
+                  if (!pair || pv[s ^ 1] >= pv[s]) mma_commit(&bars->w_free[g % kWide]);
+                  moved = true;
+                }
+              }
+            }
+            if (moved) {
+              idle = 0;
+            } else if ((++idle & 63u) == 0) {
+              if (idle == 64u) since = (uint32_t)global_timer_ns();
+              if (*abort || (uint32_t)global_timer_ns() - since > p.wait_ns) {
+                ok = false;
+                break;
+              }
+            }
+          }
+          g0 += walk.p1 - walk.p0;
+          ++part;
+        }
+        if (!ok && !*abort) give_up(bars, p.status);
+        mma_commit(&bars->mma_done);
+        bounded_wait(&bars->mma_done, 0, nullptr, kWaitLimitNs);
+      }
+      __syncwarp();
+    }
+  } else if (warp < 12) {
+    setmaxnreg_inc<kRegsSoftmax>();
+    // ------------------------------------------------------------- softmax
+    const int s = warp >= 8, quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t s_tmem = tmem + lane_off + s * 128, o_tmem = s_tmem + 256;
+    const float c = p.score_log2;
+    const int i_tok = row / p.G;
+    uint32_t done = 0;  // pages of this stream so far
+    bool ok = true;
+    while (ok && walk.next()) {
+      const Tile& t = walk.t;
+      const bool pair = walk.pair();
+      const int n = walk.stream_pages(s);
+      const int ntok = pair ? (s ? t.ntok - p.C : p.C) : t.ntok;
+      const bool valid = i_tok < ntok;
+      const int tok = i_tok + (pair && s ? p.C : 0);  // within the tile
+      const int pos = t.pos0 + tok;
+      const int32_t* table = p.block_table + t.b * p.bt_stride + t.page0;
+      float m = -INFINITY, l = 0.f;  // m: scores in units of 1 (not log2)
+      int page = n > 0 ? __ldg(table + walk.p0 + walk.stream_page(s, 0)) : 0;
+      for (int i = 0; i < n; ++i, ++done) {
+        const int j = walk.p0 + walk.stream_page(s, i);
+        const bool there = page >= 0 && page < p.num_pages;
+        if (i + 1 < n) page = __ldg(table + walk.p0 + walk.stream_page(s, i + 1));
+        // the last key of the page that this row attends to
+        const int lim = there ? pos - (t.page0 + j) * kPage : -1;
+        if (!all_wait(bars, &bars->s_full[s], done & 1, p)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t r[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(s_tmem + q * 32, r[q]);
+        tmem_wait_ld();
+        if (__any_sync(0xffffffffu, lim < kPage - 1)) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (q * 32 + e > lim) r[q][e] = 0xFF800000u;  // -inf
+        }
+        float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(r[q][e]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // O and l are moved to a new reference only where the maximum has
+        // grown by more than 2^kLag.  PV of the page before has completed:
+        // this page's QK was issued after it.
+        const bool grown = i == 0 || (top - m) * c > kLag || (m == -INFINITY && top > m);
+        if (__any_sync(0xffffffffu, grown)) {
+          const float f = m == -INFINITY ? 0.f : ex2_approx((m - top) * c);
+          if (i > 0) {
+            l *= f;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              uint32_t o[32];
+              tmem_ld32(o_tmem + q * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(o_tmem + q * 32, o);
+            }
+          }
+          m = top;
+        }
+        const float off = m == -INFINITY ? 0.f : kPShift - m * c;
+        float lq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t* x = &r[half * 2 + (e >> 4)][2 * (e & 15)];
+            const float a = ex2_approx(fmaf(__uint_as_float(x[0]), c, off));
+            const float b = ex2_approx(fmaf(__uint_as_float(x[1]), c, off));
+            lq[(2 * e) & 3] += a;
+            lq[(2 * e + 1) & 3] += b;
+            const __half2 h = __floats2half2_rn(a, b);
+            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          tmem_st32(s_tmem + half * 32, w);
+        }
+        l += (lq[0] + lq[1]) + (lq[2] + lq[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[s]);
+      }
+      if (!ok) break;
+      // the part: O / l and log2 of the row's sum
+      const int64_t prow = part_row(blockIdx.x, walk.cur_h, walk.cur_tile, walk.shared_tiles, t.tok0,
+                                    p.T, p.G) +
+                           (s ? (pair ? p.C : t.ntok) * p.G : 0) + row;
+      if (n > 0) {
+        if (!all_wait(bars, &bars->pv_done[s], (done - 1) & 1, p)) break;
+        tc_fence_after();
+        bool poison = __any_sync(0xffffffffu, *(volatile int*)&bars->nan_seen != 0);
+        int* nan_key = bars->nan_key[warp - 4];
+        if (poison) {
+          // A NaN lies among the V codes of some valid key.  Widening wrote
+          // it as 0, since a probability of 0 must hide it; now each warp
+          // finds, for each column, the first position of this part that has
+          // one (a rare path: no care is taken of its speed).
+          __syncwarp();
+          for (int k = lane; k < kD; k += 32) nan_key[k] = INT_MAX;
+          __syncwarp();
+          for (int i = 0; i < n; ++i) {
+            const int j = walk.p0 + walk.stream_page(s, i);
+            const int pg = __ldg(table + j);
+            if (pg < 0 || pg >= p.num_pages) continue;
+            const uint8_t* v = p.kv + ((int64_t)pg * p.Hkv + walk.cur_h) * kPage * (2 * kD) + kD;
+            const int base = (t.page0 + j) * kPage;
+            for (int k = 0; k < kPage && base + k < t.seq; ++k) {
+              const uint32_t bad = nan_bytes(
+                  __ldg(reinterpret_cast<const uint32_t*>(v + k * (2 * kD)) + lane));
+              for (int e = 0; e < 4; ++e)
+                if ((bad >> (8 * e)) & 0x80u)
+                  nan_key[lane * 4 + e] = min(nan_key[lane * 4 + e], base + k);
+            }
+          }
+          __syncwarp();
+        }
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t o[32];
+          tmem_ld32(o_tmem + q * 32, o);
+          tmem_wait_ld();
+          if (valid) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float v = __uint_as_float(o[e]) * inv;
+              if (poison && nan_key[q * 32 + e] <= pos) v = NAN;
+              o[e] = __float_as_uint(v);
+            }
+            uint32_t* dst = reinterpret_cast<uint32_t*>(p.part_o + prow * kD) + q * 32;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              st_global_v8(dst + e, o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5],
+                           o[e + 6], o[e + 7]);
+          }
+        }
+        tc_fence_before();
+      }
+      if (valid)
+        p.part_lse[prow] = n > 0 && l != 0.f ? m * c - kPShift + log2f(l) : -INFINITY;
+    }
+  } else {
+    setmaxnreg_dec<kRegsWiden>();
+    // -------------------------------------------------------------- widen
+    // 128 threads: a page's V codes in 16-code chunks; chunk e is codes
+    // 16 (e % 8) .. of key e / 8, read through the TMA's 128-byte swizzle and
+    // written as two 16-byte chunks of the f16 tile [keys][dims], two blocks
+    // of 64 dims, 128-byte swizzle.
+    const int wt = tid - 384;
+    int g = 0;
+    bool ok = true;
+    while (ok && walk.next()) {
+      const Tile& t = walk.t;
+      const int32_t* table = p.block_table + t.b * p.bt_stride + t.page0;
+      for (int j = walk.p0; j < walk.p1; ++j, ++g) {
+        const int page = __ldg(table + j);
+        const int keys =
+            page >= 0 && page < p.num_pages ? min(kPage, t.seq - (t.page0 + j) * kPage) : 0;
+        if (!all_wait(bars, &bars->v_full[g % kRaw], (g / kRaw) & 1, p) ||
+            (g >= kWide && !all_wait(bars, &bars->w_free[g % kWide], ((g / kWide) - 1) & 1, p))) {
+          ok = false;
+          break;
+        }
+        const uint8_t* src = smem + kOffV + (g % kRaw) * kTileBytes;
+        uint8_t* dst = smem + kOffW + (g % kWide) * 2 * kTileBytes;
+        bool nan = false;
+#pragma unroll 4
+        for (int u = 0; u < 8; ++u) {
+          const int e = wt + u * 128, key = e >> 3, ch = e & 7;
+          uint4 v = *reinterpret_cast<const uint4*>(src + key * 128 + ((ch ^ (key & 7)) << 4));
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          if (key >= keys) w[0] = w[1] = w[2] = w[3] = 0u;
+          const uint32_t bad = nan_bytes(w[0]) | nan_bytes(w[1]) | nan_bytes(w[2]) | nan_bytes(w[3]);
+          if (bad) {
+            nan = true;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] &= ~((nan_bytes(w[k]) >> 7) * 0xFFu);
+          }
+          const uint2 a = widen4(w[0]), b = widen4(w[1]), cc = widen4(w[2]), d = widen4(w[3]);
+          uint8_t* row = dst + (ch >> 2) * kTileBytes + key * 128;
+          const int c0 = (ch & 3) * 2;
+          *reinterpret_cast<uint4*>(row + ((c0 ^ (key & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+          *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (key & 7)) << 4)) =
+              make_uint4(cc.x, cc.y, d.x, d.y);
+        }
+        if (nan) *(volatile int*)&bars->nan_seen = 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars->v_free[g % kRaw]);
+          mbar_arrive(&bars->w_full[g % kWide]);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ----------------------------------------------------------------- combine
+
+constexpr int kCombineWarps = 8;
+
+struct CombineParams {
+  const PlanHead* head;
+  const Tile* tiles;
+  const int32_t* req_tile;
+  const int32_t* cu_q;
+  int B, T, Hq, Hkv, G, C, ctas;
+  const float* part_o;
+  const float* part_lse;
+  float v_scale;
+  uint16_t* out;
+  float* lse;
+};
+
+// One row (token, query head): kTeam warps share its parts.
+template <int kTeam>
+__global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const CombineParams p) {
+  __shared__ float s_acc[kTeam > 1 ? kCombineWarps : 1][kD];
+  __shared__ float s_m[kCombineWarps], s_l[kCombineWarps];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int member = warp % kTeam;
+  const int64_t r = ((int64_t)blockIdx.x * kCombineWarps + warp) / kTeam;
+  const PlanHead hd = *p.head;
+  const int T = p.cu_q[p.B];
+  const int tok = (int)min(r / p.Hq, (int64_t)p.T), hq = (int)(r % p.Hq);
+  // rows behind the last sequence keep what they hold
+  const bool live = r < (int64_t)p.T * p.Hq && (hd.bad || tok < T);
+  if (kTeam == 1 && !live) return;
+  float m = -INFINITY, l = 0.f;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  if (live && !hd.bad) {
+    const int h = hq / p.G, g = hq - h * p.G;
+    const int b = min(warp_request_of(p.cu_q, p.B, tok), p.B - 1);
+    const int64_t share = share_of((int64_t)hd.cost * p.Hkv, p.ctas);
+    for (int kind = hd.shared_tiles > 0 ? 0 : 1; kind < 2; ++kind) {
+      const int tile = kind == 0
+                           ? tok / (2 * p.C)
+                           : hd.shared_tiles + p.req_tile[b] + (tok - p.cu_q[b]) / (2 * p.C);
+      const Tile t = p.tiles[tile];
+      const bool pair = t.ntok > p.C;
+      const int rate = tile_rate(t.ntok, p.C);
+      const int64_t t0 = (int64_t)h * hd.cost + t.start;
+      const int64_t t1 = t0 + tile_cost(t.ntok, t.npages, p.C);
+      const int i0 = (int)(t0 / share), i1 = (int)((t1 - 1) / share);
+      const int o = tok - t.tok0;
+      // entries: (CTA, stream) of a solo tile, CTA of a pair
+      const int entries = (i1 - i0 + 1) * (pair ? 1 : 2);
+      for (int e0 = member * 32; e0 < entries; e0 += kTeam * 32) {
+        const int e = e0 + lane;
+        float le = -INFINITY;
+        int64_t row = 0;
+        if (e < entries) {
+          const int cta = i0 + (pair ? e : e >> 1), s = pair ? o >= p.C : e & 1;
+          const int pa = pages_before(max(cta * share, t0) - t0, t.npages, rate);
+          const int pb = pages_before(min((cta + 1) * share, t1) - t0, t.npages, rate);
+          if (pb > pa) {
+            row = part_row(cta, h, tile, hd.shared_tiles, t.tok0, p.T, p.G) +
+                  (s ? (pair ? p.C : t.ntok) * p.G : 0) + (pair && s ? o - p.C : o) * p.G + g;
+            le = __ldg(p.part_lse + row);
+          }
+        }
+        float top = le;
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+        top = fmaxf(top, m);
+        if (top > m) {
+          const float f = m == -INFINITY ? 0.f : exp2f(m - top);
+          l *= f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[k] *= f;
+          m = top;
+        }
+        // NaN (a NaN score) stays one
+        const float w = le == -INFINITY ? 0.f : exp2f(le - (m == -INFINITY ? 0.f : m));
+        uint32_t bits = __ballot_sync(0xffffffffu, w != 0.f);
+        while (bits) {
+          float4 v[8];
+          float wj[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int j = bits ? __ffs(bits) - 1 : 0;
+            wj[k] = bits ? __shfl_sync(0xffffffffu, w, j) : 0.f;
+            const int64_t rj = __shfl_sync(0xffffffffu, row, j);
+            v[k] = bits ? __ldcg(reinterpret_cast<const float4*>(p.part_o + rj * kD) + lane)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+            bits &= bits - 1;
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            l += wj[k];
+            acc[0] = fmaf(wj[k], v[k].x, acc[0]);
+            acc[1] = fmaf(wj[k], v[k].y, acc[1]);
+            acc[2] = fmaf(wj[k], v[k].z, acc[2]);
+            acc[3] = fmaf(wj[k], v[k].w, acc[3]);
+          }
+        }
+      }
+    }
+  }
+  if (kTeam > 1) {
+    if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+    *reinterpret_cast<float4*>(&s_acc[warp][lane * 4]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    __syncthreads();
+    if (member != 0 || !live) return;
+    float top = -INFINITY;
+    for (int k = 0; k < kTeam; ++k) top = fmaxf(top, s_m[warp + k]);
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = 0.f;
+    for (int k = 0; k < kTeam; ++k) {
+      const float f = s_m[warp + k] == -INFINITY && s_l[warp + k] == 0.f
+                          ? 0.f
+                          : exp2f(s_m[warp + k] - (top == -INFINITY ? 0.f : top));
+      const float f2 = s_l[warp + k] == s_l[warp + k] ? f : s_l[warp + k];
+      l += f2 * s_l[warp + k];
+      const float4 v = *reinterpret_cast<const float4*>(&s_acc[warp + k][lane * 4]);
+      acc[0] = fmaf(f2, v.x, acc[0]);
+      acc[1] = fmaf(f2, v.y, acc[1]);
+      acc[2] = fmaf(f2, v.z, acc[2]);
+      acc[3] = fmaf(f2, v.w, acc[3]);
+    }
+    m = top;
+  }
+  const float scale = l == 0.f ? 0.f : p.v_scale / l;
+  const uint2 v = make_uint2(pack_bf16x2(acc[0] * scale, acc[1] * scale),
+                             pack_bf16x2(acc[2] * scale, acc[3] * scale));
+  *reinterpret_cast<uint2*>(p.out + r * kD + lane * 4) = v;
+  if (p.lse && lane == 0)
+    p.lse[r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+}
+
+// -------------------------------------------------------------------- host
+
+struct Layout {
+  size_t head, tiles, req_tile, part_o, part_lse, total;
+};
+
+bool layout(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t prefix, int64_t max_k, int ctas,
+            Layout* l) {
+  const int64_t G = Hq / Hkv, C = kTileM / G;
+  const int64_t tiles = max_tiles(B, T, C, prefix);
+  // costs and partial rows in range of their integers
+  if ((double)tiles * (double)(ceil_div(max_k, kPage) * kCostPair + kCostTile) > 1.0e9) return false;
+  const int64_t rows = 256 * ((int64_t)ctas + 1) + Hkv * (prefix > 0 ? 4 : 2) * T * G;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  l->head = 0;
+  l->tiles = 256;
+  l->req_tile = l->tiles + up((size_t)tiles * sizeof(Tile));
+  l->part_lse = l->req_tile + up((size_t)(B + 1) * sizeof(int32_t));
+  l->part_o = l->part_lse + up((size_t)rows * sizeof(float));
+  l->total = l->part_o + (size_t)rows * kD * sizeof(float);
+  return true;
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static std::atomic<EncodeTiledFn> fn{nullptr};
+  EncodeTiledFn f = fn.load();
+  if (!f) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn.store(f = reinterpret_cast<EncodeTiledFn>(ptr));
+  }
+  return f;
+}
+
+bool encode(EncodeTiledFn enc, CUtensorMap* map, const void* base, int dims, const cuuint64_t* size,
+            const cuuint64_t* stride, const cuuint32_t* box) {
+  const cuuint32_t one[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, dims, const_cast<void*>(base), size, stride, box,
+             one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+size_t prefix_workspace(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t prefix_pages,
+                        int64_t max_k) {
+  Layout l;
+  return layout(B, T, Hq, Hkv, prefix_pages, max_k, num_sms(), &l) ? l.total : 0;
+}
+
+cudaError_t launch_prefix_attention(const PrefixArgs& a, void* ws, cudaStream_t stream) {
+  const int ctas = num_sms();
+  const int G = (int)(a.Hq / a.Hkv), C = kTileM / G;
+  Layout l;
+  if (!layout(a.B, a.T, a.Hq, a.Hkv, a.prefix_pages, a.max_k, ctas, &l)) return cudaErrorInvalidValue;
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  CUtensorMap kv_map, q_map;
+  const cuuint64_t kv_size[2] = {2 * kD, (cuuint64_t)(std::max<int64_t>(a.num_pages, 1) * a.Hkv * kPage)};
+  const cuuint64_t kv_stride[1] = {2 * kD};
+  const cuuint32_t kv_box[2] = {kD, kPage};
+  const cuuint64_t q_size[3] = {kD, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
+  const cuuint64_t q_stride[2] = {kD, (cuuint64_t)(a.Hq * kD)};
+  const cuuint32_t q_box[3] = {kD, (cuuint32_t)G, (cuuint32_t)C};
+  if (!encode(enc, &kv_map, a.kv, 2, kv_size, kv_stride, kv_box) ||
+      !encode(enc, &q_map, a.q, 3, q_size, q_stride, q_box))
+    return cudaErrorInvalidValue;
+  char* base = static_cast<char*>(ws);
+  PlanHead* head = reinterpret_cast<PlanHead*>(base + l.head);
+  Tile* tiles = reinterpret_cast<Tile*>(base + l.tiles);
+  int32_t* req_tile = reinterpret_cast<int32_t*>(base + l.req_tile);
+  float* part_lse = reinterpret_cast<float*>(base + l.part_lse);
+  float* part_o = reinterpret_cast<float*>(base + l.part_o);
+
+  const PlanParams pp = {a.cu_q, a.cu_k, (int)a.B, (int)a.T, C, (int)a.prefix_pages, a.max_q,
+                         a.max_k, head, tiles, req_tile, a.status};
+  cudaError_t e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pp);
+  if (e != cudaSuccess) return e;
+
+  constexpr int kMaxDevices = 64;
+  static std::atomic<bool> attr_set[kMaxDevices];
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices || !attr_set[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices) attr_set[dev].store(true, std::memory_order_release);
+  }
+  const AttendParams ap = {head, tiles, a.block_table, a.bt_stride, a.kv, (int)a.num_pages,
+                           (int)a.T, G, C, (int)a.Hkv, a.score_log2, part_o, part_lse, a.status,
+                           (uint32_t)std::min<uint64_t>(pipeline_wait_limit_ns(), kWaitLimitNs)};
+  e = launch_pdl(attend_kernel, dim3((unsigned)ctas), dim3(kThreads), (size_t)kSmem, stream, kv_map,
+                 q_map, ap);
+  if (e != cudaSuccess) return e;
+
+  const CombineParams cp = {head, tiles, req_tile, a.cu_q, (int)a.B, (int)a.T, (int)a.Hq,
+                            (int)a.Hkv, G, C, ctas, part_o, part_lse, a.v_scale, a.out, a.lse};
+  const int64_t rows = a.T * a.Hq;
+  // few rows have many parts each: a CTA per row; else a warp per row
+  if (rows <= 2048)
+    return launch_pdl(combine_kernel<kCombineWarps>, dim3((unsigned)rows),
+                      dim3(kCombineWarps * 32), 0, stream, cp);
+  return launch_pdl(combine_kernel<1>, dim3((unsigned)ceil_div(rows, kCombineWarps)),
+                    dim3(kCombineWarps * 32), 0, stream, cp);
+}
+
+}  // namespace msa

@@ -202,6 +202,58 @@ def msa_kv_read_nvfp4(kv4, k_scale, v_scale, block_table, cu_tokens, total_token
                  total_tokens, starts, dtype, k, v, status, stream)
 
 
+def prefix_attention_workspace_bytes(B, T, Hq, Hkv, prefix_pages, max_seqlen_q,
+                                     max_seqlen_k) -> int:
+    n = ctypes.c_size_t()
+    _check(load().msa_prefix_attention_workspace_bytes(B, T, Hq, Hkv, prefix_pages, max_seqlen_q,
+                                                       max_seqlen_k, ctypes.byref(n)),
+           "msa_prefix_attention_workspace_bytes")
+    return n.value
+
+
+def msa_prefix_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_table,
+                         cu_seqlens_q, cu_seqlens_k, prefix_pages, max_seqlen_q, max_seqlen_k,
+                         workspace=None, out=None, lse=None, want_lse=True, status=None,
+                         stream=None):
+    """Dense causal attention over the E4M3 pool for a batch whose requests
+    share their first prefix_pages pages, whose part is computed once for all
+    (0: nothing shared).  q E4M3 [T, Hq, 128]; lengths as in msa_plan, all
+    queries behind the shared pages.  status: an int32 [1] tensor that
+    MSA_STATUS_* bits are OR-ed into.  Returns (out bf16 [T, Hq, 128], lse
+    fp32 [T, Hq] or None)."""
+    pages, Hkv = _pool(kv, False)
+    _tensor(q, "q", _E4M3, (None, None, HEAD_DIM))
+    T, Hq, _ = q.shape
+    B = _requests(cu_seqlens_q, "cu_seqlens_q")
+    _requests(cu_seqlens_k, "cu_seqlens_k", B)
+    width = _table(block_table, B)
+    _status(status)
+    if out is not None:
+        _tensor(out, "out", (torch.bfloat16,), (T, Hq, HEAD_DIM))
+    if lse is not None:
+        _tensor(lse, "lse", _F32, (T, Hq))
+    need = prefix_attention_workspace_bytes(B, T, Hq, Hkv, prefix_pages, max_seqlen_q,
+                                            max_seqlen_k)
+    if workspace is not None:
+        _tensor(workspace, "workspace", (torch.uint8,))
+        if workspace.numel() < need:
+            _fail("workspace too small: %d < %d bytes", workspace.numel(), need)
+    dev = _place(q, kv, block_table, cu_seqlens_q, cu_seqlens_k, workspace, out, lse, status)
+    handle = _handle(stream, dev)
+    if workspace is None:
+        workspace = _new(need, torch.uint8, dev, handle)
+    if out is None:
+        out = _new((T, Hq, HEAD_DIM), torch.bfloat16, dev, handle)
+    if lse is None and want_lse:
+        lse = _new((T, Hq), torch.float32, dev, handle)
+    _check(load().msa_prefix_attention(
+        q.data_ptr(), kv.data_ptr(), pages, q_scale, k_scale, v_scale, softmax_scale,
+        block_table.data_ptr(), width, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, T, Hq,
+        Hkv, prefix_pages, max_seqlen_q, max_seqlen_k, workspace.data_ptr(), workspace.numel(),
+        out.data_ptr(), _ptr(lse), _ptr(status), handle), "msa_prefix_attention")
+    return out, lse
+
+
 def _verify(name, target, drafts, uniforms, draft_probs, counts, tokens, accepted, stream):
     greedy = name == "msa_verify_greedy"
     _tensor(target, "target", _TYPES, (None, None, None), contiguous=False)

@@ -533,6 +533,51 @@ MSA_API int msa_kv_read_nvfp4(const uint8_t *kv4, int64_t num_pages, float k_sca
                       void *stream);
 
 /*
+ * Dense causal attention over the paged E4M3 cache for a batch whose requests
+ * share their first pages (a system prompt, a document): every query token
+ * attends to all keys up to its own position, the part over the shared pages
+ * is computed once for all requests, and each request's own pages are read
+ * for its tokens alone.  prefix_pages = 0 is plain dense attention.
+ *   q, kv, num_pages, the scales, block_table, bt_stride  as in msa_prefill
+ *   cu_seqlens_q  int32 [B + 1] as in msa_plan, but the last may be less than
+ *                 T: rows behind it (the padding of a captured batch) keep
+ *                 their contents; requests without query tokens are left out
+ *   cu_seqlens_k  int32 [B + 1] as in msa_plan; request b's queries are the
+ *                 last q_len_b of its seq_len_b positions
+ *   prefix_pages  shared pages: the first prefix_pages entries of every
+ *                 request's block_table row are the same, and its queries lie
+ *                 behind them (seq_len - q_len >= 128 * prefix_pages); the
+ *                 row of the first request with query tokens is read
+ *   max_seqlen_q, max_seqlen_k  host-known bounds, max_seqlen_k <= 2^30
+ *   workspace     msa_prefix_attention_workspace_bytes() bytes, 256-byte
+ *                 aligned; calls whose work may overlap need one each
+ *   out           bf16 [T][Hq][128]
+ *   lse           fp32 [T][Hq] natural-log sum of exp(score), or NULL
+ *   status        device word that MSA_STATUS_* bits are OR-ed into, or NULL:
+ *                 BAD_SEQLENS (lengths inconsistent, past the bounds, or
+ *                 queries inside the shared pages: the whole call then gives
+ *                 zeros and lse -inf on all T rows), BAD_BLOCK (an entry that
+ *                 is not a page: its keys are left out), TIMEOUT
+ * QK runs as E4M3 MMAs, the probabilities are rounded to f16 and V widened to
+ * f16 (exactly), sums are fp32: the output is within its bf16 rounding of
+ * exact attention for all practical purposes.  A NaN among the K of a key a
+ * row attends to makes the row NaN, one among its V that column; codes behind
+ * a request's end, or behind a row's position, have no effect on the row.
+ * Hq / Hkv in 1 .. 128.  Three kernels on `stream`, no host synchronisation.
+ */
+MSA_API int msa_prefix_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv,
+                                         int64_t prefix_pages, int64_t max_seqlen_q,
+                                         int64_t max_seqlen_k, size_t *bytes);
+MSA_API int msa_prefix_attention(const uint8_t *q, const uint8_t *kv, int64_t num_pages,
+                         float q_scale, float k_scale, float v_scale, float softmax_scale,
+                         const int32_t *block_table, int64_t bt_stride,
+                         const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int64_t B,
+                         int64_t T, int64_t Hq, int64_t Hkv, int64_t prefix_pages,
+                         int64_t max_seqlen_q, int64_t max_seqlen_k, void *workspace,
+                         size_t workspace_bytes, uint16_t *out, float *lse, uint32_t *status,
+                         void *stream);
+
+/*
  * Verification of drafted tokens, the step after a speculative-verify decode:
  * which of a request's drafts stand, and the token that follows them.  With
  * p_i the target's and q_i the draft model's probabilities at draft i and

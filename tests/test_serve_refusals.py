@@ -110,3 +110,47 @@ def test_library_refusals():
         assert fn(n=0) == 1 and fn(n=33) == 1 and fn(V=0) == 1 and fn(V=2 ** 19) == 1 and fn(B=-1) == 1
         assert fn(t=P(4098)) == 3 and fn(x=P(4097)) == 3 and fn(acc=P(4097)) == 3
     assert verify(u=None) == 6 and verify(d=P(4097)) == 3 and verify(u=P(4097)) == 3
+
+
+def test_prefix_attention_refusals():
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    q, kv = torch.zeros((6, 4, 128), dtype=torch.uint8), torch.zeros((4, 2, 128, 256), dtype=torch.uint8)
+    a = {"q": q, "kv": kv, "table": i32(2, 3), "cu_q": i32(3), "cu_k": i32(3), "prefix": 1, "max_q": 6, "max_k": 300}
+
+    def run(**kw):
+        c = dict(a, **{k: v for k, v in kw.items() if k in a})
+        return _err(msa.msa_prefix_attention, c["q"], c["kv"], 1.0, 1.0, 1.0, 0.1, c["table"], c["cu_q"], c["cu_k"], c["prefix"], c["max_q"], c["max_k"],
+                    **{k: v for k, v in kw.items() if k not in a})
+
+    assert "CUDA" in run()
+    assert "q has dtype" in run(q=q.to(torch.bfloat16)) and "q must be [any, any, 128]" in run(q=q[0])
+    assert "q must be contiguous" in run(q=torch.zeros((6, 8, 128), dtype=torch.uint8)[:, ::2])
+    assert "block_table must be" in run(table=i32(3, 3)) and "cu_seqlens_k must be" in run(cu_k=i32(2))
+    assert "out must be" in run(out=torch.zeros((6, 2, 128), dtype=torch.bfloat16)) and "lse must be" in run(lse=torch.zeros((6, 3)))
+    assert "workspace too small" in run(workspace=torch.zeros(100, dtype=torch.uint8))
+    assert "unsupported" in run(q=torch.zeros((6, 3, 128), dtype=torch.uint8))
+    assert "unsupported" in run(q=torch.zeros((1, 258, 128), dtype=torch.uint8))
+    for bad in (dict(prefix=-1), dict(prefix=3), dict(max_q=-1), dict(max_q=301), dict(max_k=2 ** 30 + 1)):
+        assert "out of range" in run(**bad)
+
+
+def test_prefix_attention_library_refusals():
+    lib, P = msa.load(), ctypes.c_void_p
+    a = P(4096)
+
+    def run(q=a, kv=a, pages=4, s=1.0, table=a, width=3, cu=a, B=2, T=6, Hq=4, Hkv=2, prefix=1, ws=a, size=1 << 40, out=a, lse=None, status=None):
+        return lib.msa_prefix_attention(q, kv, pages, s, 1.0, 1.0, 0.1, table, width, cu, a, B, T, Hq, Hkv, prefix, 6, 300, ws, size, out, lse, status, None)
+
+    assert run(B=0) == 0 and run(T=0) == 0
+    assert run(q=None) == 6 and run(kv=None) == 6 and run(table=None) == 6 and run(cu=None) == 6 and run(out=None) == 6
+    assert run(width=2) == 1 and run(pages=-1) == 1 and run(pages=2 ** 23) == 1 and run(B=-1) == 1 and run(prefix=-1) == 1
+    for s in (0.0, -1.0, float("nan"), float("inf")):
+        assert run(s=s) == 1
+    assert run(Hq=3) == 2 and run(Hq=0) == 1 and run(Hq=258) == 2
+    assert run(ws=None) == 4 and run(size=1000) == 4 and run(ws=P(4096 + 128)) == 3
+    assert run(q=P(4104)) == 3 and run(out=P(4100)) == 3 and run(lse=P(4098)) == 3 and run(status=P(4097)) == 3
+    n = ctypes.c_size_t()
+    size = lambda *v: lib.msa_prefix_attention_workspace_bytes(*v, ctypes.byref(n))  # noqa: E731
+    assert size(2, 6, 4, 2, 1, 6, 300) == 0 and n.value > 0
+    assert size(2, 6, 4, 2, 1, 6, 100) == 1 and size(2, -6, 4, 2, 1, 6, 300) == 1 and size(2, 6, 5, 2, 1, 6, 300) == 2
+    assert lib.msa_prefix_attention_workspace_bytes(2, 6, 4, 2, 1, 6, 300, None) == 6
