@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
 
 constexpr int kThreads = 512;
 constexpr int kTileBytes = 128 * 128;       // an E4M3 tile of 128 x 128
-constexpr int kRaw = 3;                     // K and V pages in flight
+constexpr int kRaw = 4;                     // K and V pages in flight
 constexpr int kWide = 2;                    // V pages widened to f16
 constexpr int kOffQ = 0;
 constexpr int kOffK = kOffQ + 2 * kTileBytes;
@@ -233,23 +233,25 @@ struct Bars {
   uint64_t q_full, q_free;
   uint64_t k_full[kRaw], k_free[kRaw], v_full[kRaw], v_free[kRaw];
   uint64_t w_full[kWide], w_free[kWide];
-  uint64_t s_full[2], p_full[2], pv_done[2], mma_done;
+  // [stream][buffer]
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], mma_done[2];
   uint32_t tmem_base;
   int abort;
   int nan_seen;      // a NaN among the V codes of valid keys
   int first_tile;
-  int nan_key[8][kD];  // per softmax warp
 };
 constexpr int kSmem = kOffBars + (int)sizeof(Bars) + 1024;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
-constexpr int kTmemCols = 512;  // S of the two streams, then their O
-// 512 threads with 128 registers: control 64, softmax 2 x 192, widening 64
-constexpr int kRegsControl = 64, kRegsSoftmax = 192, kRegsWiden = 64;
+constexpr int kTmemCols = 512;  // S of the two streams (two buffers each), their O
+constexpr int kHalf = kPage / 2;  // keys of an S buffer
+// 512 threads with 128 registers each, shared out anew among the roles
+constexpr int kRegsControl = 64, kRegsSoftmax = 176, kRegsWiden = 96;
 static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsWiden <= 512, "registers");
 // P is kept as 2^(s - m + 7): with m allowed to lag the maximum by 8 the
-// largest P is 2^15, in f16's range, and f16's subnormals begin 2^-21 below
-// the maximum instead of 2^-14
-constexpr float kLag = 8.f, kPShift = 7.f;
+// largest P is 2^15, in f16's range (a larger one, up to infinity, is found
+// before it is used), and f16's subnormals begin 2^-21 below the reference
+// instead of 2^-14
+constexpr float kPShift = 7.f, kMostP = 32768.f;
 
 struct AttendParams {
   const PlanHead* head;
@@ -348,23 +350,24 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
 
   if (tid == 0) {
     mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_free, 1);
+    mbar_init(&bars->q_free, 2);
     for (int i = 0; i < kRaw; ++i) {
       mbar_init(&bars->k_full[i], 1);
-      mbar_init(&bars->k_free[i], 1);
+      mbar_init(&bars->k_free[i], 2);
       mbar_init(&bars->v_full[i], 1);
       mbar_init(&bars->v_free[i], 4);
     }
     for (int i = 0; i < kWide; ++i) {
       mbar_init(&bars->w_full[i], 4);
-      mbar_init(&bars->w_free[i], 1);
+      mbar_init(&bars->w_free[i], 2);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars->s_full[s], 1);
-      mbar_init(&bars->p_full[s], 4);
-      mbar_init(&bars->pv_done[s], 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bars->s_full[i >> 1][i & 1], 1);
+      mbar_init(&bars->p_full[i >> 1][i & 1], 4);
+      mbar_init(&bars->pv_done[i >> 1][i & 1], 1);
     }
-    mbar_init(&bars->mma_done, 1);
+    mbar_init(&bars->mma_done[0], 1);
+    mbar_init(&bars->mma_done[1], 1);
     bars->abort = 0;
     bars->nan_seen = 0;
     bars->first_tile = 0;
@@ -401,7 +404,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
     if (warp == 0) {
       // ---------------------------------------------------------- producer
       int g = 0, part = 0;  // pages and parts so far
-      int q_loads = 0;
+      int q_loads = 0, k_loads = 0, v_loads = 0;
       bool ok = true;
       while (ok && walk.next()) {
         const Tile& t = walk.t;
@@ -438,6 +441,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
                 } else {
                   mbar_arrive(&bars->k_full[slot]);
                 }
+                ++k_loads;
                 if (g >= kRaw) ok = bounded_wait(&bars->v_free[slot], ph, abort, p.wait_ns);
                 if (ok) {
                   if (there) {
@@ -447,10 +451,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
                   } else {
                     mbar_arrive(&bars->v_full[slot]);
                   }
-                } else {
-                  // the K load of this page has no V load beside it: waited
-                  // for here, the drain below counts whole pages
-                  bounded_wait(&bars->k_full[slot], (g / kRaw) & 1, nullptr, kWaitLimitNs);
+                  ++v_loads;
                 }
               }
             }
@@ -462,89 +463,120 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
       if (lane == 0) {
         if (!ok && !*abort) give_up(bars, p.status);
         // every copy lands before the CTA may end
-        for (int i = max(0, g - kRaw); i < g; ++i) {
+        for (int i = max(0, k_loads - kRaw); i < k_loads; ++i)
           bounded_wait(&bars->k_full[i % kRaw], (i / kRaw) & 1, nullptr, kWaitLimitNs);
+        for (int i = max(0, v_loads - kRaw); i < v_loads; ++i)
           bounded_wait(&bars->v_full[i % kRaw], (i / kRaw) & 1, nullptr, kWaitLimitNs);
-        }
         if (q_loads > 0)
           bounded_wait(&bars->q_full, (q_loads - 1) & 1, nullptr, kWaitLimitNs);
       }
       __syncwarp();
-    } else if (warp == 1) {
-      if (lane == 0) {
-        // ------------------------------------------------------ MMA issuer
-        // Per stream QK(0) PV(0) QK(1) PV(1) ..., each as soon as what it
-        // needs is there; the streams are independent.  P overwrites its S,
-        // so QK(i + 1) waits until PV(i) has completed.
-        constexpr uint32_t kQk = idesc_e4m3_f32(128, 128, false);
+    } else if (warp <= 2) {
+      if (elect_one()) {
+        // -------------------------------------------- MMA issuer of a stream
+        // One thread per stream: a single one for both was busy all the time
+        // and held either back.  The unit is a half page (64 keys): QK(u)
+        // into one of the stream's two S buffers, PV(u) from the P that
+        // replaces it; QK(u + 2) waits until PV(u) has completed, while the
+        // softmax works on unit u + 1.
+        constexpr uint32_t kQk = idesc_e4m3_f32(128, kHalf, false);
         constexpr uint32_t kPv = idesc_f16_f32(128, 128, true);
-        int g0 = 0, part = 0;
-        uint32_t done_s[2] = {0, 0};  // S tiles, PVs issued per stream
+        const int s = warp - 1;
+        const uint64_t desc_k = smem_desc_sw128(smem_u32(smem + kOffK), 16, 1024);
+        const uint64_t desc_w = smem_desc_sw128(smem_u32(smem + kOffW), kTileBytes, 1024);
+        const uint32_t s_tmem = tmem + s * 128, o_tmem = tmem + 256 + s * 128;
+        uint32_t g0 = 0, part = 0, base = 0;  // pages, parts, own units so far
         bool ok = true;
+        // In a solo part a page has one user; the other stream waits for it
+        // too and frees its share.  So no slot moves on before both streams
+        // have seen its phase: a barrier tells a phase only from the next.
+        uint32_t k_seen = 0, w_seen = 0;  // pages used or passed
+        auto pass_k = [&](uint32_t to) {
+          for (; k_seen < to; ++k_seen) {
+            if (!bounded_wait(&bars->k_full[k_seen % kRaw], (k_seen / kRaw) & 1, abort, p.wait_ns))
+              return false;
+            mbar_arrive(&bars->k_free[k_seen % kRaw]);
+          }
+          return true;
+        };
+        auto pass_w = [&](uint32_t to) {
+          for (; w_seen < to; ++w_seen) {
+            if (!bounded_wait(&bars->w_full[w_seen % kWide], (w_seen / kWide) & 1, abort,
+                              p.wait_ns))
+              return false;
+            mbar_arrive(&bars->w_free[w_seen % kWide]);
+          }
+          return true;
+        };
         while (ok && walk.next()) {
           const bool pair = walk.pair();
-          const int n[2] = {walk.stream_pages(0), walk.stream_pages(1)};
-          int qk[2] = {0, 0}, pv[2] = {0, 0};
-          bool have_q = false;
-          uint32_t idle = 0, since = 0;
-          while (pv[0] < n[0] || pv[1] < n[1]) {
-            bool moved = false;
+          const uint32_t n = 2u * walk.stream_pages(s);
+          const uint64_t desc_q =
+              smem_desc_sw128(smem_u32(smem + kOffQ + (pair ? s : 0) * kTileBytes), 16, 1024);
+          const uint32_t g1 = g0 + (walk.p1 - walk.p0);
+          // the ring position of the page of unit i
+          auto page_of = [&](uint32_t i) { return g0 + (pair ? i >> 1 : (i & ~1u) + s); };
+          auto qk = [&](uint32_t i) {
+            const uint32_t u = base + i, buf = u & 1, half = i & 1, g = page_of(i);
+            if (!half &&
+                !(pass_k(g) &&
+                  bounded_wait(&bars->k_full[g % kRaw], (g / kRaw) & 1, abort, p.wait_ns)))
+              return false;
+            tc_fence_after();
+            const uint64_t b =
+                desc_k + (g % kRaw) * (kTileBytes / 16) + half * (kHalf * 128 / 16);
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              if (qk[s] == pv[s] && qk[s] < n[s]) {
-                const int g = g0 + walk.stream_page(s, qk[s]);
-                if ((have_q || (have_q = mbar_test(&bars->q_full, part & 1))) &&
-                    (done_s[s] == 0 || mbar_test(&bars->pv_done[s], (done_s[s] - 1) & 1)) &&
-                    mbar_test(&bars->k_full[g % kRaw], (g / kRaw) & 1)) {
-                  tc_fence_after();
-                  const uint32_t qa =
-                      smem_u32(smem + kOffQ + (pair ? s : 0) * kTileBytes);
-                  const uint32_t kb = smem_u32(smem + kOffK + (g % kRaw) * kTileBytes);
-#pragma unroll
-                  for (int kk = 0; kk < 4; ++kk)
-                    mma_f8f6f4(tmem + s * 128, smem_desc_sw128(qa + kk * 32, 16, 1024),
-                               smem_desc_sw128(kb + kk * 32, 16, 1024), kQk, kk > 0);
-                  mma_commit(&bars->s_full[s]);
-                  ++qk[s];
-                  if (!pair || qk[s ^ 1] >= qk[s]) mma_commit(&bars->k_free[g % kRaw]);
-                  if (qk[0] == n[0] && qk[1] == n[1]) mma_commit(&bars->q_free);
-                  moved = true;
-                }
-              } else if (pv[s] < qk[s]) {
-                const int g = g0 + walk.stream_page(s, pv[s]);
-                if (mbar_test(&bars->p_full[s], done_s[s] & 1) &&
-                    mbar_test(&bars->w_full[g % kWide], (g / kWide) & 1)) {
-                  tc_fence_after();
-                  const uint32_t vb = smem_u32(smem + kOffW + (g % kWide) * 2 * kTileBytes);
-#pragma unroll
-                  for (int kk = 0; kk < 8; ++kk)
-                    mma_f16_ts(tmem + 256 + s * 128, tmem + s * 128 + kk * 8,
-                               smem_desc_sw128(vb + kk * 16 * 128, kTileBytes, 1024), kPv,
-                               pv[s] > 0 || kk > 0);
-                  mma_commit(&bars->pv_done[s]);
-                  ++pv[s];
-                  ++done_s[s];
-                  if (!pair || pv[s ^ 1] >= pv[s]) mma_commit(&bars->w_free[g % kWide]);
-                  moved = true;
-                }
-              }
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f8f6f4(s_tmem + buf * kHalf, desc_q + kk * 2, b + kk * 2, kQk, kk > 0);
+            mma_commit(&bars->s_full[s][buf]);
+            if (half) mma_commit(&bars->k_free[g % kRaw]), k_seen = g + 1;
+            if (i + 1 == n) {
+              mma_commit(&bars->q_free);
+              return pass_k(g1);
             }
-            if (moved) {
-              idle = 0;
-            } else if ((++idle & 63u) == 0) {
-              if (idle == 64u) since = (uint32_t)global_timer_ns();
-              if (*abort || (uint32_t)global_timer_ns() - since > p.wait_ns) {
-                ok = false;
-                break;
-              }
-            }
+            return true;
+          };
+          ok = bounded_wait(&bars->q_full, part & 1, abort, p.wait_ns);
+          // both S buffers are free: the softmax has finished the part before
+          // (its P of this part's first units is waited for below), and that
+          // part's PVs were complete before it wrote its results
+          for (uint32_t i = 0; ok && i < 2 && i < n; ++i) {
+            const uint32_t u = base + i;
+            ok = (u < 2 || bounded_wait(&bars->pv_done[s][u & 1], ((u >> 1) - 1) & 1, abort,
+                                        p.wait_ns)) &&
+                 qk(i);
           }
-          g0 += walk.p1 - walk.p0;
+          if (ok && n == 0) {
+            mbar_arrive(&bars->q_free);
+            ok = pass_k(g1);
+          }
+          for (uint32_t i = 0; ok && i < n; ++i) {
+            const uint32_t u = base + i, buf = u & 1, half = i & 1, g = page_of(i);
+            ok = (half || (pass_w(g) && bounded_wait(&bars->w_full[g % kWide], (g / kWide) & 1,
+                                                     abort, p.wait_ns))) &&
+                 bounded_wait(&bars->p_full[s][buf], (u >> 1) & 1, abort, p.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t b =
+                desc_w + (g % kWide) * (2 * kTileBytes / 16) + half * (kHalf * 128 / 16);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16_ts(o_tmem, s_tmem + buf * kHalf + kk * 8, b + kk * (16 * 128 / 16), kPv,
+                         kk > 0 || i > 0);
+            mma_commit(&bars->pv_done[s][buf]);
+            if (half) mma_commit(&bars->w_free[g % kWide]), w_seen = g + 1;
+            if (i + 2 < n)
+              ok = bounded_wait(&bars->pv_done[s][buf], (u >> 1) & 1, abort, p.wait_ns) &&
+                   qk(i + 2);
+          }
+          ok = ok && pass_w(g1);
+          g0 = g1;
+          base += n;
           ++part;
         }
         if (!ok && !*abort) give_up(bars, p.status);
-        mma_commit(&bars->mma_done);
-        bounded_wait(&bars->mma_done, 0, nullptr, kWaitLimitNs);
+        mma_commit(&bars->mma_done[s]);
+        bounded_wait(&bars->mma_done[s], 0, nullptr, kWaitLimitNs);
       }
       __syncwarp();
     }
@@ -556,7 +588,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
     const uint32_t s_tmem = tmem + lane_off + s * 128, o_tmem = s_tmem + 256;
     const float c = p.score_log2;
     const int i_tok = row / p.G;
-    uint32_t done = 0;  // pages of this stream so far
+    uint32_t done = 0;  // units (half pages) of this stream so far
     bool ok = true;
     while (ok && walk.next()) {
       const Tile& t = walk.t;
@@ -567,43 +599,88 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
       const int tok = i_tok + (pair && s ? p.C : 0);  // within the tile
       const int pos = t.pos0 + tok;
       const int32_t* table = p.block_table + t.b * p.bt_stride + t.page0;
+      // the first position of the warp's rows: pages before it need no mask
+      const int least = __reduce_min_sync(0xffffffffu, pos);
       float m = -INFINITY, l = 0.f;  // m: scores in units of 1 (not log2)
+      float off = 0.f;
       int page = n > 0 ? __ldg(table + walk.p0 + walk.stream_page(s, 0)) : 0;
-      for (int i = 0; i < n; ++i, ++done) {
-        const int j = walk.p0 + walk.stream_page(s, i);
-        const bool there = page >= 0 && page < p.num_pages;
-        if (i + 1 < n) page = __ldg(table + walk.p0 + walk.stream_page(s, i + 1));
-        // the last key of the page that this row attends to
-        const int lim = there ? pos - (t.page0 + j) * kPage : -1;
-        if (!all_wait(bars, &bars->s_full[s], done & 1, p)) {
+      int key0 = 0;      // the unit's first key
+      bool there = true; // its page is one
+#pragma unroll 1
+      for (int i = 0; i < 2 * n; ++i, ++done) {
+        if ((i & 1) == 0) {
+          key0 = (t.page0 + walk.p0 + walk.stream_page(s, i >> 1)) * kPage;
+          there = page >= 0 && page < p.num_pages;
+          if (i + 2 < 2 * n) page = __ldg(table + walk.p0 + walk.stream_page(s, (i >> 1) + 1));
+        } else {
+          key0 += kHalf;
+        }
+        const uint32_t buf = done & 1, s_cols = s_tmem + buf * kHalf;
+        if (!all_wait(bars, &bars->s_full[s][buf], (done >> 1) & 1, p)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        uint32_t r[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(s_tmem + q * 32, r[q]);
+        uint32_t r[2][32];
+        tmem_ld32(s_cols, r[0]);
+        tmem_ld32(s_cols + 32, r[1]);
         tmem_wait_ld();
-        if (__any_sync(0xffffffffu, lim < kPage - 1)) {
+        if (!there || key0 + kHalf - 1 > least) {
+          const int lim = there ? pos - key0 : -1;  // the last key this row attends to
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+          for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (q * 32 + e > lim) r[q][e] = 0xFF800000u;  // -inf
         }
-        float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+        const float2 c2 = make_float2(c, c);
+        float2 sum[2];
+        uint32_t w[32];
+        // P against the present reference m, and the largest of them
+        auto exponentials = [&]() {
+          const float2 off2 = make_float2(off, off);
+          sum[0] = sum[1] = make_float2(0.f, 0.f);
+          __half2 most[2] = {__half2half2(__ushort_as_half(0)), __half2half2(__ushort_as_half(0))};
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(r[q][e]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        // O and l are moved to a new reference only where the maximum has
-        // grown by more than 2^kLag.  PV of the page before has completed:
-        // this page's QK was issued after it.
-        const bool grown = i == 0 || (top - m) * c > kLag || (m == -INFINITY && top > m);
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t* x = &r[e >> 4][2 * (e & 15)];
+            float2 a = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, off2);
+            a.x = ex2_approx(a.x);
+            a.y = ex2_approx(a.y);
+            sum[e & 1] = add2(sum[e & 1], a);
+            const __half2 h = __floats2half2_rn(a.x, a.y);
+            most[e & 1] = __hmax2(most[e & 1], h);
+            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          most[0] = __hmax2(most[0], most[1]);
+          return __hmax(__low2half(most[0]), __high2half(most[0]));
+        };
+        // The reference is the maximum of the row's first unit and moves (O
+        // and l with it) only where a P passes kMostP: the unit's
+        // own maximum is not waited for.
+        bool grown = i == 0;
+        if (i > 0) {
+          const __half most = exponentials();
+          grown = m == -INFINITY || __hgt(most, __float2half(kMostP));
+        }
         if (__any_sync(0xffffffffu, grown)) {
-          const float f = m == -INFINITY ? 0.f : ex2_approx((m - top) * c);
+          float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(r[q][e]));
+          // only the rows that need it move: what a row gives does not depend
+          // on the others of its warp
+          const float top = grown ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) : m;
           if (i > 0) {
+            // every PV of the stream has to be complete: the one before this
+            // unit is the last issued
+            if (!all_wait(bars, &bars->pv_done[s][buf ^ 1], ((done - 1) >> 1) & 1, p)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const float f = !grown ? 1.f : m == -INFINITY ? 0.f : ex2_approx((m - top) * c);
             l *= f;
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
@@ -616,29 +693,15 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
             }
           }
           m = top;
+          off = m == -INFINITY ? 0.f : kPShift - m * c;
+          exponentials();
         }
-        const float off = m == -INFINITY ? 0.f : kPShift - m * c;
-        float lq[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t w[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const uint32_t* x = &r[half * 2 + (e >> 4)][2 * (e & 15)];
-            const float a = ex2_approx(fmaf(__uint_as_float(x[0]), c, off));
-            const float b = ex2_approx(fmaf(__uint_as_float(x[1]), c, off));
-            lq[(2 * e) & 3] += a;
-            lq[(2 * e + 1) & 3] += b;
-            const __half2 h = __floats2half2_rn(a, b);
-            w[e] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          tmem_st32(s_tmem + half * 32, w);
-        }
-        l += (lq[0] + lq[1]) + (lq[2] + lq[3]);
+        tmem_st32(s_cols, w);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[s]);
+        if (lane == 0) mbar_arrive(&bars->p_full[s][buf]);
       }
       if (!ok) break;
       // the part: O / l and log2 of the row's sum
@@ -646,33 +709,29 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
                                     p.T, p.G) +
                            (s ? (pair ? p.C : t.ntok) * p.G : 0) + row;
       if (n > 0) {
-        if (!all_wait(bars, &bars->pv_done[s], (done - 1) & 1, p)) break;
+        if (!all_wait(bars, &bars->pv_done[s][(done - 1) & 1], ((done - 1) >> 1) & 1, p)) break;
         tc_fence_after();
         bool poison = __any_sync(0xffffffffu, *(volatile int*)&bars->nan_seen != 0);
-        int* nan_key = bars->nan_key[warp - 4];
+        int nan_key[4] = {INT_MAX, INT_MAX, INT_MAX, INT_MAX};  // columns 4 lane ..
         if (poison) {
           // A NaN lies among the V codes of some valid key.  Widening wrote
           // it as 0, since a probability of 0 must hide it; now each warp
           // finds, for each column, the first position of this part that has
           // one (a rare path: no care is taken of its speed).
-          __syncwarp();
-          for (int k = lane; k < kD; k += 32) nan_key[k] = INT_MAX;
-          __syncwarp();
           for (int i = 0; i < n; ++i) {
             const int j = walk.p0 + walk.stream_page(s, i);
             const int pg = __ldg(table + j);
             if (pg < 0 || pg >= p.num_pages) continue;
             const uint8_t* v = p.kv + ((int64_t)pg * p.Hkv + walk.cur_h) * kPage * (2 * kD) + kD;
-            const int base = (t.page0 + j) * kPage;
-            for (int k = 0; k < kPage && base + k < t.seq; ++k) {
+            const int first = (t.page0 + j) * kPage;
+            for (int k = 0; k < kPage && first + k < t.seq; ++k) {
               const uint32_t bad = nan_bytes(
                   __ldg(reinterpret_cast<const uint32_t*>(v + k * (2 * kD)) + lane));
+#pragma unroll
               for (int e = 0; e < 4; ++e)
-                if ((bad >> (8 * e)) & 0x80u)
-                  nan_key[lane * 4 + e] = min(nan_key[lane * 4 + e], base + k);
+                if ((bad >> (8 * e)) & 0x80u) nan_key[e] = min(nan_key[e], first + k);
             }
           }
-          __syncwarp();
         }
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
 #pragma unroll 1
@@ -680,13 +739,15 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
           uint32_t o[32];
           tmem_ld32(o_tmem + q * 32, o);
           tmem_wait_ld();
-          if (valid) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              float v = __uint_as_float(o[e]) * inv;
-              if (poison && nan_key[q * 32 + e] <= pos) v = NAN;
-              o[e] = __float_as_uint(v);
-            }
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+          if (poison) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (__shfl_sync(0xffffffffu, nan_key[e & 3], q * 8 + (e >> 2)) <= pos)
+                o[e] = 0x7FFFFFFFu;
+          }
+          if (valid) {
             uint32_t* dst = reinterpret_cast<uint32_t*>(p.part_o + prow * kD) + q * 32;
 #pragma unroll
             for (int e = 0; e < 32; e += 8)
@@ -723,27 +784,52 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         }
         const uint8_t* src = smem + kOffV + (g % kRaw) * kTileBytes;
         uint8_t* dst = smem + kOffW + (g % kWide) * 2 * kTileBytes;
-        bool nan = false;
-#pragma unroll 4
+        // all loads first, and one test for the rare NaN: the conversions of
+        // the 8 chunks then overlap
+        uint32_t w[8][4];
+#pragma unroll
         for (int u = 0; u < 8; ++u) {
           const int e = wt + u * 128, key = e >> 3, ch = e & 7;
-          uint4 v = *reinterpret_cast<const uint4*>(src + key * 128 + ((ch ^ (key & 7)) << 4));
-          uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          if (key >= keys) w[0] = w[1] = w[2] = w[3] = 0u;
-          const uint32_t bad = nan_bytes(w[0]) | nan_bytes(w[1]) | nan_bytes(w[2]) | nan_bytes(w[3]);
-          if (bad) {
-            nan = true;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] &= ~((nan_bytes(w[k]) >> 7) * 0xFFu);
-          }
-          const uint2 a = widen4(w[0]), b = widen4(w[1]), cc = widen4(w[2]), d = widen4(w[3]);
-          uint8_t* row = dst + (ch >> 2) * kTileBytes + key * 128;
-          const int c0 = (ch & 3) * 2;
-          *reinterpret_cast<uint4*>(row + ((c0 ^ (key & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-          *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (key & 7)) << 4)) =
-              make_uint4(cc.x, cc.y, d.x, d.y);
+          const uint4 v = *reinterpret_cast<const uint4*>(src + key * 128 + ((ch ^ (key & 7)) << 4));
+          w[u][0] = v.x, w[u][1] = v.y, w[u][2] = v.z, w[u][3] = v.w;
         }
-        if (nan) *(volatile int*)&bars->nan_seen = 1;
+        if (keys < kPage) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (((wt + u * 128) >> 3) >= keys) w[u][0] = w[u][1] = w[u][2] = w[u][3] = 0u;
+        }
+        // f16 tile of the chunks; the result is NaN if one of the codes is
+        auto store = [&]() {
+          __half2 sick = __half2half2(__ushort_as_half(0));
+          const __half2 zero = sick;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int e = wt + u * 128, key = e >> 3, ch = e & 7;
+            uint32_t h[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint2 two = widen4(w[u][k]);
+              h[2 * k] = two.x, h[2 * k + 1] = two.y;
+              sick = __hfma2(*reinterpret_cast<const __half2*>(&two.x), zero, sick);
+              sick = __hfma2(*reinterpret_cast<const __half2*>(&two.y), zero, sick);
+            }
+            uint8_t* row = dst + (ch >> 2) * kTileBytes + key * 128;
+            const int c0 = (ch & 3) * 2;
+            *reinterpret_cast<uint4*>(row + ((c0 ^ (key & 7)) << 4)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (key & 7)) << 4)) =
+                make_uint4(h[4], h[5], h[6], h[7]);
+          }
+          return __hisnan(__low2half(sick)) || __hisnan(__high2half(sick));
+        };
+        if (store()) {
+          *(volatile int*)&bars->nan_seen = 1;
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[u][k] &= ~((nan_bytes(w[u][k]) >> 7) * 0xFFu);
+          store();
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
