@@ -32,7 +32,6 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
-#include "lookup.cuh"
 #include "partial.cuh"
 #include "ptx.cuh"
 
@@ -41,9 +40,10 @@ namespace {
 
 // ------------------------------------------------------------------- tiles
 
-// Cost of a tile: its pages by kind, and its start and end (Q, epilogue).
-constexpr int kCostSolo = 2, kCostPair = 4, kCostTile = 4;
-constexpr int kMinShare = 8;  // least cost of a CTA's range
+// Cost of a tile: its pages by kind, and its start and end (Q, epilogue), in
+// the proportions measured (about 0.9, 1.8 and 4.5 us).
+constexpr int kCostSolo = 2, kCostPair = 4, kCostTile = 10;
+constexpr int kMinShare = 12;  // least cost of a CTA's range
 
 // Behind every key (positions are below 2^30), with room for a tile's tokens.
 constexpr int kNoMask = INT_MAX - 1024;
@@ -229,29 +229,33 @@ constexpr int kOffK = kOffQ + 2 * kTileBytes;
 constexpr int kOffV = kOffK + kRaw * kTileBytes;
 constexpr int kOffW = kOffV + kRaw * kTileBytes;
 constexpr int kOffBars = kOffW + kWide * 2 * kTileBytes;
+constexpr int kThere = 16;  // more than the roles can be apart
 struct Bars {
   uint64_t q_full, q_free;
   uint64_t k_full[kRaw], k_free[kRaw], v_full[kRaw], v_free[kRaw];
   uint64_t w_full[kWide], w_free[kWide];
-  // [stream][buffer]
-  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], mma_done[2];
+  uint64_t s_full[2], s_free[2];             // per stream
+  uint64_t p_full[2][2], pv_done[2][2];      // [stream][buffer]
+  uint64_t mma_done[2];
   uint32_t tmem_base;
   int abort;
   int nan_seen;      // a NaN among the V codes of valid keys
   int first_tile;
+  uint8_t there[kThere];  // whether a ring position's page is one, by the producer
 };
 constexpr int kSmem = kOffBars + (int)sizeof(Bars) + 1024;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
-constexpr int kTmemCols = 512;  // S of the two streams (two buffers each), their O
-constexpr int kHalf = kPage / 2;  // keys of an S buffer
+constexpr int kHalf = kPage / 2;  // keys of a unit: of one S, and one P
+// Tensor memory, per stream s: S at column 128 s, two P buffers (f16, 32
+// columns each) at 128 s + 64, O at 256 + 128 s
+constexpr int kTmemCols = 512, kColP = 64, kColO = 256;
 // 512 threads with 128 registers each, shared out anew among the roles
-constexpr int kRegsControl = 64, kRegsSoftmax = 176, kRegsWiden = 96;
+constexpr int kRegsControl = 80, kRegsSoftmax = 168, kRegsWiden = 96;
 static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsWiden <= 512, "registers");
-// P is kept as 2^(s - m + 7): with m allowed to lag the maximum by 8 the
-// largest P is 2^15, in f16's range (a larger one, up to infinity, is found
-// before it is used), and f16's subnormals begin 2^-21 below the reference
+// P is kept as 2^(s - m + 7): a unit whose P add up to at most 2^15 has none
+// outside f16's range, and f16's subnormals begin 2^-21 below the reference
 // instead of 2^-14
-constexpr float kPShift = 7.f, kMostP = 32768.f;
+constexpr float kPShift = 7.f, kMostSum = 32768.f;
 
 struct AttendParams {
   const PlanHead* head;
@@ -274,7 +278,7 @@ struct Walk {
   int ntiles, shared_tiles;
   int64_t cost, x, end, share;
   int h, tile;
-  Tile t;
+  Tile t, ahead;
   int p0, p1;        // pages of the tile in this range
   __device__ Walk(const AttendParams& prm, const PlanHead& hd, int first_tile)
       : p(prm), ntiles(hd.ntiles), shared_tiles(hd.shared_tiles), cost(hd.cost), tile(first_tile) {
@@ -283,11 +287,12 @@ struct Walk {
     x = min(total, blockIdx.x * share);
     end = min(total, x + share);
     h = cost > 0 ? (int)(x / cost) : 0;
+    if (x < end) ahead = p.tiles[tile];
   }
   // The next part with pages; false at the range's end.
   __device__ __forceinline__ bool next() {
     while (x < end) {
-      t = p.tiles[tile];
+      t = ahead;
       const int rate = tile_rate(t.ntok, p.C);
       const int64_t t0 = h * cost + t.start;
       const int64_t t1 = t0 + tile_cost(t.ntok, t.npages, p.C);
@@ -298,6 +303,7 @@ struct Walk {
       cur_tile = tile;
       x = e;
       if (e == t1 && ++tile == ntiles) tile = 0, ++h;
+      if (x < end) ahead = p.tiles[tile];  // in flight while this part is worked on
       if (p1 > p0) return true;
     }
     return false;
@@ -361,8 +367,11 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
       mbar_init(&bars->w_full[i], 4);
       mbar_init(&bars->w_free[i], 2);
     }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->s_full[s], 1);
+      mbar_init(&bars->s_free[s], 4);
+    }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&bars->s_full[i >> 1][i & 1], 1);
       mbar_init(&bars->p_full[i >> 1][i & 1], 4);
       mbar_init(&bars->pv_done[i >> 1][i & 1], 1);
     }
@@ -431,6 +440,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
               const int slot = g % kRaw;
               const uint32_t ph = ((g / kRaw) - 1) & 1;
               const bool there = page >= 0 && page < p.num_pages;
+              bars->there[g % kThere] = there;
               if (!there && p.status) atomicOr(p.status, (unsigned)MSA_STATUS_BAD_BLOCK);
               const int y = there ? (page * p.Hkv + walk.cur_h) * kPage : 0;
               if (g >= kRaw) ok = bounded_wait(&bars->k_free[slot], ph, abort, p.wait_ns);
@@ -475,16 +485,17 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
       if (elect_one()) {
         // -------------------------------------------- MMA issuer of a stream
         // One thread per stream: a single one for both was busy all the time
-        // and held either back.  The unit is a half page (64 keys): QK(u)
-        // into one of the stream's two S buffers, PV(u) from the P that
-        // replaces it; QK(u + 2) waits until PV(u) has completed, while the
-        // softmax works on unit u + 1.
+        // and held either back.  The unit is a half page (64 keys).  QK(u + 1)
+        // is issued as soon as the softmax has S(u) in registers, and runs
+        // under its exponentials; PV(u) when P(u) is there.  In this order,
+        // QK(u)'s commit also says that PV(u - 2) is complete, whose P buffer
+        // unit u writes.
         constexpr uint32_t kQk = idesc_e4m3_f32(128, kHalf, false);
         constexpr uint32_t kPv = idesc_f16_f32(128, 128, true);
         const int s = warp - 1;
         const uint64_t desc_k = smem_desc_sw128(smem_u32(smem + kOffK), 16, 1024);
         const uint64_t desc_w = smem_desc_sw128(smem_u32(smem + kOffW), kTileBytes, 1024);
-        const uint32_t s_tmem = tmem + s * 128, o_tmem = tmem + 256 + s * 128;
+        const uint32_t s_tmem = tmem + s * 128, o_tmem = tmem + kColO + s * 128;
         uint32_t g0 = 0, part = 0, base = 0;  // pages, parts, own units so far
         bool ok = true;
         // In a solo part a page has one user; the other stream waits for it
@@ -517,7 +528,9 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
           // the ring position of the page of unit i
           auto page_of = [&](uint32_t i) { return g0 + (pair ? i >> 1 : (i & ~1u) + s); };
           auto qk = [&](uint32_t i) {
-            const uint32_t u = base + i, buf = u & 1, half = i & 1, g = page_of(i);
+            const uint32_t u = base + i, half = i & 1, g = page_of(i);
+            if (u > 0 && !bounded_wait(&bars->s_free[s], (u - 1) & 1, abort, p.wait_ns))
+              return false;
             if (!half &&
                 !(pass_k(g) &&
                   bounded_wait(&bars->k_full[g % kRaw], (g / kRaw) & 1, abort, p.wait_ns)))
@@ -527,8 +540,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
                 desc_k + (g % kRaw) * (kTileBytes / 16) + half * (kHalf * 128 / 16);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_f8f6f4(s_tmem + buf * kHalf, desc_q + kk * 2, b + kk * 2, kQk, kk > 0);
-            mma_commit(&bars->s_full[s][buf]);
+              mma_f8f6f4(s_tmem, desc_q + kk * 2, b + kk * 2, kQk, kk > 0);
+            mma_commit(&bars->s_full[s]);
             if (half) mma_commit(&bars->k_free[g % kRaw]), k_seen = g + 1;
             if (i + 1 == n) {
               mma_commit(&bars->q_free);
@@ -537,22 +550,20 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
             return true;
           };
           ok = bounded_wait(&bars->q_full, part & 1, abort, p.wait_ns);
-          // both S buffers are free: the softmax has finished the part before
-          // (its P of this part's first units is waited for below), and that
-          // part's PVs were complete before it wrote its results
-          for (uint32_t i = 0; ok && i < 2 && i < n; ++i) {
-            const uint32_t u = base + i;
-            ok = (u < 2 || bounded_wait(&bars->pv_done[s][u & 1], ((u >> 1) - 1) & 1, abort,
-                                        p.wait_ns)) &&
-                 qk(i);
-          }
           if (ok && n == 0) {
             mbar_arrive(&bars->q_free);
             ok = pass_k(g1);
           }
+          if (ok && n > 0) ok = qk(0);
           for (uint32_t i = 0; ok && i < n; ++i) {
             const uint32_t u = base + i, buf = u & 1, half = i & 1, g = page_of(i);
-            ok = (half || (pass_w(g) && bounded_wait(&bars->w_full[g % kWide], (g / kWide) & 1,
+            // the next QK first, unless its page has yet to arrive
+            const uint32_t next = i + 1 < n ? page_of(i + 1) : 0;
+            const bool early = i + 1 < n && (!half || mbar_test(&bars->k_full[next % kRaw],
+                                                                (next / kRaw) & 1));
+            if (early) ok = qk(i + 1);
+            ok = ok &&
+                 (half || (pass_w(g) && bounded_wait(&bars->w_full[g % kWide], (g / kWide) & 1,
                                                      abort, p.wait_ns))) &&
                  bounded_wait(&bars->p_full[s][buf], (u >> 1) & 1, abort, p.wait_ns);
             if (!ok) break;
@@ -561,13 +572,11 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
                 desc_w + (g % kWide) * (2 * kTileBytes / 16) + half * (kHalf * 128 / 16);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_f16_ts(o_tmem, s_tmem + buf * kHalf + kk * 8, b + kk * (16 * 128 / 16), kPv,
-                         kk > 0 || i > 0);
+              mma_f16_ts(o_tmem, s_tmem + kColP + buf * (kHalf / 2) + kk * 8,
+                         b + kk * (16 * 128 / 16), kPv, kk > 0 || i > 0);
             mma_commit(&bars->pv_done[s][buf]);
             if (half) mma_commit(&bars->w_free[g % kWide]), w_seen = g + 1;
-            if (i + 2 < n)
-              ok = bounded_wait(&bars->pv_done[s][buf], (u >> 1) & 1, abort, p.wait_ns) &&
-                   qk(i + 2);
+            if (i + 1 < n && !early) ok = qk(i + 1);
           }
           ok = ok && pass_w(g1);
           g0 = g1;
@@ -585,10 +594,11 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
     // ------------------------------------------------------------- softmax
     const int s = warp >= 8, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t s_tmem = tmem + lane_off + s * 128, o_tmem = s_tmem + 256;
+    const uint32_t s_tmem = tmem + lane_off + s * 128, o_tmem = s_tmem + kColO;
     const float c = p.score_log2;
     const int i_tok = row / p.G;
     uint32_t done = 0;  // units (half pages) of this stream so far
+    uint32_t g0 = 0;    // pages of the parts before
     bool ok = true;
     while (ok && walk.next()) {
       const Tile& t = walk.t;
@@ -603,28 +613,28 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
       const int least = __reduce_min_sync(0xffffffffu, pos);
       float m = -INFINITY, l = 0.f;  // m: scores in units of 1 (not log2)
       float off = 0.f;
-      int page = n > 0 ? __ldg(table + walk.p0 + walk.stream_page(s, 0)) : 0;
-      int key0 = 0;      // the unit's first key
-      bool there = true; // its page is one
+      int key0 = 0;  // the unit's first key
 #pragma unroll 1
       for (int i = 0; i < 2 * n; ++i, ++done) {
         if ((i & 1) == 0) {
           key0 = (t.page0 + walk.p0 + walk.stream_page(s, i >> 1)) * kPage;
-          there = page >= 0 && page < p.num_pages;
-          if (i + 2 < 2 * n) page = __ldg(table + walk.p0 + walk.stream_page(s, (i >> 1) + 1));
         } else {
           key0 += kHalf;
         }
-        const uint32_t buf = done & 1, s_cols = s_tmem + buf * kHalf;
-        if (!all_wait(bars, &bars->s_full[s][buf], (done >> 1) & 1, p)) {
+        const uint32_t buf = done & 1, p_cols = s_tmem + kColP + buf * (kHalf / 2);
+        if (!all_wait(bars, &bars->s_full[s], done & 1, p)) {
           ok = false;
           break;
         }
         tc_fence_after();
         uint32_t r[2][32];
-        tmem_ld32(s_cols, r[0]);
-        tmem_ld32(s_cols + 32, r[1]);
+        tmem_ld32(s_tmem, r[0]);
+        tmem_ld32(s_tmem + 32, r[1]);
         tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->s_free[s]);
+        const bool there = bars->there[(g0 + walk.stream_page(s, i >> 1)) % kThere];
         if (!there || key0 + kHalf - 1 > least) {
           const int lim = there ? pos - key0 : -1;  // the last key this row attends to
 #pragma unroll
@@ -634,70 +644,79 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
               if (q * 32 + e > lim) r[q][e] = 0xFF800000u;  // -inf
         }
         const float2 c2 = make_float2(c, c);
-        float2 sum[2];
-        uint32_t w[32];
-        // P against the present reference m, and the largest of them
-        auto exponentials = [&]() {
-          const float2 off2 = make_float2(off, off);
-          sum[0] = sum[1] = make_float2(0.f, 0.f);
-          __half2 most[2] = {__half2half2(__ushort_as_half(0)), __half2half2(__ushort_as_half(0))};
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const uint32_t* x = &r[e >> 4][2 * (e & 15)];
-            float2 a = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, off2);
-            a.x = ex2_approx(a.x);
-            a.y = ex2_approx(a.y);
-            sum[e & 1] = add2(sum[e & 1], a);
-            const __half2 h = __floats2half2_rn(a.x, a.y);
-            most[e & 1] = __hmax2(most[e & 1], h);
-            w[e] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          most[0] = __hmax2(most[0], most[1]);
-          return __hmax(__low2half(most[0]), __high2half(most[0]));
-        };
-        // The reference is the maximum of the row's first unit and moves (O
-        // and l with it) only where a P passes kMostP: the unit's
-        // own maximum is not waited for.
-        bool grown = i == 0;
-        if (i > 0) {
-          const __half most = exponentials();
-          grown = m == -INFINITY || __hgt(most, __float2half(kMostP));
-        }
-        if (__any_sync(0xffffffffu, grown)) {
-          float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(r[q][e]));
-          // only the rows that need it move: what a row gives does not depend
-          // on the others of its warp
-          const float top = grown ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) : m;
-          if (i > 0) {
-            // every PV of the stream has to be complete: the one before this
-            // unit is the last issued
-            if (!all_wait(bars, &bars->pv_done[s][buf ^ 1], ((done - 1) >> 1) & 1, p)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const float f = !grown ? 1.f : m == -INFINITY ? 0.f : ex2_approx((m - top) * c);
-            l *= f;
+        // The reference m is the maximum of the row's first unit.  Later
+        // maxima are not waited for: only where the unit's P add up to more
+        // than kMostSum (so that one could pass f16's range) m moves to the
+        // maximum, O and l with it, and the unit is done again.
+        bool move = m == -INFINITY;
+        float sum;
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              uint32_t o[32];
-              tmem_ld32(o_tmem + q * 32, o);
-              tmem_wait_ld();
+        for (;;) {
+          if (__any_sync(0xffffffffu, move)) {
+            float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(o_tmem + q * 32, o);
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(r[q][e]));
+            // only the rows that need it move: what a row gives does not
+            // depend on the others of its warp
+            const float top = move ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) : m;
+            if (i > 0) {
+              // every PV of the stream has to be complete: the one before
+              // this unit is the last issued
+              if (!all_wait(bars, &bars->pv_done[s][buf ^ 1], ((done - 1) >> 1) & 1, p)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const float f = !move ? 1.f : m == -INFINITY ? 0.f : ex2_approx((m - top) * c);
+              l *= f;
+#pragma unroll 1
+              for (int q = 0; q < 4; ++q) {
+                uint32_t o[32];
+                tmem_ld32(o_tmem + q * 32, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(o_tmem + q * 32, o);
+              }
             }
+            m = top;
+            off = m == -INFINITY ? 0.f : kPShift - m * c;
           }
-          m = top;
-          off = m == -INFINITY ? 0.f : kPShift - m * c;
-          exponentials();
+          // P into its buffer, in groups of 8 pairs, exponentials first, so
+          // that their latencies overlap; each half is stored as it is done
+          const float2 off2 = make_float2(off, off);
+          float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 16; k += 8) {
+              float2 a[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                a[e] = fma2(make_float2(__uint_as_float(r[q][2 * (k + e)]),
+                                        __uint_as_float(r[q][2 * (k + e) + 1])),
+                            c2, off2);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) a[e].x = ex2_approx(a[e].x), a[e].y = ex2_approx(a[e].y);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                sums[e & 1] = add2(sums[e & 1], a[e]);
+                const __half2 h = __floats2half2_rn(a[e].x, a[e].y);
+                w[k + e] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+            }
+            tmem_st16(p_cols + q * 16, w);
+          }
+          sum = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+          const bool again = !move && sum > kMostSum;
+          if (!__any_sync(0xffffffffu, again)) break;
+          move = again;
         }
-        tmem_st32(s_cols, w);
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        if (!ok) break;
+        l += sum;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -757,6 +776,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         }
         tc_fence_before();
       }
+      g0 += walk.p1 - walk.p0;
       if (valid)
         p.part_lse[prow] = n > 0 && l != 0.f ? m * c - kPShift + log2f(l) : -INFINITY;
     }
@@ -772,39 +792,40 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
     bool ok = true;
     while (ok && walk.next()) {
       const Tile& t = walk.t;
-      const int32_t* table = p.block_table + t.b * p.bt_stride + t.page0;
       for (int j = walk.p0; j < walk.p1; ++j, ++g) {
-        const int page = __ldg(table + j);
-        const int keys =
-            page >= 0 && page < p.num_pages ? min(kPage, t.seq - (t.page0 + j) * kPage) : 0;
         if (!all_wait(bars, &bars->v_full[g % kRaw], (g / kRaw) & 1, p) ||
             (g >= kWide && !all_wait(bars, &bars->w_free[g % kWide], ((g / kWide) - 1) & 1, p))) {
           ok = false;
           break;
         }
+        const int keys =
+            bars->there[g % kThere] ? min(kPage, t.seq - (t.page0 + j) * kPage) : 0;
         const uint8_t* src = smem + kOffV + (g % kRaw) * kTileBytes;
         uint8_t* dst = smem + kOffW + (g % kWide) * 2 * kTileBytes;
-        // all loads first, and one test for the rare NaN: the conversions of
-        // the 8 chunks then overlap
-        uint32_t w[8][4];
+        // the loads of four chunks first, so that their conversions overlap;
+        // the loop stays rolled: the roles' loops share the instruction cache
+        bool nan = false;
+#pragma unroll 1
+        for (int u0 = 0; u0 < 8; u0 += 4) {
+        uint32_t w[4][4];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int e = wt + u * 128, key = e >> 3, ch = e & 7;
+        for (int u = 0; u < 4; ++u) {
+          const int e = wt + (u0 + u) * 128, key = e >> 3, ch = e & 7;
           const uint4 v = *reinterpret_cast<const uint4*>(src + key * 128 + ((ch ^ (key & 7)) << 4));
           w[u][0] = v.x, w[u][1] = v.y, w[u][2] = v.z, w[u][3] = v.w;
         }
         if (keys < kPage) {
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
-            if (((wt + u * 128) >> 3) >= keys) w[u][0] = w[u][1] = w[u][2] = w[u][3] = 0u;
+          for (int u = 0; u < 4; ++u)
+            if (((wt + (u0 + u) * 128) >> 3) >= keys) w[u][0] = w[u][1] = w[u][2] = w[u][3] = 0u;
         }
         // f16 tile of the chunks; the result is NaN if one of the codes is
         auto store = [&]() {
           __half2 sick = __half2half2(__ushort_as_half(0));
           const __half2 zero = sick;
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int e = wt + u * 128, key = e >> 3, ch = e & 7;
+          for (int u = 0; u < 4; ++u) {
+            const int e = wt + (u0 + u) * 128, key = e >> 3, ch = e & 7;
             uint32_t h[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -823,13 +844,15 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
           return __hisnan(__low2half(sick)) || __hisnan(__high2half(sick));
         };
         if (store()) {
-          *(volatile int*)&bars->nan_seen = 1;
+          nan = true;
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
+          for (int u = 0; u < 4; ++u)
 #pragma unroll
             for (int k = 0; k < 4; ++k) w[u][k] &= ~((nan_bytes(w[u][k]) >> 7) * 0xFFu);
           store();
         }
+        }
+        if (nan) *(volatile int*)&bars->nan_seen = 1;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -852,13 +875,14 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
 // ----------------------------------------------------------------- combine
 
 constexpr int kCombineWarps = 8;
+constexpr int kMaxParts = 2 * 192;  // parts of a tile: two streams a CTA
 
 struct CombineParams {
   const PlanHead* head;
   const Tile* tiles;
-  const int32_t* req_tile;
   const int32_t* cu_q;
   int B, T, Hq, Hkv, G, C, ctas;
+  int rows;  // rows of a tile that a CTA takes
   const float* part_o;
   const float* part_lse;
   float v_scale;
@@ -866,123 +890,178 @@ struct CombineParams {
   float* lse;
 };
 
-// One row (token, query head): kTeam warps share its parts.
+// A CTA takes some rows of a tile of a request's own pages (blockIdx.x) of a
+// KV head (.y): first the parts of that tile and of the shared tiles (two at
+// most) that its tokens lie in are listed, then kTeam warps merge the parts
+// of each row: weights 2^(lse - m), fp32 sums.  The tile numbers past the
+// batch's tiles clear the rows of a batch that was refused.
 template <int kTeam>
 __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const CombineParams p) {
+  // per listed tile: its parts' first rows (of the tile's first token and
+  // head), in line order
+  __shared__ int s_row[3][kMaxParts];
+  __shared__ int s_n[3];
+  __shared__ Tile s_tile[3];
   __shared__ float s_acc[kTeam > 1 ? kCombineWarps : 1][kD];
   __shared__ float s_m[kCombineWarps], s_l[kCombineWarps];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int member = warp % kTeam;
-  const int64_t r = ((int64_t)blockIdx.x * kCombineWarps + warp) / kTeam;
+  const int h = blockIdx.y;
   const PlanHead hd = *p.head;
-  const int T = p.cu_q[p.B];
-  const int tok = (int)min(r / p.Hq, (int64_t)p.T), hq = (int)(r % p.Hq);
-  // rows behind the last sequence keep what they hold
-  const bool live = r < (int64_t)p.T * p.Hq && (hd.bad || tok < T);
-  if (kTeam == 1 && !live) return;
-  float m = -INFINITY, l = 0.f;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  if (live && !hd.bad) {
-    const int h = hq / p.G, g = hq - h * p.G;
-    const int b = min(warp_request_of(p.cu_q, p.B, tok), p.B - 1);
-    const int64_t share = share_of((int64_t)hd.cost * p.Hkv, p.ctas);
-    for (int kind = hd.shared_tiles > 0 ? 0 : 1; kind < 2; ++kind) {
-      const int tile = kind == 0
-                           ? tok / (2 * p.C)
-                           : hd.shared_tiles + p.req_tile[b] + (tok - p.cu_q[b]) / (2 * p.C);
-      const Tile t = p.tiles[tile];
+  if (hd.bad) {  // every row empty
+    const int64_t n = (int64_t)p.T * p.G * (kD / 8);
+    const int64_t step = (int64_t)gridDim.x * gridDim.z * blockDim.x;
+    for (int64_t e = ((int64_t)blockIdx.z * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x;
+         e < n; e += step) {
+      const int64_t r = e / (kD / 8);
+      const int64_t row = r / p.G * p.Hq + h * p.G + r % p.G;
+      // 8-byte stores: out need not be aligned to more
+      uint2* dst = reinterpret_cast<uint2*>(p.out + row * kD) + 2 * (e % (kD / 8));
+      dst[0] = dst[1] = make_uint2(0u, 0u);
+      if (p.lse && e % (kD / 8) == 0) p.lse[row] = -INFINITY;
+    }
+    return;
+  }
+  const int tile = hd.shared_tiles + blockIdx.x;
+  if (tile >= hd.ntiles) return;
+  const Tile own = p.tiles[tile];
+  const int row0 = blockIdx.z * p.rows, rows = min(p.rows, own.ntok * p.G - row0);
+  if (rows <= 0) return;
+  if (warp < 3) {  // warp 0: the own tile, 1 and 2: the shared ones
+    const int first = own.tok0 / (2 * p.C), last = (own.tok0 + own.ntok - 1) / (2 * p.C);
+    const int ti = warp == 0 ? tile : first + warp - 1;
+    int n = 0;
+    if (warp == 0 || (hd.shared_tiles > 0 && ti <= last)) {
+      const Tile t = warp == 0 ? own : p.tiles[ti];
       const bool pair = t.ntok > p.C;
       const int rate = tile_rate(t.ntok, p.C);
+      const int64_t share = share_of((int64_t)hd.cost * p.Hkv, p.ctas);
       const int64_t t0 = (int64_t)h * hd.cost + t.start;
       const int64_t t1 = t0 + tile_cost(t.ntok, t.npages, p.C);
       const int i0 = (int)(t0 / share), i1 = (int)((t1 - 1) / share);
-      const int o = tok - t.tok0;
-      // entries: (CTA, stream) of a solo tile, CTA of a pair
-      const int entries = (i1 - i0 + 1) * (pair ? 1 : 2);
-      for (int e0 = member * 32; e0 < entries; e0 += kTeam * 32) {
-        const int e = e0 + lane;
-        float le = -INFINITY;
-        int64_t row = 0;
-        if (e < entries) {
-          const int cta = i0 + (pair ? e : e >> 1), s = pair ? o >= p.C : e & 1;
-          const int pa = pages_before(max(cta * share, t0) - t0, t.npages, rate);
-          const int pb = pages_before(min((cta + 1) * share, t1) - t0, t.npages, rate);
-          if (pb > pa) {
-            row = part_row(cta, h, tile, hd.shared_tiles, t.tok0, p.T, p.G) +
-                  (s ? (pair ? p.C : t.ntok) * p.G : 0) + (pair && s ? o - p.C : o) * p.G + g;
-            le = __ldg(p.part_lse + row);
-          }
+      for (int c0 = i0; c0 <= i1; c0 += 32) {
+        const int cta = c0 + lane;
+        int pa = 0, pb = 0;
+        if (cta <= i1) {
+          pa = pages_before(max(cta * share, t0) - t0, t.npages, rate);
+          pb = pages_before(min((cta + 1) * share, t1) - t0, t.npages, rate);
         }
-        float top = le;
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-        top = fmaxf(top, m);
-        if (top > m) {
-          const float f = m == -INFINITY ? 0.f : exp2f(m - top);
-          l *= f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[k] *= f;
-          m = top;
+        // a solo part's second stream has pages where there are two
+        const int streams = pb > pa ? (pair ? 1 : min(2, pb - pa)) : 0;
+        const uint32_t one = __ballot_sync(0xffffffffu, streams > 0);
+        const uint32_t two = __ballot_sync(0xffffffffu, streams > 1);
+        const uint32_t below = (1u << lane) - 1u;
+        if (streams > 0) {
+          const int at = n + __popc(one & below) + __popc(two & below);
+          const int row = (int)part_row(cta, h, ti, hd.shared_tiles, t.tok0, p.T, p.G);
+          if (at < kMaxParts) s_row[warp][at] = row;
+          if (streams > 1 && at + 1 < kMaxParts) s_row[warp][at + 1] = row + t.ntok * p.G;
         }
-        // NaN (a NaN score) stays one
-        const float w = le == -INFINITY ? 0.f : exp2f(le - (m == -INFINITY ? 0.f : m));
-        uint32_t bits = __ballot_sync(0xffffffffu, w != 0.f);
-        while (bits) {
-          float4 v[8];
-          float wj[8];
+        n += __popc(one) + __popc(two);
+      }
+      if (lane == 0) s_tile[warp] = t;
+    }
+    if (lane == 0) s_n[warp] = min(n, kMaxParts);
+  }
+  __syncthreads();
+  const int member = warp % kTeam;
+  constexpr int kRows = kCombineWarps / kTeam;  // rows at a time
+  for (int r0 = 0; r0 < rows; r0 += kRows) {
+    const int r = row0 + r0 + warp / kTeam;
+    const bool live = r0 + warp / kTeam < rows;
+    float m = -INFINITY, l = 0.f;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const int tok = own.tok0 + (live ? r / p.G : 0);
+    if (live) {
+      for (int k = 0; k < 3; ++k) {
+        const int n = s_n[k];
+        if (n == 0) continue;
+        const int o = tok - s_tile[k].tok0;  // the token within the listed tile
+        if (o < 0 || o >= s_tile[k].ntok) continue;
+        // rows of a pair: C tokens of the first stream, then the second's:
+        // the same as token order
+        const int off = o * p.G + r % p.G;
+        for (int e0 = member * 32; e0 < n; e0 += kTeam * 32) {
+          const int e = e0 + lane;
+          const int row = e < n ? s_row[k][e] + off : 0;
+          const float le = e < n ? __ldcg(p.part_lse + row) : -INFINITY;
+          float top = le;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int j = bits ? __ffs(bits) - 1 : 0;
-            wj[k] = bits ? __shfl_sync(0xffffffffu, w, j) : 0.f;
-            const int64_t rj = __shfl_sync(0xffffffffu, row, j);
-            v[k] = bits ? __ldcg(reinterpret_cast<const float4*>(p.part_o + rj * kD) + lane)
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
-            bits &= bits - 1;
+          for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          if (top > m) {
+            const float f = m == -INFINITY ? 0.f : exp2f(m - top);
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < 4; ++d) acc[d] *= f;
+            m = top;
           }
+          // NaN (a NaN score) stays one
+          const float w = le == -INFINITY ? 0.f : exp2f(le - (m == -INFINITY ? 0.f : m));
+          uint32_t bits = __ballot_sync(0xffffffffu, w != 0.f);
+          while (bits) {
+            float4 v[8];
+            float wj[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            l += wj[k];
-            acc[0] = fmaf(wj[k], v[k].x, acc[0]);
-            acc[1] = fmaf(wj[k], v[k].y, acc[1]);
-            acc[2] = fmaf(wj[k], v[k].z, acc[2]);
-            acc[3] = fmaf(wj[k], v[k].w, acc[3]);
+            for (int d = 0; d < 8; ++d) {
+              const int j = bits ? __ffs(bits) - 1 : 0;
+              wj[d] = bits ? __shfl_sync(0xffffffffu, w, j) : 0.f;
+              const int rj = __shfl_sync(0xffffffffu, row, j);
+              v[d] = bits ? __ldcg(reinterpret_cast<const float4*>(p.part_o + (int64_t)rj * kD) +
+                                   lane)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+              bits &= bits - 1;
+            }
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+              l += wj[d];
+              acc[0] = fmaf(wj[d], v[d].x, acc[0]);
+              acc[1] = fmaf(wj[d], v[d].y, acc[1]);
+              acc[2] = fmaf(wj[d], v[d].z, acc[2]);
+              acc[3] = fmaf(wj[d], v[d].w, acc[3]);
+            }
           }
         }
       }
     }
-  }
-  if (kTeam > 1) {
-    if (lane == 0) s_m[warp] = m, s_l[warp] = l;
-    *reinterpret_cast<float4*>(&s_acc[warp][lane * 4]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    __syncthreads();
-    if (member != 0 || !live) return;
-    float top = -INFINITY;
-    for (int k = 0; k < kTeam; ++k) top = fmaxf(top, s_m[warp + k]);
-    l = 0.f;
+    if constexpr (kTeam > 1) {
+      if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+      *reinterpret_cast<float4*>(&s_acc[warp][lane * 4]) =
+          make_float4(acc[0], acc[1], acc[2], acc[3]);
+      __syncthreads();
+      if (member == 0 && live) {
+        float top = -INFINITY;
+        for (int k = 0; k < kTeam; ++k) top = fmaxf(top, s_m[warp + k]);
+        l = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = 0.f;
-    for (int k = 0; k < kTeam; ++k) {
-      const float f = s_m[warp + k] == -INFINITY && s_l[warp + k] == 0.f
-                          ? 0.f
-                          : exp2f(s_m[warp + k] - (top == -INFINITY ? 0.f : top));
-      const float f2 = s_l[warp + k] == s_l[warp + k] ? f : s_l[warp + k];
-      l += f2 * s_l[warp + k];
-      const float4 v = *reinterpret_cast<const float4*>(&s_acc[warp + k][lane * 4]);
-      acc[0] = fmaf(f2, v.x, acc[0]);
-      acc[1] = fmaf(f2, v.y, acc[1]);
-      acc[2] = fmaf(f2, v.z, acc[2]);
-      acc[3] = fmaf(f2, v.w, acc[3]);
+        for (int d = 0; d < 4; ++d) acc[d] = 0.f;
+        for (int k = 0; k < kTeam; ++k) {
+          const float lk = s_l[warp + k];
+          // a member without parts has l = 0; one with a NaN keeps it
+          const float f = lk == 0.f ? 0.f
+                          : lk == lk ? exp2f(s_m[warp + k] - (top == -INFINITY ? 0.f : top))
+                                     : lk;
+          l += f * lk;
+          const float4 v = *reinterpret_cast<const float4*>(&s_acc[warp + k][lane * 4]);
+          acc[0] = fmaf(f, v.x, acc[0]);
+          acc[1] = fmaf(f, v.y, acc[1]);
+          acc[2] = fmaf(f, v.z, acc[2]);
+          acc[3] = fmaf(f, v.w, acc[3]);
+        }
+        m = top;
+      }
     }
-    m = top;
+    if (member == 0 && live) {
+      const float scale = l == 0.f ? 0.f : p.v_scale / l;
+      const int64_t row = (int64_t)tok * p.Hq + h * p.G + r % p.G;
+      *reinterpret_cast<uint2*>(p.out + row * kD + lane * 4) =
+          make_uint2(pack_bf16x2(acc[0] * scale, acc[1] * scale),
+                     pack_bf16x2(acc[2] * scale, acc[3] * scale));
+      if (p.lse && lane == 0)
+        p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+    }
+    if constexpr (kTeam > 1) __syncthreads();
   }
-  const float scale = l == 0.f ? 0.f : p.v_scale / l;
-  const uint2 v = make_uint2(pack_bf16x2(acc[0] * scale, acc[1] * scale),
-                             pack_bf16x2(acc[2] * scale, acc[3] * scale));
-  *reinterpret_cast<uint2*>(p.out + r * kD + lane * 4) = v;
-  if (p.lse && lane == 0)
-    p.lse[r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
 // -------------------------------------------------------------------- host
@@ -998,6 +1077,7 @@ bool layout(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t prefix, int64
   // costs and partial rows in range of their integers
   if ((double)tiles * (double)(ceil_div(max_k, kPage) * kCostPair + kCostTile) > 1.0e9) return false;
   const int64_t rows = 256 * ((int64_t)ctas + 1) + Hkv * (prefix > 0 ? 4 : 2) * T * G;
+  if (rows >= INT_MAX || 2 * ctas > kMaxParts) return false;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   l->head = 0;
   l->tiles = 256;
@@ -1089,15 +1169,19 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, void* ws, cudaStream_t 
                  q_map, ap);
   if (e != cudaSuccess) return e;
 
-  const CombineParams cp = {head, tiles, req_tile, a.cu_q, (int)a.B, (int)a.T, (int)a.Hq,
-                            (int)a.Hkv, G, C, ctas, part_o, part_lse, a.v_scale, a.out, a.lse};
-  const int64_t rows = a.T * a.Hq;
-  // few rows have many parts each: a CTA per row; else a warp per row
-  if (rows <= 2048)
-    return launch_pdl(combine_kernel<kCombineWarps>, dim3((unsigned)rows),
-                      dim3(kCombineWarps * 32), 0, stream, cp);
-  return launch_pdl(combine_kernel<1>, dim3((unsigned)ceil_div(rows, kCombineWarps)),
-                    dim3(kCombineWarps * 32), 0, stream, cp);
+  // rows of a tile by CTA, and warps by row: while there are few rows, each
+  // has many parts, and more warps share them
+  const int64_t rows = a.T * a.Hq, tile_rows = std::min<int64_t>(2 * C, a.max_q) * G;
+  const int team = rows <= 1024 ? 8 : rows <= 4096 ? 2 : 1;
+  const int cta_rows = rows <= 16384 ? kCombineWarps / team : 4 * kCombineWarps;
+  const CombineParams cp = {head, tiles, a.cu_q, (int)a.B, (int)a.T, (int)a.Hq, (int)a.Hkv, G, C,
+                            ctas, cta_rows, part_o, part_lse, a.v_scale, a.out, a.lse};
+  const int64_t own = std::min<int64_t>(a.T, ceil_div(a.T, 2 * C) + a.B);
+  const dim3 grid((unsigned)own, (unsigned)a.Hkv, (unsigned)std::max<int64_t>(1, ceil_div(tile_rows, cta_rows)));
+  const dim3 block(kCombineWarps * 32);
+  if (team == 8) return launch_pdl(combine_kernel<8>, grid, block, 0, stream, cp);
+  if (team == 2) return launch_pdl(combine_kernel<2>, grid, block, 0, stream, cp);
+  return launch_pdl(combine_kernel<1>, grid, block, 0, stream, cp);
 }
 
 }  // namespace msa
