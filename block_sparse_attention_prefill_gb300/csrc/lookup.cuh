@@ -28,6 +28,23 @@ __device__ __forceinline__ int warp_request_of(const int32_t* __restrict__ cu, i
   return lo;
 }
 
+// The same for 32 consecutive tokens at once, lane i's being `first + i`: the
+// first one's request by the search above; lanes whose token lies behind it
+// search on from there.
+__device__ __forceinline__ int lane_request_of(const int32_t* __restrict__ cu, int B, int first) {
+  const int t = first + (int)(threadIdx.x & 31);
+  int lo = warp_request_of(cu, B, first);
+  if (lo < B && __ldg(cu + lo + 1) <= t) {
+    int hi = B;  // the answer lies in (lo, hi]
+    ++lo;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (__ldg(cu + mid + 1) <= t) lo = mid + 1; else hi = mid;
+    }
+  }
+  return lo;
+}
+
 // The row of the pool (page * 128 + offset) that position `pos` of request b
 // lies in, or -1 with a status bit in *bad.
 __device__ __forceinline__ int64_t pool_row(const int32_t* __restrict__ block_table,

@@ -380,6 +380,16 @@ __device__ __forceinline__ void st_global_v8(void* p, uint32_t a0, uint32_t a1,
       : "memory");
 }
 
+// 32-byte load of data that the kernel does not write and reads once; p must
+// be 32-byte aligned.
+__device__ __forceinline__ void ldg_nc_v8(const void* p, uint32_t (&a)[8]) {
+  asm volatile(
+      "ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]),
+        "=r"(a[7])
+      : "l"(p));
+}
+
 // st_global_v8 with an L2 cache policy.
 __device__ __forceinline__ void st_global_v8_hint(void* p, uint32_t a0, uint32_t a1,
                                                   uint32_t a2, uint32_t a3,

@@ -37,7 +37,9 @@ def _tensor(t, name, dtypes, shape=None, contiguous=True):
         _fail("%s is required", name)
     if t.dtype not in dtypes:
         _fail("%s has dtype %s, expected one of %s", name, t.dtype, dtypes)
-    if shape is not None:
+    # equal shapes end the comparison at once: these checks run on every call
+    # of a decode step
+    if shape is not None and t.shape != shape:
         have = t.shape
         if len(have) != len(shape) or any(w is not None and w != h for w, h in zip(shape, have)):
             _fail("%s must be [%s], got %s", name,
@@ -47,29 +49,32 @@ def _tensor(t, name, dtypes, shape=None, contiguous=True):
 
 
 def _place(first, *others):
-    """The device that all given tensors share, which must be the current one."""
-    if not first.is_cuda:
+    """The index of the device that all given tensors share, which must be the
+    current one."""
+    dev = first.get_device()
+    if dev < 0:
         _fail("tensors must be CUDA tensors")
-    dev = first.device
     for t in others:
-        if t is not None and t.device != dev:
-            _fail("tensors are on different devices: %s and %s", dev, t.device)
-    if dev.index != torch.cuda.current_device():
-        _fail("tensors are on %s, the current device is cuda:%d", dev, torch.cuda.current_device())
+        if t is not None and t.get_device() != dev:
+            _fail("tensors are on different devices: %s and %s", first.device, t.device)
+    if dev != torch._C._cuda_getDevice():
+        _fail("tensors are on cuda:%d, the current device is cuda:%d", dev,
+              torch.cuda.current_device())
     return dev
 
 
 def _handle(stream, dev):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index)
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _new(shape, dtype, dev, handle):
-    """A tensor for use on the stream `handle`, whichever stream is current."""
-    t = torch.empty(shape, dtype=dtype, device=dev)
-    if handle != torch._C._cuda_getCurrentRawStream(dev.index):
-        t.record_stream(torch.cuda.ExternalStream(handle, device=dev))
+def _new(shape, dtype, like, dev, handle):
+    """A tensor on like's device for use on the stream `handle`, whichever
+    stream is current."""
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if handle != torch._C._cuda_getCurrentRawStream(dev):
+        t.record_stream(torch.cuda.ExternalStream(handle, device=like.device))
     return t
 
 
@@ -80,15 +85,21 @@ def _ptr(t):
 def _pool(kv, fp4):
     """(num_pages, Hkv) of a page pool."""
     if fp4:
-        _tensor(kv, "kv4", (torch.uint8,), (None, None, 2, NVFP4_SLOT_BYTES))
+        _tensor(kv, "kv4", (torch.uint8,))
+        shape = kv.shape
+        if len(shape) != 4 or shape[2] != 2 or shape[3] != NVFP4_SLOT_BYTES:
+            _fail("kv4 must be [any, any, 2, %d], got %s", NVFP4_SLOT_BYTES, tuple(shape))
     else:
-        _tensor(kv, "kv", _E4M3, (None, None, PAGE_SIZE, 2 * HEAD_DIM))
-    return kv.shape[0], kv.shape[1]
+        _tensor(kv, "kv", _E4M3)
+        shape = kv.shape
+        if len(shape) != 4 or shape[2] != PAGE_SIZE or shape[3] != 2 * HEAD_DIM:
+            _fail("kv must be [any, any, 128, 256], got %s", tuple(shape))
+    return shape[0], shape[1]
 
 
-def _rows(t, name, T, Hkv):
+def _rows(t, name, shape):
     """Strides of K or V rows [T, Hkv, 128] whose 128 values are contiguous."""
-    _tensor(t, name, _TYPES, (T, Hkv, HEAD_DIM), contiguous=False)
+    _tensor(t, name, _TYPES, shape, False)
     token, head, one = t.stride()
     if one != 1:
         _fail("%s must have its 128 values contiguous", name)
@@ -96,14 +107,18 @@ def _rows(t, name, T, Hkv):
 
 
 def _table(block_table, B):
-    _tensor(block_table, "block_table", _I32, (B, None))
-    return block_table.shape[1]
+    _tensor(block_table, "block_table", _I32)
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != B:
+        _fail("block_table must be [%d, any], got %s", B, tuple(shape))
+    return shape[1]
 
 
-def _requests(cu, name, B=None):
-    _tensor(cu, name, _I32, (None if B is None else B + 1,))
-    if cu.shape[0] < 1:
-        _fail("%s must have at least one element", name)
+def _requests(cu, name):
+    """B of prefix sums [B + 1]."""
+    _tensor(cu, name, _I32)
+    if cu.dim() != 1 or cu.shape[0] < 1:
+        _fail("%s must be one-dimensional with at least one element", name)
     return cu.shape[0] - 1
 
 
@@ -115,12 +130,13 @@ def _status(status):
 def _write(name, fp4, k, v, kv, k_scale, v_scale, block_table, cu_q, cu_k, status, stream):
     pages, Hkv = _pool(kv, fp4)
     B = _requests(cu_q, "cu_seqlens_q")
-    _requests(cu_k, "cu_seqlens_k", B)
+    _tensor(cu_k, "cu_seqlens_k", _I32, (B + 1,))
     width = _table(block_table, B)
     if k is None or v is None or k.dim() != 3:
         _fail("k and v must be [T, Hkv, 128]")
     T = k.shape[0]
-    ks, vs = _rows(k, "k", T, Hkv), _rows(v, "v", T, Hkv)
+    shape = (T, Hkv, HEAD_DIM)
+    ks, vs = _rows(k, "k", shape), _rows(v, "v", shape)
     if k.dtype != v.dtype:
         _fail("k and v have different dtypes: %s and %s", k.dtype, v.dtype)
     _status(status)
@@ -169,9 +185,10 @@ def _read(name, fp4, kv, k_scale, v_scale, block_table, cu, T, starts, dtype, k,
     if k is None:
         if dtype not in _TYPES:
             _fail("dtype must be one of %s", tuple(_TYPES))
-        k = _new((T, Hkv, HEAD_DIM), dtype, dev, handle)
-        v = _new((T, Hkv, HEAD_DIM), dtype, dev, handle)
-    ks, vs = _rows(k, "k", T, Hkv), _rows(v, "v", T, Hkv)
+        k = _new((T, Hkv, HEAD_DIM), dtype, kv, dev, handle)
+        v = _new((T, Hkv, HEAD_DIM), dtype, kv, dev, handle)
+    shape = (T, Hkv, HEAD_DIM)
+    ks, vs = _rows(k, "k", shape), _rows(v, "v", shape)
     if k.dtype != v.dtype:
         _fail("k and v have different dtypes: %s and %s", k.dtype, v.dtype)
     if (T > 1 and 0 in (ks[0], vs[0])) or (Hkv > 1 and 0 in (ks[1], vs[1])):
@@ -222,10 +239,12 @@ def msa_prefix_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_
     MSA_STATUS_* bits are OR-ed into.  Returns (out bf16 [T, Hq, 128], lse
     fp32 [T, Hq] or None)."""
     pages, Hkv = _pool(kv, False)
-    _tensor(q, "q", _E4M3, (None, None, HEAD_DIM))
+    _tensor(q, "q", _E4M3)
+    if q.dim() != 3 or q.shape[2] != HEAD_DIM:
+        _fail("q must be [any, any, 128], got %s", tuple(q.shape))
     T, Hq, _ = q.shape
     B = _requests(cu_seqlens_q, "cu_seqlens_q")
-    _requests(cu_seqlens_k, "cu_seqlens_k", B)
+    _tensor(cu_seqlens_k, "cu_seqlens_k", _I32, (B + 1,))
     width = _table(block_table, B)
     _status(status)
     if out is not None:
@@ -241,11 +260,11 @@ def msa_prefix_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_
     dev = _place(q, kv, block_table, cu_seqlens_q, cu_seqlens_k, workspace, out, lse, status)
     handle = _handle(stream, dev)
     if workspace is None:
-        workspace = _new(need, torch.uint8, dev, handle)
+        workspace = _new(need, torch.uint8, q, dev, handle)
     if out is None:
-        out = _new((T, Hq, HEAD_DIM), torch.bfloat16, dev, handle)
+        out = _new((T, Hq, HEAD_DIM), torch.bfloat16, q, dev, handle)
     if lse is None and want_lse:
-        lse = _new((T, Hq), torch.float32, dev, handle)
+        lse = _new((T, Hq), torch.float32, q, dev, handle)
     _check(load().msa_prefix_attention(
         q.data_ptr(), kv.data_ptr(), pages, q_scale, k_scale, v_scale, softmax_scale,
         block_table.data_ptr(), width, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, T, Hq,
@@ -256,7 +275,9 @@ def msa_prefix_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_
 
 def _verify(name, target, drafts, uniforms, draft_probs, counts, tokens, accepted, stream):
     greedy = name == "msa_verify_greedy"
-    _tensor(target, "target", _TYPES, (None, None, None), contiguous=False)
+    _tensor(target, "target", _TYPES, None, False)
+    if target.dim() != 3:
+        _fail("target must be [any, any, any], got %s", tuple(target.shape))
     B, n, V = target.shape
     if n < 1:
         _fail("target must have at least one row a request")
@@ -274,11 +295,11 @@ def _verify(name, target, drafts, uniforms, draft_probs, counts, tokens, accepte
     dev = _place(target, drafts, uniforms, draft_probs, counts, tokens, accepted)
     handle = _handle(stream, dev)
     if tokens is None:
-        tokens = _new((B, n), torch.int32, dev, handle)
+        tokens = _new((B, n), torch.int32, target, dev, handle)
     else:
         _tensor(tokens, "tokens", _I32, (B, n))
     if accepted is None:
-        accepted = _new((B,), torch.int32, dev, handle)
+        accepted = _new((B,), torch.int32, target, dev, handle)
     else:
         _tensor(accepted, "accepted", _I32, (B,))
     t_req, t_row, _ = target.stride()
