@@ -24,9 +24,9 @@
 //
 // Greedy: draft i stands iff it is the first of the largest values of its
 // row.  The same cluster scans the request's rows in order, each CTA its
-// eighth; a CTA that has seen a draft beaten tells the others (a plain
-// shared-memory minimum in each CTA, no barrier), who then leave out the
-// rows behind it: those rows cannot matter.
+// eighth, each warp by itself; a warp that has seen a draft beaten tells all
+// CTAs (a minimum in their shared memory, no barrier), and rows behind it
+// are left out: they cannot matter.
 #include <algorithm>
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -40,7 +40,7 @@ namespace msa {
 namespace {
 
 constexpr int kCluster = 8;
-constexpr int kVThreads = 512;
+constexpr int kVThreads = 256;
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kMaxVerify = 32;  // rows of one request
 
@@ -48,26 +48,74 @@ __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 
+// N consecutive elements as they lie in memory (16 bytes, or one element).
 template <typename T, int N>
-struct Vec {
-  T v[N];
-};
-template <typename T, int N>
-__device__ __forceinline__ void load_vec(const T* p, float (&x)[N]) {
-  if constexpr (N * sizeof(T) == 16) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-    const Vec<T, N>& t = reinterpret_cast<const Vec<T, N>&>(w);
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = to_f32(t.v[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = to_f32(p[i]);
+struct Raw {
+  static constexpr bool kVec = N * sizeof(T) == 16;
+  uint32_t w[kVec ? 4 : 1];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kVec) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (sizeof(T) == 4) {
+      w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    } else {
+      w[0] = __ldg(reinterpret_cast<const uint16_t*>(p));
+    }
   }
-}
+  __device__ __forceinline__ void fill(uint32_t bits) {
+#pragma unroll
+    for (int i = 0; i < (kVec ? 4 : 1); ++i) w[i] = bits;
+  }
+  // the elements from v on that lie before hi; the others' bits are `rest`
+  // (a word of two equal elements for the 2-byte types)
+  __device__ __forceinline__ void load_to(const T* row, int v, int hi, uint32_t rest) {
+    if (v + N <= hi) {
+      load(row + v);
+    } else {
+      fill(rest);
+      if constexpr (kVec) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          if (v + i < hi) {
+            if constexpr (sizeof(T) == 4) {
+              w[i] = __ldg(reinterpret_cast<const uint32_t*>(row + v + i));
+            } else {
+              const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(row + v + i));
+              w[i >> 1] = i & 1 ? (w[i >> 1] & 0xFFFFu) | (h << 16) : (w[i >> 1] & 0xFFFF0000u) | h;
+            }
+          }
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(w[i]);
+    } else {
+      const uint16_t h = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+      return to_f32(*reinterpret_cast<const T*>(&h));
+    }
+  }
+};
 
-// The weight of a token in steps of 2^-44 (NaN and negative values: 0).
+// The weight of a token in steps of 2^-44 (NaN and negative values: 0), as
+// its upper and lower 22 bits plus the constant kMagic each.  A sum that is
+// rounded towards zero onto 2^23 has its whole part in the last 23 bits:
+// w 2^22 is split without the slow conversions to integers (and what is left
+// of it is exact).
+constexpr uint32_t kMagic = 0x4B000000u;  // the bits of 2^23
+__device__ __forceinline__ void weight_parts(float p, float q, uint32_t& hi, uint32_t& lo) {
+  const float w = __saturatef(p - q);
+  const float t = __fmaf_rz(w, 4194304.f, 8388608.f);
+  const float rest = fmaf(w, 4194304.f, 8388608.f - t);
+  hi = __float_as_uint(t);
+  lo = __float_as_uint(__fmaf_rz(rest, 4194304.f, 8388608.f));
+}
 __device__ __forceinline__ uint64_t weight(float p, float q) {
-  return __float2ull_rz(fminf(fmaxf(p - q, 0.f), 1.f) * 17592186044416.f);
+  uint32_t hi, lo;
+  weight_parts(p, q, hi, lo);
+  return ((uint64_t)(hi - kMagic) << 22) + (lo - kMagic);
 }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
@@ -83,10 +131,17 @@ __device__ __forceinline__ uint64_t threshold(float u, uint64_t total) {
   return k * (total >> 31) + ((k * (total & 0x7FFFFFFFu)) >> 31);
 }
 
-// N consecutive weights a lane: 32 * N a warp step.
+// N consecutive weights a lane: 32 * N a warp step.  A warp takes kBatch steps
+// at a time, and the next kBatch are loaded before these are used.  Their sums
+// are kept, so that the threshold is placed by reading one batch again.
 template <typename T, int N>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVThreads)
-verify_kernel(const VerifyArgs a, int64_t seg) {
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVThreads, 4)
+verify_kernel(const VerifyArgs a, int seg) {
+  constexpr int kBatch = N == 1 ? 8 : 2;
+  constexpr int kSpan = kBatch * 32 * N;  // elements of a batch
+  // batches of a warp: V < 2^19 over the cluster's warps
+  constexpr int kMaxBatches = MSA_VERIFY_MAX_VOCAB / (kCluster * kVWarps * kSpan) + 2;
+  __shared__ uint64_t batch_tot[kVWarps][kMaxBatches];
   __shared__ uint64_t warp_tot[kVWarps];
   __shared__ uint64_t cta_tot[kCluster];
   __shared__ int s_acc;
@@ -97,21 +152,24 @@ verify_kernel(const VerifyArgs a, int64_t seg) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = (int)cluster.block_rank();
   const int64_t b = blockIdx.x / kCluster;
-  const int n = a.n;
+  const int n = a.n, V = (int)a.V;
   const T* target = static_cast<const T*>(a.target) + b * a.t_req;
   const T* draft = a.draft ? static_cast<const T*>(a.draft) + b * a.d_req : nullptr;
+  const float u = __ldg(a.u + b * n + n - 1);
 
   // which drafts stand: lane i decides draft i (every CTA for itself)
   const int drafts = a.counts ? min(max(__ldg(a.counts + b), 0), n - 1) : n - 1;
   if (warp == 0) {
     bool ok = false;
     int x = -1;
-    if (lane < drafts) {
+    if (lane < n - 1) {
+      // a draft behind this request's last changes nothing, and its token
+      // need not be waited for
       x = __ldg(a.tokens_in + b * (n - 1) + lane);
-      if (x >= 0 && x < a.V) {
+      if (x >= 0 && x < V) {
         const double p = to_f32(target[lane * a.t_row + x]);
         const double q = draft ? (double)to_f32(draft[lane * a.d_row + x]) : 1.0;
-        ok = (double)__ldg(a.u + b * n + lane) * q < p;
+        ok = lane < drafts && (double)__ldg(a.u + b * n + lane) * q < p;
       }
     }
     const uint32_t fell = ~__ballot_sync(0xffffffffu, ok);
@@ -133,49 +191,55 @@ verify_kernel(const VerifyArgs a, int64_t seg) {
   const T* prow = target + acc * a.t_row;
   const T* qrow = refused && draft ? draft + acc * a.d_row : nullptr;
   // a certain draft (no draft probabilities) that fell is left out
-  const int64_t skip = refused && !draft ? s_used : -1;
+  int skip = refused && !draft ? s_used : -1;
 
-  // this CTA's part of the row, cut among its warps in whole warp steps
-  const int64_t lo = min(a.V, rank * seg), hi = min(a.V, lo + seg);
-  const int64_t steps = (hi - lo + 32 * N - 1) / (32 * N);
-  const int64_t wsteps = (steps + kVWarps - 1) / kVWarps;
-  const int64_t wlo = min(hi, lo + warp * wsteps * (32 * N));
-  const int64_t whi = min(hi, wlo + wsteps * (32 * N));
+  // this CTA's part of the row, cut among its warps in whole batches
+  const int lo = min(V, rank * seg), hi = min(V, lo + seg);
+  const int batches = ((hi - lo + kSpan - 1) / kSpan + kVWarps - 1) / kVWarps;
+  const int wlo = min(hi, lo + warp * batches * kSpan);
+  const int whi = min(hi, wlo + batches * kSpan);
 
-  auto weights_at = [&](int64_t v, const T* q, uint64_t (&w)[N]) {
-    if (N == 1 || v + N <= whi) {
-      float p[N], d[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) p[i] = d[i] = 0.f;
-      if (v < whi) {
-        load_vec<T, N>(prow + v, p);
-        if (q) load_vec<T, N>(q + v, d);
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) w[i] = v + i == skip ? 0 : weight(p[i], d[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        w[i] = v + i < whi && v + i != skip
-                   ? weight(to_f32(prow[v + i]), q ? to_f32(q[v + i]) : 0.f)
-                   : 0;
-    }
-  };
-
-  const float u = __ldg(a.u + b * n + n - 1);
   for (int pass = 0; pass < 2; ++pass) {
     // pass 1 only where p <= q everywhere and yet a draft fell (distributions
     // that do not add up to one): the token is drawn from p itself
     const T* q = pass == 0 ? qrow : nullptr;
+    if (pass == 1) skip = -1;
     uint64_t sum = 0;
-#pragma unroll 4
-    for (int64_t v = wlo + lane * N; v < whi; v += 32 * N) {
-      uint64_t w[N];
-      weights_at(v, q, w);
+    Raw<T, N> rp[2][kBatch], rq[2][kBatch];
+    auto load = [&](int buf, int v0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) sum += w[i];
+      for (int k = 0; k < kBatch; ++k) rp[buf][k].load_to(prow, v0 + (k * 32 + lane) * N, whi, 0u);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (q) rq[buf][k].load_to(q, v0 + (k * 32 + lane) * N, whi, 0u); else rq[buf][k].fill(0u);
+    };
+    auto add = [&](int buf, int v0, int i) {
+      // at most 16 weights: their parts' sums stay in 32 bits
+      uint32_t h = 0u - kBatch * N * kMagic, l = h;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          uint32_t x, y;
+          weight_parts(rp[buf][k].at(e), rq[buf][k].at(e), x, y);
+          h += x, l += y;
+        }
+      uint64_t own = ((uint64_t)h << 22) + l;
+      const int o = skip - v0 - lane * N;  // the token left out, from this lane's first
+      if (o >= 0 && o < kSpan && o % (32 * N) < N && skip < whi) own -= weight(to_f32(prow[skip]), 0.f);
+      own = warp_sum(own);
+      if (lane == 0) batch_tot[warp][i] = own;
+      sum += own;
+    };
+    if (wlo < whi) load(0, wlo);
+    for (int i = 0, v0 = wlo; v0 < whi; i += 2, v0 += 2 * kSpan) {
+      if (v0 + kSpan < whi) load(1, v0 + kSpan);
+      add(0, v0, i);
+      if (v0 + kSpan < whi) {
+        if (v0 + 2 * kSpan < whi) load(0, v0 + 2 * kSpan);
+        add(1, v0 + kSpan, i + 1);
+      }
     }
-    sum = warp_sum(sum);
     if (lane == 0) warp_tot[warp] = sum;
     __syncthreads();
     if (threadIdx.x < kCluster) {
@@ -207,11 +271,23 @@ verify_kernel(const VerifyArgs a, int64_t seg) {
       t -= warp_tot[i];
     }
     if (t >= warp_tot[warp]) return;
-    for (int64_t v0 = wlo; v0 < whi; v0 += 32 * N) {
+    // this warp's: the batch that passes the threshold once more, its steps'
+    // sums, then the step that does
+    int i = 0;
+    while (t >= batch_tot[warp][i]) t -= batch_tot[warp][i++];
+    const int v0 = wlo + i * kSpan;
+    load(0, v0);
+    for (int k = 0; k < kBatch; ++k) {
       uint64_t w[N], own = 0;
-      weights_at(v0 + lane * N, q, w);
 #pragma unroll
-      for (int i = 0; i < N; ++i) own += w[i];
+      for (int e = 0; e < N; ++e) {
+        float x = 0.f, y = 0.f;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (j == k) x = rp[0][j].at(e), y = rq[0][j].at(e);
+        w[e] = v0 + (k * 32 + lane) * N + e == skip ? 0 : weight(x, y);
+        own += w[e];
+      }
       uint64_t incl = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -221,10 +297,10 @@ verify_kernel(const VerifyArgs a, int64_t seg) {
       const uint32_t past = __ballot_sync(0xffffffffu, incl > t);
       if (past) {
         if (lane == __ffs(past) - 1) {
-          uint64_t at = incl - own;
-          int i = 0;
-          while (i < N - 1 && at + w[i] <= t) at += w[i++];
-          a.tokens[b * n + acc] = (int32_t)(v0 + lane * N + i);
+          uint64_t sofar = incl - own;
+          int e = 0;
+          while (e < N - 1 && sofar + w[e] <= t) sofar += w[e++];
+          a.tokens[b * n + acc] = v0 + (k * 32 + lane) * N + e;
         }
         return;
       }
@@ -243,87 +319,115 @@ __device__ __forceinline__ uint64_t best_key(float x, uint32_t place) {
 }
 
 template <typename T, int N>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVThreads)
-greedy_kernel(const VerifyArgs a, int64_t seg) {
-  __shared__ uint64_t warp_best[kVWarps];
-  __shared__ uint64_t row_best[kCluster][kMaxVerify];  // rank 0's is complete
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVThreads, 4)
+greedy_kernel(const VerifyArgs a, int seg) {
+  constexpr int kBatch = N == 1 ? 16 : 4;
+  constexpr int kSpan = kBatch * 32 * N;
+  __shared__ uint64_t warp_best[kMaxVerify][kVWarps];
+  __shared__ uint64_t draft_key[kMaxVerify];
+  __shared__ uint64_t cta_best[kCluster];  // rank 0's is complete
   __shared__ int beaten;  // a row known to end the accepted drafts
   cg::cluster_group cluster = cg::this_cluster();
-  if (threadIdx.x == 0) beaten = a.n;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = (int)cluster.block_rank();
   const int64_t b = blockIdx.x / kCluster;
-  const int n = a.n;
+  const int n = a.n, V = (int)a.V;
   const T* target = static_cast<const T*>(a.target) + b * a.t_req;
   const int drafts = a.counts ? min(max(__ldg(a.counts + b), 0), n - 1) : n - 1;
-  const int64_t lo = min(a.V, rank * seg), hi = min(a.V, lo + seg);
+  // this CTA's part of every row, cut among its warps in whole batches
+  const int lo = min(V, rank * seg), hi = min(V, lo + seg);
+  const int batches = max(1, ((hi - lo + kSpan - 1) / kSpan + kVWarps - 1) / kVWarps);
+  const int wlo = min(hi, lo + warp * batches * kSpan);
+  const int whi = min(hi, wlo + batches * kSpan);
+  // batch j of this warp: of row j / batches; a place past the part is NaN,
+  // which is never the best
+  Raw<T, N> r[2][kBatch];
+  const uint32_t nan = sizeof(T) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+  auto load = [&](int buf, int row, int part) {
+    const T* p = target + row * a.t_row;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      r[buf][k].load_to(p, wlo + part * kSpan + (k * 32 + lane) * N, whi, nan);
+  };
+  load(0, 0, 0);
+  if (warp == 0) {
+    // the keys to beat; 0, which any value beats, for what is no token or NaN
+    uint64_t key = ~0ull;
+    if (lane < n - 1) {
+      const int x = __ldg(a.tokens_in + b * (n - 1) + lane);
+      const float mine = x >= 0 && x < V ? to_f32(target[lane * a.t_row + x]) : NAN;
+      key = mine == mine ? best_key(mine, (uint32_t)x) : 0;
+    }
+    // the first draft that cannot stand, or the end of them
+    const uint32_t bad = __ballot_sync(0xffffffffu, lane < drafts && key == 0);
+    draft_key[lane] = key;
+    if (lane == 0) beaten = bad ? __ffs(bad) - 1 : drafts;
+  }
   cluster.sync();  // every CTA's `beaten` is set before another lowers it
 
-  for (int i = 0; i <= drafts; ++i) {
-    // the row's best in this CTA's part: a thread's places ascend, so the
-    // first of equal values stays
-    float best = -INFINITY;
-    uint32_t place = 0xFFFFFFFFu;
-    const T* row = target + i * a.t_row;
-#pragma unroll 4
-    for (int64_t v = lo + threadIdx.x * N; v < hi; v += kVThreads * N) {
-      if (v + N <= hi) {
-        float x[N];
-        load_vec<T, N>(row + v, x);
+  // The rows in order, each warp by itself, the next batch (of this row or
+  // the next) in flight while one is looked through.  A warp that sees a
+  // draft beaten lowers every CTA's `beaten`; rows behind that one are not
+  // looked through.
+  float best = -INFINITY;
+  uint32_t place = 0xFFFFFFFFu;
+  int row = 0, part = 0;
+  auto look = [&](int buf) {  // false: done
+    if (part == 0) {
+      if (row > __shfl_sync(0xffffffffu, *(volatile int*)&beaten, 0)) return false;
+      best = -INFINITY, place = 0xFFFFFFFFu;
+    }
+    const bool last = part + 1 == batches;
+    const int next_row = last ? row + 1 : row, next_part = last ? 0 : part + 1;
+    if (next_row <= drafts) load(buf ^ 1, next_row, next_part);
+    // a thread's places ascend, so the first of equal values stays
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-          if (x[k] > best || (x[k] == best && place == 0xFFFFFFFFu))
-            best = x[k], place = (uint32_t)(v + k);
-      } else {
-        for (int k = 0; v + k < hi; ++k) {
-          const float x = to_f32(row[v + k]);
-          if (x > best || (x == best && place == 0xFFFFFFFFu)) best = x, place = (uint32_t)(v + k);
-        }
+    for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float x = r[buf][k].at(e);
+        if (x > best || (x == best && place == 0xFFFFFFFFu))
+          best = x, place = (uint32_t)(wlo + part * kSpan + (k * 32 + lane) * N + e);
       }
-    }
-    uint64_t key = place == 0xFFFFFFFFu ? 0 : best_key(best, place);  // 0: nothing but NaN
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
-      key = other > key ? other : key;
-    }
-    if (lane == 0) warp_best[warp] = key;
-    __syncthreads();
-    if (warp == 0) {
-      key = lane < kVWarps ? warp_best[lane] : 0;
+    if (last) {
+      uint64_t key = place == 0xFFFFFFFFu ? 0 : best_key(best, place);  // 0: nothing but NaN
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
         key = other > key ? other : key;
       }
-      if (lane == 0) *cluster.map_shared_rank(&row_best[rank][i], 0) = key;
-      if (i < drafts) {
-        const int x = __ldg(a.tokens_in + b * (n - 1) + i);
-        const float mine = x >= 0 && x < a.V ? to_f32(row[x]) : NAN;
-        if (!(mine == mine) || key > best_key(mine, (uint32_t)x))
-          if (lane < kCluster) atomicMin(cluster.map_shared_rank(&beaten, lane), i);
-      }
+      if (lane == 0) warp_best[row][warp] = key;
+      if (row < drafts && key > draft_key[row] && lane < kCluster)
+        atomicMin(cluster.map_shared_rank(&beaten, lane), row);
     }
-    // one decision for the whole CTA: other CTAs lower `beaten` at any time
-    if (__syncthreads_or(*(volatile int*)&beaten <= i)) break;
+    row = next_row, part = next_part;
+    return row <= drafts;
+  };
+  while (look(0) && look(1)) {
+  }
+  cluster.sync();
+  // every warp has scanned row `beaten`, and no draft before it is beaten:
+  // that row's best is the next token
+  const int acc = beaten;
+  if (warp == 0) {
+    uint64_t key = lane < kVWarps ? warp_best[acc][lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
+      key = other > key ? other : key;
+    }
+    if (lane == 0) *cluster.map_shared_rank(&cta_best[rank], 0) = key;
   }
   cluster.sync();
   if (rank != 0 || warp != 0) return;
-  // rows up to the first whose draft is beaten were scanned by every CTA
   uint64_t key = 0;
-  int x = -1;
-  if (lane <= drafts) {
-    if (lane <= beaten)
-      for (int c = 0; c < kCluster; ++c) key = row_best[c][lane] > key ? row_best[c][lane] : key;
-    if (lane < drafts) x = __ldg(a.tokens_in + b * (n - 1) + lane);
-  }
-  const int first = key ? (int)(0xFFFFFFFFu - (uint32_t)key) : -1;
-  const bool ok = lane < drafts && lane <= beaten && x == first && x >= 0;
-  const uint32_t fell = ~__ballot_sync(0xffffffffu, ok);
-  const int acc = min(fell ? __ffs(fell) - 1 : 32, drafts);
-  if (lane < n) a.tokens[b * n + lane] = lane < acc ? x : lane == acc ? first : -1;
+  for (int c = 0; c < kCluster; ++c) key = cta_best[c] > key ? cta_best[c] : key;
+  const int next = key ? (int)(0xFFFFFFFFu - (uint32_t)key) : -1;
+  if (lane < n)
+    a.tokens[b * n + lane] =
+        lane < acc ? __ldg(a.tokens_in + b * (n - 1) + lane) : lane == acc ? next : -1;
   if (lane == 0) a.accepted[b] = acc;
 }
 
@@ -340,7 +444,7 @@ cudaError_t launch_verify_type(const VerifyArgs& a, bool greedy, cudaStream_t st
   // (an odd vocabulary's rows start anywhere)
   const bool vec = vector_rows<T>(a.target, a.t_req, a.t_row) &&
                    (greedy || !a.draft || vector_rows<T>(a.draft, a.d_req, a.d_row));
-  const int64_t seg = ceil_div(ceil_div(a.V, kCluster), 32 * N) * (32 * N);
+  const int seg = (int)(ceil_div(ceil_div(a.V, kCluster), 32 * N) * (32 * N));
   const dim3 grid((unsigned)(a.B * kCluster));
   auto run = [&](auto kernel) {
     return launch_pdl(kernel, grid, dim3(kVThreads), 0, stream, a, seg);

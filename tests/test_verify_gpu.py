@@ -117,6 +117,18 @@ def test_edges():
     assert want[0][0, 0] == -1 and want[0][2, 0] >= 0
 
 
+def test_certain_draft_refused_where_nothing_else_has_probability():
+    # p has weight at the draft alone, and too little of it to stand: without
+    # the draft nothing is left, so the token is drawn from p, the draft again
+    for V in (7, 5003):
+        target = torch.zeros((2, 2, V), device="cuda")
+        target[:, 0, 5], target[:, 1, 1] = 0.3, 1.0
+        drafts = torch.full((2, 1), 5, dtype=torch.int32, device="cuda")
+        u = torch.tensor([[0.9, 0.5], [0.2, 0.5]], device="cuda")
+        want = _check(target, None, drafts, u)
+        assert want[0].tolist() == [[5, -1], [5, 1]] and want[1].tolist() == [0, 1]
+
+
 def test_uniforms_reproduce_the_distribution():
     # N evenly spread uniforms over one row: each token is drawn N p times,
     # up to one either side of its interval's two ends
