@@ -61,11 +61,19 @@ struct __align__(16) Tile {
 struct PlanHead {
   int ntiles, cost, shared_tiles;
   int bad;  // lengths inconsistent: every output row becomes empty
+  int T;    // tokens of the batch
+  int pad[3];
 };
+// The tiles of a head in line order: those over the shared pages, then each
+// request's own.  In memory the own ones begin at a place that the sizes
+// alone give, so that reading one need not wait for the plan's head.
+__host__ __device__ inline int64_t own_base(int64_t T, int64_t C, int64_t prefix) {
+  return prefix > 0 ? ceil_div(T, 2 * C) : 0;
+}
 
 __host__ __device__ inline int64_t max_tiles(int64_t B, int64_t T, int64_t C, int64_t prefix) {
   const int64_t n = ceil_div(T, 2 * C);
-  return (prefix > 0 ? n : 0) + (T < n + B ? T : n + B);
+  return own_base(T, C, prefix) + (T < n + B ? T : n + B);
 }
 
 __device__ __forceinline__ int tile_rate(int ntok, int C) { return ntok > C ? kCostPair : kCostSolo; }
@@ -79,7 +87,8 @@ __device__ __forceinline__ int pages_before(int64_t y, int npages, int rate) {
   return p < npages ? (int)p : npages;
 }
 __device__ __forceinline__ int64_t share_of(int64_t total, int ctas) {
-  const int64_t s = (total + ctas - 1) / ctas;
+  const int64_t s = total <= INT_MAX - ctas ? ((int)total + ctas - 1) / ctas
+                                            : (total + ctas - 1) / ctas;
   return s > kMinShare ? s : kMinShare;
 }
 
@@ -133,6 +142,7 @@ struct PlanParams {
   int64_t max_q, max_k;
   PlanHead* head;
   Tile* tiles;
+  int own_base;
   int32_t* req_tile;  // [B + 1] first suffix tile of each request
   uint32_t* status;
 };
@@ -171,7 +181,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   __syncthreads();  // also makes req_tile visible to this CTA
   if (s_bad) {
     if (tid == 0) {
-      *p.head = PlanHead{0, 0, 0, 1};
+      *p.head = PlanHead{0, 0, 0, 1, 0, {0, 0, 0}};
       if (p.status) atomicOr(p.status, (unsigned)MSA_STATUS_BAD_SEQLENS);
     }
     return;
@@ -213,9 +223,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     int total;
     t.start = cost + block_excl_scan(c, &total);
     cost += total;
-    if (i < ntiles) p.tiles[i] = t;
+    if (i < ntiles)
+      p.tiles[i < shared_tiles ? i : p.own_base + i - shared_tiles] = t;
   }
-  if (tid == 0) *p.head = PlanHead{ntiles, cost, shared_tiles, 0};
+  if (tid == 0) *p.head = PlanHead{ntiles, cost, shared_tiles, 0, T, {0, 0, 0}};
 }
 
 // ------------------------------------------------------------------ attend
@@ -260,6 +271,7 @@ constexpr float kPShift = 7.f, kMostSum = 32768.f;
 struct AttendParams {
   const PlanHead* head;
   const Tile* tiles;
+  int own_base;
   const int32_t* block_table;
   int64_t bt_stride;
   const uint8_t* kv;
@@ -287,7 +299,10 @@ struct Walk {
     x = min(total, blockIdx.x * share);
     end = min(total, x + share);
     h = cost > 0 ? (int)(x / cost) : 0;
-    if (x < end) ahead = p.tiles[tile];
+    if (x < end) ahead = at(tile);
+  }
+  __device__ __forceinline__ const Tile& at(int i) const {
+    return p.tiles[i < shared_tiles ? i : p.own_base + i - shared_tiles];
   }
   // The next part with pages; false at the range's end.
   __device__ __forceinline__ bool next() {
@@ -303,7 +318,7 @@ struct Walk {
       cur_tile = tile;
       x = e;
       if (e == t1 && ++tile == ntiles) tile = 0, ++h;
-      if (x < end) ahead = p.tiles[tile];  // in flight while this part is worked on
+      if (x < end) ahead = at(tile);  // in flight while this part is worked on
       if (p1 > p0) return true;
     }
     return false;
@@ -400,9 +415,11 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
     const int64_t x = blockIdx.x * share_of(total, gridDim.x);
     if (x < total) {
       const int r = (int)(x % hd.cost);
+      auto start = [&](int i) {
+        return p.tiles[i < hd.shared_tiles ? i : p.own_base + i - hd.shared_tiles].start;
+      };
       for (int i = tid; i < hd.ntiles; i += kThreads)
-        if (p.tiles[i].start <= r && (i + 1 == hd.ntiles || p.tiles[i + 1].start > r))
-          bars->first_tile = i;
+        if (start(i) <= r && (i + 1 == hd.ntiles || start(i + 1) > r)) bars->first_tile = i;
     }
   }
   __syncthreads();
@@ -879,9 +896,8 @@ constexpr int kMaxParts = 2 * 192;  // parts of a tile: two streams a CTA
 
 struct CombineParams {
   const PlanHead* head;
-  const Tile* tiles;
-  const int32_t* cu_q;
-  int B, T, Hq, Hkv, G, C, ctas;
+  const Tile* own;  // the own tiles
+  int T, Hq, Hkv, G, C, ctas, prefix;
   int rows;  // rows of a tile that a CTA takes
   const float* part_o;
   const float* part_lse;
@@ -892,23 +908,29 @@ struct CombineParams {
 
 // A CTA takes some rows of a tile of a request's own pages (blockIdx.x) of a
 // KV head (.y): first the parts of that tile and of the shared tiles (two at
-// most) that its tokens lie in are listed, then kTeam warps merge the parts
-// of each row: weights 2^(lse - m), fp32 sums.  The tile numbers past the
-// batch's tiles clear the rows of a batch that was refused.
-template <int kTeam>
+// most) that its tokens lie in are listed, then groups of kLanes lanes merge
+// the parts of a row each, or kTeam groups together: weights 2^(lse - m), fp32
+// sums, eight 16-byte loads in flight per lane.  Rows with few parts go four
+// to a warp, rows with many have a warp or several.  A batch that was refused
+// gives empty rows.
+template <int kLanes, int kTeam>
 __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const CombineParams p) {
   // per listed tile: its parts' first rows (of the tile's first token and
   // head), in line order
   __shared__ int s_row[3][kMaxParts];
   __shared__ int s_n[3];
   __shared__ Tile s_tile[3];
-  __shared__ float s_acc[kTeam > 1 ? kCombineWarps : 1][kD];
-  __shared__ float s_m[kCombineWarps], s_l[kCombineWarps];
+  constexpr int kGroups = kCombineWarps * 32 / kLanes;
+  constexpr int kQ = 32 / kLanes;     // float4 of a row per lane
+  constexpr int kFlight = 8 / kQ;     // parts in flight
+  __shared__ float s_acc[kTeam > 1 ? kGroups : 1][kD];
+  __shared__ float s_m[kGroups], s_l[kGroups];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int h = blockIdx.y;
   const PlanHead hd = *p.head;
+  const Tile own = p.own[blockIdx.x];
   if (hd.bad) {  // every row empty
     const int64_t n = (int64_t)p.T * p.G * (kD / 8);
     const int64_t step = (int64_t)gridDim.x * gridDim.z * blockDim.x;
@@ -925,7 +947,6 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
   }
   const int tile = hd.shared_tiles + blockIdx.x;
   if (tile >= hd.ntiles) return;
-  const Tile own = p.tiles[tile];
   const int row0 = blockIdx.z * p.rows, rows = min(p.rows, own.ntok * p.G - row0);
   if (rows <= 0) return;
   if (warp < 3) {  // warp 0: the own tile, 1 and 2: the shared ones
@@ -933,13 +954,22 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
     const int ti = warp == 0 ? tile : first + warp - 1;
     int n = 0;
     if (warp == 0 || (hd.shared_tiles > 0 && ti <= last)) {
-      const Tile t = warp == 0 ? own : p.tiles[ti];
+      Tile t = own;
+      if (warp > 0) {  // a shared tile: all of one size but the last
+        t.tok0 = ti * 2 * p.C;
+        t.ntok = min(2 * p.C, hd.T - t.tok0);
+        t.npages = p.prefix;
+        t.start = ti * tile_cost(2 * p.C, p.prefix, p.C);
+      }
       const bool pair = t.ntok > p.C;
       const int rate = tile_rate(t.ntok, p.C);
       const int64_t share = share_of((int64_t)hd.cost * p.Hkv, p.ctas);
       const int64_t t0 = (int64_t)h * hd.cost + t.start;
       const int64_t t1 = t0 + tile_cost(t.ntok, t.npages, p.C);
-      const int i0 = (int)(t0 / share), i1 = (int)((t1 - 1) / share);
+      // (64-bit divisions are slow; costs rarely need them)
+      const bool small = t1 <= INT_MAX && share <= INT_MAX;
+      const int i0 = small ? (int)t0 / (int)share : (int)(t0 / share);
+      const int i1 = small ? (int)(t1 - 1) / (int)share : (int)((t1 - 1) / share);
       for (int c0 = i0; c0 <= i1; c0 += 32) {
         const int cta = c0 + lane;
         int pa = 0, pb = 0;
@@ -965,14 +995,19 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
     if (lane == 0) s_n[warp] = min(n, kMaxParts);
   }
   __syncthreads();
-  const int member = warp % kTeam;
-  constexpr int kRows = kCombineWarps / kTeam;  // rows at a time
+  const int group = threadIdx.x / kLanes, sub = threadIdx.x % kLanes;
+  const uint32_t peers = kLanes == 32 ? 0xFFFFFFFFu : ((1u << (kLanes & 31)) - 1u) << (lane - sub);
+  const int member = group % kTeam;
+  constexpr int kRows = kGroups / kTeam;  // rows at a time
   for (int r0 = 0; r0 < rows; r0 += kRows) {
-    const int r = row0 + r0 + warp / kTeam;
-    const bool live = r0 + warp / kTeam < rows;
-    float m = -INFINITY, l = 0.f;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const int r = row0 + r0 + group / kTeam;
+    const bool live = r0 + group / kTeam < rows;
     const int tok = own.tok0 + (live ? r / p.G : 0);
+    float m = -INFINITY, l = 0.f;
+    // lane `sub` has columns 4 (kLanes q + sub) .. + 3 of the row
+    float4 acc[kQ];
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (live) {
       for (int k = 0; k < 3; ++k) {
         const int n = s_n[k];
@@ -982,71 +1017,78 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
         // rows of a pair: C tokens of the first stream, then the second's:
         // the same as token order
         const int off = o * p.G + r % p.G;
-        for (int e0 = member * 32; e0 < n; e0 += kTeam * 32) {
-          const int e = e0 + lane;
+        for (int e0 = member * kLanes; e0 < n; e0 += kTeam * kLanes) {
+          const int e = e0 + sub;
           const int row = e < n ? s_row[k][e] + off : 0;
           const float le = e < n ? __ldcg(p.part_lse + row) : -INFINITY;
           float top = le;
 #pragma unroll
-          for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          for (int d = kLanes / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(peers, top, d));
           if (top > m) {
             const float f = m == -INFINITY ? 0.f : exp2f(m - top);
             l *= f;
 #pragma unroll
-            for (int d = 0; d < 4; ++d) acc[d] *= f;
+            for (int q = 0; q < kQ; ++q) acc[q].x *= f, acc[q].y *= f, acc[q].z *= f, acc[q].w *= f;
             m = top;
           }
           // NaN (a NaN score) stays one
           const float w = le == -INFINITY ? 0.f : exp2f(le - (m == -INFINITY ? 0.f : m));
-          uint32_t bits = __ballot_sync(0xffffffffu, w != 0.f);
-          while (bits) {
-            float4 v[8];
-            float wj[8];
+          const int count = min(kLanes, n - e0);
+          for (int j = 0; j < count; j += kFlight) {
+            float4 v[kFlight][kQ];
+            float wj[kFlight];
 #pragma unroll
-            for (int d = 0; d < 8; ++d) {
-              const int j = bits ? __ffs(bits) - 1 : 0;
-              wj[d] = bits ? __shfl_sync(0xffffffffu, w, j) : 0.f;
-              const int rj = __shfl_sync(0xffffffffu, row, j);
-              v[d] = bits ? __ldcg(reinterpret_cast<const float4*>(p.part_o + (int64_t)rj * kD) +
-                                   lane)
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
-              bits &= bits - 1;
+            for (int d = 0; d < kFlight; ++d) {
+              wj[d] = __shfl_sync(peers, w, j + d, kLanes);
+              const int rj = __shfl_sync(peers, row, j + d, kLanes);
+              const float4* src = reinterpret_cast<const float4*>(p.part_o + (int64_t)rj * kD);
+#pragma unroll
+              for (int q = 0; q < kQ; ++q)
+                v[d][q] = wj[d] != 0.f ? __ldcg(src + q * kLanes + sub)
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
-            for (int d = 0; d < 8; ++d) {
+            for (int d = 0; d < kFlight; ++d) {
               l += wj[d];
-              acc[0] = fmaf(wj[d], v[d].x, acc[0]);
-              acc[1] = fmaf(wj[d], v[d].y, acc[1]);
-              acc[2] = fmaf(wj[d], v[d].z, acc[2]);
-              acc[3] = fmaf(wj[d], v[d].w, acc[3]);
+#pragma unroll
+              for (int q = 0; q < kQ; ++q) {
+                acc[q].x = fmaf(wj[d], v[d][q].x, acc[q].x);
+                acc[q].y = fmaf(wj[d], v[d][q].y, acc[q].y);
+                acc[q].z = fmaf(wj[d], v[d][q].z, acc[q].z);
+                acc[q].w = fmaf(wj[d], v[d][q].w, acc[q].w);
+              }
             }
           }
         }
       }
     }
     if constexpr (kTeam > 1) {
-      if (lane == 0) s_m[warp] = m, s_l[warp] = l;
-      *reinterpret_cast<float4*>(&s_acc[warp][lane * 4]) =
-          make_float4(acc[0], acc[1], acc[2], acc[3]);
+      if (sub == 0) s_m[group] = m, s_l[group] = l;
+#pragma unroll
+      for (int q = 0; q < kQ; ++q)
+        *reinterpret_cast<float4*>(&s_acc[group][4 * (q * kLanes + sub)]) = acc[q];
       __syncthreads();
       if (member == 0 && live) {
         float top = -INFINITY;
-        for (int k = 0; k < kTeam; ++k) top = fmaxf(top, s_m[warp + k]);
+        for (int k = 0; k < kTeam; ++k) top = fmaxf(top, s_m[group + k]);
         l = 0.f;
 #pragma unroll
-        for (int d = 0; d < 4; ++d) acc[d] = 0.f;
+        for (int q = 0; q < kQ; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < kTeam; ++k) {
-          const float lk = s_l[warp + k];
+          const float lk = s_l[group + k];
           // a member without parts has l = 0; one with a NaN keeps it
           const float f = lk == 0.f ? 0.f
-                          : lk == lk ? exp2f(s_m[warp + k] - (top == -INFINITY ? 0.f : top))
+                          : lk == lk ? exp2f(s_m[group + k] - (top == -INFINITY ? 0.f : top))
                                      : lk;
           l += f * lk;
-          const float4 v = *reinterpret_cast<const float4*>(&s_acc[warp + k][lane * 4]);
-          acc[0] = fmaf(f, v.x, acc[0]);
-          acc[1] = fmaf(f, v.y, acc[1]);
-          acc[2] = fmaf(f, v.z, acc[2]);
-          acc[3] = fmaf(f, v.w, acc[3]);
+#pragma unroll
+          for (int q = 0; q < kQ; ++q) {
+            const float4 v = *reinterpret_cast<const float4*>(&s_acc[group + k][4 * (q * kLanes + sub)]);
+            acc[q].x = fmaf(f, v.x, acc[q].x);
+            acc[q].y = fmaf(f, v.y, acc[q].y);
+            acc[q].z = fmaf(f, v.z, acc[q].z);
+            acc[q].w = fmaf(f, v.w, acc[q].w);
+          }
         }
         m = top;
       }
@@ -1054,10 +1096,12 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
     if (member == 0 && live) {
       const float scale = l == 0.f ? 0.f : p.v_scale / l;
       const int64_t row = (int64_t)tok * p.Hq + h * p.G + r % p.G;
-      *reinterpret_cast<uint2*>(p.out + row * kD + lane * 4) =
-          make_uint2(pack_bf16x2(acc[0] * scale, acc[1] * scale),
-                     pack_bf16x2(acc[2] * scale, acc[3] * scale));
-      if (p.lse && lane == 0)
+#pragma unroll
+      for (int q = 0; q < kQ; ++q)
+        *reinterpret_cast<uint2*>(p.out + row * kD + 4 * (q * kLanes + sub)) =
+            make_uint2(pack_bf16x2(acc[q].x * scale, acc[q].y * scale),
+                       pack_bf16x2(acc[q].z * scale, acc[q].w * scale));
+      if (p.lse && sub == 0)
         p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
     }
     if constexpr (kTeam > 1) __syncthreads();
@@ -1147,8 +1191,9 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, void* ws, cudaStream_t 
   float* part_lse = reinterpret_cast<float*>(base + l.part_lse);
   float* part_o = reinterpret_cast<float*>(base + l.part_o);
 
+  const int own0 = (int)own_base(a.T, C, a.prefix_pages);
   const PlanParams pp = {a.cu_q, a.cu_k, (int)a.B, (int)a.T, C, (int)a.prefix_pages, a.max_q,
-                         a.max_k, head, tiles, req_tile, a.status};
+                         a.max_k, head, tiles, own0, req_tile, a.status};
   cudaError_t e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pp);
   if (e != cudaSuccess) return e;
 
@@ -1162,26 +1207,29 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, void* ws, cudaStream_t 
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) attr_set[dev].store(true, std::memory_order_release);
   }
-  const AttendParams ap = {head, tiles, a.block_table, a.bt_stride, a.kv, (int)a.num_pages,
+  const AttendParams ap = {head, tiles, own0, a.block_table, a.bt_stride, a.kv, (int)a.num_pages,
                            (int)a.T, G, C, (int)a.Hkv, a.score_log2, part_o, part_lse, a.status,
                            (uint32_t)std::min<uint64_t>(pipeline_wait_limit_ns(), kWaitLimitNs)};
   e = launch_pdl(attend_kernel, dim3((unsigned)ctas), dim3(kThreads), (size_t)kSmem, stream, kv_map,
                  q_map, ap);
   if (e != cudaSuccess) return e;
 
-  // rows of a tile by CTA, and warps by row: while there are few rows, each
-  // has many parts, and more warps share them
-  const int64_t rows = a.T * a.Hq, tile_rows = std::min<int64_t>(2 * C, a.max_q) * G;
-  const int team = rows <= 1024 ? 8 : rows <= 4096 ? 2 : 1;
-  const int cta_rows = rows <= 16384 ? kCombineWarps / team : 4 * kCombineWarps;
-  const CombineParams cp = {head, tiles, a.cu_q, (int)a.B, (int)a.T, (int)a.Hq, (int)a.Hkv, G, C,
-                            ctas, cta_rows, part_o, part_lse, a.v_scale, a.out, a.lse};
+  // parts of a row, about: of the shared tile or of the own one
+  const int64_t tile_rows = std::min<int64_t>(2 * C, a.max_q) * G;
+  const int64_t tiles_n =
+      a.prefix_pages > 0 ? ceil_div(a.T, 2 * C) : std::min(a.T, ceil_div(a.T, 2 * C) + a.B);
+  const int64_t parts =
+      (int64_t)ctas * (a.T <= C || a.prefix_pages == 0 ? 2 : 1) / (a.Hkv * tiles_n);
+  const int lanes = parts >= 6 ? 32 : 8, team = parts >= 48 ? 8 : parts >= 6 ? 2 : 1;
+  const int cta_rows = kCombineWarps * 32 / lanes / team;
+  const CombineParams cp = {head, tiles + own0, (int)a.T, (int)a.Hq, (int)a.Hkv, G, C, ctas,
+                            (int)a.prefix_pages, cta_rows, part_o, part_lse, a.v_scale, a.out, a.lse};
   const int64_t own = std::min<int64_t>(a.T, ceil_div(a.T, 2 * C) + a.B);
   const dim3 grid((unsigned)own, (unsigned)a.Hkv, (unsigned)std::max<int64_t>(1, ceil_div(tile_rows, cta_rows)));
   const dim3 block(kCombineWarps * 32);
-  if (team == 8) return launch_pdl(combine_kernel<8>, grid, block, 0, stream, cp);
-  if (team == 2) return launch_pdl(combine_kernel<2>, grid, block, 0, stream, cp);
-  return launch_pdl(combine_kernel<1>, grid, block, 0, stream, cp);
+  if (team == 8) return launch_pdl(combine_kernel<32, 8>, grid, block, 0, stream, cp);
+  if (team == 2) return launch_pdl(combine_kernel<32, 2>, grid, block, 0, stream, cp);
+  return launch_pdl(combine_kernel<8, 1>, grid, block, 0, stream, cp);
 }
 
 }  // namespace msa
