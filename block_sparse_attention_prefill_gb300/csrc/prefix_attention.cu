@@ -341,7 +341,7 @@ __device__ __forceinline__ void give_up(Bars* bars, uint32_t* status) {
 // A wait of a whole warp: all lanes poll (bounded_wait), all agree.
 __device__ __forceinline__ bool all_wait(Bars* bars, uint64_t* bar, uint32_t parity,
                                          const AttendParams& p) {
-  const bool ok = bounded_wait(bar, parity, &bars->abort, p.wait_ns);
+  const bool ok = bounded_wait_long(bar, parity, &bars->abort, p.wait_ns);
   if (__all_sync(0xffffffffu, ok)) return true;
   if ((threadIdx.x & 31) == 0 && !*(volatile int*)&bars->abort) give_up(bars, p.status);
   return false;
@@ -435,7 +435,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
       while (ok && walk.next()) {
         const Tile& t = walk.t;
         if (lane == 0) {
-          if (part > 0) ok = bounded_wait(&bars->q_free, (part - 1) & 1, abort, p.wait_ns);
+          if (part > 0) ok = bounded_wait_long(&bars->q_free, (part - 1) & 1, abort, p.wait_ns);
           if (ok) {
             const int boxes = walk.pair() ? 2 : 1;
             mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(boxes * p.C * p.G * kD));
@@ -460,7 +460,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
               bars->there[g % kThere] = there;
               if (!there && p.status) atomicOr(p.status, (unsigned)MSA_STATUS_BAD_BLOCK);
               const int y = there ? (page * p.Hkv + walk.cur_h) * kPage : 0;
-              if (g >= kRaw) ok = bounded_wait(&bars->k_free[slot], ph, abort, p.wait_ns);
+              if (g >= kRaw) ok = bounded_wait_long(&bars->k_free[slot], ph, abort, p.wait_ns);
               if (ok) {
                 if (there) {
                   mbar_arrive_expect_tx(&bars->k_full[slot], kTileBytes);
@@ -469,7 +469,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
                   mbar_arrive(&bars->k_full[slot]);
                 }
                 ++k_loads;
-                if (g >= kRaw) ok = bounded_wait(&bars->v_free[slot], ph, abort, p.wait_ns);
+                if (g >= kRaw) ok = bounded_wait_long(&bars->v_free[slot], ph, abort, p.wait_ns);
                 if (ok) {
                   if (there) {
                     mbar_arrive_expect_tx(&bars->v_full[slot], kTileBytes);
@@ -491,11 +491,11 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         if (!ok && !*abort) give_up(bars, p.status);
         // every copy lands before the CTA may end
         for (int i = max(0, k_loads - kRaw); i < k_loads; ++i)
-          bounded_wait(&bars->k_full[i % kRaw], (i / kRaw) & 1, nullptr, kWaitLimitNs);
+          bounded_wait_long(&bars->k_full[i % kRaw], (i / kRaw) & 1, nullptr, kWaitLimitNs);
         for (int i = max(0, v_loads - kRaw); i < v_loads; ++i)
-          bounded_wait(&bars->v_full[i % kRaw], (i / kRaw) & 1, nullptr, kWaitLimitNs);
+          bounded_wait_long(&bars->v_full[i % kRaw], (i / kRaw) & 1, nullptr, kWaitLimitNs);
         if (q_loads > 0)
-          bounded_wait(&bars->q_full, (q_loads - 1) & 1, nullptr, kWaitLimitNs);
+          bounded_wait_long(&bars->q_full, (q_loads - 1) & 1, nullptr, kWaitLimitNs);
       }
       __syncwarp();
     } else if (warp <= 2) {
@@ -521,7 +521,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         uint32_t k_seen = 0, w_seen = 0;  // pages used or passed
         auto pass_k = [&](uint32_t to) {
           for (; k_seen < to; ++k_seen) {
-            if (!bounded_wait(&bars->k_full[k_seen % kRaw], (k_seen / kRaw) & 1, abort, p.wait_ns))
+            if (!bounded_wait_long(&bars->k_full[k_seen % kRaw], (k_seen / kRaw) & 1, abort, p.wait_ns))
               return false;
             mbar_arrive(&bars->k_free[k_seen % kRaw]);
           }
@@ -529,7 +529,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         };
         auto pass_w = [&](uint32_t to) {
           for (; w_seen < to; ++w_seen) {
-            if (!bounded_wait(&bars->w_full[w_seen % kWide], (w_seen / kWide) & 1, abort,
+            if (!bounded_wait_long(&bars->w_full[w_seen % kWide], (w_seen / kWide) & 1, abort,
                               p.wait_ns))
               return false;
             mbar_arrive(&bars->w_free[w_seen % kWide]);
@@ -546,11 +546,11 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
           auto page_of = [&](uint32_t i) { return g0 + (pair ? i >> 1 : (i & ~1u) + s); };
           auto qk = [&](uint32_t i) {
             const uint32_t u = base + i, half = i & 1, g = page_of(i);
-            if (u > 0 && !bounded_wait(&bars->s_free[s], (u - 1) & 1, abort, p.wait_ns))
+            if (u > 0 && !bounded_wait_long(&bars->s_free[s], (u - 1) & 1, abort, p.wait_ns))
               return false;
             if (!half &&
                 !(pass_k(g) &&
-                  bounded_wait(&bars->k_full[g % kRaw], (g / kRaw) & 1, abort, p.wait_ns)))
+                  bounded_wait_long(&bars->k_full[g % kRaw], (g / kRaw) & 1, abort, p.wait_ns)))
               return false;
             tc_fence_after();
             const uint64_t b =
@@ -566,7 +566,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
             }
             return true;
           };
-          ok = bounded_wait(&bars->q_full, part & 1, abort, p.wait_ns);
+          ok = bounded_wait_long(&bars->q_full, part & 1, abort, p.wait_ns);
           if (ok && n == 0) {
             mbar_arrive(&bars->q_free);
             ok = pass_k(g1);
@@ -580,9 +580,9 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
                                                                 (next / kRaw) & 1));
             if (early) ok = qk(i + 1);
             ok = ok &&
-                 (half || (pass_w(g) && bounded_wait(&bars->w_full[g % kWide], (g / kWide) & 1,
+                 (half || (pass_w(g) && bounded_wait_long(&bars->w_full[g % kWide], (g / kWide) & 1,
                                                      abort, p.wait_ns))) &&
-                 bounded_wait(&bars->p_full[s][buf], (u >> 1) & 1, abort, p.wait_ns);
+                 bounded_wait_long(&bars->p_full[s][buf], (u >> 1) & 1, abort, p.wait_ns);
             if (!ok) break;
             tc_fence_after();
             const uint64_t b =
@@ -602,7 +602,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         }
         if (!ok && !*abort) give_up(bars, p.status);
         mma_commit(&bars->mma_done[s]);
-        bounded_wait(&bars->mma_done[s], 0, nullptr, kWaitLimitNs);
+        bounded_wait_long(&bars->mma_done[s], 0, nullptr, kWaitLimitNs);
       }
       __syncwarp();
     }

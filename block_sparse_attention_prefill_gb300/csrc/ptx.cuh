@@ -81,6 +81,20 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// A try_wait that may suspend the thread for up to about 50 us: a waiting warp
+// takes fewer issue slots from the working ones.
+__device__ __forceinline__ bool mbar_try_wait_long(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(50000u)
+      : "memory");
+  return ok != 0;
+}
+
 // Wait until the phase with the given parity has completed.  Gives up after
 // `limit_ns` of wall time, or as soon as *abort becomes non-zero; returns
 // false in both cases so the caller can leave its loop cleanly.  A null
@@ -98,6 +112,19 @@ __device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity,
       if (abort != nullptr && *abort) return false;
       if ((uint32_t)global_timer_ns() - t0 > limit_ns) return false;
     }
+  }
+}
+
+// bounded_wait with long suspensions; the clock and *abort are looked at after
+// each.
+__device__ __forceinline__ bool bounded_wait_long(uint64_t* bar, uint32_t parity,
+                                                  const volatile int* abort, uint32_t limit_ns) {
+  if (mbar_try_wait_long(bar, parity)) return true;
+  const uint32_t t0 = (uint32_t)global_timer_ns();
+  for (;;) {
+    if (mbar_try_wait_long(bar, parity)) return true;
+    if (abort != nullptr && *abort) return false;
+    if ((uint32_t)global_timer_ns() - t0 > limit_ns) return false;
   }
 }
 
