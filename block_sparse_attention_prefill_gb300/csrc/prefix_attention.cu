@@ -245,8 +245,7 @@ struct Bars {
   uint64_t q_full, q_free;
   uint64_t k_full[kRaw], k_free[kRaw], v_full[kRaw], v_free[kRaw];
   uint64_t w_full[kWide], w_free[kWide];
-  uint64_t s_full[2], s_free[2];             // per stream
-  uint64_t p_full[2][2], pv_done[2][2];      // [stream][buffer]
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [stream][buffer]
   uint64_t mma_done[2];
   uint32_t tmem_base;
   int abort;
@@ -257,9 +256,9 @@ struct Bars {
 constexpr int kSmem = kOffBars + (int)sizeof(Bars) + 1024;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 constexpr int kHalf = kPage / 2;  // keys of a unit: of one S, and one P
-// Tensor memory, per stream s: S at column 128 s, two P buffers (f16, 32
-// columns each) at 128 s + 64, O at 256 + 128 s
-constexpr int kTmemCols = 512, kColP = 64, kColO = 256;
+// Tensor memory, per stream s: two buffers of S (64 columns each) from column
+// 128 s on, O at 256 + 128 s.  P (f16, 32 columns) replaces its S.
+constexpr int kTmemCols = 512, kColO = 256;
 // 512 threads with 128 registers each, shared out anew among the roles
 constexpr int kRegsControl = 80, kRegsSoftmax = 168, kRegsWiden = 96;
 static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsWiden <= 512, "registers");
@@ -382,11 +381,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
       mbar_init(&bars->w_full[i], 4);
       mbar_init(&bars->w_free[i], 2);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars->s_full[s], 1);
-      mbar_init(&bars->s_free[s], 4);
-    }
     for (int i = 0; i < 4; ++i) {
+      mbar_init(&bars->s_full[i >> 1][i & 1], 1);
       mbar_init(&bars->p_full[i >> 1][i & 1], 4);
       mbar_init(&bars->pv_done[i >> 1][i & 1], 1);
     }
@@ -502,11 +498,10 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
       if (elect_one()) {
         // -------------------------------------------- MMA issuer of a stream
         // One thread per stream: a single one for both was busy all the time
-        // and held either back.  The unit is a half page (64 keys).  QK(u + 1)
-        // is issued as soon as the softmax has S(u) in registers, and runs
-        // under its exponentials; PV(u) when P(u) is there.  In this order,
-        // QK(u)'s commit also says that PV(u - 2) is complete, whose P buffer
-        // unit u writes.
+        // and held either back.  The unit is a half page (64 keys): QK(u)
+        // into one of the stream's two S buffers, PV(u) from the P that
+        // replaces it; QK(u + 2) when PV(u) is complete, while the softmax
+        // works on unit u + 1.
         constexpr uint32_t kQk = idesc_e4m3_f32(128, kHalf, false);
         constexpr uint32_t kPv = idesc_f16_f32(128, 128, true);
         const int s = warp - 1;
@@ -545,8 +540,9 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
           // the ring position of the page of unit i
           auto page_of = [&](uint32_t i) { return g0 + (pair ? i >> 1 : (i & ~1u) + s); };
           auto qk = [&](uint32_t i) {
-            const uint32_t u = base + i, half = i & 1, g = page_of(i);
-            if (u > 0 && !bounded_wait_long(&bars->s_free[s], (u - 1) & 1, abort, p.wait_ns))
+            const uint32_t u = base + i, buf = u & 1, half = i & 1, g = page_of(i);
+            if (u > 1 &&
+                !bounded_wait_long(&bars->pv_done[s][buf], ((u >> 1) - 1) & 1, abort, p.wait_ns))
               return false;
             if (!half &&
                 !(pass_k(g) &&
@@ -557,8 +553,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
                 desc_k + (g % kRaw) * (kTileBytes / 16) + half * (kHalf * 128 / 16);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_f8f6f4(s_tmem, desc_q + kk * 2, b + kk * 2, kQk, kk > 0);
-            mma_commit(&bars->s_full[s]);
+              mma_f8f6f4(s_tmem + buf * kHalf, desc_q + kk * 2, b + kk * 2, kQk, kk > 0);
+            mma_commit(&bars->s_full[s][buf]);
             if (half) mma_commit(&bars->k_free[g % kRaw]), k_seen = g + 1;
             if (i + 1 == n) {
               mma_commit(&bars->q_free);
@@ -571,17 +567,11 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
             mbar_arrive(&bars->q_free);
             ok = pass_k(g1);
           }
-          if (ok && n > 0) ok = qk(0);
+          if (ok && n > 0) ok = qk(0) && qk(1);
           for (uint32_t i = 0; ok && i < n; ++i) {
             const uint32_t u = base + i, buf = u & 1, half = i & 1, g = page_of(i);
-            // the next QK first, unless its page has yet to arrive
-            const uint32_t next = i + 1 < n ? page_of(i + 1) : 0;
-            const bool early = i + 1 < n && (!half || mbar_test(&bars->k_full[next % kRaw],
-                                                                (next / kRaw) & 1));
-            if (early) ok = qk(i + 1);
-            ok = ok &&
-                 (half || (pass_w(g) && bounded_wait_long(&bars->w_full[g % kWide], (g / kWide) & 1,
-                                                     abort, p.wait_ns))) &&
+            ok = (half || (pass_w(g) && bounded_wait_long(&bars->w_full[g % kWide],
+                                                          (g / kWide) & 1, abort, p.wait_ns))) &&
                  bounded_wait_long(&bars->p_full[s][buf], (u >> 1) & 1, abort, p.wait_ns);
             if (!ok) break;
             tc_fence_after();
@@ -589,11 +579,10 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
                 desc_w + (g % kWide) * (2 * kTileBytes / 16) + half * (kHalf * 128 / 16);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_f16_ts(o_tmem, s_tmem + kColP + buf * (kHalf / 2) + kk * 8,
-                         b + kk * (16 * 128 / 16), kPv, kk > 0 || i > 0);
+              mma_f16_ts(o_tmem, s_tmem + buf * kHalf + kk * 8, b + kk * (16 * 128 / 16), kPv, kk > 0 || i > 0);
             mma_commit(&bars->pv_done[s][buf]);
             if (half) mma_commit(&bars->w_free[g % kWide]), w_seen = g + 1;
-            if (i + 1 < n && !early) ok = qk(i + 1);
+            if (i + 2 < n) ok = qk(i + 2);
           }
           ok = ok && pass_w(g1);
           g0 = g1;
@@ -638,19 +627,16 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         } else {
           key0 += kHalf;
         }
-        const uint32_t buf = done & 1, p_cols = s_tmem + kColP + buf * (kHalf / 2);
-        if (!all_wait(bars, &bars->s_full[s], done & 1, p)) {
+        const uint32_t buf = done & 1, s_cols = s_tmem + buf * kHalf;
+        if (!all_wait(bars, &bars->s_full[s][buf], (done >> 1) & 1, p)) {
           ok = false;
           break;
         }
         tc_fence_after();
         uint32_t r[2][32];
-        tmem_ld32(s_tmem, r[0]);
-        tmem_ld32(s_tmem + 32, r[1]);
+        tmem_ld32(s_cols, r[0]);
+        tmem_ld32(s_cols + 32, r[1]);
         tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->s_free[s]);
         const bool there = bars->there[(g0 + walk.stream_page(s, i >> 1)) % kThere];
         if (!there || key0 + kHalf - 1 > least) {
           const int lim = there ? pos - key0 : -1;  // the last key this row attends to
@@ -725,7 +711,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
                 w[k + e] = *reinterpret_cast<const uint32_t*>(&h);
               }
             }
-            tmem_st16(p_cols + q * 16, w);
+            tmem_st16(s_cols + q * 16, w);
           }
           sum = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
           const bool again = !move && sum > kMostSum;
