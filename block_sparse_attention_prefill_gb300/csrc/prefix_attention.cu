@@ -383,7 +383,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bars->s_full[i >> 1][i & 1], 1);
-      mbar_init(&bars->p_full[i >> 1][i & 1], 4);
+      mbar_init(&bars->p_full[i >> 1][i & 1], 128);
       mbar_init(&bars->pv_done[i >> 1][i & 1], 1);
     }
     mbar_init(&bars->mma_done[0], 1);
@@ -722,8 +722,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         l += sum;
         tmem_wait_st();
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[s][buf]);
+        mbar_arrive(&bars->p_full[s][buf]);
       }
       if (!ok) break;
       // the part: O / l and log2 of the row's sum
@@ -786,11 +785,15 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
   } else {
     setmaxnreg_dec<kRegsWiden>();
     // -------------------------------------------------------------- widen
-    // 128 threads: a page's V codes in 16-code chunks; chunk e is codes
-    // 16 (e % 8) .. of key e / 8, read through the TMA's 128-byte swizzle and
-    // written as two 16-byte chunks of the f16 tile [keys][dims], two blocks
-    // of 64 dims, 128-byte swizzle.
-    const int wt = tid - 384;
+    // 128 threads: a page's V codes in 16-code chunks; thread wt has chunk
+    // wt % 8 of keys wt / 8, + 16, ..., read through the TMA's 128-byte
+    // swizzle and written as two 16-byte chunks of the f16 tile [keys][dims],
+    // two blocks of 64 dims, 128-byte swizzle (its keys are alike modulo 8,
+    // so the swizzle is the same for all).
+    const int wt = tid - 384, key0 = wt >> 3, ch = wt & 7;
+    const int src0 = key0 * 128 + ((ch ^ (key0 & 7)) << 4);
+    const int dst0 = (ch >> 2) * kTileBytes + key0 * 128;
+    const int dst1 = (((ch & 3) * 2) ^ (key0 & 7)) << 4, dst2 = (((ch & 3) * 2 + 1) ^ (key0 & 7)) << 4;
     int g = 0;
     bool ok = true;
     while (ok && walk.next()) {
@@ -803,59 +806,44 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         }
         const int keys =
             bars->there[g % kThere] ? min(kPage, t.seq - (t.page0 + j) * kPage) : 0;
-        const uint8_t* src = smem + kOffV + (g % kRaw) * kTileBytes;
-        uint8_t* dst = smem + kOffW + (g % kWide) * 2 * kTileBytes;
+        // Every row of the tile sees all of a whole page: a NaN in it may
+        // flow through PV.  In the others a probability of 0 has to hide one:
+        // it is written as 0, and put back where it is seen in the end.
+        const bool whole = keys == kPage && (t.page0 + j + 1) * kPage <= t.pos0 + 1;
+        const uint8_t* src = smem + kOffV + (g % kRaw) * kTileBytes + src0;
+        uint8_t* dst = smem + kOffW + (g % kWide) * 2 * kTileBytes + dst0;
         // the loads of four chunks first, so that their conversions overlap;
         // the loop stays rolled: the roles' loops share the instruction cache
-        bool nan = false;
 #pragma unroll 1
         for (int u0 = 0; u0 < 8; u0 += 4) {
-        uint32_t w[4][4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int e = wt + (u0 + u) * 128, key = e >> 3, ch = e & 7;
-          const uint4 v = *reinterpret_cast<const uint4*>(src + key * 128 + ((ch ^ (key & 7)) << 4));
-          w[u][0] = v.x, w[u][1] = v.y, w[u][2] = v.z, w[u][3] = v.w;
-        }
-        if (keys < kPage) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (((wt + (u0 + u) * 128) >> 3) >= keys) w[u][0] = w[u][1] = w[u][2] = w[u][3] = 0u;
-        }
-        // f16 tile of the chunks; the result is NaN if one of the codes is
-        auto store = [&]() {
-          __half2 sick = __half2half2(__ushort_as_half(0));
-          const __half2 zero = sick;
+          uint32_t w[4][4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const int e = wt + (u0 + u) * 128, key = e >> 3, ch = e & 7;
-            uint32_t h[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint2 two = widen4(w[u][k]);
-              h[2 * k] = two.x, h[2 * k + 1] = two.y;
-              sick = __hfma2(*reinterpret_cast<const __half2*>(&two.x), zero, sick);
-              sick = __hfma2(*reinterpret_cast<const __half2*>(&two.y), zero, sick);
-            }
-            uint8_t* row = dst + (ch >> 2) * kTileBytes + key * 128;
-            const int c0 = (ch & 3) * 2;
-            *reinterpret_cast<uint4*>(row + ((c0 ^ (key & 7)) << 4)) =
-                make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (key & 7)) << 4)) =
-                make_uint4(h[4], h[5], h[6], h[7]);
+            const uint4 v = *reinterpret_cast<const uint4*>(src + (u0 + u) * 16 * 128);
+            w[u][0] = v.x, w[u][1] = v.y, w[u][2] = v.z, w[u][3] = v.w;
           }
-          return __hisnan(__low2half(sick)) || __hisnan(__high2half(sick));
-        };
-        if (store()) {
-          nan = true;
+          if (!whole) {
+            uint32_t bad = 0;
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 4; ++u)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[u][k] &= ~((nan_bytes(w[u][k]) >> 7) * 0xFFu);
-          store();
+              for (int k = 0; k < 4; ++k) {
+                if (key0 + (u0 + u) * 16 >= keys) w[u][k] = 0u;
+                const uint32_t nan = nan_bytes(w[u][k]);
+                bad |= nan;
+                w[u][k] &= ~((nan >> 7) * 0xFFu);
+              }
+            if (bad) *(volatile int*)&bars->nan_seen = 1;
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint2 h0 = widen4(w[u][0]), h1 = widen4(w[u][1]), h2 = widen4(w[u][2]),
+                        h3 = widen4(w[u][3]);
+            uint8_t* row = dst + (u0 + u) * 16 * 128;
+            *reinterpret_cast<uint4*>(row + dst1) = make_uint4(h0.x, h0.y, h1.x, h1.y);
+            *reinterpret_cast<uint4*>(row + dst2) = make_uint4(h2.x, h2.y, h3.x, h3.y);
+          }
         }
-        }
-        if (nan) *(volatile int*)&bars->nan_seen = 1;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
