@@ -234,18 +234,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
 constexpr int kThreads = 512;
 constexpr int kTileBytes = 128 * 128;       // an E4M3 tile of 128 x 128
 constexpr int kRaw = 4;                     // K and V pages in flight
-constexpr int kWide = 2;                    // V pages widened to f16
+constexpr int kWide = 4;                    // half pages of V widened to f16
 constexpr int kOffQ = 0;
 constexpr int kOffK = kOffQ + 2 * kTileBytes;
 constexpr int kOffV = kOffK + kRaw * kTileBytes;
 constexpr int kOffW = kOffV + kRaw * kTileBytes;
-constexpr int kOffBars = kOffW + kWide * 2 * kTileBytes;
+constexpr int kOffBars = kOffW + kWide * kTileBytes;
 constexpr int kThere = 16;  // more than the roles can be apart
 struct Bars {
   uint64_t q_full, q_free;
   uint64_t k_full[kRaw], k_free[kRaw], v_full[kRaw], v_free[kRaw];
   uint64_t w_full[kWide], w_free[kWide];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [stream][buffer]
+  uint64_t part_done;
   uint64_t mma_done[2];
   uint32_t tmem_base;
   int abort;
@@ -332,6 +333,32 @@ struct Walk {
   __device__ __forceinline__ int stream_page(int s, int i) const { return pair() ? i : 2 * i + s; }
 };
 
+// A ring of four slots that both streams use: in a pair part both use every
+// item in turn (v: the item's number within the part); in a solo part each
+// stream has two slots of its own (v: its number within the stream), so that
+// neither waits for the other's progress.  A barrier tells a phase only from
+// the next, so all who use a ring count every use of every slot: `odd` has a
+// bit for each slot, set after an odd number of uses in earlier parts.
+struct Ring {
+  uint32_t odd = 0;
+  static __device__ __forceinline__ uint32_t slot(bool pair, int s, uint32_t v) {
+    return pair ? v & 3u : 2u * s + (v & 1u);
+  }
+  // the parity of this use's phase of the slot; its complement's phase is the
+  // one before (complete at once on a new barrier)
+  __device__ __forceinline__ uint32_t phase(bool pair, uint32_t slot, uint32_t v) const {
+    return ((odd >> slot) ^ (pair ? v >> 2 : v >> 1)) & 1u;
+  }
+  // a part with n0 and n1 items of the two streams (pair: n0 in all) is over
+  __device__ __forceinline__ void advance(bool pair, uint32_t n0, uint32_t n1) {
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) {
+      const uint32_t n = pair ? n0 : k < 2 ? n0 : n1;
+      odd ^= ((pair ? (n + 3 - k) >> 2 : (n + 1 - (k & 1)) >> 1) & 1u) << k;
+    }
+  }
+};
+
 __device__ __forceinline__ void give_up(Bars* bars, uint32_t* status) {
   *(volatile int*)&bars->abort = 1;
   if (status) atomicOr(status, (unsigned)MSA_STATUS_TIMEOUT);
@@ -386,6 +413,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
       mbar_init(&bars->p_full[i >> 1][i & 1], 128);
       mbar_init(&bars->pv_done[i >> 1][i & 1], 1);
     }
+    mbar_init(&bars->part_done, 2);
     mbar_init(&bars->mma_done[0], 1);
     mbar_init(&bars->mma_done[1], 1);
     bars->abort = 0;
@@ -426,37 +454,28 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
     if (warp == 0) {
       // ---------------------------------------------------------- producer
       int g = 0, part = 0;  // pages and parts so far
-      int q_loads = 0, k_loads = 0, v_loads = 0;
+      int q_loads = 0, v_loads = 0;
+      uint32_t k_used = 0, k_odd = 0;  // by slot: loaded, parity of the last load's phase
+      Ring ring;
       bool ok = true;
       while (ok && walk.next()) {
         const Tile& t = walk.t;
-        if (lane == 0) {
-          if (part > 0) ok = bounded_wait_long(&bars->q_free, (part - 1) & 1, abort, p.wait_ns);
-          if (ok) {
-            const int boxes = walk.pair() ? 2 : 1;
-            mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(boxes * p.C * p.G * kD));
-            for (int s = 0; s < boxes; ++s)
-              tma_load_3d(smem + kOffQ + s * kTileBytes, &q_map, &bars->q_full, 0,
-                          walk.cur_h * p.G, t.tok0 + s * p.C);
-            ++q_loads;
-          }
-        }
-        ++part;
+        const bool pair = walk.pair();
         const int32_t* table = p.block_table + t.b * p.bt_stride + t.page0;
-        ok = __shfl_sync(0xffffffffu, ok, 0);
         for (int j0 = walk.p0; ok && j0 < walk.p1; j0 += 32) {
           const int mine = j0 + lane < walk.p1 ? __ldg(table + j0 + lane) : 0;
           const int n = min(32, walk.p1 - j0);
           for (int j = 0; j < n; ++j, ++g) {
             const int page = __shfl_sync(0xffffffffu, mine, j);
             if (lane == 0) {
-              const int slot = g % kRaw;
-              const uint32_t ph = ((g / kRaw) - 1) & 1;
+              const int i = j0 + j - walk.p0;  // within the part
+              const uint32_t v = pair ? i : i >> 1;
+              const uint32_t slot = Ring::slot(pair, i & 1, v), ph = ring.phase(pair, slot, v);
               const bool there = page >= 0 && page < p.num_pages;
               bars->there[g % kThere] = there;
               if (!there && p.status) atomicOr(p.status, (unsigned)MSA_STATUS_BAD_BLOCK);
               const int y = there ? (page * p.Hkv + walk.cur_h) * kPage : 0;
-              if (g >= kRaw) ok = bounded_wait_long(&bars->k_free[slot], ph, abort, p.wait_ns);
+              ok = bounded_wait_long(&bars->k_free[slot], ph ^ 1, abort, p.wait_ns);
               if (ok) {
                 if (there) {
                   mbar_arrive_expect_tx(&bars->k_full[slot], kTileBytes);
@@ -464,17 +483,32 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
                 } else {
                   mbar_arrive(&bars->k_full[slot]);
                 }
-                ++k_loads;
-                if (g >= kRaw) ok = bounded_wait_long(&bars->v_free[slot], ph, abort, p.wait_ns);
+                k_used |= 1u << slot;
+                k_odd = (k_odd & ~(1u << slot)) | (ph << slot);
+                ok = bounded_wait_long(&bars->v_free[g % kRaw], ((g / kRaw) & 1) ^ 1, abort,
+                                       p.wait_ns);
+              }
+              if (ok) {
+                const int vs = g % kRaw;
+                if (there) {
+                  mbar_arrive_expect_tx(&bars->v_full[vs], kTileBytes);
+                  tma_load_2d(smem + kOffV + vs * kTileBytes, &kv_map, &bars->v_full[vs], kD, y);
+                } else {
+                  mbar_arrive(&bars->v_full[vs]);
+                }
+                ++v_loads;
+              }
+              // Q behind the part's first page (its copy needs no wait for the
+              // part before, Q's does)
+              if (ok && i == 0) {
+                if (part > 0) ok = bounded_wait_long(&bars->q_free, (part - 1) & 1, abort, p.wait_ns);
                 if (ok) {
-                  if (there) {
-                    mbar_arrive_expect_tx(&bars->v_full[slot], kTileBytes);
-                    tma_load_2d(smem + kOffV + slot * kTileBytes, &kv_map, &bars->v_full[slot], kD,
-                                y);
-                  } else {
-                    mbar_arrive(&bars->v_full[slot]);
-                  }
-                  ++v_loads;
+                  const int boxes = pair ? 2 : 1;
+                  mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(boxes * p.C * p.G * kD));
+                  for (int s = 0; s < boxes; ++s)
+                    tma_load_3d(smem + kOffQ + s * kTileBytes, &q_map, &bars->q_full, 0,
+                                walk.cur_h * p.G, t.tok0 + s * p.C);
+                  ++q_loads;
                 }
               }
             }
@@ -482,12 +516,15 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
             if (!ok) break;
           }
         }
+        ring.advance(pair, walk.stream_pages(0), walk.stream_pages(1));
+        ++part;
       }
       if (lane == 0) {
         if (!ok && !*abort) give_up(bars, p.status);
         // every copy lands before the CTA may end
-        for (int i = max(0, k_loads - kRaw); i < k_loads; ++i)
-          bounded_wait_long(&bars->k_full[i % kRaw], (i / kRaw) & 1, nullptr, kWaitLimitNs);
+        for (int i = 0; i < kRaw; ++i)
+          if (k_used >> i & 1u)
+            bounded_wait_long(&bars->k_full[i], k_odd >> i & 1u, nullptr, kWaitLimitNs);
         for (int i = max(0, v_loads - kRaw); i < v_loads; ++i)
           bounded_wait_long(&bars->v_full[i % kRaw], (i / kRaw) & 1, nullptr, kWaitLimitNs);
         if (q_loads > 0)
@@ -506,86 +543,69 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         constexpr uint32_t kPv = idesc_f16_f32(128, 128, true);
         const int s = warp - 1;
         const uint64_t desc_k = smem_desc_sw128(smem_u32(smem + kOffK), 16, 1024);
-        const uint64_t desc_w = smem_desc_sw128(smem_u32(smem + kOffW), kTileBytes, 1024);
+        const uint64_t desc_w = smem_desc_sw128(smem_u32(smem + kOffW), kTileBytes / 2, 1024);
         const uint32_t s_tmem = tmem + s * 128, o_tmem = tmem + kColO + s * 128;
-        uint32_t g0 = 0, part = 0, base = 0;  // pages, parts, own units so far
+        uint32_t part = 0, base = 0;  // parts, own units so far
+        Ring k_ring, w_ring;          // K pages, widened half pages
         bool ok = true;
-        // In a solo part a page has one user; the other stream waits for it
-        // too and frees its share.  So no slot moves on before both streams
-        // have seen its phase: a barrier tells a phase only from the next.
-        uint32_t k_seen = 0, w_seen = 0;  // pages used or passed
-        auto pass_k = [&](uint32_t to) {
-          for (; k_seen < to; ++k_seen) {
-            if (!bounded_wait_long(&bars->k_full[k_seen % kRaw], (k_seen / kRaw) & 1, abort, p.wait_ns))
-              return false;
-            mbar_arrive(&bars->k_free[k_seen % kRaw]);
-          }
-          return true;
-        };
-        auto pass_w = [&](uint32_t to) {
-          for (; w_seen < to; ++w_seen) {
-            if (!bounded_wait_long(&bars->w_full[w_seen % kWide], (w_seen / kWide) & 1, abort,
-                              p.wait_ns))
-              return false;
-            mbar_arrive(&bars->w_free[w_seen % kWide]);
-          }
-          return true;
-        };
         while (ok && walk.next()) {
           const bool pair = walk.pair();
-          const uint32_t n = 2u * walk.stream_pages(s);
+          const uint32_t n0 = walk.stream_pages(0), n1 = walk.stream_pages(1);
+          const uint32_t n = 2u * (s ? n1 : n0);
           const uint64_t desc_q =
               smem_desc_sw128(smem_u32(smem + kOffQ + (pair ? s : 0) * kTileBytes), 16, 1024);
-          const uint32_t g1 = g0 + (walk.p1 - walk.p0);
-          // the ring position of the page of unit i
-          auto page_of = [&](uint32_t i) { return g0 + (pair ? i >> 1 : (i & ~1u) + s); };
+          // both streams free a slot; in a solo part its owner for both
+          auto free_slot = [&](uint64_t* bar) {
+            mma_commit(bar);
+            if (!pair) mma_commit(bar);
+          };
           auto qk = [&](uint32_t i) {
-            const uint32_t u = base + i, buf = u & 1, half = i & 1, g = page_of(i);
+            const uint32_t u = base + i, buf = u & 1, half = i & 1;
+            const uint32_t slot = Ring::slot(pair, s, i >> 1);
             if (u > 1 &&
                 !bounded_wait_long(&bars->pv_done[s][buf], ((u >> 1) - 1) & 1, abort, p.wait_ns))
               return false;
-            if (!half &&
-                !(pass_k(g) &&
-                  bounded_wait_long(&bars->k_full[g % kRaw], (g / kRaw) & 1, abort, p.wait_ns)))
+            if (!half && !bounded_wait_long(&bars->k_full[slot], k_ring.phase(pair, slot, i >> 1),
+                                            abort, p.wait_ns))
               return false;
             tc_fence_after();
-            const uint64_t b =
-                desc_k + (g % kRaw) * (kTileBytes / 16) + half * (kHalf * 128 / 16);
+            const uint64_t b = desc_k + slot * (kTileBytes / 16) + half * (kHalf * 128 / 16);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_f8f6f4(s_tmem + buf * kHalf, desc_q + kk * 2, b + kk * 2, kQk, kk > 0);
             mma_commit(&bars->s_full[s][buf]);
-            if (half) mma_commit(&bars->k_free[g % kRaw]), k_seen = g + 1;
-            if (i + 1 == n) {
-              mma_commit(&bars->q_free);
-              return pass_k(g1);
-            }
+            if (half) free_slot(&bars->k_free[slot]);
+            if (i + 1 == n) mma_commit(&bars->q_free);
             return true;
           };
+          // Q is there when both streams have issued all QKs of the part
+          // before, so every earlier use of the K slots is over
           ok = bounded_wait_long(&bars->q_full, part & 1, abort, p.wait_ns);
-          if (ok && n == 0) {
-            mbar_arrive(&bars->q_free);
-            ok = pass_k(g1);
-          }
+          if (ok && n == 0) mbar_arrive(&bars->q_free);
           if (ok && n > 0) ok = qk(0) && qk(1);
+          // and both streams' PVs of that part, the uses of the W slots
+          if (ok && part > 0)
+            ok = bounded_wait_long(&bars->part_done, (part - 1) & 1, abort, p.wait_ns);
           for (uint32_t i = 0; ok && i < n; ++i) {
-            const uint32_t u = base + i, buf = u & 1, half = i & 1, g = page_of(i);
-            ok = (half || (pass_w(g) && bounded_wait_long(&bars->w_full[g % kWide],
-                                                          (g / kWide) & 1, abort, p.wait_ns))) &&
+            const uint32_t u = base + i, buf = u & 1;
+            const uint32_t slot = Ring::slot(pair, s, i);
+            ok = bounded_wait_long(&bars->w_full[slot], w_ring.phase(pair, slot, i), abort,
+                                   p.wait_ns) &&
                  bounded_wait_long(&bars->p_full[s][buf], (u >> 1) & 1, abort, p.wait_ns);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t b =
-                desc_w + (g % kWide) * (2 * kTileBytes / 16) + half * (kHalf * 128 / 16);
+            const uint64_t b = desc_w + slot * (kTileBytes / 16);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_f16_ts(o_tmem, s_tmem + buf * kHalf + kk * 8, b + kk * (16 * 128 / 16), kPv, kk > 0 || i > 0);
+              mma_f16_ts(o_tmem, s_tmem + buf * kHalf + kk * 8, b + kk * (16 * 128 / 16), kPv,
+                         kk > 0 || i > 0);
             mma_commit(&bars->pv_done[s][buf]);
-            if (half) mma_commit(&bars->w_free[g % kWide]), w_seen = g + 1;
+            free_slot(&bars->w_free[slot]);
             if (i + 2 < n) ok = qk(i + 2);
           }
-          ok = ok && pass_w(g1);
-          g0 = g1;
+          if (ok) mma_commit(&bars->part_done);
+          k_ring.advance(pair, n0, n1);
+          w_ring.advance(pair, 2 * n0, 2 * n1);
           base += n;
           ++part;
         }
@@ -787,20 +807,21 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
     // -------------------------------------------------------------- widen
     // 128 threads: a page's V codes in 16-code chunks; thread wt has chunk
     // wt % 8 of keys wt / 8, + 16, ..., read through the TMA's 128-byte
-    // swizzle and written as two 16-byte chunks of the f16 tile [keys][dims],
-    // two blocks of 64 dims, 128-byte swizzle (its keys are alike modulo 8,
-    // so the swizzle is the same for all).
+    // swizzle and written as two 16-byte chunks of an f16 tile [64 keys]
+    // [dims], two blocks of 64 dims, 128-byte swizzle (its keys are alike
+    // modulo 8, so the swizzle is the same for all).
     const int wt = tid - 384, key0 = wt >> 3, ch = wt & 7;
     const int src0 = key0 * 128 + ((ch ^ (key0 & 7)) << 4);
-    const int dst0 = (ch >> 2) * kTileBytes + key0 * 128;
+    const int dst0 = (ch >> 2) * (kTileBytes / 2) + key0 * 128;
     const int dst1 = (((ch & 3) * 2) ^ (key0 & 7)) << 4, dst2 = (((ch & 3) * 2 + 1) ^ (key0 & 7)) << 4;
     int g = 0;
+    Ring ring;
     bool ok = true;
     while (ok && walk.next()) {
       const Tile& t = walk.t;
+      const bool pair = walk.pair();
       for (int j = walk.p0; j < walk.p1; ++j, ++g) {
-        if (!all_wait(bars, &bars->v_full[g % kRaw], (g / kRaw) & 1, p) ||
-            (g >= kWide && !all_wait(bars, &bars->w_free[g % kWide], ((g / kWide) - 1) & 1, p))) {
+        if (!all_wait(bars, &bars->v_full[g % kRaw], (g / kRaw) & 1, p)) {
           ok = false;
           break;
         }
@@ -811,11 +832,19 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         // it is written as 0, and put back where it is seen in the end.
         const bool whole = keys == kPage && (t.page0 + j + 1) * kPage <= t.pos0 + 1;
         const uint8_t* src = smem + kOffV + (g % kRaw) * kTileBytes + src0;
-        uint8_t* dst = smem + kOffW + (g % kWide) * 2 * kTileBytes + dst0;
-        // the loads of four chunks first, so that their conversions overlap;
-        // the loop stays rolled: the roles' loops share the instruction cache
+        // the loads of four chunks (a half page) first, so that their
+        // conversions overlap; the loop stays rolled: the roles' loops share
+        // the instruction cache
 #pragma unroll 1
-        for (int u0 = 0; u0 < 8; u0 += 4) {
+        for (int half = 0; half < 2; ++half) {
+          const int i = j - walk.p0, u0 = 4 * half;  // the page within the part
+          const uint32_t x = pair ? 2 * i + half : (i & ~1) + half;
+          const uint32_t slot = Ring::slot(pair, i & 1, x);
+          if (!all_wait(bars, &bars->w_free[slot], ring.phase(pair, slot, x) ^ 1, p)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = smem + kOffW + slot * kTileBytes + dst0;
           uint32_t w[4][4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
@@ -839,18 +868,20 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
           for (int u = 0; u < 4; ++u) {
             const uint2 h0 = widen4(w[u][0]), h1 = widen4(w[u][1]), h2 = widen4(w[u][2]),
                         h3 = widen4(w[u][3]);
-            uint8_t* row = dst + (u0 + u) * 16 * 128;
+            uint8_t* row = dst + u * 16 * 128;
             *reinterpret_cast<uint4*>(row + dst1) = make_uint4(h0.x, h0.y, h1.x, h1.y);
             *reinterpret_cast<uint4*>(row + dst2) = make_uint4(h2.x, h2.y, h3.x, h3.y);
           }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (half) mbar_arrive(&bars->v_free[g % kRaw]);
+            mbar_arrive(&bars->w_full[slot]);
+          }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bars->v_free[g % kRaw]);
-          mbar_arrive(&bars->w_full[g % kWide]);
-        }
+        if (!ok) break;
       }
+      ring.advance(pair, 2 * walk.stream_pages(0), 2 * walk.stream_pages(1));
     }
   }
 
