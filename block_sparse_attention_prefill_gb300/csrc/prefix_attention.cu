@@ -375,10 +375,12 @@ __device__ __forceinline__ bool all_wait(Bars* bars, uint64_t* bar, uint32_t par
 
 // Four E4M3 codes -> four f16 in two words (exact).
 __device__ __forceinline__ uint2 widen4(uint32_t c) {
-  const __half2_raw a =
-      __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xFFFFu), __NV_E4M3);
-  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> 16), __NV_E4M3);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  uint2 h;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}\n"
+      : "=r"(h.x), "=r"(h.y)
+      : "r"(c));
+  return h;
 }
 // 0x80 in each byte of w whose E4M3 code is NaN (0x7F or 0xFF).
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
@@ -805,15 +807,15 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
   } else {
     setmaxnreg_dec<kRegsWiden>();
     // -------------------------------------------------------------- widen
-    // 128 threads: a page's V codes in 16-code chunks; thread wt has chunk
-    // wt % 8 of keys wt / 8, + 16, ..., read through the TMA's 128-byte
-    // swizzle and written as two 16-byte chunks of an f16 tile [64 keys]
-    // [dims], two blocks of 64 dims, 128-byte swizzle (its keys are alike
-    // modulo 8, so the swizzle is the same for all).
-    const int wt = tid - 384, key0 = wt >> 3, ch = wt & 7;
-    const int src0 = key0 * 128 + ((ch ^ (key0 & 7)) << 4);
-    const int dst0 = (ch >> 2) * (kTileBytes / 2) + key0 * 128;
-    const int dst1 = (((ch & 3) * 2) ^ (key0 & 7)) << 4, dst2 = (((ch & 3) * 2 + 1) ^ (key0 & 7)) << 4;
+    // 128 threads: a page's V codes in pieces of 8; thread wt has piece
+    // wt % 16 of keys wt / 16, + 8, ..., read through the TMA's 128-byte
+    // swizzle and written as one 16-byte chunk of an f16 tile [64 keys][dims],
+    // two blocks of 64 dims, 128-byte swizzle (its keys are alike modulo 8, so
+    // the swizzle is the same for all; eight lanes write a whole row of a
+    // block, without bank conflicts).
+    const int wt = tid - 384, key0 = wt >> 4, piece = wt & 15;
+    const int src0 = key0 * 128 + (((piece >> 1) ^ key0) << 4) + (piece & 1) * 8;
+    const int dst0 = (piece >> 3) * (kTileBytes / 2) + key0 * 128 + (((piece & 7) ^ key0) << 4);
     int g = 0;
     Ring ring;
     bool ok = true;
@@ -832,12 +834,25 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         // it is written as 0, and put back where it is seen in the end.
         const bool whole = keys == kPage && (t.page0 + j + 1) * kPage <= t.pos0 + 1;
         const uint8_t* src = smem + kOffV + (g % kRaw) * kTileBytes + src0;
-        // the loads of four chunks (a half page) first, so that their
-        // conversions overlap; the loop stays rolled: the roles' loops share
-        // the instruction cache
-#pragma unroll 1
+        // all loads first, so that the conversions overlap
+        uint2 w[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) w[u] = *reinterpret_cast<const uint2*>(src + u * 8 * 128);
+        if (!whole) {
+          uint32_t bad = 0;
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            if (key0 + u * 8 >= keys) w[u] = make_uint2(0u, 0u);
+            const uint32_t x = nan_bytes(w[u].x), y = nan_bytes(w[u].y);
+            bad |= x | y;
+            w[u].x &= ~((x >> 7) * 0xFFu);
+            w[u].y &= ~((y >> 7) * 0xFFu);
+          }
+          if (bad) *(volatile int*)&bars->nan_seen = 1;
+        }
+#pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const int i = j - walk.p0, u0 = 4 * half;  // the page within the part
+          const int i = j - walk.p0;  // the page within the part
           const uint32_t x = pair ? 2 * i + half : (i & ~1) + half;
           const uint32_t slot = Ring::slot(pair, i & 1, x);
           if (!all_wait(bars, &bars->w_free[slot], ring.phase(pair, slot, x) ^ 1, p)) {
@@ -845,32 +860,10 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
             break;
           }
           uint8_t* dst = smem + kOffW + slot * kTileBytes + dst0;
-          uint32_t w[4][4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint4 v = *reinterpret_cast<const uint4*>(src + (u0 + u) * 16 * 128);
-            w[u][0] = v.x, w[u][1] = v.y, w[u][2] = v.z, w[u][3] = v.w;
-          }
-          if (!whole) {
-            uint32_t bad = 0;
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if (key0 + (u0 + u) * 16 >= keys) w[u][k] = 0u;
-                const uint32_t nan = nan_bytes(w[u][k]);
-                bad |= nan;
-                w[u][k] &= ~((nan >> 7) * 0xFFu);
-              }
-            if (bad) *(volatile int*)&bars->nan_seen = 1;
-          }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint2 h0 = widen4(w[u][0]), h1 = widen4(w[u][1]), h2 = widen4(w[u][2]),
-                        h3 = widen4(w[u][3]);
-            uint8_t* row = dst + u * 16 * 128;
-            *reinterpret_cast<uint4*>(row + dst1) = make_uint4(h0.x, h0.y, h1.x, h1.y);
-            *reinterpret_cast<uint4*>(row + dst2) = make_uint4(h2.x, h2.y, h3.x, h3.y);
+          for (int u = 0; u < 8; ++u) {
+            const uint2 a = widen4(w[8 * half + u].x), b = widen4(w[8 * half + u].y);
+            *reinterpret_cast<uint4*>(dst + u * 8 * 128) = make_uint4(a.x, a.y, b.x, b.y);
           }
           fence_proxy_async_smem();
           __syncwarp();
