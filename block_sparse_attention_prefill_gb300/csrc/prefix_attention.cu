@@ -106,6 +106,7 @@ __device__ __forceinline__ int64_t part_row(int cta, int h, int tile, int shared
 
 constexpr int kPlanThreads = 1024;
 
+template <int kThreads>
 __device__ __forceinline__ int block_excl_scan(int v, int* total) {
   __shared__ int sums[33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -118,7 +119,7 @@ __device__ __forceinline__ int block_excl_scan(int v, int* total) {
   if (lane == 31) sums[warp] = incl;
   __syncthreads();
   if (warp == 0) {
-    const int s = sums[lane];
+    const int s = lane < kThreads / 32 ? sums[lane] : 0;
     int si = s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -143,23 +144,23 @@ struct PlanParams {
   PlanHead* head;
   Tile* tiles;
   int own_base;
-  int32_t* req_tile;  // [B + 1] first suffix tile of each request
+  int* req;  // [B] own tiles of the requests before each
   uint32_t* status;
 };
 
 // Lists the tiles of one head (every head has the same): first those over the
-// shared pages, then each request's own.
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
+// shared pages, then each request's own.  Run by a whole CTA; req is room for
+// B ints that it can see.  Every thread gets the plan's head.
+template <int kThreads>
+__device__ __forceinline__ PlanHead make_plan(const PlanParams& p, int* req) {
   __shared__ int s_bad, s_first;
-  pdl_wait();
-  pdl_trigger();
   const int tid = threadIdx.x;
   if (tid == 0) s_bad = 0, s_first = INT_MAX;
   __syncthreads();
   const int T = p.cu_q[p.B];
   bool bad = p.cu_q[0] != 0 || T < 0 || T > p.T;
   int run = 0;  // tiles of the requests before this round's
-  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
     const int b = b0 + tid;
     int n = 0;
     if (b < p.B) {
@@ -172,24 +173,24 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
         n = (int)((q + 2 * p.C - 1) / (2 * p.C)), atomicMin(&s_first, b);
     }
     int total;
-    const int before = block_excl_scan(n, &total);
-    if (b < p.B) p.req_tile[b] = run + before;
+    const int before = block_excl_scan<kThreads>(n, &total);
+    if (b < p.B) req[b] = run + before;
     run += total;
   }
   if (bad) s_bad = 1;
-  if (tid == 0) p.req_tile[p.B] = run;
-  __syncthreads();  // also makes req_tile visible to this CTA
+  __syncthreads();  // also makes req visible to this CTA
   if (s_bad) {
+    const PlanHead hd = {0, 0, 0, 1, 0, {0, 0, 0}};
     if (tid == 0) {
-      *p.head = PlanHead{0, 0, 0, 1, 0, {0, 0, 0}};
+      *p.head = hd;
       if (p.status) atomicOr(p.status, (unsigned)MSA_STATUS_BAD_SEQLENS);
     }
-    return;
+    return hd;
   }
   const int shared_tiles = p.prefix > 0 ? (T + 2 * p.C - 1) / (2 * p.C) : 0;
   const int ntiles = shared_tiles + run;
   int cost = 0;
-  for (int i0 = 0; i0 < ntiles; i0 += kPlanThreads) {
+  for (int i0 = 0; i0 < ntiles; i0 += kThreads) {
     const int i = i0 + tid;
     Tile t = {};
     int c = 0;
@@ -203,13 +204,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
         t.pos0 = kNoMask;
         t.seq = p.prefix * kPage;
       } else {
-        int lo = 0, hi = p.B - 1;  // the last request with req_tile[b] <= i
+        int lo = 0, hi = p.B - 1;  // the last request with req[b] <= i
         while (lo < hi) {
           const int mid = (lo + hi + 1) / 2;
-          if (p.req_tile[mid] <= i - shared_tiles) lo = mid; else hi = mid - 1;
+          if (req[mid] <= i - shared_tiles) lo = mid; else hi = mid - 1;
         }
         const int q = p.cu_q[lo + 1] - p.cu_q[lo], k = p.cu_k[lo + 1] - p.cu_k[lo];
-        const int o = (i - shared_tiles - p.req_tile[lo]) * 2 * p.C;
+        const int o = (i - shared_tiles - req[lo]) * 2 * p.C;
         t.b = lo;
         t.tok0 = p.cu_q[lo] + o;
         t.ntok = min(2 * p.C, q - o);
@@ -221,12 +222,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
       c = tile_cost(t.ntok, t.npages, p.C);
     }
     int total;
-    t.start = cost + block_excl_scan(c, &total);
+    t.start = cost + block_excl_scan<kThreads>(c, &total);
     cost += total;
     if (i < ntiles)
       p.tiles[i < shared_tiles ? i : p.own_base + i - shared_tiles] = t;
   }
-  if (tid == 0) *p.head = PlanHead{ntiles, cost, shared_tiles, 0, T, {0, 0, 0}};
+  const PlanHead hd = {ntiles, cost, shared_tiles, 0, T, {0, 0, 0}};
+  if (tid == 0) *p.head = hd;
+  return hd;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
+  pdl_wait();
+  pdl_trigger();
+  make_plan<kPlanThreads>(p, p.req);
 }
 
 // ------------------------------------------------------------------ attend
@@ -261,7 +270,7 @@ constexpr int kHalf = kPage / 2;  // keys of a unit: of one S, and one P
 // 128 s on, O at 256 + 128 s.  P (f16, 32 columns) replaces its S.
 constexpr int kTmemCols = 512, kColO = 256;
 // 512 threads with 128 registers each, shared out anew among the roles
-constexpr int kRegsControl = 80, kRegsSoftmax = 168, kRegsWiden = 96;
+constexpr int kRegsControl = 104, kRegsSoftmax = 160, kRegsWiden = 88;
 static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsWiden <= 512, "registers");
 // P is kept as 2^(s - m + 7): a unit whose P add up to at most 2^15 has none
 // outside f16's range, and f16's subnormals begin 2^-21 below the reference
@@ -269,7 +278,8 @@ static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsWiden <= 512, "registers");
 constexpr float kPShift = 7.f, kMostSum = 32768.f;
 
 struct AttendParams {
-  const PlanHead* head;
+  PlanParams plan;
+  int plan_here;  // each CTA makes the plan for itself (all write the same)
   const Tile* tiles;
   int own_base;
   const int32_t* block_table;
@@ -430,11 +440,18 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
   }
   pdl_wait();
   pdl_trigger();
+  // The workspace's plan: by a kernel of its own, or, while it takes one
+  // round of this CTA's threads, here: the CTAs write the same values to the
+  // same places, and each reads what it has written itself.
+  PlanHead hd;
+  if (p.plan_here)
+    hd = make_plan<kThreads>(p.plan, reinterpret_cast<int*>(smem + kOffW));
+  else
+    hd = *p.plan.head;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  const PlanHead hd = *p.head;
   // the tile that this CTA's range starts in
   {
     const int64_t total = (int64_t)hd.cost * p.Hkv;
@@ -1192,8 +1209,15 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, void* ws, cudaStream_t 
   const int own0 = (int)own_base(a.T, C, a.prefix_pages);
   const PlanParams pp = {a.cu_q, a.cu_k, (int)a.B, (int)a.T, C, (int)a.prefix_pages, a.max_q,
                          a.max_k, head, tiles, own0, req_tile, a.status};
-  cudaError_t e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pp);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
+  // decode batches: the plan is made in the attention kernel's prologue (a
+  // launch and about 2 us less)
+  const bool plan_here =
+      a.B <= kThreads && max_tiles(a.B, a.T, C, a.prefix_pages) <= kThreads;
+  if (!plan_here) {
+    e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pp);
+    if (e != cudaSuccess) return e;
+  }
 
   constexpr int kMaxDevices = 64;
   static std::atomic<bool> attr_set[kMaxDevices];
@@ -1205,7 +1229,7 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, void* ws, cudaStream_t 
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) attr_set[dev].store(true, std::memory_order_release);
   }
-  const AttendParams ap = {head, tiles, own0, a.block_table, a.bt_stride, a.kv, (int)a.num_pages,
+  const AttendParams ap = {pp, plan_here, tiles, own0, a.block_table, a.bt_stride, a.kv, (int)a.num_pages,
                            (int)a.T, G, C, (int)a.Hkv, a.score_log2, part_o, part_lse, a.status,
                            (uint32_t)std::min<uint64_t>(pipeline_wait_limit_ns(), kWaitLimitNs)};
   e = launch_pdl(attend_kernel, dim3((unsigned)ctas), dim3(kThreads), (size_t)kSmem, stream, kv_map,
