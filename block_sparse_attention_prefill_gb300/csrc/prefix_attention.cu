@@ -93,15 +93,14 @@ __device__ __forceinline__ int64_t share_of(int64_t total, int ctas) {
 }
 
 // Rows of the partials.  A tile's part at CTA i starts at row 256 i + (its
-// head's rows) + twice the tokens before it: parts in line order never
-// overlap, because a part has at most 256 rows (moving on by a CTA) and at
-// most twice its tile's rows (moving on by a tile).
+// head's rows) + (the rows before it): parts in line order never overlap,
+// because a part has its tile's rows, at most 256 of them.
 __device__ __forceinline__ int64_t part_row(int cta, int h, int tile, int shared_tiles, int tok0,
                                             int T, int G) {
-  const int64_t rows = 2 * (int64_t)T * G;
+  const int64_t rows = (int64_t)T * G;
   const int64_t per_head = shared_tiles > 0 ? 2 * rows : rows;
   return 256 * (int64_t)cta + h * per_head + (tile >= shared_tiles && shared_tiles > 0 ? rows : 0) +
-         2 * (int64_t)tok0 * G;
+         (int64_t)tok0 * G;
 }
 
 constexpr int kPlanThreads = 1024;
@@ -242,25 +241,27 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
 
 constexpr int kThreads = 512;
 constexpr int kTileBytes = 128 * 128;       // an E4M3 tile of 128 x 128
-constexpr int kRaw = 4;                     // K and V pages in flight
+constexpr int kRawK = 4, kRawV = 3;         // K and V pages in flight
 constexpr int kWide = 4;                    // half pages of V widened to f16
 constexpr int kOffQ = 0;
 constexpr int kOffK = kOffQ + 2 * kTileBytes;
-constexpr int kOffV = kOffK + kRaw * kTileBytes;
-constexpr int kOffW = kOffV + kRaw * kTileBytes;
+constexpr int kOffV = kOffK + kRawK * kTileBytes;
+constexpr int kOffW = kOffV + kRawV * kTileBytes;
 constexpr int kOffBars = kOffW + kWide * kTileBytes;
 constexpr int kThere = 16;  // more than the roles can be apart
 struct Bars {
   uint64_t q_full, q_free;
-  uint64_t k_full[kRaw], k_free[kRaw], v_full[kRaw], v_free[kRaw];
+  uint64_t k_full[kRawK], k_free[kRawK], v_full[kRawV], v_free[kRawV];
   uint64_t w_full[kWide], w_free[kWide];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [stream][buffer]
   uint64_t part_done;
+  uint64_t exchanged, read;  // the streams' results at the end of a solo part
   uint64_t mma_done[2];
   uint32_t tmem_base;
   int abort;
   int nan_seen;      // a NaN among the V codes of valid keys
   int first_tile;
+  float2 ml[2][128];  // a solo part's m and l by stream and row
   uint8_t there[kThere];  // whether a ring position's page is one, by the producer
 };
 constexpr int kSmem = kOffBars + (int)sizeof(Bars) + 1024;
@@ -270,7 +271,7 @@ constexpr int kHalf = kPage / 2;  // keys of a unit: of one S, and one P
 // 128 s on, O at 256 + 128 s.  P (f16, 32 columns) replaces its S.
 constexpr int kTmemCols = 512, kColO = 256;
 // 512 threads with 128 registers each, shared out anew among the roles
-constexpr int kRegsControl = 104, kRegsSoftmax = 160, kRegsWiden = 88;
+constexpr int kRegsControl = 120, kRegsSoftmax = 144, kRegsWiden = 104;
 static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsWiden <= 512, "registers");
 // P is kept as 2^(s - m + 7): a unit whose P add up to at most 2^15 has none
 // outside f16's range, and f16's subnormals begin 2^-21 below the reference
@@ -298,42 +299,47 @@ struct AttendParams {
 struct Walk {
   const AttendParams& p;
   int ntiles, shared_tiles;
-  int64_t cost, x, end, share;
+  int left;          // cost of the range still ahead
+  int at;            // cost of the tile before the range
   int h, tile;
   Tile t, ahead;
   int p0, p1;        // pages of the tile in this range
+  int cur_h, cur_tile;
   __device__ Walk(const AttendParams& prm, const PlanHead& hd, int first_tile)
-      : p(prm), ntiles(hd.ntiles), shared_tiles(hd.shared_tiles), cost(hd.cost), tile(first_tile) {
-    const int64_t total = cost * p.Hkv;
-    share = share_of(total, gridDim.x);
-    x = min(total, blockIdx.x * share);
-    end = min(total, x + share);
-    h = cost > 0 ? (int)(x / cost) : 0;
-    if (x < end) ahead = at(tile);
+      : p(prm), ntiles(hd.ntiles), shared_tiles(hd.shared_tiles), tile(first_tile) {
+    const int64_t total = (int64_t)hd.cost * p.Hkv, share = share_of(total, gridDim.x);
+    const int64_t x = blockIdx.x * share;
+    left = x < total ? (int)min(share, total - x) : 0;
+    h = left > 0 ? (int)(x / hd.cost) : 0;
+    if (left > 0) {
+      ahead = tile_at(tile);
+      at = (int)(x - (int64_t)h * hd.cost) - ahead.start;
+    }
   }
-  __device__ __forceinline__ const Tile& at(int i) const {
+  __device__ __forceinline__ const Tile& tile_at(int i) const {
     return p.tiles[i < shared_tiles ? i : p.own_base + i - shared_tiles];
   }
   // The next part with pages; false at the range's end.
   __device__ __forceinline__ bool next() {
-    while (x < end) {
+    while (left > 0) {
       t = ahead;
-      const int rate = tile_rate(t.ntok, p.C);
-      const int64_t t0 = h * cost + t.start;
-      const int64_t t1 = t0 + tile_cost(t.ntok, t.npages, p.C);
-      const int64_t e = min(end, t1);
-      p0 = pages_before(x - t0, t.npages, rate);
-      p1 = pages_before(e - t0, t.npages, rate);
+      const int rate = tile_rate(t.ntok, p.C), cost = tile_cost(t.ntok, t.npages, p.C);
+      const int take = min(left, cost - at);
+      p0 = pages_before(at, t.npages, rate);
+      p1 = pages_before(at + take, t.npages, rate);
       cur_h = h;
       cur_tile = tile;
-      x = e;
-      if (e == t1 && ++tile == ntiles) tile = 0, ++h;
-      if (x < end) ahead = at(tile);  // in flight while this part is worked on
+      left -= take;
+      at += take;
+      if (at == cost) {
+        at = 0;
+        if (++tile == ntiles) tile = 0, ++h;
+      }
+      if (left > 0) ahead = tile_at(tile);  // in flight while this part is worked on
       if (p1 > p0) return true;
     }
     return false;
   }
-  int cur_h, cur_tile;
   __device__ __forceinline__ bool pair() const { return t.ntok > p.C; }
   // pages that stream s handles of this part
   __device__ __forceinline__ int stream_pages(int s) const {
@@ -410,9 +416,11 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
   if (tid == 0) {
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_free, 2);
-    for (int i = 0; i < kRaw; ++i) {
+    for (int i = 0; i < kRawK; ++i) {
       mbar_init(&bars->k_full[i], 1);
       mbar_init(&bars->k_free[i], 2);
+    }
+    for (int i = 0; i < kRawV; ++i) {
       mbar_init(&bars->v_full[i], 1);
       mbar_init(&bars->v_free[i], 4);
     }
@@ -426,6 +434,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
       mbar_init(&bars->pv_done[i >> 1][i & 1], 1);
     }
     mbar_init(&bars->part_done, 2);
+    mbar_init(&bars->exchanged, 256);
+    mbar_init(&bars->read, 256);
     mbar_init(&bars->mma_done[0], 1);
     mbar_init(&bars->mma_done[1], 1);
     bars->abort = 0;
@@ -468,173 +478,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
   __syncthreads();
   Walk walk(p, hd, bars->first_tile);
 
-  if (warp < 4) {
-    setmaxnreg_dec<kRegsControl>();
-    if (warp == 0) {
-      // ---------------------------------------------------------- producer
-      int g = 0, part = 0;  // pages and parts so far
-      int q_loads = 0, v_loads = 0;
-      uint32_t k_used = 0, k_odd = 0;  // by slot: loaded, parity of the last load's phase
-      Ring ring;
-      bool ok = true;
-      while (ok && walk.next()) {
-        const Tile& t = walk.t;
-        const bool pair = walk.pair();
-        const int32_t* table = p.block_table + t.b * p.bt_stride + t.page0;
-        for (int j0 = walk.p0; ok && j0 < walk.p1; j0 += 32) {
-          const int mine = j0 + lane < walk.p1 ? __ldg(table + j0 + lane) : 0;
-          const int n = min(32, walk.p1 - j0);
-          for (int j = 0; j < n; ++j, ++g) {
-            const int page = __shfl_sync(0xffffffffu, mine, j);
-            if (lane == 0) {
-              const int i = j0 + j - walk.p0;  // within the part
-              const uint32_t v = pair ? i : i >> 1;
-              const uint32_t slot = Ring::slot(pair, i & 1, v), ph = ring.phase(pair, slot, v);
-              const bool there = page >= 0 && page < p.num_pages;
-              bars->there[g % kThere] = there;
-              if (!there && p.status) atomicOr(p.status, (unsigned)MSA_STATUS_BAD_BLOCK);
-              const int y = there ? (page * p.Hkv + walk.cur_h) * kPage : 0;
-              ok = bounded_wait_long(&bars->k_free[slot], ph ^ 1, abort, p.wait_ns);
-              if (ok) {
-                if (there) {
-                  mbar_arrive_expect_tx(&bars->k_full[slot], kTileBytes);
-                  tma_load_2d(smem + kOffK + slot * kTileBytes, &kv_map, &bars->k_full[slot], 0, y);
-                } else {
-                  mbar_arrive(&bars->k_full[slot]);
-                }
-                k_used |= 1u << slot;
-                k_odd = (k_odd & ~(1u << slot)) | (ph << slot);
-                ok = bounded_wait_long(&bars->v_free[g % kRaw], ((g / kRaw) & 1) ^ 1, abort,
-                                       p.wait_ns);
-              }
-              if (ok) {
-                const int vs = g % kRaw;
-                if (there) {
-                  mbar_arrive_expect_tx(&bars->v_full[vs], kTileBytes);
-                  tma_load_2d(smem + kOffV + vs * kTileBytes, &kv_map, &bars->v_full[vs], kD, y);
-                } else {
-                  mbar_arrive(&bars->v_full[vs]);
-                }
-                ++v_loads;
-              }
-              // Q behind the part's first page (its copy needs no wait for the
-              // part before, Q's does)
-              if (ok && i == 0) {
-                if (part > 0) ok = bounded_wait_long(&bars->q_free, (part - 1) & 1, abort, p.wait_ns);
-                if (ok) {
-                  const int boxes = pair ? 2 : 1;
-                  mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(boxes * p.C * p.G * kD));
-                  for (int s = 0; s < boxes; ++s)
-                    tma_load_3d(smem + kOffQ + s * kTileBytes, &q_map, &bars->q_full, 0,
-                                walk.cur_h * p.G, t.tok0 + s * p.C);
-                  ++q_loads;
-                }
-              }
-            }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
-          }
-        }
-        ring.advance(pair, walk.stream_pages(0), walk.stream_pages(1));
-        ++part;
-      }
-      if (lane == 0) {
-        if (!ok && !*abort) give_up(bars, p.status);
-        // every copy lands before the CTA may end
-        for (int i = 0; i < kRaw; ++i)
-          if (k_used >> i & 1u)
-            bounded_wait_long(&bars->k_full[i], k_odd >> i & 1u, nullptr, kWaitLimitNs);
-        for (int i = max(0, v_loads - kRaw); i < v_loads; ++i)
-          bounded_wait_long(&bars->v_full[i % kRaw], (i / kRaw) & 1, nullptr, kWaitLimitNs);
-        if (q_loads > 0)
-          bounded_wait_long(&bars->q_full, (q_loads - 1) & 1, nullptr, kWaitLimitNs);
-      }
-      __syncwarp();
-    } else if (warp <= 2) {
-      if (elect_one()) {
-        // -------------------------------------------- MMA issuer of a stream
-        // One thread per stream: a single one for both was busy all the time
-        // and held either back.  The unit is a half page (64 keys): QK(u)
-        // into one of the stream's two S buffers, PV(u) from the P that
-        // replaces it; QK(u + 2) when PV(u) is complete, while the softmax
-        // works on unit u + 1.
-        constexpr uint32_t kQk = idesc_e4m3_f32(128, kHalf, false);
-        constexpr uint32_t kPv = idesc_f16_f32(128, 128, true);
-        const int s = warp - 1;
-        const uint64_t desc_k = smem_desc_sw128(smem_u32(smem + kOffK), 16, 1024);
-        const uint64_t desc_w = smem_desc_sw128(smem_u32(smem + kOffW), kTileBytes / 2, 1024);
-        const uint32_t s_tmem = tmem + s * 128, o_tmem = tmem + kColO + s * 128;
-        uint32_t part = 0, base = 0;  // parts, own units so far
-        Ring k_ring, w_ring;          // K pages, widened half pages
-        bool ok = true;
-        while (ok && walk.next()) {
-          const bool pair = walk.pair();
-          const uint32_t n0 = walk.stream_pages(0), n1 = walk.stream_pages(1);
-          const uint32_t n = 2u * (s ? n1 : n0);
-          const uint64_t desc_q =
-              smem_desc_sw128(smem_u32(smem + kOffQ + (pair ? s : 0) * kTileBytes), 16, 1024);
-          // both streams free a slot; in a solo part its owner for both
-          auto free_slot = [&](uint64_t* bar) {
-            mma_commit(bar);
-            if (!pair) mma_commit(bar);
-          };
-          auto qk = [&](uint32_t i) {
-            const uint32_t u = base + i, buf = u & 1, half = i & 1;
-            const uint32_t slot = Ring::slot(pair, s, i >> 1);
-            if (u > 1 &&
-                !bounded_wait_long(&bars->pv_done[s][buf], ((u >> 1) - 1) & 1, abort, p.wait_ns))
-              return false;
-            if (!half && !bounded_wait_long(&bars->k_full[slot], k_ring.phase(pair, slot, i >> 1),
-                                            abort, p.wait_ns))
-              return false;
-            tc_fence_after();
-            const uint64_t b = desc_k + slot * (kTileBytes / 16) + half * (kHalf * 128 / 16);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f8f6f4(s_tmem + buf * kHalf, desc_q + kk * 2, b + kk * 2, kQk, kk > 0);
-            mma_commit(&bars->s_full[s][buf]);
-            if (half) free_slot(&bars->k_free[slot]);
-            if (i + 1 == n) mma_commit(&bars->q_free);
-            return true;
-          };
-          // Q is there when both streams have issued all QKs of the part
-          // before, so every earlier use of the K slots is over
-          ok = bounded_wait_long(&bars->q_full, part & 1, abort, p.wait_ns);
-          if (ok && n == 0) mbar_arrive(&bars->q_free);
-          if (ok && n > 0) ok = qk(0) && qk(1);
-          // and both streams' PVs of that part, the uses of the W slots
-          if (ok && part > 0)
-            ok = bounded_wait_long(&bars->part_done, (part - 1) & 1, abort, p.wait_ns);
-          for (uint32_t i = 0; ok && i < n; ++i) {
-            const uint32_t u = base + i, buf = u & 1;
-            const uint32_t slot = Ring::slot(pair, s, i);
-            ok = bounded_wait_long(&bars->w_full[slot], w_ring.phase(pair, slot, i), abort,
-                                   p.wait_ns) &&
-                 bounded_wait_long(&bars->p_full[s][buf], (u >> 1) & 1, abort, p.wait_ns);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t b = desc_w + slot * (kTileBytes / 16);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f16_ts(o_tmem, s_tmem + buf * kHalf + kk * 8, b + kk * (16 * 128 / 16), kPv,
-                         kk > 0 || i > 0);
-            mma_commit(&bars->pv_done[s][buf]);
-            free_slot(&bars->w_free[slot]);
-            if (i + 2 < n) ok = qk(i + 2);
-          }
-          if (ok) mma_commit(&bars->part_done);
-          k_ring.advance(pair, n0, n1);
-          w_ring.advance(pair, 2 * n0, 2 * n1);
-          base += n;
-          ++part;
-        }
-        if (!ok && !*abort) give_up(bars, p.status);
-        mma_commit(&bars->mma_done[s]);
-        bounded_wait_long(&bars->mma_done[s], 0, nullptr, kWaitLimitNs);
-      }
-      __syncwarp();
-    }
-  } else if (warp < 12) {
+  if (warp >= 4 && warp < 12) {
     setmaxnreg_inc<kRegsSoftmax>();
     // ------------------------------------------------------------- softmax
     const int s = warp >= 8, quad = warp & 3, row = quad * 32 + lane;
@@ -644,6 +488,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
     const int i_tok = row / p.G;
     uint32_t done = 0;  // units (half pages) of this stream so far
     uint32_t g0 = 0;    // pages of the parts before
+    uint32_t solos = 0; // solo parts so far
     bool ok = true;
     while (ok && walk.next()) {
       const Tile& t = walk.t;
@@ -760,6 +605,11 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         if (!ok) break;
         l += sum;
         tmem_wait_st();
+        // the first PV of a part overwrites O: the other stream has read it
+        if (i == 0 && solos > 0 && !all_wait(bars, &bars->read, (solos - 1) & 1, p)) {
+          ok = false;
+          break;
+        }
         tc_fence_before();
         mbar_arrive(&bars->p_full[s][buf]);
       }
@@ -767,61 +617,87 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
       // the part: O / l and log2 of the row's sum
       const int64_t prow = part_row(blockIdx.x, walk.cur_h, walk.cur_tile, walk.shared_tiles, t.tok0,
                                     p.T, p.G) +
-                           (s ? (pair ? p.C : t.ntok) * p.G : 0) + row;
-      if (n > 0) {
-        if (!all_wait(bars, &bars->pv_done[s][(done - 1) & 1], ((done - 1) >> 1) & 1, p)) break;
-        tc_fence_after();
-        bool poison = __any_sync(0xffffffffu, *(volatile int*)&bars->nan_seen != 0);
-        int nan_key[4] = {INT_MAX, INT_MAX, INT_MAX, INT_MAX};  // columns 4 lane ..
-        if (poison) {
-          // A NaN lies among the V codes of some valid key.  Widening wrote
-          // it as 0, since a probability of 0 must hide it; now each warp
-          // finds, for each column, the first position of this part that has
-          // one (a rare path: no care is taken of its speed).
-          for (int i = 0; i < n; ++i) {
-            const int j = walk.p0 + walk.stream_page(s, i);
-            const int pg = __ldg(table + j);
-            if (pg < 0 || pg >= p.num_pages) continue;
-            const uint8_t* v = p.kv + ((int64_t)pg * p.Hkv + walk.cur_h) * kPage * (2 * kD) + kD;
-            const int first = (t.page0 + j) * kPage;
-            for (int k = 0; k < kPage && first + k < t.seq; ++k) {
-              const uint32_t bad = nan_bytes(
-                  __ldg(reinterpret_cast<const uint32_t*>(v + k * (2 * kD)) + lane));
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if ((bad >> (8 * e)) & 0x80u) nan_key[e] = min(nan_key[e], first + k);
-            }
-          }
-        }
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t o[32];
-          tmem_ld32(o_tmem + q * 32, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
-          if (poison) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (__shfl_sync(0xffffffffu, nan_key[e & 3], q * 8 + (e >> 2)) <= pos)
-                o[e] = 0x7FFFFFFFu;
-          }
-          if (valid) {
-            uint32_t* dst = reinterpret_cast<uint32_t*>(p.part_o + prow * kD) + q * 32;
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              st_global_v8(dst + e, o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5],
-                           o[e + 6], o[e + 7]);
-          }
-        }
-        tc_fence_before();
-      }
+                           (pair && s ? p.C * p.G : 0) + row;
       g0 += walk.p1 - walk.p0;
-      if (valid)
-        p.part_lse[prow] = n > 0 && l != 0.f ? m * c - kPShift + log2f(l) : -INFINITY;
+      if (n > 0 &&
+          !all_wait(bars, &bars->pv_done[s][(done - 1) & 1], ((done - 1) >> 1) & 1, p))
+        break;
+      tc_fence_after();
+      // In a solo part the streams have the same rows, in the same lanes of
+      // tensor memory: either writes half the columns of both streams' sum.
+      // Weights of the own and the other stream's O (0: nothing, whatever it
+      // holds; a NaN among the scores makes l, and so the row, NaN).
+      float wa = l == 0.f ? 0.f : 1.f, wb = 0.f, lt = l, mt = m;
+      if (!pair) {
+        if (solos > 0 && !all_wait(bars, &bars->read, (solos - 1) & 1, p)) break;
+        bars->ml[s][row] = make_float2(m, l);
+        tc_fence_before();
+        mbar_arrive(&bars->exchanged);
+        if (!all_wait(bars, &bars->exchanged, solos & 1, p)) break;
+        tc_fence_after();
+        const float2 z = bars->ml[s ^ 1][row];
+        mt = fmaxf(m, z.x);
+        wa = l == 0.f ? 0.f : m == -INFINITY ? 1.f : ex2_approx((m - mt) * c);
+        wb = z.y == 0.f ? 0.f : z.x == -INFINITY ? 1.f : ex2_approx((z.x - mt) * c);
+        lt = (wa == 0.f ? 0.f : l * wa) + (wb == 0.f ? 0.f : z.y * wb);
+      }
+      const bool poison = __any_sync(0xffffffffu, *(volatile int*)&bars->nan_seen != 0);
+      int nan_key[4] = {INT_MAX, INT_MAX, INT_MAX, INT_MAX};  // columns 4 lane ..
+      if (poison) {
+        // A NaN lies among the V codes of some valid key.  Widening wrote it
+        // as 0, since a probability of 0 must hide it; now each warp finds,
+        // for each column, the first position of this part that has one (a
+        // rare path: no care is taken of its speed).
+        for (int j = walk.p0; j < walk.p1; ++j) {
+          const int pg = __ldg(table + j);
+          if (pg < 0 || pg >= p.num_pages) continue;
+          const uint8_t* v = p.kv + ((int64_t)pg * p.Hkv + walk.cur_h) * kPage * (2 * kD) + kD;
+          const int first = (t.page0 + j) * kPage;
+          for (int k = 0; k < kPage && first + k < t.seq; ++k) {
+            const uint32_t bad = nan_bytes(
+                __ldg(reinterpret_cast<const uint32_t*>(v + k * (2 * kD)) + lane));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if ((bad >> (8 * e)) & 0x80u) nan_key[e] = min(nan_key[e], first + k);
+          }
+        }
+      }
+      const float inv = lt == 0.f ? 0.f : 1.f / lt;
+      const float fa = wa * inv, fb = wb * inv;
+      const int q0 = pair ? 0 : 4 * s, q1 = pair ? 8 : q0 + 4;
+#pragma unroll 1
+      for (int q = q0; q < q1; ++q) {
+        uint32_t o[16], x[16];
+        tmem_ld16(o_tmem + q * 16, o);
+        tmem_ld16(o_tmem + q * 16 + (s ? -128 : 128), x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          o[e] = __float_as_uint((wa == 0.f ? 0.f : __uint_as_float(o[e]) * fa) +
+                                 (wb == 0.f ? 0.f : __uint_as_float(x[e]) * fb));
+        if (poison) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (__shfl_sync(0xffffffffu, nan_key[e & 3], q * 4 + (e >> 2)) <= pos)
+              o[e] = 0x7FFFFFFFu;
+        }
+        if (valid) {
+          uint32_t* dst = reinterpret_cast<uint32_t*>(p.part_o + prow * kD) + q * 16;
+#pragma unroll
+          for (int e = 0; e < 16; e += 8)
+            st_global_v8(dst + e, o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6],
+                         o[e + 7]);
+        }
+      }
+      tc_fence_before();
+      if (!pair) {
+        mbar_arrive(&bars->read);
+        ++solos;
+      }
+      if (valid && (pair || s == 0))
+        p.part_lse[prow] = lt == 0.f ? -INFINITY : mt * c - kPShift + log2f(lt);
     }
-  } else {
+  } else if (warp >= 12) {
     setmaxnreg_dec<kRegsWiden>();
     // -------------------------------------------------------------- widen
     // 128 threads: a page's V codes in pieces of 8; thread wt has piece
@@ -840,7 +716,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
       const Tile& t = walk.t;
       const bool pair = walk.pair();
       for (int j = walk.p0; j < walk.p1; ++j, ++g) {
-        if (!all_wait(bars, &bars->v_full[g % kRaw], (g / kRaw) & 1, p)) {
+        if (!all_wait(bars, &bars->v_full[g % kRawV], (g / kRawV) & 1, p)) {
           ok = false;
           break;
         }
@@ -850,7 +726,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         // flow through PV.  In the others a probability of 0 has to hide one:
         // it is written as 0, and put back where it is seen in the end.
         const bool whole = keys == kPage && (t.page0 + j + 1) * kPage <= t.pos0 + 1;
-        const uint8_t* src = smem + kOffV + (g % kRaw) * kTileBytes + src0;
+        const uint8_t* src = smem + kOffV + (g % kRawV) * kTileBytes + src0;
         // all loads first, so that the conversions overlap
         uint2 w[16];
 #pragma unroll
@@ -885,13 +761,179 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (half) mbar_arrive(&bars->v_free[g % kRaw]);
+            if (half) mbar_arrive(&bars->v_free[g % kRawV]);
             mbar_arrive(&bars->w_full[slot]);
           }
         }
         if (!ok) break;
       }
       ring.advance(pair, 2 * walk.stream_pages(0), 2 * walk.stream_pages(1));
+    }
+  } else {
+    setmaxnreg_dec<kRegsControl>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      int g = 0, part = 0;  // pages and parts so far
+      int q_loads = 0, v_loads = 0;
+      uint32_t k_used = 0, k_odd = 0;  // by slot: loaded, parity of the last load's phase
+      Ring ring;
+      bool ok = true;
+      while (ok && walk.next()) {
+        const Tile& t = walk.t;
+        const bool pair = walk.pair();
+        const int32_t* table = p.block_table + t.b * p.bt_stride + t.page0;
+        for (int j0 = walk.p0; ok && j0 < walk.p1; j0 += 32) {
+          const int mine = j0 + lane < walk.p1 ? __ldg(table + j0 + lane) : 0;
+          const int n = min(32, walk.p1 - j0);
+          for (int j = 0; j < n; ++j, ++g) {
+            const int page = __shfl_sync(0xffffffffu, mine, j);
+            if (lane == 0) {
+              const int i = j0 + j - walk.p0;  // within the part
+              const uint32_t v = pair ? i : i >> 1;
+              const uint32_t slot = Ring::slot(pair, i & 1, v), ph = ring.phase(pair, slot, v);
+              const bool there = page >= 0 && page < p.num_pages;
+              bars->there[g % kThere] = there;
+              if (!there && p.status) atomicOr(p.status, (unsigned)MSA_STATUS_BAD_BLOCK);
+              const int y = there ? (page * p.Hkv + walk.cur_h) * kPage : 0;
+              ok = bounded_wait_long(&bars->k_free[slot], ph ^ 1, abort, p.wait_ns);
+              if (ok) {
+                if (there) {
+                  mbar_arrive_expect_tx(&bars->k_full[slot], kTileBytes);
+                  tma_load_2d(smem + kOffK + slot * kTileBytes, &kv_map, &bars->k_full[slot], 0, y);
+                } else {
+                  mbar_arrive(&bars->k_full[slot]);
+                }
+                k_used |= 1u << slot;
+                k_odd = (k_odd & ~(1u << slot)) | (ph << slot);
+                ok = bounded_wait_long(&bars->v_free[g % kRawV], ((g / kRawV) & 1) ^ 1, abort,
+                                       p.wait_ns);
+              }
+              if (ok) {
+                const int vs = g % kRawV;
+                if (there) {
+                  mbar_arrive_expect_tx(&bars->v_full[vs], kTileBytes);
+                  tma_load_2d(smem + kOffV + vs * kTileBytes, &kv_map, &bars->v_full[vs], kD, y);
+                } else {
+                  mbar_arrive(&bars->v_full[vs]);
+                }
+                ++v_loads;
+              }
+              // Q behind the part's first page (its copy needs no wait for the
+              // part before, Q's does)
+              if (ok && i == 0) {
+                if (part > 0) ok = bounded_wait_long(&bars->q_free, (part - 1) & 1, abort, p.wait_ns);
+                if (ok) {
+                  const int boxes = pair ? 2 : 1;
+                  mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(boxes * p.C * p.G * kD));
+                  for (int s = 0; s < boxes; ++s)
+                    tma_load_3d(smem + kOffQ + s * kTileBytes, &q_map, &bars->q_full, 0,
+                                walk.cur_h * p.G, t.tok0 + s * p.C);
+                  ++q_loads;
+                }
+              }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+          }
+        }
+        ring.advance(pair, walk.stream_pages(0), walk.stream_pages(1));
+        ++part;
+      }
+      if (lane == 0) {
+        if (!ok && !*abort) give_up(bars, p.status);
+        // every copy lands before the CTA may end
+        for (int i = 0; i < kRawK; ++i)
+          if (k_used >> i & 1u)
+            bounded_wait_long(&bars->k_full[i], k_odd >> i & 1u, nullptr, kWaitLimitNs);
+        for (int i = max(0, v_loads - kRawV); i < v_loads; ++i)
+          bounded_wait_long(&bars->v_full[i % kRawV], (i / kRawV) & 1, nullptr, kWaitLimitNs);
+        if (q_loads > 0)
+          bounded_wait_long(&bars->q_full, (q_loads - 1) & 1, nullptr, kWaitLimitNs);
+      }
+      __syncwarp();
+    } else if (warp <= 2) {
+      if (elect_one()) {
+        // -------------------------------------------- MMA issuer of a stream
+        // One thread per stream: a single one for both was busy all the time
+        // and held either back.  The unit is a half page (64 keys): QK(u)
+        // into one of the stream's two S buffers, PV(u) from the P that
+        // replaces it; QK(u + 2) when PV(u) is complete, while the softmax
+        // works on unit u + 1.
+        constexpr uint32_t kQk = idesc_e4m3_f32(128, kHalf, false);
+        constexpr uint32_t kPv = idesc_f16_f32(128, 128, true);
+        const int s = warp - 1;
+        const uint64_t desc_k = smem_desc_sw128(smem_u32(smem + kOffK), 16, 1024);
+        const uint64_t desc_w = smem_desc_sw128(smem_u32(smem + kOffW), kTileBytes / 2, 1024);
+        const uint32_t s_tmem = tmem + s * 128, o_tmem = tmem + kColO + s * 128;
+        uint32_t part = 0, base = 0;  // parts, own units so far
+        Ring k_ring, w_ring;          // K pages, widened half pages
+        bool ok = true;
+        while (ok && walk.next()) {
+          const bool pair = walk.pair();
+          const uint32_t n0 = walk.stream_pages(0), n1 = walk.stream_pages(1);
+          const uint32_t n = 2u * (s ? n1 : n0);
+          const uint64_t desc_q =
+              smem_desc_sw128(smem_u32(smem + kOffQ + (pair ? s : 0) * kTileBytes), 16, 1024);
+          // both streams free a slot; in a solo part its owner for both
+          auto free_slot = [&](uint64_t* bar) {
+            mma_commit(bar);
+            if (!pair) mma_commit(bar);
+          };
+          auto qk = [&](uint32_t i) {
+            const uint32_t u = base + i, buf = u & 1, half = i & 1;
+            const uint32_t slot = Ring::slot(pair, s, i >> 1);
+            if (u > 1 &&
+                !bounded_wait_long(&bars->pv_done[s][buf], ((u >> 1) - 1) & 1, abort, p.wait_ns))
+              return false;
+            if (!half && !bounded_wait_long(&bars->k_full[slot], k_ring.phase(pair, slot, i >> 1),
+                                            abort, p.wait_ns))
+              return false;
+            tc_fence_after();
+            const uint64_t b = desc_k + slot * (kTileBytes / 16) + half * (kHalf * 128 / 16);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f8f6f4(s_tmem + buf * kHalf, desc_q + kk * 2, b + kk * 2, kQk, kk > 0);
+            mma_commit(&bars->s_full[s][buf]);
+            if (half) free_slot(&bars->k_free[slot]);
+            if (i + 1 == n) mma_commit(&bars->q_free);
+            return true;
+          };
+          // Q is there when both streams have issued all QKs of the part
+          // before, so every earlier use of the K slots is over
+          ok = bounded_wait_long(&bars->q_full, part & 1, abort, p.wait_ns);
+          if (ok && n == 0) mbar_arrive(&bars->q_free);
+          if (ok && n > 0) ok = qk(0) && qk(1);
+          // and both streams' PVs of that part, the uses of the W slots
+          if (ok && part > 0)
+            ok = bounded_wait_long(&bars->part_done, (part - 1) & 1, abort, p.wait_ns);
+          for (uint32_t i = 0; ok && i < n; ++i) {
+            const uint32_t u = base + i, buf = u & 1;
+            const uint32_t slot = Ring::slot(pair, s, i);
+            ok = bounded_wait_long(&bars->w_full[slot], w_ring.phase(pair, slot, i), abort,
+                                   p.wait_ns) &&
+                 bounded_wait_long(&bars->p_full[s][buf], (u >> 1) & 1, abort, p.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t b = desc_w + slot * (kTileBytes / 16);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16_ts(o_tmem, s_tmem + buf * kHalf + kk * 8, b + kk * (16 * 128 / 16), kPv,
+                         kk > 0 || i > 0);
+            mma_commit(&bars->pv_done[s][buf]);
+            free_slot(&bars->w_free[slot]);
+            if (i + 2 < n) ok = qk(i + 2);
+          }
+          if (ok) mma_commit(&bars->part_done);
+          k_ring.advance(pair, n0, n1);
+          w_ring.advance(pair, 2 * n0, 2 * n1);
+          base += n;
+          ++part;
+        }
+        if (!ok && !*abort) give_up(bars, p.status);
+        mma_commit(&bars->mma_done[s]);
+        bounded_wait_long(&bars->mma_done[s], 0, nullptr, kWaitLimitNs);
+      }
+      __syncwarp();
     }
   }
 
@@ -907,7 +949,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
 // ----------------------------------------------------------------- combine
 
 constexpr int kCombineWarps = 8;
-constexpr int kMaxParts = 2 * 192;  // parts of a tile: two streams a CTA
+constexpr int kMaxParts = 192;  // parts of a tile: one a CTA
 
 struct CombineParams {
   const PlanHead* head;
@@ -976,7 +1018,6 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
         t.npages = p.prefix;
         t.start = ti * tile_cost(2 * p.C, p.prefix, p.C);
       }
-      const bool pair = t.ntok > p.C;
       const int rate = tile_rate(t.ntok, p.C);
       const int64_t share = share_of((int64_t)hd.cost * p.Hkv, p.ctas);
       const int64_t t0 = (int64_t)h * hd.cost + t.start;
@@ -992,18 +1033,13 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
           pa = pages_before(max(cta * share, t0) - t0, t.npages, rate);
           pb = pages_before(min((cta + 1) * share, t1) - t0, t.npages, rate);
         }
-        // a solo part's second stream has pages where there are two
-        const int streams = pb > pa ? (pair ? 1 : min(2, pb - pa)) : 0;
-        const uint32_t one = __ballot_sync(0xffffffffu, streams > 0);
-        const uint32_t two = __ballot_sync(0xffffffffu, streams > 1);
-        const uint32_t below = (1u << lane) - 1u;
-        if (streams > 0) {
-          const int at = n + __popc(one & below) + __popc(two & below);
-          const int row = (int)part_row(cta, h, ti, hd.shared_tiles, t.tok0, p.T, p.G);
-          if (at < kMaxParts) s_row[warp][at] = row;
-          if (streams > 1 && at + 1 < kMaxParts) s_row[warp][at + 1] = row + t.ntok * p.G;
+        const uint32_t some = __ballot_sync(0xffffffffu, pb > pa);
+        if (pb > pa) {
+          const int at = n + __popc(some & ((1u << lane) - 1u));
+          if (at < kMaxParts)
+            s_row[warp][at] = (int)part_row(cta, h, ti, hd.shared_tiles, t.tok0, p.T, p.G);
         }
-        n += __popc(one) + __popc(two);
+        n += __popc(some);
       }
       if (lane == 0) s_tile[warp] = t;
     }
@@ -1135,8 +1171,8 @@ bool layout(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t prefix, int64
   const int64_t tiles = max_tiles(B, T, C, prefix);
   // costs and partial rows in range of their integers
   if ((double)tiles * (double)(ceil_div(max_k, kPage) * kCostPair + kCostTile) > 1.0e9) return false;
-  const int64_t rows = 256 * ((int64_t)ctas + 1) + Hkv * (prefix > 0 ? 4 : 2) * T * G;
-  if (rows >= INT_MAX || 2 * ctas > kMaxParts) return false;
+  const int64_t rows = 256 * ((int64_t)ctas + 1) + Hkv * (prefix > 0 ? 2 : 1) * T * G;
+  if (rows >= INT_MAX || ctas > kMaxParts) return false;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   l->head = 0;
   l->tiles = 256;
@@ -1240,9 +1276,8 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, void* ws, cudaStream_t 
   const int64_t tile_rows = std::min<int64_t>(2 * C, a.max_q) * G;
   const int64_t tiles_n =
       a.prefix_pages > 0 ? ceil_div(a.T, 2 * C) : std::min(a.T, ceil_div(a.T, 2 * C) + a.B);
-  const int64_t parts =
-      (int64_t)ctas * (a.T <= C || a.prefix_pages == 0 ? 2 : 1) / (a.Hkv * tiles_n);
-  const int lanes = parts >= 6 ? 32 : 8, team = parts >= 48 ? 8 : parts >= 6 ? 2 : 1;
+  const int64_t parts = (int64_t)ctas / (a.Hkv * tiles_n);
+  const int lanes = parts >= 4 ? 32 : 8, team = parts >= 24 ? 8 : parts >= 4 ? 2 : 1;
   const int cta_rows = kCombineWarps * 32 / lanes / team;
   const CombineParams cp = {head, tiles + own0, (int)a.T, (int)a.Hq, (int)a.Hkv, G, C, ctas,
                             (int)a.prefix_pages, cta_rows, part_o, part_lse, a.v_scale, a.out, a.lse};
