@@ -2,7 +2,9 @@
 // checks, workspace layout and the launch sequence of each call.  Nothing
 // here allocates device memory or synchronises, except msa_read_status /
 // msa_read_counters, which are documented to synchronise.
+#include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -703,8 +705,11 @@ int msa_prefix_attention(const uint8_t* q, const uint8_t* kv, int64_t num_pages,
   if (num_pages < 0 || num_pages * Hkv * kPage >= kI32Max ||
       bt_stride < ceil_div(max_seqlen_k, kPage) || bt_stride > (1 << 24))
     return MSA_ERR_SHAPE;
+  // the largest score of E4M3 codes, 128 * 448^2 products, has to be finite
+  const double score = (double)q_scale * (double)k_scale * (double)softmax_scale *
+                       1.4426950408889634074;
   if (!(q_scale > 0.f) || !(k_scale > 0.f) || !(v_scale > 0.f) || !(softmax_scale > 0.f) ||
-      !std::isfinite(q_scale * k_scale * softmax_scale) || !std::isfinite(v_scale))
+      !(score * kD * 448.0 * 448.0 < FLT_MAX) || !std::isfinite(v_scale))
     return MSA_ERR_SHAPE;
   if (B == 0 || T == 0) return MSA_OK;
   if (!q || !kv || !block_table || !cu_seqlens_q || !cu_seqlens_k || !out) return MSA_ERR_NULL;
@@ -718,8 +723,8 @@ int msa_prefix_attention(const uint8_t* q, const uint8_t* kv, int64_t num_pages,
   a.q = q;
   a.kv = kv;
   a.num_pages = num_pages;
-  a.score_log2 = (float)((double)q_scale * (double)k_scale * (double)softmax_scale *
-                         1.4426950408889634074);
+  // never 0, by which a masked score of -inf would become NaN
+  a.score_log2 = std::max((float)score, FLT_MIN);
   a.v_scale = v_scale;
   a.block_table = block_table;
   a.bt_stride = bt_stride;

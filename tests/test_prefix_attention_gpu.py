@@ -137,6 +137,16 @@ def test_flat_and_peaked_scores(gain):
     _compare(w, (out, lse))
 
 
+def test_scales_whose_product_vanishes():
+    # scores below 2^-100: every key has the same weight; what is masked has none
+    w = _batch(8, 2, [40, 2], [300, 4], 2, seed=12)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = msa.msa_prefix_attention(w["q"], w["kv"], 1e-30, 1e-25, VS, SM, w["table"], w["cu_q"], w["cu_k"], w["prefix"], w["max_q"], w["max_k"],
+                                   status=status)
+    assert status.item() == 0
+    _compare(dict(w, q=torch.zeros_like(w["q"].view(torch.uint8)).view(torch.float8_e4m3fn)), got)
+
+
 def test_prefix_equals_no_prefix():
     # the same keys, once as shared pages and once as every request's own
     w = _batch(16, 2, [8, 1, 40], [50, 300, 41], 6, seed=4)
@@ -254,3 +264,21 @@ def test_graph_streams_and_repeats():
         torch.cuda.synchronize()
         _compare(dict(w, seqs=seqs), (out, lse))
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_short_wait_limit_expires_and_the_next_call_is_clean():
+    # a limit below a page load's latency: a wait runs out, the call returns
+    # with the status bit, and the next one on the same workspace is exact
+    lib = msa.load()
+    w = _batch(16, 2, [8] * 4, [1000, 2000, 3001, 4100], 30, seed=13)
+    need = msa.prefix_attention_workspace_bytes(4, 32, 16, 2, 30, 8, w["max_k"])
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    want = _run(w, workspace=ws)
+    assert want[2] == 0
+    try:
+        assert lib.msa_test_set_wait_limit_ns(300) == 0
+        assert _run(w, workspace=ws)[2] & msa.STATUS_TIMEOUT
+    finally:
+        lib.msa_test_set_wait_limit_ns(0)
+    got = _run(w, workspace=ws)
+    assert got[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

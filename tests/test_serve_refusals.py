@@ -146,6 +146,7 @@ def test_prefix_attention_library_refusals():
     assert run(width=2) == 1 and run(pages=-1) == 1 and run(pages=2 ** 23) == 1 and run(B=-1) == 1 and run(prefix=-1) == 1
     for s in (0.0, -1.0, float("nan"), float("inf")):
         assert run(s=s) == 1
+    assert run(s=1e32) == 1 and run(s=1e30, B=0) == 0  # the largest score: 1e32 * 0.1 * log2 e * 128 * 448^2 > 3.4e38
     assert run(Hq=3) == 2 and run(Hq=0) == 1 and run(Hq=258) == 2
     assert run(ws=None) == 4 and run(size=1000) == 4 and run(ws=P(4096 + 128)) == 3
     assert run(q=P(4104)) == 3 and run(out=P(4100)) == 3 and run(lse=P(4098)) == 3 and run(status=P(4097)) == 3
