@@ -32,18 +32,13 @@ def _check(rc, what):
 
 
 def _tensor(t, name, dtypes, shape=None, contiguous=True):
-    """Type and shape (None: any size in its place) of a required tensor."""
+    """Type and shape of a required tensor."""
     if t is None:
         _fail("%s is required", name)
     if t.dtype not in dtypes:
         _fail("%s has dtype %s, expected one of %s", name, t.dtype, dtypes)
-    # equal shapes end the comparison at once: these checks run on every call
-    # of a decode step
     if shape is not None and t.shape != shape:
-        have = t.shape
-        if len(have) != len(shape) or any(w is not None and w != h for w, h in zip(shape, have)):
-            _fail("%s must be [%s], got %s", name,
-                  ", ".join("any" if w is None else str(w) for w in shape), tuple(have))
+        _fail("%s must be %s, got %s", name, list(shape), tuple(t.shape))
     if contiguous and not t.is_contiguous():
         _fail("%s must be contiguous", name)
 
@@ -72,7 +67,7 @@ def _handle(stream, dev):
 def _new(shape, dtype, like, dev, handle):
     """A tensor on like's device for use on the stream `handle`, whichever
     stream is current."""
-    t = torch.empty(shape, dtype=dtype, device=like.device)
+    t = like.new_empty(shape, dtype=dtype)
     if handle != torch._C._cuda_getCurrentRawStream(dev):
         t.record_stream(torch.cuda.ExternalStream(handle, device=like.device))
     return t
@@ -273,48 +268,55 @@ def msa_prefix_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_
     return out, lse
 
 
+def _probs(t, name, dtypes):
+    """Shape and strides of rows [B, n, V] whose values are contiguous."""
+    _tensor(t, name, dtypes, None, False)
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3:
+        _fail("%s must be [any, any, any], got %s", name, tuple(shape))
+    if strides[2] != 1 and shape[2] > 1:
+        _fail("%s's rows must be contiguous", name)
+    return shape, strides
+
+
 def _verify(name, target, drafts, uniforms, draft_probs, counts, tokens, accepted, stream):
     greedy = name == "msa_verify_greedy"
-    _tensor(target, "target", _TYPES, None, False)
-    if target.dim() != 3:
-        _fail("target must be [any, any, any], got %s", tuple(target.shape))
-    B, n, V = target.shape
+    (B, n, V), (t_req, t_row, _) = _probs(target, "target", _TYPES)
     if n < 1:
         _fail("target must have at least one row a request")
-    if target.stride(2) != 1 and V > 1:
-        _fail("target's rows must be contiguous")
     _tensor(drafts, "draft_tokens", _I32, (B, n - 1))
     if not greedy:
         _tensor(uniforms, "uniforms", _F32, (B, n))
+    d_ptr, d_req, d_row = None, 0, 0
     if draft_probs is not None:
-        _tensor(draft_probs, "draft_probs", (target.dtype,), (B, n - 1, V), contiguous=False)
-        if draft_probs.stride(2) != 1 and V > 1:
-            _fail("draft_probs' rows must be contiguous")
+        shape, strides = _probs(draft_probs, "draft_probs", (target.dtype,))
+        if shape != (B, n - 1, V):
+            _fail("draft_probs must be %s, got %s", [B, n - 1, V], tuple(shape))
+        if n > 1:
+            d_ptr, d_req, d_row = draft_probs.data_ptr(), strides[0], strides[1]
     if counts is not None:
         _tensor(counts, "num_drafts", _I32, (B,))
     dev = _place(target, drafts, uniforms, draft_probs, counts, tokens, accepted)
     handle = _handle(stream, dev)
     if tokens is None:
-        tokens = _new((B, n), torch.int32, target, dev, handle)
+        tokens = _new((B, n), torch.int32, drafts, dev, handle)
     else:
         _tensor(tokens, "tokens", _I32, (B, n))
     if accepted is None:
-        accepted = _new((B,), torch.int32, target, dev, handle)
+        accepted = _new((B,), torch.int32, drafts, dev, handle)
     else:
         _tensor(accepted, "accepted", _I32, (B,))
-    t_req, t_row, _ = target.stride()
-    lib = load()
     if greedy:
-        rc = lib.msa_verify_greedy(target.data_ptr(), t_req, t_row, _TYPES[target.dtype],
-                                   drafts.data_ptr(), _ptr(counts), B, n, V, tokens.data_ptr(),
-                                   accepted.data_ptr(), handle)
+        rc = load().msa_verify_greedy(target.data_ptr(), t_req, t_row, _TYPES[target.dtype],
+                                      drafts.data_ptr(), _ptr(counts), B, n, V,
+                                      tokens.data_ptr(), accepted.data_ptr(), handle)
     else:
-        d = draft_probs if draft_probs is not None and n > 1 else None
-        d_req, d_row = d.stride()[:2] if d is not None else (0, 0)
-        rc = lib.msa_verify(target.data_ptr(), t_req, t_row, _ptr(d), d_req, d_row,
-                            _TYPES[target.dtype], drafts.data_ptr(), uniforms.data_ptr(),
-                            _ptr(counts), B, n, V, tokens.data_ptr(), accepted.data_ptr(), handle)
-    _check(rc, name)
+        rc = load().msa_verify(target.data_ptr(), t_req, t_row, d_ptr, d_req, d_row,
+                               _TYPES[target.dtype], drafts.data_ptr(), uniforms.data_ptr(),
+                               _ptr(counts), B, n, V, tokens.data_ptr(), accepted.data_ptr(),
+                               handle)
+    if rc:
+        _check(rc, name)
     return tokens, accepted
 
 
