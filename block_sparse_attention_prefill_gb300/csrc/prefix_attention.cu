@@ -256,7 +256,7 @@ struct Bars {
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [stream][buffer]
   uint64_t part_done;
   uint64_t exchanged, read;  // the streams' results at the end of a solo part
-  uint64_t mma_done[2];
+  uint64_t mma_done[3];
   uint32_t tmem_base;
   int abort;
   int nan_seen;      // a NaN among the V codes of valid keys
@@ -415,10 +415,10 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
 
   if (tid == 0) {
     mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_free, 2);
+    mbar_init(&bars->q_free, 1);
     for (int i = 0; i < kRawK; ++i) {
       mbar_init(&bars->k_full[i], 1);
-      mbar_init(&bars->k_free[i], 2);
+      mbar_init(&bars->k_free[i], 1);
     }
     for (int i = 0; i < kRawV; ++i) {
       mbar_init(&bars->v_full[i], 1);
@@ -436,8 +436,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
     mbar_init(&bars->part_done, 2);
     mbar_init(&bars->exchanged, 256);
     mbar_init(&bars->read, 256);
-    mbar_init(&bars->mma_done[0], 1);
-    mbar_init(&bars->mma_done[1], 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&bars->mma_done[i], 1);
     bars->abort = 0;
     bars->nan_seen = 0;
     bars->first_tile = 0;
@@ -851,67 +850,72 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
           bounded_wait_long(&bars->q_full, (q_loads - 1) & 1, nullptr, kWaitLimitNs);
       }
       __syncwarp();
-    } else if (warp <= 2) {
-      if (elect_one()) {
-        // -------------------------------------------- MMA issuer of a stream
-        // One thread per stream: a single one for both was busy all the time
-        // and held either back.  The unit is a half page (64 keys): QK(u)
-        // into one of the stream's two S buffers, PV(u) from the P that
-        // replaces it; QK(u + 2) when PV(u) is complete, while the softmax
-        // works on unit u + 1.
+    } else if (elect_one()) {
+      // ------------------------------------------------------- MMA issuers
+      // The unit is a half page (64 keys): QK(u) into one of a stream's two S
+      // buffers, PV(u) from the P that replaces it, QK(u + 2) when PV(u) is
+      // complete, while the softmax works on unit u + 1.  One thread issues
+      // the QKs of both streams, and one for each stream its PVs, so that a
+      // PV whose P is ready does not wait behind a QK whose buffer is not.
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return bounded_wait_long(bar, parity, abort, p.wait_ns);
+      };
+      uint32_t part = 0;
+      bool ok = true;
+      if (warp == 3) {
         constexpr uint32_t kQk = idesc_e4m3_f32(128, kHalf, false);
-        constexpr uint32_t kPv = idesc_f16_f32(128, 128, true);
-        const int s = warp - 1;
         const uint64_t desc_k = smem_desc_sw128(smem_u32(smem + kOffK), 16, 1024);
-        const uint64_t desc_w = smem_desc_sw128(smem_u32(smem + kOffW), kTileBytes / 2, 1024);
-        const uint32_t s_tmem = tmem + s * 128, o_tmem = tmem + kColO + s * 128;
-        uint32_t part = 0, base = 0;  // parts, own units so far
-        Ring k_ring, w_ring;          // K pages, widened half pages
-        bool ok = true;
+        const uint64_t desc_q = smem_desc_sw128(smem_u32(smem + kOffQ), 16, 1024);
+        uint32_t base[2] = {0, 0};  // units of the streams so far
+        Ring ring;
         while (ok && walk.next()) {
           const bool pair = walk.pair();
-          const uint32_t n0 = walk.stream_pages(0), n1 = walk.stream_pages(1);
-          const uint32_t n = 2u * (s ? n1 : n0);
-          const uint64_t desc_q =
-              smem_desc_sw128(smem_u32(smem + kOffQ + (pair ? s : 0) * kTileBytes), 16, 1024);
-          // both streams free a slot; in a solo part its owner for both
-          auto free_slot = [&](uint64_t* bar) {
-            mma_commit(bar);
-            if (!pair) mma_commit(bar);
-          };
-          auto qk = [&](uint32_t i) {
-            const uint32_t u = base + i, buf = u & 1, half = i & 1;
-            const uint32_t slot = Ring::slot(pair, s, i >> 1);
-            if (u > 1 &&
-                !bounded_wait_long(&bars->pv_done[s][buf], ((u >> 1) - 1) & 1, abort, p.wait_ns))
-              return false;
-            if (!half && !bounded_wait_long(&bars->k_full[slot], k_ring.phase(pair, slot, i >> 1),
-                                            abort, p.wait_ns))
-              return false;
-            tc_fence_after();
-            const uint64_t b = desc_k + slot * (kTileBytes / 16) + half * (kHalf * 128 / 16);
+          const uint32_t n[2] = {2u * walk.stream_pages(0), 2u * walk.stream_pages(1)};
+          // Q is there when all QKs of the part before are complete
+          ok = wait(&bars->q_full, part & 1);
+          for (uint32_t i = 0; ok && i < n[0]; ++i) {  // n[0] >= n[1]
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f8f6f4(s_tmem + buf * kHalf, desc_q + kk * 2, b + kk * 2, kQk, kk > 0);
-            mma_commit(&bars->s_full[s][buf]);
-            if (half) free_slot(&bars->k_free[slot]);
-            if (i + 1 == n) mma_commit(&bars->q_free);
-            return true;
-          };
-          // Q is there when both streams have issued all QKs of the part
-          // before, so every earlier use of the K slots is over
-          ok = bounded_wait_long(&bars->q_full, part & 1, abort, p.wait_ns);
-          if (ok && n == 0) mbar_arrive(&bars->q_free);
-          if (ok && n > 0) ok = qk(0) && qk(1);
-          // and both streams' PVs of that part, the uses of the W slots
-          if (ok && part > 0)
-            ok = bounded_wait_long(&bars->part_done, (part - 1) & 1, abort, p.wait_ns);
+            for (int s = 0; s < 2; ++s) {
+              if (i >= n[s]) continue;
+              const uint32_t u = base[s] + i, buf = u & 1, half = i & 1;
+              const uint32_t slot = Ring::slot(pair, s, i >> 1);
+              ok = (u < 2 || wait(&bars->pv_done[s][buf], ((u >> 1) - 1) & 1)) &&
+                   (half || wait(&bars->k_full[slot], ring.phase(pair, slot, i >> 1)));
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t a = desc_q + (pair ? s : 0) * (kTileBytes / 16);
+              const uint64_t b = desc_k + slot * (kTileBytes / 16) + half * (kHalf * 128 / 16);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_f8f6f4(tmem + s * 128 + buf * kHalf, a + kk * 2, b + kk * 2, kQk, kk > 0);
+              mma_commit(&bars->s_full[s][buf]);
+              // (stream 0's QKs of a pair's page are issued before stream 1's)
+              if (half && (!pair || s == 1)) mma_commit(&bars->k_free[slot]);
+            }
+          }
+          if (ok) mma_commit(&bars->q_free);
+          ring.advance(pair, n[0] / 2, n[1] / 2);
+          base[0] += n[0], base[1] += n[1];
+          ++part;
+        }
+      } else {
+        constexpr uint32_t kPv = idesc_f16_f32(128, 128, true);
+        const int s = warp - 1;
+        const uint64_t desc_w = smem_desc_sw128(smem_u32(smem + kOffW), kTileBytes / 2, 1024);
+        const uint32_t s_tmem = tmem + s * 128, o_tmem = s_tmem + kColO;
+        uint32_t base = 0;  // own units so far
+        Ring ring;
+        while (ok && walk.next()) {
+          const bool pair = walk.pair();
+          const uint32_t n0 = 2u * walk.stream_pages(0), n1 = 2u * walk.stream_pages(1);
+          const uint32_t n = s ? n1 : n0;
+          // the W slots' uses in the part before, of both streams, are over
+          if (part > 0) ok = wait(&bars->part_done, (part - 1) & 1);
           for (uint32_t i = 0; ok && i < n; ++i) {
             const uint32_t u = base + i, buf = u & 1;
             const uint32_t slot = Ring::slot(pair, s, i);
-            ok = bounded_wait_long(&bars->w_full[slot], w_ring.phase(pair, slot, i), abort,
-                                   p.wait_ns) &&
-                 bounded_wait_long(&bars->p_full[s][buf], (u >> 1) & 1, abort, p.wait_ns);
+            ok = wait(&bars->w_full[slot], ring.phase(pair, slot, i)) &&
+                 wait(&bars->p_full[s][buf], (u >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
             const uint64_t b = desc_w + slot * (kTileBytes / 16);
@@ -920,21 +924,21 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
               mma_f16_ts(o_tmem, s_tmem + buf * kHalf + kk * 8, b + kk * (16 * 128 / 16), kPv,
                          kk > 0 || i > 0);
             mma_commit(&bars->pv_done[s][buf]);
-            free_slot(&bars->w_free[slot]);
-            if (i + 2 < n) ok = qk(i + 2);
+            // both streams free a slot; in a solo part its owner for both
+            mma_commit(&bars->w_free[slot]);
+            if (!pair) mma_commit(&bars->w_free[slot]);
           }
           if (ok) mma_commit(&bars->part_done);
-          k_ring.advance(pair, n0, n1);
-          w_ring.advance(pair, 2 * n0, 2 * n1);
+          ring.advance(pair, n0, n1);
           base += n;
           ++part;
         }
-        if (!ok && !*abort) give_up(bars, p.status);
-        mma_commit(&bars->mma_done[s]);
-        bounded_wait_long(&bars->mma_done[s], 0, nullptr, kWaitLimitNs);
       }
-      __syncwarp();
+      if (!ok && !*abort) give_up(bars, p.status);
+      mma_commit(&bars->mma_done[warp - 1]);
+      bounded_wait_long(&bars->mma_done[warp - 1], 0, nullptr, kWaitLimitNs);
     }
+    __syncwarp();
   }
 
   tc_fence_before();
