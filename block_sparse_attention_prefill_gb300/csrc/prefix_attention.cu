@@ -1282,12 +1282,18 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, void* ws, cudaStream_t 
                  q_map, ap);
   if (e != cudaSuccess) return e;
 
-  // parts of a row, about: of the shared tile or of the own one
+  // Threads of a row in the combine.  Few rows of many parts: a row gets a CTA
+  // (76 parts of 256 rows: 24.7 us in all, with two warps 26.2, with 8 lanes
+  // 39.8); some more rows: two warps (4 parts of 2048 rows: 128.4, with 8 lanes
+  // 130.6, with a CTA 137.3); rows that fill the GPU anyway: 8 lanes (5 parts
+  // of 8192 rows: 341.5, with two warps 353.9, with a CTA 397.1).
   const int64_t tile_rows = std::min<int64_t>(2 * C, a.max_q) * G;
   const int64_t tiles_n =
       a.prefix_pages > 0 ? ceil_div(a.T, 2 * C) : std::min(a.T, ceil_div(a.T, 2 * C) + a.B);
-  const int64_t parts = (int64_t)ctas / (a.Hkv * tiles_n);
-  const int lanes = parts >= 4 ? 32 : 8, team = parts >= 24 ? 8 : parts >= 4 ? 2 : 1;
+  const int64_t parts = (int64_t)ctas / (a.Hkv * tiles_n);  // of a row, about
+  const int64_t all_rows = a.T * a.Hq;
+  const int team = parts >= 24 && all_rows <= 1024 ? 8 : parts >= 3 && all_rows <= 4096 ? 2 : 1;
+  const int lanes = team > 1 ? 32 : 8;
   const int cta_rows = kCombineWarps * 32 / lanes / team;
   const CombineParams cp = {head, tiles + own0, (int)a.T, (int)a.Hq, (int)a.Hkv, G, C, ctas,
                             (int)a.prefix_pages, cta_rows, part_o, part_lse, a.v_scale, a.out, a.lse};
