@@ -290,7 +290,8 @@ kv_cache_kernel(const KvCacheArgs a, const CacheScales sc) {
   const int n = (int)min((int64_t)sc.tokens, a.T - t0);
   const int64_t page_bytes = (int64_t)a.Hkv * (kFp4 ? kFp4PageHead : kPage * 2 * kD);
   // up to kStaged requests: one load brings all lengths into shared memory,
-  // where the search costs no round trip to L2
+  // where the search costs no round trip to L2 (decode step of 64 requests:
+  // 4.0 us, searched in L2 4.7)
   const bool staged = a.B <= kStaged;
   if (staged) {
     for (int i = threadIdx.x; i <= a.B; i += kCacheThreads) {
@@ -426,9 +427,11 @@ template <typename T>
 cudaError_t launch_type(const KvCacheArgs& a, cudaStream_t stream) {
   constexpr int kSlots = kCacheThreads * kVals<T> / (2 * kD);
   const int64_t step = std::max<int64_t>(1, kSlots / a.Hkv);
-  // tokens per CTA: as many as leave four CTAs an SM, up to eight pieces a
-  // thread (decode steps: one)
-  const int64_t rounds = std::min<int64_t>(8, std::max<int64_t>(1, a.T / (step * num_sms() * 4)));
+  // tokens per CTA: as many as make one wave of four CTAs an SM, up to eight
+  // pieces a thread.  512 tokens x 2 heads: one piece 4.0 us, eight 5.5 (few
+  // CTAs); 57 k x 8 heads: eight 60.8 us, four 68, one 208 (the look-ups);
+  // NVFP4, 15 k x 2 heads: one wave 14.8 us, a wave and a half 17.4
+  const int64_t rounds = std::min<int64_t>(8, ceil_div(a.T, step * num_sms() * 4));
   const int64_t tokens = std::min<int64_t>(kMaxTokens, rounds * step);
   CacheScales sc;
   sc.k = recip_of(a.k_scale), sc.v = recip_of(a.v_scale);
@@ -438,6 +441,8 @@ cudaError_t launch_type(const KvCacheArgs& a, cudaStream_t stream) {
   auto on32 = [&](const void* p, int64_t token, int64_t head) {
     return reinterpret_cast<uintptr_t>(p) % 32 == 0 && token * es % 32 == 0 && head * es % 32 == 0;
   };
+  // 32-byte accesses where all rows allow them: NVFP4 read to fp32 31 us, by
+  // 16 bytes 40; 1M tokens to bf16 238 us, by 16 bytes 246
   sc.wide = on32(a.k, a.k_token, a.k_head) && on32(a.v, a.v_token, a.v_head);
   const int64_t grid = ceil_div(a.T, tokens);
   auto run = [&](auto kernel) {

@@ -1256,8 +1256,10 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, void* ws, cudaStream_t 
   const PlanParams pp = {a.cu_q, a.cu_k, (int)a.B, (int)a.T, C, (int)a.prefix_pages, a.max_q,
                          a.max_k, head, tiles, own0, req_tile, a.status};
   cudaError_t e;
-  // decode batches: the plan is made in the attention kernel's prologue (a
-  // launch and about 2 us less)
+  // where the CTA's threads list all tiles in one round the plan is made in
+  // the attention kernel's prologue: a launch less (16 requests over 32k keys:
+  // 24.6 us, with a kernel for the plan 25.8; five chunks of 1 .. 700 tokens:
+  // 111 and 127)
   const bool plan_here =
       a.B <= kThreads && max_tiles(a.B, a.T, C, a.prefix_pages) <= kThreads;
   if (!plan_here) {

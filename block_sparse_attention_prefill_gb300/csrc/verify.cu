@@ -441,7 +441,9 @@ template <typename T>
 cudaError_t launch_verify_type(const VerifyArgs& a, bool greedy, cudaStream_t stream) {
   constexpr int N = 16 / sizeof(T);
   // 16-byte loads where every row starts on 16 bytes; else one value a load
-  // (an odd vocabulary's rows start anywhere)
+  // (an odd vocabulary's rows start anywhere).  Greedy, 64 x 8 bf16 rows of
+  // 131072: 23.5 us, by single values 44; one row of 32000 fp32 drawn from:
+  // 5.3 us and 5.7
   const bool vec = vector_rows<T>(a.target, a.t_req, a.t_row) &&
                    (greedy || !a.draft || vector_rows<T>(a.draft, a.d_req, a.d_row));
   const int seg = (int)(ceil_div(ceil_div(a.V, kCluster), 32 * N) * (32 * N));
