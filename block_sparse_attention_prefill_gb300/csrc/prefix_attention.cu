@@ -103,6 +103,22 @@ __device__ __forceinline__ int64_t part_row(int cta, int h, int tile, int shared
          (int64_t)tok0 * G;
 }
 
+// Where a part's O of a row lies, in floats from its first row's: the rows of
+// a stream go in blocks of 32 (a warp's), a block as 16 chunks of 8 columns,
+// [chunk][row][8], so that a warp's stores of a chunk, and loads of
+// neighbouring rows, are contiguous (rows one after another: 111 us instead of
+// 105 for five chunks of 1 .. 700 tokens, by the cache's tag look-ups).
+struct RowPlace {
+  int first;  // of column 0
+  int chunk;  // from one chunk to the next
+};
+__device__ __forceinline__ RowPlace row_place(int off, int ntok, int C, int G) {
+  const int s0 = ntok > C && off >= C * G ? C * G : 0;
+  const int rows = s0 > 0 ? (ntok - C) * G : (ntok > C ? C : ntok) * G;
+  const int w = off - s0, block = w & ~31;
+  return {(s0 + block) * kD + (w & 31) * 8, min(32, rows - block) * 8};
+}
+
 constexpr int kPlanThreads = 1024;
 
 template <int kThreads>
@@ -289,7 +305,7 @@ struct AttendParams {
   int num_pages;
   int T, G, C, Hkv;
   float score_log2;
-  float* part_o;    // rows of 128 fp32, normalised
+  float* part_o;    // rows of 128 fp32, normalised, as in row_place
   float* part_lse;  // base-2 log-sum-exp of the row's part
   uint32_t* status;
   uint32_t wait_ns;
@@ -620,9 +636,9 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
       }
       if (!ok) break;
       // the part: O / l and log2 of the row's sum
-      const int64_t prow = part_row(blockIdx.x, walk.cur_h, walk.cur_tile, walk.shared_tiles, t.tok0,
-                                    p.T, p.G) +
-                           (pair && s ? p.C * p.G : 0) + row;
+      const int64_t first_row = part_row(blockIdx.x, walk.cur_h, walk.cur_tile, walk.shared_tiles,
+                                         t.tok0, p.T, p.G);
+      const int off_row = (pair && s ? p.C * p.G : 0) + row;
       g0 += walk.p1 - walk.p0;
       if (n > 0 &&
           !all_wait(bars, &bars->pv_done[s][(done - 1) & 1], ((done - 1) >> 1) & 1, p))
@@ -669,6 +685,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
       }
       const float inv = lt == 0.f ? 0.f : 1.f / lt;
       const float fa = wa * inv, fb = wb * inv;
+      const RowPlace place = row_place(off_row, t.ntok, p.C, p.G);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.part_o + first_row * kD) + place.first;
       const int q0 = pair ? 0 : 4 * s, q1 = pair ? 8 : q0 + 4;
 #pragma unroll 1
       for (int q = q0; q < q1; ++q) {
@@ -687,11 +705,10 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
               o[e] = 0x7FFFFFFFu;
         }
         if (valid) {
-          uint32_t* dst = reinterpret_cast<uint32_t*>(p.part_o + prow * kD) + q * 16;
 #pragma unroll
           for (int e = 0; e < 16; e += 8)
-            st_global_v8(dst + e, o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6],
-                         o[e + 7]);
+            st_global_v8(dst + (2 * q + e / 8) * place.chunk, o[e], o[e + 1], o[e + 2], o[e + 3],
+                         o[e + 4], o[e + 5], o[e + 6], o[e + 7]);
         }
       }
       tc_fence_before();
@@ -700,7 +717,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         ++solos;
       }
       if (valid && (pair || s == 0))
-        p.part_lse[prow] = lt == 0.f ? -INFINITY : mt * c - kPShift + log2f(lt);
+        p.part_lse[first_row + off_row] = lt == 0.f ? -INFINITY : mt * c - kPShift + log2f(lt);
     }
   } else if (warp >= 12) {
     setmaxnreg_dec<kRegsWiden>();
@@ -975,23 +992,22 @@ struct CombineParams {
 
 // A CTA takes some rows of a tile of a request's own pages (blockIdx.x) of a
 // KV head (.y): first the parts of that tile and of the shared tiles (two at
-// most) that its tokens lie in are listed, then groups of kLanes lanes merge
-// the parts of a row each, or kTeam groups together: weights 2^(lse - m), fp32
-// sums, eight 16-byte loads in flight per lane.  Rows with few parts go four
-// to a warp, rows with many have a warp or several.  A batch that was refused
-// gives empty rows.
-template <int kLanes, int kTeam>
+// most) that its tokens lie in are listed, then each warp merges the parts of
+// four neighbouring rows, 8 lanes a row, or kTeam warps together: weights
+// 2^(lse - m), fp32 sums, eight or more 16-byte loads in flight per lane.  A
+// batch that was refused gives empty rows.
+template <int kTeam>
 __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const CombineParams p) {
   // per listed tile: its parts' first rows (of the tile's first token and
   // head), in line order
   __shared__ int s_row[3][kMaxParts];
   __shared__ int s_n[3];
   __shared__ Tile s_tile[3];
-  constexpr int kGroups = kCombineWarps * 32 / kLanes;
-  constexpr int kQ = 32 / kLanes;     // float4 of a row per lane
-  constexpr int kFlight = 8 / kQ;     // parts in flight
-  __shared__ float s_acc[kTeam > 1 ? kGroups : 1][kD];
-  __shared__ float s_m[kGroups], s_l[kGroups];
+  constexpr int kLanes = 8;
+  constexpr int kQ = 32 / kLanes;             // float4 of a row per lane
+  constexpr int kFlight = kTeam == 8 ? 8 : 2;  // parts in flight
+  __shared__ float s_acc[kTeam > 1 ? kCombineWarps * 4 : 1][kD];
+  __shared__ float s_m[kCombineWarps * 4], s_l[kCombineWarps * 4];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1056,13 +1072,13 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
     if (lane == 0) s_n[warp] = min(n, kMaxParts);
   }
   __syncthreads();
-  const int group = threadIdx.x / kLanes, sub = threadIdx.x % kLanes;
-  const uint32_t peers = kLanes == 32 ? 0xFFFFFFFFu : ((1u << (kLanes & 31)) - 1u) << (lane - sub);
-  const int member = group % kTeam;
-  constexpr int kRows = kGroups / kTeam;  // rows at a time
+  const int sub = lane % kLanes, in_warp = lane / kLanes;
+  const uint32_t peers = 0xFFu << (lane - sub);
+  const int member = warp % kTeam, slot = warp / kTeam * 4 + in_warp;
+  constexpr int kRows = kCombineWarps / kTeam * 4;  // rows at a time
   for (int r0 = 0; r0 < rows; r0 += kRows) {
-    const int r = row0 + r0 + group / kTeam;
-    const bool live = r0 + group / kTeam < rows;
+    const int r = row0 + r0 + slot;
+    const bool live = r0 + slot < rows;
     const int tok = own.tok0 + (live ? r / p.G : 0);
     float m = -INFINITY, l = 0.f;
     // lane `sub` has columns 4 (kLanes q + sub) .. + 3 of the row
@@ -1078,10 +1094,13 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
         // rows of a pair: C tokens of the first stream, then the second's:
         // the same as token order
         const int off = o * p.G + r % p.G;
-        for (int e0 = member * kLanes; e0 < n; e0 += kTeam * kLanes) {
-          const int e = e0 + sub;
-          const int row = e < n ? s_row[k][e] + off : 0;
-          const float le = e < n ? __ldcg(p.part_lse + row) : -INFINITY;
+        const RowPlace place = row_place(off, s_tile[k].ntok, p.C, p.G);
+        const float* col = p.part_o + place.first + (sub >> 1) * place.chunk + (sub & 1) * 4;
+        // a member's parts are every kTeam-th, 8 of them a round
+        for (int e0 = member; e0 < n; e0 += kTeam * kLanes) {
+          const int e = e0 + kTeam * sub;
+          const int row = e < n ? s_row[k][e] : 0;
+          const float le = e < n ? __ldcg(p.part_lse + row + off) : -INFINITY;
           float top = le;
 #pragma unroll
           for (int d = kLanes / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(peers, top, d));
@@ -1094,7 +1113,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
           }
           // NaN (a NaN score) stays one
           const float w = le == -INFINITY ? 0.f : exp2f(le - (m == -INFINITY ? 0.f : m));
-          const int count = min(kLanes, n - e0);
+          const int count = min(kLanes, (n - e0 + kTeam - 1) / kTeam);
           for (int j = 0; j < count; j += kFlight) {
             float4 v[kFlight][kQ];
             float wj[kFlight];
@@ -1102,11 +1121,12 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
             for (int d = 0; d < kFlight; ++d) {
               wj[d] = __shfl_sync(peers, w, j + d, kLanes);
               const int rj = __shfl_sync(peers, row, j + d, kLanes);
-              const float4* src = reinterpret_cast<const float4*>(p.part_o + (int64_t)rj * kD);
+              const float* src = col + (int64_t)rj * kD;
 #pragma unroll
               for (int q = 0; q < kQ; ++q)
-                v[d][q] = wj[d] != 0.f ? __ldcg(src + q * kLanes + sub)
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[d][q] = wj[d] != 0.f
+                              ? __ldcg(reinterpret_cast<const float4*>(src + 4 * q * place.chunk))
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
             for (int d = 0; d < kFlight; ++d) {
@@ -1124,27 +1144,28 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
       }
     }
     if constexpr (kTeam > 1) {
-      if (sub == 0) s_m[group] = m, s_l[group] = l;
+      const int mine = slot * kTeam + member;
+      if (sub == 0) s_m[mine] = m, s_l[mine] = l;
 #pragma unroll
       for (int q = 0; q < kQ; ++q)
-        *reinterpret_cast<float4*>(&s_acc[group][4 * (q * kLanes + sub)]) = acc[q];
+        *reinterpret_cast<float4*>(&s_acc[mine][4 * (q * kLanes + sub)]) = acc[q];
       __syncthreads();
       if (member == 0 && live) {
         float top = -INFINITY;
-        for (int k = 0; k < kTeam; ++k) top = fmaxf(top, s_m[group + k]);
+        for (int k = 0; k < kTeam; ++k) top = fmaxf(top, s_m[mine + k]);
         l = 0.f;
 #pragma unroll
         for (int q = 0; q < kQ; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < kTeam; ++k) {
-          const float lk = s_l[group + k];
+          const float lk = s_l[mine + k];
           // a member without parts has l = 0; one with a NaN keeps it
           const float f = lk == 0.f ? 0.f
-                          : lk == lk ? exp2f(s_m[group + k] - (top == -INFINITY ? 0.f : top))
+                          : lk == lk ? exp2f(s_m[mine + k] - (top == -INFINITY ? 0.f : top))
                                      : lk;
           l += f * lk;
 #pragma unroll
           for (int q = 0; q < kQ; ++q) {
-            const float4 v = *reinterpret_cast<const float4*>(&s_acc[group + k][4 * (q * kLanes + sub)]);
+            const float4 v = *reinterpret_cast<const float4*>(&s_acc[mine + k][4 * (q * kLanes + sub)]);
             acc[q].x = fmaf(f, v.x, acc[q].x);
             acc[q].y = fmaf(f, v.y, acc[q].y);
             acc[q].z = fmaf(f, v.z, acc[q].z);
@@ -1284,27 +1305,26 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, void* ws, cudaStream_t 
                  q_map, ap);
   if (e != cudaSuccess) return e;
 
-  // Threads of a row in the combine.  Few rows of many parts: a row gets a CTA
-  // (76 parts of 256 rows: 24.7 us in all, with two warps 26.2, with 8 lanes
-  // 39.8); some more rows: two warps (4 parts of 2048 rows: 128.4, with 8 lanes
-  // 130.6, with a CTA 137.3); rows that fill the GPU anyway: 8 lanes (5 parts
-  // of 8192 rows: 341.5, with two warps 353.9, with a CTA 397.1).
+  // Warps that share four rows in the combine, by about how many parts a row
+  // has and how many rows there are.  Many parts of few rows: 8 (76 parts of
+  // 256 rows: 22.0 us in all, with two warps 27.1, with one 40.9).  Some parts
+  // of more rows: 2 (4 parts of 2048 rows: 128.1, with 8 warps 130.5, with one
+  // 134.0).  Two parts of 25 thousand rows: 1 (105, with two warps 168).
   const int64_t tile_rows = std::min<int64_t>(2 * C, a.max_q) * G;
   const int64_t tiles_n =
       a.prefix_pages > 0 ? ceil_div(a.T, 2 * C) : std::min(a.T, ceil_div(a.T, 2 * C) + a.B);
   const int64_t parts = (int64_t)ctas / (a.Hkv * tiles_n);  // of a row, about
   const int64_t all_rows = a.T * a.Hq;
-  const int team = parts >= 24 && all_rows <= 1024 ? 8 : parts >= 3 && all_rows <= 4096 ? 2 : 1;
-  const int lanes = team > 1 ? 32 : 8;
-  const int cta_rows = kCombineWarps * 32 / lanes / team;
+  const int team = parts >= 24 && all_rows <= 4096 ? 8 : parts >= 3 && all_rows <= 16384 ? 2 : 1;
+  const int cta_rows = kCombineWarps / team * 4;
   const CombineParams cp = {head, tiles + own0, (int)a.T, (int)a.Hq, (int)a.Hkv, G, C, ctas,
                             (int)a.prefix_pages, cta_rows, part_o, part_lse, a.v_scale, a.out, a.lse};
   const int64_t own = std::min<int64_t>(a.T, ceil_div(a.T, 2 * C) + a.B);
   const dim3 grid((unsigned)own, (unsigned)a.Hkv, (unsigned)std::max<int64_t>(1, ceil_div(tile_rows, cta_rows)));
   const dim3 block(kCombineWarps * 32);
-  if (team == 8) return launch_pdl(combine_kernel<32, 8>, grid, block, 0, stream, cp);
-  if (team == 2) return launch_pdl(combine_kernel<32, 2>, grid, block, 0, stream, cp);
-  return launch_pdl(combine_kernel<8, 1>, grid, block, 0, stream, cp);
+  if (team == 8) return launch_pdl(combine_kernel<8>, grid, block, 0, stream, cp);
+  if (team == 2) return launch_pdl(combine_kernel<2>, grid, block, 0, stream, cp);
+  return launch_pdl(combine_kernel<1>, grid, block, 0, stream, cp);
 }
 
 }  // namespace msa
