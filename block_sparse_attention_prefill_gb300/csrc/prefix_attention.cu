@@ -469,6 +469,13 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
   }
+  // Where G does not divide 128 no copy writes the last rows of Q.  They give
+  // no output, but a NaN that shared memory held there would have the softmax
+  // move its reference at every unit (94 us became 145).
+  for (int i = p.C * p.G * kD + tid * 16; i < kTileBytes; i += kThreads * 16)
+    for (int s = 0; s < 2; ++s)
+      *reinterpret_cast<uint4*>(smem + kOffQ + s * kTileBytes + i) = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
   pdl_wait();
   pdl_trigger();
   // The workspace's plan: by a kernel of its own, or, while it takes one
