@@ -233,6 +233,7 @@ def test_offsets_beyond_32_bits():
     msa.msa_kv_write(x, 2 * x, pool, 0.01, 0.02, table, cu, cu)
     k, v = msa.msa_kv_read(pool, 0.01, 0.02, table, cu, 130, dtype=torch.float32)
     assert torch.equal(k * 2, v)
+    x = x.clamp(-4.48, 4.48)  # codes saturate at 448: 448 * 0.01; about 0.2 values of |x| > 4.48 are expected among 33280 normal ones
     assert ((k - x).abs() <= x.abs() * 2.0 ** -4 + 0.01 * 2.0 ** -10).all()
     assert not pool[3, :, 2:].any()
 
