@@ -20,8 +20,25 @@
 // end and weighted by pages, are cut into one equal range per CTA, so no
 // CTA waits for a last wave and only tiles that a cut meets are split.
 //
-// Kernels: plan (one CTA: tiles and their place in the line), attend (one
-// persistent CTA per SM), combine.
+// Kernels: plan (one CTA: tiles and their place in the line; of a small batch
+// every attend CTA makes it for itself), attend (one persistent CTA per SM),
+// combine.
+//
+// Attend, by warps: 0 copies pages and Q (TMA), 3 issues the QKs, 1 and 2 the
+// PVs of a stream, 4-7 and 8-11 are a stream's softmax (a row a thread), 12-15
+// widen V.  Tensor memory holds, for each stream, two S of 64 keys (P takes
+// its S's place) and O: all 512 columns.  The unit of 64 keys, not 128, is what
+// lets QK of one unit, softmax of the next and PV run at the same time within
+// a stream.
+//
+// Bounds and what was measured (whole calls): 512 tokens x 16 heads over 128k
+// shared keys 337 us, 1.65 PFLOP/s; QK at twice and PV at the bf16 rate would
+// take 217.  A unit of both streams takes 1440 cycles, of which the tensor
+// pipes are busy 0.6 (ncu), the issue slots 0.58: what is left is the latency
+// of the hops S -> softmax -> P -> PV -> next QK, with all of tensor memory
+// in use.  16 requests of 8 tokens over 80k keys of their own each: 129 us, 678 MB at
+// 5.25 TB/s.  16 single tokens over 32k shared keys: 21.7 us, latency (plan
+// and first loads 4, 6 units 5, epilogue 3, combine 5 us).
 #include <cuda.h>
 
 #include <algorithm>

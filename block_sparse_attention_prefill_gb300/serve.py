@@ -64,12 +64,15 @@ def _handle(stream, dev):
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _new(shape, dtype, like, dev, handle):
-    """A tensor on like's device for use on the stream `handle`, whichever
+_DEVICES = [torch.device("cuda", i) for i in range(64)]
+
+
+def _new(shape, dtype, dev, handle):
+    """A tensor on device `dev` for use on the stream `handle`, whichever
     stream is current."""
-    t = like.new_empty(shape, dtype=dtype)
+    t = torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
     if handle != torch._C._cuda_getCurrentRawStream(dev):
-        t.record_stream(torch.cuda.ExternalStream(handle, device=like.device))
+        t.record_stream(torch.cuda.ExternalStream(handle, device=t.device))
     return t
 
 
@@ -180,8 +183,8 @@ def _read(name, fp4, kv, k_scale, v_scale, block_table, cu, T, starts, dtype, k,
     if k is None:
         if dtype not in _TYPES:
             _fail("dtype must be one of %s", tuple(_TYPES))
-        k = _new((T, Hkv, HEAD_DIM), dtype, kv, dev, handle)
-        v = _new((T, Hkv, HEAD_DIM), dtype, kv, dev, handle)
+        k = _new((T, Hkv, HEAD_DIM), dtype, dev, handle)
+        v = _new((T, Hkv, HEAD_DIM), dtype, dev, handle)
     shape = (T, Hkv, HEAD_DIM)
     ks, vs = _rows(k, "k", shape), _rows(v, "v", shape)
     if k.dtype != v.dtype:
@@ -255,11 +258,11 @@ def msa_prefix_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_
     dev = _place(q, kv, block_table, cu_seqlens_q, cu_seqlens_k, workspace, out, lse, status)
     handle = _handle(stream, dev)
     if workspace is None:
-        workspace = _new(need, torch.uint8, q, dev, handle)
+        workspace = _new(need, torch.uint8, dev, handle)
     if out is None:
-        out = _new((T, Hq, HEAD_DIM), torch.bfloat16, q, dev, handle)
+        out = _new((T, Hq, HEAD_DIM), torch.bfloat16, dev, handle)
     if lse is None and want_lse:
-        lse = _new((T, Hq), torch.float32, q, dev, handle)
+        lse = _new((T, Hq), torch.float32, dev, handle)
     _check(load().msa_prefix_attention(
         q.data_ptr(), kv.data_ptr(), pages, q_scale, k_scale, v_scale, softmax_scale,
         block_table.data_ptr(), width, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, T, Hq,
@@ -299,11 +302,11 @@ def _verify(name, target, drafts, uniforms, draft_probs, counts, tokens, accepte
     dev = _place(target, drafts, uniforms, draft_probs, counts, tokens, accepted)
     handle = _handle(stream, dev)
     if tokens is None:
-        tokens = _new((B, n), torch.int32, drafts, dev, handle)
+        tokens = _new((B, n), torch.int32, dev, handle)
     else:
         _tensor(tokens, "tokens", _I32, (B, n))
     if accepted is None:
-        accepted = _new((B,), torch.int32, drafts, dev, handle)
+        accepted = _new((B,), torch.int32, dev, handle)
     else:
         _tensor(accepted, "accepted", _I32, (B,))
     if greedy:

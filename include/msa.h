@@ -563,7 +563,9 @@ MSA_API int msa_kv_read_nvfp4(const uint8_t *kv4, int64_t num_pages, float k_sca
  * exact attention for all practical purposes.  A NaN among the K of a key a
  * row attends to makes the row NaN, one among its V that column; codes behind
  * a request's end, or behind a row's position, have no effect on the row.
- * Hq / Hkv in 1 .. 128.  Three kernels on `stream`, no host synchronisation.
+ * Scores have to be finite: q_scale * k_scale * softmax_scale below about
+ * 9e30.  Hq / Hkv in 1 .. 128.  Two kernels on `stream` (three where the
+ * batch has more than 512 requests or tiles), no host synchronisation.
  */
 MSA_API int msa_prefix_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv,
                                          int64_t prefix_pages, int64_t max_seqlen_q,
