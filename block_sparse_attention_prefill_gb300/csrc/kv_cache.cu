@@ -429,8 +429,8 @@ cudaError_t launch_type(const KvCacheArgs& a, cudaStream_t stream) {
   const int64_t step = std::max<int64_t>(1, kSlots / a.Hkv);
   // tokens per CTA: as many as make one wave of four CTAs an SM, up to eight
   // pieces a thread.  512 tokens x 2 heads: one piece 4.0 us, eight 5.5 (few
-  // CTAs); 57 k x 8 heads: eight 60.8 us, four 68, one 208 (the look-ups);
-  // NVFP4, 15 k x 2 heads: one wave 14.8 us, a wave and a half 17.4
+  // CTAs); 59 k x 8 heads: eight 60.8 us, four 68, one 208 (the look-ups);
+  // NVFP4, 17 k x 2 heads: one wave 14.8 us, a wave and a half 17.4
   const int64_t rounds = std::min<int64_t>(8, ceil_div(a.T, step * num_sms() * 4));
   const int64_t tokens = std::min<int64_t>(kMaxTokens, rounds * step);
   CacheScales sc;
