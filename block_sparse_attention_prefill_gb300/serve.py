@@ -5,6 +5,10 @@ Argument marshalling only, as in the package's ``__init__`` (whose public
 names these are); ``include/msa.h`` has each call's meaning.  These calls
 check every shape, type, stride and device here, because the library sees
 only pointers; tensors have to be on the current device.
+
+A decode step waits for these checks, so each call first looks whether all of
+them hold in one expression (about half the time of the checks one by one),
+and goes through them one by one, with their messages, only where not.
 """
 from __future__ import annotations
 
@@ -15,11 +19,16 @@ import torch
 from . import (DTYPE_BF16, DTYPE_F16, DTYPE_F32, HEAD_DIM, MsaError, NVFP4_SLOT_BYTES, PAGE_SIZE,
                load, status_string)
 
+# What the checks below raise on a sound call's shortcut for what is not a
+# tensor or has other dimensions.
+_NOT_SOUND = (AttributeError, TypeError, ValueError)
+
 _TYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
 _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 _I32 = (torch.int32,)
 _F32 = (torch.float32,)
 _WORD = (torch.int32, torch.uint32)
+_PAGE, _PAGE4 = (PAGE_SIZE, 2 * HEAD_DIM), (2, NVFP4_SLOT_BYTES)
 
 
 def _fail(what, *args):
@@ -125,24 +134,46 @@ def _status(status):
         _tensor(status, "status", _WORD, (1,))
 
 
-def _write(name, fp4, k, v, kv, k_scale, v_scale, block_table, cu_q, cu_k, status, stream):
-    pages, Hkv = _pool(kv, fp4)
+def _check_write(fp4, k, v, kv, block_table, cu_q, cu_k, status):
+    _, Hkv = _pool(kv, fp4)
     B = _requests(cu_q, "cu_seqlens_q")
     _tensor(cu_k, "cu_seqlens_k", _I32, (B + 1,))
-    width = _table(block_table, B)
+    _table(block_table, B)
     if k is None or v is None or k.dim() != 3:
         _fail("k and v must be [T, Hkv, 128]")
-    T = k.shape[0]
-    shape = (T, Hkv, HEAD_DIM)
-    ks, vs = _rows(k, "k", shape), _rows(v, "v", shape)
+    shape = (k.shape[0], Hkv, HEAD_DIM)
+    _rows(k, "k", shape), _rows(v, "v", shape)
     if k.dtype != v.dtype:
         _fail("k and v have different dtypes: %s and %s", k.dtype, v.dtype)
     _status(status)
-    dev = _place(kv, k, v, block_table, cu_q, cu_k, status)
-    _check(getattr(load(), name)(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
-                                 _TYPES[k.dtype], kv.data_ptr(), pages, k_scale, v_scale,
-                                 block_table.data_ptr(), width, cu_q.data_ptr(), cu_k.data_ptr(),
-                                 B, T, Hkv, _ptr(status), _handle(stream, dev)), name)
+    _place(kv, k, v, block_table, cu_q, cu_k, status)
+
+
+def _write(name, fp4, k, v, kv, k_scale, v_scale, block_table, cu_q, cu_k, status, stream):
+    try:
+        shape, pool, table = k.shape, kv.shape, block_table.shape
+        ks, vs = k.stride(), v.stride()
+        dev = kv.get_device()
+        sound = (
+            (kv.dtype is torch.uint8 or (kv.dtype in _E4M3 and not fp4))
+            and pool[2:] == (_PAGE4 if fp4 else _PAGE) and shape[1:] == (pool[1], HEAD_DIM)
+            and len(table) == 2 and cu_q.shape == cu_k.shape == (table[0] + 1,)
+            and v.shape == shape and ks[2] == 1 == vs[2] and k.dtype is v.dtype
+            and k.dtype in _TYPES and cu_q.dtype is cu_k.dtype is block_table.dtype is torch.int32
+            and kv.is_contiguous() and block_table.is_contiguous() and cu_q.is_contiguous()
+            and cu_k.is_contiguous() and status is None and dev >= 0
+            and dev == k.get_device() == v.get_device() == block_table.get_device()
+            == cu_q.get_device() == cu_k.get_device() == torch._C._cuda_getDevice())
+    except _NOT_SOUND:
+        sound = False
+    if not sound:
+        _check_write(fp4, k, v, kv, block_table, cu_q, cu_k, status)
+    rc = getattr(load(), name)(
+        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _TYPES[k.dtype], kv.data_ptr(),
+        pool[0], k_scale, v_scale, block_table.data_ptr(), table[1], cu_q.data_ptr(),
+        cu_k.data_ptr(), table[0], shape[0], pool[1], _ptr(status), _handle(stream, dev))
+    if rc:
+        _check(rc, name)
 
 
 def msa_kv_write(k, v, kv, k_scale, v_scale, block_table, cu_seqlens_q, cu_seqlens_k,
@@ -165,36 +196,59 @@ def msa_kv_write_nvfp4(k, v, kv4, k_scale, v_scale, block_table, cu_seqlens_q, c
            cu_seqlens_k, status, stream)
 
 
-def _read(name, fp4, kv, k_scale, v_scale, block_table, cu, T, starts, dtype, k, v, status,
-          stream):
-    pages, Hkv = _pool(kv, fp4)
+def _check_read(fp4, kv, block_table, cu, starts, k, v, status):
+    _pool(kv, fp4)
     B = _requests(cu, "cu_tokens")
-    width = _table(block_table, B)
+    _table(block_table, B)
     if starts is not None:
         _tensor(starts, "starts", _I32, (B,))
     _status(status)
-    dev = _place(kv, block_table, cu, starts, k, v, status)
+    _place(kv, block_table, cu, starts, k, v, status)
+
+
+def _read(name, fp4, kv, k_scale, v_scale, block_table, cu, T, starts, dtype, k, v, status,
+          stream):
+    try:
+        pool, table = kv.shape, block_table.shape
+        dev = kv.get_device()
+        sound = (
+            (kv.dtype is torch.uint8 or (kv.dtype in _E4M3 and not fp4))
+            and pool[2:] == (_PAGE4 if fp4 else _PAGE)
+            and len(table) == 2 and cu.shape == (table[0] + 1,)
+            and cu.dtype is block_table.dtype is torch.int32
+            and kv.is_contiguous() and block_table.is_contiguous() and cu.is_contiguous()
+            and (starts is None or (starts.dtype is torch.int32 and starts.shape == (table[0],)
+                                    and starts.is_contiguous() and starts.get_device() == dev))
+            and k is None and v is None and status is None and dev >= 0
+            and dev == block_table.get_device() == cu.get_device() == torch._C._cuda_getDevice())
+    except _NOT_SOUND:
+        sound = False
+    if not sound:
+        _check_read(fp4, kv, block_table, cu, starts, k, v, status)
     handle = _handle(stream, dev)
     T = int(T)
     if T < 0:
         _fail("total_tokens must not be negative")
     if (k is None) != (v is None):
         _fail("give both of k and v, or neither")
+    shape = (T, pool[1], HEAD_DIM)
     if k is None:
         if dtype not in _TYPES:
             _fail("dtype must be one of %s", tuple(_TYPES))
-        k = _new((T, Hkv, HEAD_DIM), dtype, dev, handle)
-        v = _new((T, Hkv, HEAD_DIM), dtype, dev, handle)
-    shape = (T, Hkv, HEAD_DIM)
-    ks, vs = _rows(k, "k", shape), _rows(v, "v", shape)
-    if k.dtype != v.dtype:
-        _fail("k and v have different dtypes: %s and %s", k.dtype, v.dtype)
-    if (T > 1 and 0 in (ks[0], vs[0])) or (Hkv > 1 and 0 in (ks[1], vs[1])):
-        _fail("rows of k and v must not overlap")
-    _check(getattr(load(), name)(kv.data_ptr(), pages, k_scale, v_scale, block_table.data_ptr(),
-                                 width, cu.data_ptr(), _ptr(starts), B, T, Hkv, k.data_ptr(),
-                                 ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _TYPES[k.dtype],
-                                 _ptr(status), handle), name)
+        k, v = _new(shape, dtype, dev, handle), _new(shape, dtype, dev, handle)
+        ks = vs = (pool[1] * HEAD_DIM, HEAD_DIM)
+    else:
+        ks, vs = _rows(k, "k", shape), _rows(v, "v", shape)
+        if k.dtype != v.dtype:
+            _fail("k and v have different dtypes: %s and %s", k.dtype, v.dtype)
+        if (T > 1 and 0 in (ks[0], vs[0])) or (pool[1] > 1 and 0 in (ks[1], vs[1])):
+            _fail("rows of k and v must not overlap")
+    rc = getattr(load(), name)(kv.data_ptr(), pool[0], k_scale, v_scale, block_table.data_ptr(),
+                               table[1], cu.data_ptr(), _ptr(starts), table[0], T, pool[1],
+                               k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+                               _TYPES[k.dtype], _ptr(status), handle)
+    if rc:
+        _check(rc, name)
     return k, v
 
 
@@ -226,6 +280,23 @@ def prefix_attention_workspace_bytes(B, T, Hq, Hkv, prefix_pages, max_seqlen_q,
     return n.value
 
 
+def _check_attention(q, kv, block_table, cu_q, cu_k, workspace, out, lse, status):
+    _pool(kv, False)
+    _tensor(q, "q", _E4M3)
+    if q.dim() != 3 or q.shape[2] != HEAD_DIM:
+        _fail("q must be [any, any, 128], got %s", tuple(q.shape))
+    B = _requests(cu_q, "cu_seqlens_q")
+    _tensor(cu_k, "cu_seqlens_k", _I32, (B + 1,))
+    _table(block_table, B)
+    _status(status)
+    if out is not None:
+        _tensor(out, "out", (torch.bfloat16,), tuple(q.shape))
+    if lse is not None:
+        _tensor(lse, "lse", _F32, tuple(q.shape[:2]))
+    if workspace is not None:
+        _tensor(workspace, "workspace", (torch.uint8,))
+
+
 def msa_prefix_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_table,
                          cu_seqlens_q, cu_seqlens_k, prefix_pages, max_seqlen_q, max_seqlen_k,
                          workspace=None, out=None, lse=None, want_lse=True, status=None,
@@ -236,26 +307,30 @@ def msa_prefix_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_
     queries behind the shared pages.  status: an int32 [1] tensor that
     MSA_STATUS_* bits are OR-ed into.  Returns (out bf16 [T, Hq, 128], lse
     fp32 [T, Hq] or None)."""
-    pages, Hkv = _pool(kv, False)
-    _tensor(q, "q", _E4M3)
-    if q.dim() != 3 or q.shape[2] != HEAD_DIM:
-        _fail("q must be [any, any, 128], got %s", tuple(q.shape))
-    T, Hq, _ = q.shape
-    B = _requests(cu_seqlens_q, "cu_seqlens_q")
-    _tensor(cu_seqlens_k, "cu_seqlens_k", _I32, (B + 1,))
-    width = _table(block_table, B)
-    _status(status)
-    if out is not None:
-        _tensor(out, "out", (torch.bfloat16,), (T, Hq, HEAD_DIM))
-    if lse is not None:
-        _tensor(lse, "lse", _F32, (T, Hq))
+    try:
+        pool, table, (T, Hq, dim) = kv.shape, block_table.shape, q.shape
+        dev = kv.get_device()
+        sound = (
+            kv.dtype in _E4M3 and q.dtype in _E4M3 and pool[2:] == _PAGE and dim == HEAD_DIM
+            and len(table) == 2 and cu_seqlens_q.shape == cu_seqlens_k.shape == (table[0] + 1,)
+            and cu_seqlens_q.dtype is cu_seqlens_k.dtype is block_table.dtype is torch.int32
+            and kv.is_contiguous() and q.is_contiguous() and block_table.is_contiguous()
+            and cu_seqlens_q.is_contiguous() and cu_seqlens_k.is_contiguous()
+            and out is None and lse is None and workspace is None and status is None and dev >= 0
+            and dev == q.get_device() == block_table.get_device() == cu_seqlens_q.get_device()
+            == cu_seqlens_k.get_device() == torch._C._cuda_getDevice())
+    except _NOT_SOUND:
+        sound = False
+    if not sound:
+        _check_attention(q, kv, block_table, cu_seqlens_q, cu_seqlens_k, workspace, out, lse,
+                         status)
+    B, Hkv = table[0], pool[1]
     need = prefix_attention_workspace_bytes(B, T, Hq, Hkv, prefix_pages, max_seqlen_q,
                                             max_seqlen_k)
-    if workspace is not None:
-        _tensor(workspace, "workspace", (torch.uint8,))
-        if workspace.numel() < need:
-            _fail("workspace too small: %d < %d bytes", workspace.numel(), need)
-    dev = _place(q, kv, block_table, cu_seqlens_q, cu_seqlens_k, workspace, out, lse, status)
+    if workspace is not None and workspace.numel() < need:
+        _fail("workspace too small: %d < %d bytes", workspace.numel(), need)
+    if not sound:
+        _place(q, kv, block_table, cu_seqlens_q, cu_seqlens_k, workspace, out, lse, status)
     handle = _handle(stream, dev)
     if workspace is None:
         workspace = _new(need, torch.uint8, dev, handle)
@@ -263,57 +338,82 @@ def msa_prefix_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_
         out = _new((T, Hq, HEAD_DIM), torch.bfloat16, dev, handle)
     if lse is None and want_lse:
         lse = _new((T, Hq), torch.float32, dev, handle)
-    _check(load().msa_prefix_attention(
-        q.data_ptr(), kv.data_ptr(), pages, q_scale, k_scale, v_scale, softmax_scale,
-        block_table.data_ptr(), width, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, T, Hq,
-        Hkv, prefix_pages, max_seqlen_q, max_seqlen_k, workspace.data_ptr(), workspace.numel(),
-        out.data_ptr(), _ptr(lse), _ptr(status), handle), "msa_prefix_attention")
+    rc = load().msa_prefix_attention(
+        q.data_ptr(), kv.data_ptr(), pool[0], q_scale, k_scale, v_scale, softmax_scale,
+        block_table.data_ptr(), table[1], cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, T,
+        Hq, Hkv, prefix_pages, max_seqlen_q, max_seqlen_k, workspace.data_ptr(),
+        workspace.numel(), out.data_ptr(), _ptr(lse), _ptr(status), handle)
+    if rc:
+        _check(rc, "msa_prefix_attention")
     return out, lse
 
 
 def _probs(t, name, dtypes):
-    """Shape and strides of rows [B, n, V] whose values are contiguous."""
+    """Shape of rows [B, n, V] whose values are contiguous."""
     _tensor(t, name, dtypes, None, False)
-    shape, strides = t.shape, t.stride()
+    shape = t.shape
     if len(shape) != 3:
         _fail("%s must be [any, any, any], got %s", name, tuple(shape))
-    if strides[2] != 1 and shape[2] > 1:
+    if t.stride(2) != 1 and shape[2] > 1:
         _fail("%s's rows must be contiguous", name)
-    return shape, strides
+    return shape
 
 
-def _verify(name, target, drafts, uniforms, draft_probs, counts, tokens, accepted, stream):
-    greedy = name == "msa_verify_greedy"
-    (B, n, V), (t_req, t_row, _) = _probs(target, "target", _TYPES)
+def _check_verify(greedy, target, drafts, uniforms, draft_probs, counts, tokens, accepted):
+    B, n, V = _probs(target, "target", _TYPES)
     if n < 1:
         _fail("target must have at least one row a request")
     _tensor(drafts, "draft_tokens", _I32, (B, n - 1))
     if not greedy:
         _tensor(uniforms, "uniforms", _F32, (B, n))
-    d_ptr, d_req, d_row = None, 0, 0
     if draft_probs is not None:
-        shape, strides = _probs(draft_probs, "draft_probs", (target.dtype,))
+        shape = _probs(draft_probs, "draft_probs", (target.dtype,))
         if shape != (B, n - 1, V):
             _fail("draft_probs must be %s, got %s", [B, n - 1, V], tuple(shape))
-        if n > 1:
-            d_ptr, d_req, d_row = draft_probs.data_ptr(), strides[0], strides[1]
     if counts is not None:
         _tensor(counts, "num_drafts", _I32, (B,))
-    dev = _place(target, drafts, uniforms, draft_probs, counts, tokens, accepted)
+    if tokens is not None:
+        _tensor(tokens, "tokens", _I32, (B, n))
+    if accepted is not None:
+        _tensor(accepted, "accepted", _I32, (B,))
+    _place(target, drafts, uniforms, draft_probs, counts, tokens, accepted)
+
+
+def _verify(name, target, drafts, uniforms, draft_probs, counts, tokens, accepted, stream):
+    greedy = name == "msa_verify_greedy"
+    try:
+        (B, n, V), (t_req, t_row, one) = target.shape, target.stride()
+        dev = target.get_device()
+        sound = (
+            one == 1 and n > 0 and target.dtype in _TYPES and drafts.shape == (B, n - 1)
+            and drafts.dtype is torch.int32 and drafts.is_contiguous()
+            and (greedy or (uniforms.shape == (B, n) and uniforms.dtype is torch.float32
+                            and uniforms.is_contiguous() and uniforms.get_device() == dev))
+            and (draft_probs is None
+                 or (draft_probs.shape == (B, n - 1, V) and draft_probs.dtype is target.dtype
+                     and draft_probs.stride(2) == 1 and draft_probs.get_device() == dev))
+            and (counts is None or (counts.shape == (B,) and counts.dtype is torch.int32
+                                    and counts.is_contiguous() and counts.get_device() == dev))
+            and tokens is None and accepted is None and dev >= 0
+            and dev == drafts.get_device() == torch._C._cuda_getDevice())
+    except _NOT_SOUND:
+        sound = False
+    if not sound:
+        _check_verify(greedy, target, drafts, uniforms, draft_probs, counts, tokens, accepted)
     handle = _handle(stream, dev)
     if tokens is None:
         tokens = _new((B, n), torch.int32, dev, handle)
-    else:
-        _tensor(tokens, "tokens", _I32, (B, n))
     if accepted is None:
         accepted = _new((B,), torch.int32, dev, handle)
-    else:
-        _tensor(accepted, "accepted", _I32, (B,))
     if greedy:
         rc = load().msa_verify_greedy(target.data_ptr(), t_req, t_row, _TYPES[target.dtype],
                                       drafts.data_ptr(), _ptr(counts), B, n, V,
                                       tokens.data_ptr(), accepted.data_ptr(), handle)
     else:
+        d_ptr, d_req, d_row = None, 0, 0
+        if draft_probs is not None and n > 1:
+            d_ptr = draft_probs.data_ptr()
+            d_req, d_row, _ = draft_probs.stride()
         rc = load().msa_verify(target.data_ptr(), t_req, t_row, d_ptr, d_req, d_row,
                                _TYPES[target.dtype], drafts.data_ptr(), uniforms.data_ptr(),
                                _ptr(counts), B, n, V, tokens.data_ptr(), accepted.data_ptr(),
