@@ -266,6 +266,28 @@ def test_graph_streams_and_repeats():
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
+def test_more_tiles_than_a_plan_round():
+    # 128 query heads a KV head: 2 tokens a tile, 550 own and 550 shared tiles
+    w = _batch(128, 1, [700, 400], [700, 450], 1, seed=14)
+    out, lse, status = _run(w)
+    assert status == 0
+    _compare(w, (out, lse))
+
+
+def test_pages_beyond_32_bits_and_an_unaligned_output():
+    w = _batch(16, 2, [8, 3], [300, 200], 3, seed=15)
+    want = _run(w)
+    n, high = w["kv"].shape[0], 70000  # 4.6 GB
+    pool = torch.empty((high, 2, 128, 256), dtype=torch.uint8, device="cuda")
+    pool[high - n:] = w["kv"].view(torch.uint8)
+    table = torch.where(w["table"] >= 0, w["table"] + high - n, w["table"])
+    room = torch.zeros(11 * 16 * 128 + 8, dtype=torch.bfloat16, device="cuda")
+    out = room[4:-4].view(11, 16, 128)  # on 8 bytes
+    got = _run(dict(w, kv=pool.view(torch.float8_e4m3fn), table=table), out=out)
+    assert got[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert not room[:4].any() and not room[-4:].any()
+
+
 def test_short_wait_limit_expires_and_the_next_call_is_clean():
     # a limit below a page load's latency: a wait runs out, the call returns
     # with the status bit, and the next one on the same workspace is exact
