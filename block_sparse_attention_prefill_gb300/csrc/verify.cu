@@ -21,12 +21,16 @@
 // holds the threshold reads its own few hundred weights once more (from L2)
 // to place it.  Bound: HBM for large batches, else the latency of the
 // dependent steps (gather, row, cluster barrier, placing).
+// Measured: 64 requests, 200003 fp32 values a row 25 us, 102 MB at 4.1 TB/s;
+// one request of 32000 5.3 us.
 //
 // Greedy: draft i stands iff it is the first of the largest values of its
 // row.  The same cluster scans the request's rows in order, each CTA its
 // eighth, each warp by itself; a warp that has seen a draft beaten tells all
 // CTAs (a minimum in their shared memory, no barrier), and rows behind it
 // are left out: they cannot matter.
+// Measured: 64 requests of 8 rows of 131072 bf16 values, drafts that fall
+// anywhere: 23.5 us (5.7 TB/s counting every row; two thirds of them are read).
 #include <algorithm>
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>

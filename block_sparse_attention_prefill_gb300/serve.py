@@ -13,6 +13,7 @@ and goes through them one by one, with their messages, only where not.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -280,6 +281,13 @@ def prefix_attention_workspace_bytes(B, T, Hq, Hkv, prefix_pages, max_seqlen_q,
     return n.value
 
 
+@functools.lru_cache(maxsize=64)
+def _attention_bytes(dev, B, T, Hq, Hkv, prefix_pages, max_q, max_k):
+    """The same; the size depends on these numbers and the device alone, and a
+    decode loop asks for the same one again and again."""
+    return prefix_attention_workspace_bytes(B, T, Hq, Hkv, prefix_pages, max_q, max_k)
+
+
 def _check_attention(q, kv, block_table, cu_q, cu_k, workspace, out, lse, status):
     _pool(kv, False)
     _tensor(q, "q", _E4M3)
@@ -325,8 +333,7 @@ def msa_prefix_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_
         _check_attention(q, kv, block_table, cu_seqlens_q, cu_seqlens_k, workspace, out, lse,
                          status)
     B, Hkv = table[0], pool[1]
-    need = prefix_attention_workspace_bytes(B, T, Hq, Hkv, prefix_pages, max_seqlen_q,
-                                            max_seqlen_k)
+    need = _attention_bytes(dev, B, T, Hq, Hkv, prefix_pages, max_seqlen_q, max_seqlen_k)
     if workspace is not None and workspace.numel() < need:
         _fail("workspace too small: %d < %d bytes", workspace.numel(), need)
     if not sound:
