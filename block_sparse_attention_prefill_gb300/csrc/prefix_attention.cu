@@ -13,8 +13,8 @@
 // Work.  Rows are (token, query head of one KV head).  A tile is up to 2 C
 // tokens, C = floor(128 / G), with a range of pages: the shared pages for
 // tiles over the whole batch's tokens (they lie before every query: no mask),
-// a request's own pages for tiles over its tokens.  Both are the same kind
-// of work.  A tile of more than C tokens is two 128-row halves that share
+// a request's own pages for tiles over its tokens (and the shared pages with
+// them where that costs less).  Both are the same kind of work.  A tile of more than C tokens is two 128-row halves that share
 // every page (pair); a smaller one has its pages dealt in turn to the two
 // streams, each with its own O (solo).  The tiles of all heads, laid end to
 // end and weighted by pages, are cut into one equal range per CTA, so no
@@ -97,6 +97,11 @@ __device__ __forceinline__ int tile_rate(int ntok, int C) { return ntok > C ? kC
 __device__ __forceinline__ int tile_cost(int ntok, int npages, int C) {
   return npages * tile_rate(ntok, C) + kCostTile;
 }
+// Cost of a page for all tiles of `tokens` consecutive tokens.
+__device__ __forceinline__ int rate_of(int tokens, int C) {
+  const int rest = tokens % (2 * C);
+  return tokens / (2 * C) * kCostPair + (rest > C ? kCostPair : rest > 0 ? kCostSolo : 0);
+}
 // Pages of a tile in front of cost y of its own.
 __device__ __forceinline__ int pages_before(int64_t y, int npages, int rate) {
   if (y <= kCostTile) return 0;
@@ -124,7 +129,8 @@ __device__ __forceinline__ int64_t part_row(int cta, int h, int tile, int shared
 // a stream go in blocks of 32 (a warp's), a block as 16 chunks of 8 columns,
 // [chunk][row][8], so that a warp's stores of a chunk, and loads of
 // neighbouring rows, are contiguous (rows one after another: 111 us instead of
-// 105 for five chunks of 1 .. 700 tokens, by the cache's tag look-ups).
+// 105, before the plan's last change, for five chunks of 1 .. 700 tokens, by
+// the cache's tag look-ups).
 struct RowPlace {
   int first;  // of column 0
   int chunk;  // from one chunk to the next
@@ -185,9 +191,9 @@ struct PlanParams {
 // B ints that it can see.  Every thread gets the plan's head.
 template <int kThreads>
 __device__ __forceinline__ PlanHead make_plan(const PlanParams& p, int* req) {
-  __shared__ int s_bad, s_first;
+  __shared__ int s_bad, s_first, s_rate;
   const int tid = threadIdx.x;
-  if (tid == 0) s_bad = 0, s_first = INT_MAX;
+  if (tid == 0) s_bad = 0, s_first = INT_MAX, s_rate = 0;
   __syncthreads();
   const int T = p.cu_q[p.B];
   bool bad = p.cu_q[0] != 0 || T < 0 || T > p.T;
@@ -201,8 +207,11 @@ __device__ __forceinline__ PlanHead make_plan(const PlanParams& p, int* req) {
       if (q < 0 || k < q || q > p.max_q || k > p.max_k ||
           (q > 0 && k - q < (int64_t)p.prefix * kPage))
         bad = true;
-      else if (q > 0)
-        n = (int)((q + 2 * p.C - 1) / (2 * p.C)), atomicMin(&s_first, b);
+      else if (q > 0) {
+        n = (int)((q + 2 * p.C - 1) / (2 * p.C));
+        atomicMin(&s_first, b);
+        atomicAdd(&s_rate, rate_of((int)q, p.C));
+      }
     }
     int total;
     const int before = block_excl_scan<kThreads>(n, &total);
@@ -219,7 +228,13 @@ __device__ __forceinline__ PlanHead make_plan(const PlanParams& p, int* req) {
     }
     return hd;
   }
-  const int shared_tiles = p.prefix > 0 ? (T + 2 * p.C - 1) / (2 * p.C) : 0;
+  // The shared pages as tiles of their own, or as part of each request's own
+  // tiles (one request, chunks that fill tiles, a page or two): what costs less
+  // (five chunks of 1 .. 700 tokens: 106.5 us and 102).
+  int shared_tiles = p.prefix > 0 ? (T + 2 * p.C - 1) / (2 * p.C) : 0;
+  if ((int64_t)p.prefix * (s_rate - rate_of(T, p.C)) <= (int64_t)shared_tiles * kCostTile)
+    shared_tiles = 0;
+  const int prefix = shared_tiles > 0 ? p.prefix : 0;
   const int ntiles = shared_tiles + run;
   int cost = 0;
   for (int i0 = 0; i0 < ntiles; i0 += kThreads) {
@@ -232,9 +247,9 @@ __device__ __forceinline__ PlanHead make_plan(const PlanParams& p, int* req) {
         t.tok0 = i * 2 * p.C;
         t.ntok = min(2 * p.C, T - t.tok0);
         t.page0 = 0;
-        t.npages = p.prefix;
+        t.npages = prefix;
         t.pos0 = kNoMask;
-        t.seq = p.prefix * kPage;
+        t.seq = prefix * kPage;
       } else {
         int lo = 0, hi = p.B - 1;  // the last request with req[b] <= i
         while (lo < hi) {
@@ -246,9 +261,9 @@ __device__ __forceinline__ PlanHead make_plan(const PlanParams& p, int* req) {
         t.b = lo;
         t.tok0 = p.cu_q[lo] + o;
         t.ntok = min(2 * p.C, q - o);
-        t.page0 = p.prefix;
+        t.page0 = prefix;
         t.pos0 = k - q + o;
-        t.npages = (t.pos0 + t.ntok - 1) / kPage + 1 - p.prefix;
+        t.npages = (t.pos0 + t.ntok - 1) / kPage + 1 - prefix;
         t.seq = k;
       }
       c = tile_cost(t.ntok, t.npages, p.C);

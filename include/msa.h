@@ -546,8 +546,10 @@ MSA_API int msa_kv_read_nvfp4(const uint8_t *kv4, int64_t num_pages, float k_sca
  *                 last q_len_b of its seq_len_b positions
  *   prefix_pages  shared pages: the first prefix_pages entries of every
  *                 request's block_table row are the same, and its queries lie
- *                 behind them (seq_len - q_len >= 128 * prefix_pages); the
- *                 row of the first request with query tokens is read
+ *                 behind them (seq_len - q_len >= 128 * prefix_pages); they
+ *                 are read through the rows of any requests with query
+ *                 tokens: once for all of them, or by each where that is
+ *                 less work (one request, long chunks, a page or two)
  *   max_seqlen_q, max_seqlen_k  host-known bounds, max_seqlen_k <= 2^30
  *   workspace     msa_prefix_attention_workspace_bytes() bytes, 256-byte
  *                 aligned; calls whose work may overlap need one each
