@@ -14,11 +14,12 @@
 // tokens, C = floor(128 / G), with a range of pages: the shared pages for
 // tiles over the whole batch's tokens (they lie before every query: no mask),
 // a request's own pages for tiles over its tokens (and the shared pages with
-// them where that costs less).  Both are the same kind of work.  A tile of more than C tokens is two 128-row halves that share
-// every page (pair); a smaller one has its pages dealt in turn to the two
-// streams, each with its own O (solo).  The tiles of all heads, laid end to
-// end and weighted by pages, are cut into one equal range per CTA, so no
-// CTA waits for a last wave and only tiles that a cut meets are split.
+// them where that costs less).  Both are the same kind of work.  A tile of
+// more than C tokens is two 128-row halves that share every page (pair); a
+// smaller one has its pages dealt in turn to the two streams, each with its
+// own O (solo).  The tiles of all heads, laid end to end and weighted by
+// pages, are cut into one equal range per CTA, so no CTA waits for a last
+// wave and only tiles that a cut meets are split.
 //
 // Kernels: plan (one CTA: tiles and their place in the line; of a small batch
 // every attend CTA makes it for itself), attend (one persistent CTA per SM),
