@@ -35,6 +35,7 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <utility>
 
 #include "common.cuh"
 
@@ -151,6 +152,10 @@ verify_kernel(const VerifyArgs a, int seg) {
   __shared__ int s_acc;
   __shared__ int s_used;
   cg::cluster_group cluster = cg::this_cluster();
+  // A CTA's shared memory may be written from outside only once the CTA has
+  // started: each says so here, and all are waited for just before the totals
+  // are exchanged, by when that costs nothing.
+  auto started = cluster.barrier_arrive();
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -246,6 +251,7 @@ verify_kernel(const VerifyArgs a, int seg) {
     }
     if (lane == 0) warp_tot[warp] = sum;
     __syncthreads();
+    if (pass == 0) cluster.barrier_wait(std::move(started));
     if (threadIdx.x < kCluster) {
       uint64_t t = 0;
 #pragma unroll

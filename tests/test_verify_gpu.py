@@ -226,3 +226,23 @@ def test_graph_and_other_stream():
         torch.cuda.synchronize()
         assert torch.equal(tokens[0], want[0]) and torch.equal(accepted[0], want[1])
         assert torch.equal(tokens[1], best[0]) and torch.equal(accepted[1], best[1])
+
+
+@pytest.mark.parametrize("B,k,V", [(700, 3, 1), (900, 2, 5), (600, 7, 64), (500, 3, 4096), (160, 2, 32000)])
+def test_batches_that_fill_every_sm(B, k, V):
+    # clusters that start late beside ones that run already, the smallest rows
+    # (most CTAs have no part of them, and reach the exchange of the totals at
+    # once) and rows of whole 16-byte pieces
+    target, draft, drafts, u = _inputs(B, k, V, torch.float32, B + V)
+    busy = torch.cuda.Stream()
+    a = torch.randn((4096, 4096), device="cuda", dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(busy):
+        for _ in range(4):
+            a @ a
+    want = _check(target, draft, drafts, u)
+    again = [msa.msa_verify(target, drafts, u, draft_probs=draft) for _ in range(20)]
+    torch.cuda.synchronize()
+    for tokens, accepted in again:
+        assert np.array_equal(tokens.cpu().numpy(), want[0]) and np.array_equal(accepted.cpu().numpy(), want[1])
+    _check(target, None, drafts, u)
