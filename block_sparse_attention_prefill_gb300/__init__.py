@@ -157,6 +157,27 @@ def _stream(stream):
     return ctypes.c_void_p(int(stream))
 
 
+def _empty(shape, dtype, device, stream):
+    """torch.empty for a call's kernels on `stream` (a torch.cuda.Stream, a
+    raw handle, or None for the current stream), from that stream's memory: a
+    block of the current stream's may still be in use by what is queued there.
+    The caller goes on with the tensor on the current stream, so it is not
+    handed out again before that stream is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else \
+            torch.cuda.default_stream(device)
+    if stream.cuda_stream == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
 

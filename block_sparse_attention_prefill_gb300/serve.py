@@ -18,7 +18,7 @@ import functools
 import torch
 
 from . import (DTYPE_BF16, DTYPE_F16, DTYPE_F32, HEAD_DIM, MsaError, NVFP4_SLOT_BYTES, PAGE_SIZE,
-               load, status_string)
+               _empty, load, status_string)
 
 # What the checks below raise on a sound call's shortcut for what is not a
 # tensor or has other dimensions.
@@ -80,10 +80,9 @@ _DEVICES = [torch.device("cuda", i) for i in range(64)]
 def _new(shape, dtype, dev, handle):
     """A tensor on device `dev` for use on the stream `handle`, whichever
     stream is current."""
-    t = torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
     if handle != torch._C._cuda_getCurrentRawStream(dev):
-        t.record_stream(torch.cuda.ExternalStream(handle, device=t.device))
-    return t
+        return _empty(shape, dtype, _DEVICES[dev], handle)
+    return torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
 
 
 def _ptr(t):
