@@ -200,13 +200,13 @@ def _bytes(t):
     return t.view(torch.uint8) if t.dtype != torch.uint8 else t
 
 
-def _workspace(nbytes, device, given):
+def _workspace(nbytes, device, given, stream):
     if given is not None:
         if given.numel() * given.element_size() < nbytes:
             raise MsaError("workspace too small: %d < %d bytes"
                            % (given.numel() * given.element_size(), nbytes))
         return given
-    return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
+    return _empty(max(int(nbytes), 1), torch.uint8, device, stream)
 
 
 def plan_workspace_bytes(B, T, Hq, Hkv, total_rows, max_seqlen_q) -> int:
@@ -306,7 +306,7 @@ def msa_plan(topk, cu_seqlens_q, cu_seqlens_k, block_table, num_pages, Hq,
     B = int(cu_seqlens_q.numel()) - 1
     bt_stride = int(block_table.shape[1]) if block_table.dim() == 2 else 1
     need = plan_workspace_bytes(B, T, Hq, Hkv, total_rows, max_seqlen_q)
-    ws = _workspace(need, topk.device, workspace)
+    ws = _workspace(need, topk.device, workspace, stream)
     st = MsaPlanStruct()
     args = (_ptr(cu_seqlens_q), _ptr(cu_seqlens_k), _ptr(block_table), bt_stride,
             int(num_pages), B, T, int(Hq), Hkv, int(total_rows),
@@ -413,8 +413,8 @@ def msa_nvfp4_to_e4m3(kv4, out=None, stream=None):
                        % NVFP4_SLOT_BYTES)
     P, Hkv = int(kv4.shape[0]), int(kv4.shape[1])
     if out is None:
-        out = torch.empty((P, Hkv, PAGE_SIZE, 2 * HEAD_DIM),
-                          dtype=torch.float8_e4m3fn, device=kv4.device)
+        out = _empty((P, Hkv, PAGE_SIZE, 2 * HEAD_DIM), torch.float8_e4m3fn,
+                     kv4.device, stream)
     _need(out, "out", _E4M3)
     _check(load().msa_nvfp4_to_e4m3(_ptr(kv4), P * Hkv, _ptr(_bytes(out)),
                                     _stream(stream)), "msa_nvfp4_to_e4m3")
@@ -431,12 +431,12 @@ def _prefill(name, q, kv, q_scale, k_scale, v_scale, softmax_scale,
         raise MsaError("q must be [T, Hq, 128] = %s" % ((T, Hq, HEAD_DIM),))
     _need_kv(kv, int(s.Hkv), name.endswith("nvfp4"))
     need = prefill_workspace_bytes(T, Hq)
-    ws = _workspace(need, q.device, workspace)
+    ws = _workspace(need, q.device, workspace, stream)
     if out is None:
-        out = torch.empty((T, Hq, HEAD_DIM), dtype=torch.bfloat16, device=q.device)
+        out = _empty((T, Hq, HEAD_DIM), torch.bfloat16, q.device, stream)
     _need(out, "out", (torch.bfloat16,))
     if lse is None and want_lse:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((T, Hq), torch.float32, q.device, stream)
     if lse is not None:
         _need(lse, "lse", (torch.float32,))
     bt_stride = int(block_table.shape[1]) if block_table.dim() == 2 else 1
@@ -482,7 +482,7 @@ def _attention(name, q, kv, q_scale, k_scale, v_scale, softmax_scale,
     _need(q, "q", (torch.bfloat16,) if name.endswith("bf16q") else _E4M3)
     _need_kv(kv, int(s.Hkv), name.endswith("nvfp4"))
     need = prefill_workspace_bytes(int(s.T), int(s.Hq))
-    ws = _workspace(need, q.device, workspace)
+    ws = _workspace(need, q.device, workspace, stream)
     bt_stride = int(block_table.shape[1]) if block_table.dim() == 2 else 1
     _check(getattr(load(), name)(
         _ptr(_bytes(q)), _ptr(_bytes(kv)), int(kv.shape[0]), float(q_scale),
@@ -513,10 +513,9 @@ def msa_combine(part_o, part_lse, out=None, lse=None, stream=None):
             tuple(part_lse.shape) != (rows, S):
         raise MsaError("part_o must be [rows, S, 128], part_lse [rows, S]")
     if out is None:
-        out = torch.empty((rows, HEAD_DIM), dtype=torch.bfloat16,
-                          device=part_o.device)
+        out = _empty((rows, HEAD_DIM), torch.bfloat16, part_o.device, stream)
     if lse is None:
-        lse = torch.empty((rows,), dtype=torch.float32, device=part_o.device)
+        lse = _empty((rows,), torch.float32, part_o.device, stream)
     dt = DTYPE_F32 if part_o.dtype == torch.float32 else DTYPE_BF16
     _check(load().msa_combine(_ptr(part_o), dt, _ptr(part_lse), rows, S,
                               _ptr(out), _ptr(lse), _stream(stream)),
@@ -556,12 +555,11 @@ def _decode(name, q, kv, q_scale, k_scale, v_scale, softmax_scale, topk,
     _need(seq_lens, "seq_lens", (torch.int32,))
     _need_kv(kv, Hkv, fp4)
     need = decode_workspace_bytes(B, n, Hq, Hkv, max_seqlen_k)
-    ws = _workspace(need, q.device, workspace)
+    ws = _workspace(need, q.device, workspace, stream)
     if out is None:
-        out = torch.empty((B * n, Hq, HEAD_DIM), dtype=torch.bfloat16,
-                          device=q.device)
+        out = _empty((B * n, Hq, HEAD_DIM), torch.bfloat16, q.device, stream)
     if lse is None and want_lse:
-        lse = torch.empty((B * n, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((B * n, Hq), torch.float32, q.device, stream)
     _need(out, "out", (torch.bfloat16,))
     if lse is not None:
         _need(lse, "lse", (torch.float32,))

@@ -84,3 +84,34 @@ def test_blocks_freed_on_the_current_stream_are_not_taken():
         assert not free & {t.data_ptr() for t in got}
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_older_calls_workspace_comes_from_the_streams_memory(streams):
+    t = msa._workspace(100, "cuda:0", None, 77)
+    assert t.made_on == 77 and t.used_on == [5]
+    t = msa._workspace(100, "cuda:0", None, None)
+    assert t.made_on == 5 and t.used_on == []
+
+
+@pytest.mark.gpu
+def test_older_calls_take_no_blocks_freed_on_the_current_stream():
+    import workloads
+    w = workloads.make_batch("streams", [160, 48], [2600, 700], 16, 2, seed=0).to("cuda:0")
+    want = msa.run_workload(w)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    T = w.q.shape[0]
+    part_o, part_lse = torch.randn((50, 3, 128), device="cuda"), torch.randn((50, 3), device="cuda")
+    merged = msa.msa_combine(part_o, part_lse)
+    sizes = [T * 16 * 128 * 2, T * 16 * 4, want[2].workspace.numel(), msa.prefill_workspace_bytes(T, 16), 50 * 128 * 2, 50 * 4]
+    torch.cuda.synchronize()
+    held = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(8)]
+    spans = [(t.data_ptr(), t.data_ptr() + t.numel()) for t in held]
+    del held
+    got = msa.run_workload(w, stream=side)
+    again = msa.msa_combine(part_o, part_lse, stream=side)
+    for t in (got[0], got[1], got[2].workspace, *again):
+        assert not any(a < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < b for a, b in spans)
+    side.synchronize()
+    assert got[2].status() == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert all(torch.equal(a, b) for a, b in zip(again, merged))
