@@ -326,6 +326,7 @@ static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsWiden <= 512, "registers");
 // outside f16's range, and f16's subnormals begin 2^-21 below the reference
 // instead of 2^-14
 constexpr float kPShift = 7.f, kMostSum = 32768.f;
+constexpr float kLeftOut = -1.f;  // a weight in the merge of a part's streams
 
 struct AttendParams {
   PlanParams plan;
@@ -686,9 +687,11 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
       tc_fence_after();
       // In a solo part the streams have the same rows, in the same lanes of
       // tensor memory: either writes half the columns of both streams' sum.
-      // Weights of the own and the other stream's O (0: nothing, whatever it
-      // holds; a NaN among the scores makes l, and so the row, NaN).
-      float wa = l == 0.f ? 0.f : 1.f, wb = 0.f, lt = l, mt = m;
+      // Weights of the own and the other stream's O.  What has no keys (l = 0)
+      // is left out, whatever its O holds (weight kLeftOut); a weight that
+      // underflows to 0 is no reason to, since a NaN in l (among the scores)
+      // makes the row NaN and one in O (among V) its column.
+      float wa = l == 0.f ? kLeftOut : 1.f, wb = kLeftOut, lt = l, mt = m;
       if (!pair) {
         if (solos > 0 && !all_wait(bars, &bars->read, (solos - 1) & 1, p)) break;
         bars->ml[s][row] = make_float2(m, l);
@@ -698,9 +701,9 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         tc_fence_after();
         const float2 z = bars->ml[s ^ 1][row];
         mt = fmaxf(m, z.x);
-        wa = l == 0.f ? 0.f : m == -INFINITY ? 1.f : ex2_approx((m - mt) * c);
-        wb = z.y == 0.f ? 0.f : z.x == -INFINITY ? 1.f : ex2_approx((z.x - mt) * c);
-        lt = (wa == 0.f ? 0.f : l * wa) + (wb == 0.f ? 0.f : z.y * wb);
+        wa = l == 0.f ? kLeftOut : m == -INFINITY ? 1.f : ex2_approx((m - mt) * c);
+        wb = z.y == 0.f ? kLeftOut : z.x == -INFINITY ? 1.f : ex2_approx((z.x - mt) * c);
+        lt = (wa < 0.f ? 0.f : l * wa) + (wb < 0.f ? 0.f : z.y * wb);
       }
       const bool poison = __any_sync(0xffffffffu, *(volatile int*)&bars->nan_seen != 0);
       int nan_key[4] = {INT_MAX, INT_MAX, INT_MAX, INT_MAX};  // columns 4 lane ..
@@ -724,7 +727,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         }
       }
       const float inv = lt == 0.f ? 0.f : 1.f / lt;
-      const float fa = wa * inv, fb = wb * inv;
+      const float fa = wa < 0.f ? kLeftOut : wa * inv, fb = wb < 0.f ? kLeftOut : wb * inv;
       const RowPlace place = row_place(off_row, t.ntok, p.C, p.G);
       uint32_t* dst = reinterpret_cast<uint32_t*>(p.part_o + first_row * kD) + place.first;
       const int q0 = pair ? 0 : 4 * s, q1 = pair ? 8 : q0 + 4;
@@ -736,8 +739,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          o[e] = __float_as_uint((wa == 0.f ? 0.f : __uint_as_float(o[e]) * fa) +
-                                 (wb == 0.f ? 0.f : __uint_as_float(x[e]) * fb));
+          o[e] = __float_as_uint((fa < 0.f ? 0.f : __uint_as_float(o[e]) * fa) +
+                                 (fb < 0.f ? 0.f : __uint_as_float(x[e]) * fb));
         if (poison) {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
@@ -1139,8 +1142,11 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
         // a member's parts are every kTeam-th, 8 of them a round
         for (int e0 = member; e0 < n; e0 += kTeam * kLanes) {
           const int e = e0 + kTeam * sub;
-          const int row = e < n ? s_row[k][e] : 0;
+          int row = e < n ? s_row[k][e] : 0;
           const float le = e < n ? __ldcg(p.part_lse + row + off) : -INFINITY;
+          // only a part without keys is left out: one whose weight underflows
+          // may hold a NaN
+          if (le == -INFINITY) row = -1;
           float top = le;
 #pragma unroll
           for (int d = kLanes / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(peers, top, d));
@@ -1164,7 +1170,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
               const float* src = col + (int64_t)rj * kD;
 #pragma unroll
               for (int q = 0; q < kQ; ++q)
-                v[d][q] = wj[d] != 0.f
+                v[d][q] = rj >= 0
                               ? __ldcg(reinterpret_cast<const float4*>(src + 4 * q * place.chunk))
                               : make_float4(0.f, 0.f, 0.f, 0.f);
             }

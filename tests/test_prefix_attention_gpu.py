@@ -304,3 +304,36 @@ def test_short_wait_limit_expires_and_the_next_call_is_clean():
         lib.msa_test_set_wait_limit_ns(0)
     got = _run(w, workspace=ws)
     assert got[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("low", [0, 1])
+@pytest.mark.parametrize("hq,hkv,q_lens,own,prefix", [
+    (16, 2, [1], [5000], 0),             # one token over many CTAs
+    (16, 2, [8] * 400, [300] * 400, 0),  # whole tiles to a CTA: the two streams' halves
+    (16, 2, [8] * 4, [200] * 4, 6),      # shared pages beside own ones
+    (4, 4, [150], [700], 0),             # pages that some rows see in part
+    (8, 1, [40], [41], 2),
+])
+def test_nan_of_keys_without_weight(hq, hkv, q_lens, own, prefix, low):
+    # the keys of one page lie some 800 powers of two below the others: their
+    # weight is 0 in fp32 wherever the page is merged, and a NaN there is one
+    w = _batch(hq, hkv, q_lens, own, prefix, seed=16)
+    w["q"] = torch.full(w["q"].shape, 384.0, device="cuda").to(torch.float8_e4m3fn)
+    kv = w["kv"].float()
+    kv[..., :128] = 320.0
+    kv[w["table"][:, low].long(), ..., :128] = -320.0
+    w["kv"] = kv.to(torch.float8_e4m3fn)
+    clean = _run(w)
+    assert clean[2] == 0
+    _compare(w, clean[:2])
+    raw, page = w["kv"].view(torch.uint8), w["table"][-1, low].item()
+    raw[page, 0, 20, 128 + 5] = 0x7F        # V of one of its keys: column 5
+    out, lse, status = _run(w)
+    assert status == 0
+    _compare(w, (out, lse))
+    assert torch.isnan(out[-1, 0, 5]) and not torch.isnan(lse).any()
+    raw[page, hkv - 1, 9, 7] = 0xFF         # K of another: the rows
+    out, lse, status = _run(w)
+    assert status == 0
+    _compare(w, (out, lse))
+    assert torch.isnan(out[-1, -1]).all() and torch.isnan(lse[-1, -1])
