@@ -129,11 +129,19 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
   return v;
 }
 
-// floor(u * total) for u rounded down to 31 bits, in [0, total) for total > 0
+// floor(u * total), exactly: u is a whole number of at most 24 bits times a
+// power of two, and total is below 2^63.  In [0, total) for total > 0; 0 for
+// NaN and for u <= 0, and for u >= 1, which is no uniform, that of the largest
+// 31-bit number below 1.
 __device__ __forceinline__ uint64_t threshold(float u, uint64_t total) {
-  const double x = (double)u * 2147483648.0;
-  const uint64_t k = x > 0.0 ? (uint64_t)fmin(x, 2147483647.0) : 0;  // NaN: 0
-  return k * (total >> 31) + ((k * (total & 0x7FFFFFFFu)) >> 31);
+  if (!(u > 0.f)) return 0;
+  const uint32_t bits = __float_as_uint(u);
+  const int e = max(1, (int)(bits >> 23));  // u = k 2^(e - 150)
+  uint64_t k = (bits & 0x7FFFFFu) | (bits >> 23 ? 0x800000u : 0u);
+  int shift = 150 - e;  // 24 .. 149
+  if (u >= 1.f) k = 0x7FFFFFFFu, shift = 31;
+  const uint64_t hi = __umul64hi(k, total), lo = k * total;
+  return shift < 64 ? (hi << (64 - shift)) | (lo >> shift) : shift < 128 ? hi >> (shift - 64) : 0;
 }
 
 // N consecutive weights a lane: 32 * N a warp step.  A warp takes kBatch steps

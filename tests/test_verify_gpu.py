@@ -246,3 +246,34 @@ def test_batches_that_fill_every_sm(B, k, V):
     for tokens, accepted in again:
         assert np.array_equal(tokens.cpu().numpy(), want[0]) and np.array_equal(accepted.cpu().numpy(), want[1])
     _check(target, None, drafts, u)
+
+
+def _exact_pick(w, u):
+    """The lowest v whose cumulated weight exceeds floor(u total), u taken exactly."""
+    cut = np.cumsum(w, dtype=np.uint64)
+    num, den = float(u).as_integer_ratio()
+    return int(np.searchsorted(cut, np.uint64(num * int(cut[-1]) // den), side="right"))
+
+
+@pytest.mark.parametrize("V", [1000, 4099, 200003])
+def test_small_uniforms_count_to_their_last_bit(V):
+    # uniforms far below 2^-7, whose last bits lie below 2^-31; fine weights at
+    # the row's start, so that these bits choose the token
+    B = 64
+    r = np.random.RandomState(V)
+    target = torch.zeros((B, 1, V), device="cuda")
+    target[:, :, :300] = torch.from_numpy(np.ldexp(r.rand(B, 1, 300).astype(np.float32), -36)).cuda()
+    target[:, 0, -1] = 1.0
+    sig = r.randint(2 ** 23, 2 ** 24, B) | 1
+    u = np.ldexp(sig.astype(np.float32), -24 - r.randint(28, 36, B)).astype(np.float32)
+    u[:3] = 2.0 ** -31, np.nextafter(np.float32(2.0 ** -30), np.float32(0)), 2.0 ** -149
+    tokens, accepted = msa.msa_verify(target, torch.zeros((B, 0), dtype=torch.int32, device="cuda"), torch.from_numpy(u[:, None]).cuda())
+    want = [_exact_pick(_weights(target[b, 0].cpu().numpy(), np.zeros(V, np.float32)), u[b]) for b in range(B)]
+    assert len(set(want)) > 10
+    assert tokens[:, 0].tolist() == want and not accepted.any()
+    # ordinary uniforms with low bits (below 2^-7), over a spread row
+    target = torch.softmax(2 * torch.from_numpy(r.randn(B, 1, V)).float(), -1).cuda()
+    u = np.ldexp(sig.astype(np.float32), -24 - r.randint(0, 20, B)).astype(np.float32)
+    tokens, _ = msa.msa_verify(target, torch.zeros((B, 0), dtype=torch.int32, device="cuda"), torch.from_numpy(u[:, None]).cuda())
+    want = [_exact_pick(_weights(target[b, 0].cpu().numpy(), np.zeros(V, np.float32)), u[b]) for b in range(B)]
+    assert tokens[:, 0].tolist() == want
