@@ -199,7 +199,6 @@ verify_kernel(const VerifyArgs a, int seg) {
     if (rank == 0) {  // the drafts that stand, and -1 behind the next token
       if (lane < n && lane != min(acc, drafts))
         a.tokens[b * n + lane] = lane < acc ? x : -1;
-      if (lane == 0) a.accepted[b] = min(acc, drafts);
     }
   }
   __syncthreads();
@@ -267,6 +266,9 @@ verify_kernel(const VerifyArgs a, int seg) {
       *cluster.map_shared_rank(&cta_tot[rank], threadIdx.x) = t;
     }
     cluster.sync();
+    // only now has every CTA read the request's number of drafts, which
+    // `accepted` may replace
+    if (pass == 0 && rank == 0 && threadIdx.x == 0) a.accepted[b] = s_acc;
     uint64_t total = 0, before = 0;
 #pragma unroll
     for (int i = 0; i < kCluster; ++i) {
@@ -278,7 +280,7 @@ verify_kernel(const VerifyArgs a, int seg) {
         cluster.sync();  // the totals are read before they are written again
         continue;
       }
-      if (rank == 0 && threadIdx.x == 0) a.tokens[b * n + acc] = -1;  // no probability at all
+      if (rank == 0 && threadIdx.x == 0) a.tokens[b * n + s_acc] = -1;  // no probability at all
       return;
     }
     uint64_t t = threshold(u, total);
@@ -318,7 +320,7 @@ verify_kernel(const VerifyArgs a, int seg) {
           uint64_t sofar = incl - own;
           int e = 0;
           while (e < N - 1 && sofar + w[e] <= t) sofar += w[e++];
-          a.tokens[b * n + acc] = v0 + (k * 32 + lane) * N + e;
+          a.tokens[b * n + s_acc] = v0 + (k * 32 + lane) * N + e;
         }
         return;
       }

@@ -365,6 +365,18 @@ def _probs(t, name, dtypes):
     return shape
 
 
+def _apart(out, name, inputs):
+    """Refuses an output that shares memory with one of the inputs, all
+    contiguous, by their names."""
+    if out is None:
+        return
+    at, n = out.data_ptr(), out.numel() * out.element_size()
+    for other, t in inputs.items():
+        if t is not None and at < t.data_ptr() + t.numel() * t.element_size() and \
+                t.data_ptr() < at + n:
+            _fail("%s must not share memory with %s", name, other)
+
+
 def _check_verify(greedy, target, drafts, uniforms, draft_probs, counts, tokens, accepted):
     B, n, V = _probs(target, "target", _TYPES)
     if n < 1:
@@ -382,6 +394,13 @@ def _check_verify(greedy, target, drafts, uniforms, draft_probs, counts, tokens,
         _tensor(tokens, "tokens", _I32, (B, n))
     if accepted is not None:
         _tensor(accepted, "accepted", _I32, (B,))
+    # requests are decided at the same time: an output in place of an input
+    # only where each request reads its own element alone
+    inputs = {"draft_tokens": drafts, "uniforms": uniforms, "num_drafts": counts}
+    same = tokens is not None and B == 1 and tokens.data_ptr() == drafts.data_ptr()
+    _apart(tokens, "tokens", dict(inputs, accepted=accepted, draft_tokens=None if same else drafts))
+    same = accepted is not None and counts is not None and accepted.data_ptr() == counts.data_ptr()
+    _apart(accepted, "accepted", dict(inputs, num_drafts=None if same else counts))
     _place(target, drafts, uniforms, draft_probs, counts, tokens, accepted)
 
 
@@ -435,8 +454,9 @@ def msa_verify(target_probs, draft_tokens, uniforms, draft_probs=None, num_draft
     target_probs [B, n, V] and draft_probs [B, n - 1, V] in fp32, bf16 or fp16
     (strided rows allowed; no draft_probs: the drafts were certain),
     draft_tokens int32 [B, n - 1], uniforms fp32 [B, n] in [0, 1), num_drafts
-    int32 [B] or None for n - 1 each.  Returns (tokens int32 [B, n]: the
-    drafts that stand, the next token, -1; accepted int32 [B])."""
+    int32 [B] or None for n - 1 each; accepted may be num_drafts itself, the
+    outputs share no other memory with the inputs.  Returns (tokens int32
+    [B, n]: the drafts that stand, the next token, -1; accepted int32 [B])."""
     return _verify("msa_verify", target_probs, draft_tokens, uniforms, draft_probs, num_drafts,
                    tokens, accepted, stream)
 

@@ -603,7 +603,8 @@ MSA_API int msa_prefix_attention(const uint8_t *q, const uint8_t *kv, int64_t nu
  *   num_drafts    int32 [B], drafts of each request (clamped to 0 .. n - 1),
  *                 or NULL for n - 1
  *   tokens        int32 [B][n]: the drafts that stand, the next token, -1
- *   accepted      int32 [B]: how many drafts stand
+ *   accepted      int32 [B]: how many drafts stand; may be num_drafts itself
+ *                 (the outputs share no other memory with the inputs)
  * 1 <= n <= MSA_VERIFY_MAX_TOKENS, 1 <= V < MSA_VERIFY_MAX_VOCAB.  The rows
  * need no more alignment than their elements; 16-byte aligned rows are read
  * fastest.  One kernel on `stream`.

@@ -155,3 +155,19 @@ def test_prefix_attention_library_refusals():
     assert size(2, 6, 4, 2, 1, 6, 300) == 0 and n.value > 0
     assert size(2, 6, 4, 2, 1, 6, 100) == 1 and size(2, -6, 4, 2, 1, 6, 300) == 1 and size(2, 6, 5, 2, 1, 6, 300) == 2
     assert lib.msa_prefix_attention_workspace_bytes(2, 6, 4, 2, 1, 6, 300, None) == 6
+
+
+def test_verify_refuses_outputs_over_inputs():
+    t, u = torch.zeros((2, 4, 50)), torch.zeros((2, 4))
+    room = torch.zeros(20, dtype=torch.int32)
+    x, counts = room[:6].view(2, 3), torch.zeros(2, dtype=torch.int32)
+    for fn, args in ((msa.msa_verify, (t, x, u)), (msa.msa_verify_greedy, (t, x))):
+        for at in (0, 5):
+            assert "tokens must not share memory with draft_tokens" in _err(fn, *args, tokens=room[at:at + 8].view(2, 4))
+        assert "accepted must not share memory with draft_tokens" in _err(fn, *args, accepted=room[5:7])
+        assert "tokens must not share memory with accepted" in _err(fn, *args, tokens=room[6:14].view(2, 4), accepted=room[13:15])
+        assert "accepted must not share memory with num_drafts" in _err(fn, *args, num_drafts=room[8:10], accepted=room[9:11])
+        assert "CUDA" in _err(fn, *args, tokens=room[6:14].view(2, 4), accepted=counts, num_drafts=counts)
+        one = (t[:1], room[:3].view(1, 3), u[:1])[:len(args)]
+        assert "CUDA" in _err(fn, *one, tokens=room[:4].view(1, 4))
+    assert "tokens must not share memory with uniforms" in _err(msa.msa_verify, t, x, u, tokens=u.view(torch.int32))

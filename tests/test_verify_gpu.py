@@ -277,3 +277,26 @@ def test_small_uniforms_count_to_their_last_bit(V):
     tokens, _ = msa.msa_verify(target, torch.zeros((B, 0), dtype=torch.int32, device="cuda"), torch.from_numpy(u[:, None]).cuda())
     want = [_exact_pick(_weights(target[b, 0].cpu().numpy(), np.zeros(V, np.float32)), u[b]) for b in range(B)]
     assert tokens[:, 0].tolist() == want
+
+
+def test_accepted_in_place_of_num_drafts():
+    # drafts that all fall: a number of drafts read after `accepted` replaced
+    # it would take the row behind them for theirs
+    for B, V in ((400, 3), (200, 5003)):
+        target, draft, drafts, u = _inputs(B, 5, V, torch.float32, B)
+        target[:, 0].scatter_(1, drafts[:, :1].long(), 0.0)
+        counts = torch.randint(0, 6, (B,), dtype=torch.int32, generator=torch.Generator().manual_seed(V)).cuda()
+        want = _check(target, draft, drafts, u, counts)
+        best = msa.msa_verify_greedy(target, drafts, num_drafts=counts)
+        for _ in range(5):
+            own = counts.clone()
+            tokens, accepted = msa.msa_verify(target, drafts, u, draft_probs=draft, num_drafts=own, accepted=own)
+            assert accepted is own and np.array_equal(own.cpu().numpy(), want[1]) and np.array_equal(tokens.cpu().numpy(), want[0])
+            own = counts.clone()
+            tokens, _ = msa.msa_verify_greedy(target, drafts, num_drafts=own, accepted=own)
+            assert torch.equal(own, best[1]) and torch.equal(tokens, best[0])
+        # and one request's tokens over its drafts
+        for b in (0, 1):
+            room = torch.cat((drafts[b], drafts[b, :1]))
+            msa.msa_verify(target[b:b + 1], room[:5].view(1, 5), u[b:b + 1], draft_probs=draft[b:b + 1], num_drafts=counts[b:b + 1], tokens=room.view(1, 6))
+            assert np.array_equal(room.cpu().numpy(), want[0][b])
