@@ -1049,7 +1049,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
   constexpr int kLanes = 8;
   constexpr int kQ = 32 / kLanes;             // float4 of a row per lane
   constexpr int kFlight = kTeam == 8 ? 8 : 2;  // parts in flight
-  __shared__ float s_acc[kTeam > 1 ? kCombineWarps * 4 : 1][kD];
+  __shared__ __align__(16) float s_acc[kTeam > 1 ? kCombineWarps * 4 : 1][kD];  // (as float4)
   __shared__ float s_m[kCombineWarps * 4], s_l[kCombineWarps * 4];
   pdl_wait();
   pdl_trigger();
