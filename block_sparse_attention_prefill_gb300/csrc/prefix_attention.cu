@@ -60,8 +60,8 @@ namespace {
 
 // Cost of a tile: its pages by kind, and its start and end (Q, epilogue), in
 // the proportions measured (about 0.9, 1.8 and 4.5 us).
-constexpr int kCostSolo = 2, kCostPair = 4, kCostTile = 10;
-constexpr int kMinShare = 12;  // least cost of a CTA's range
+constexpr int kCostSolo = 1, kCostPair = 2, kCostTile = 5;
+constexpr int kMinShare = 6;  // least cost of a CTA's range
 
 // Behind every key (positions are below 2^30), with room for a tile's tokens.
 constexpr int kNoMask = INT_MAX - 1024;
@@ -1246,8 +1246,11 @@ bool layout(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t prefix, int64
             Layout* l) {
   const int64_t G = Hq / Hkv, C = kTileM / G;
   const int64_t tiles = max_tiles(B, T, C, prefix);
-  // costs and partial rows in range of their integers
-  if ((double)tiles * (double)(ceil_div(max_k, kPage) * kCostPair + kCostTile) > 1.0e9) return false;
+  // the cost of a head's tiles, that of a CTA's range and the rows of the
+  // partials in range of their integers (places in 64 bits cost the attention
+  // kernel 1 to 7 %, by its registers)
+  const double cost = (double)tiles * (double)(ceil_div(max_k, kPage) * kCostPair + kCostTile);
+  if (cost > (double)INT_MAX || cost * (double)Hkv > (double)INT_MAX * ctas) return false;
   const int64_t rows = 256 * ((int64_t)ctas + 1) + Hkv * (prefix > 0 ? 2 : 1) * T * G;
   if (rows >= INT_MAX || ctas > kMaxParts) return false;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };

@@ -550,7 +550,11 @@ MSA_API int msa_kv_read_nvfp4(const uint8_t *kv4, int64_t num_pages, float k_sca
  *                 are read through the rows of any requests with query
  *                 tokens: once for all of them, or by each where that is
  *                 less work (one request, long chunks, a page or two)
- *   max_seqlen_q, max_seqlen_k  host-known bounds, max_seqlen_k <= 2^30
+ *   max_seqlen_q, max_seqlen_k  host-known bounds, max_seqlen_k <= 2^30 and
+ *                 n (2 ceil(max_seqlen_k / 128) + 5) < 2^31 for n tiles of t
+ *                 tokens, t = 2 floor(128 Hkv / Hq): n = min(T, ceil(T / t) +
+ *                 B), and ceil(T / t) more where prefix_pages > 0 (a million
+ *                 tokens of one request with Hq / Hkv = 16 are within it)
  *   workspace     msa_prefix_attention_workspace_bytes() bytes, 256-byte
  *                 aligned; calls whose work may overlap need one each
  *   out           bf16 [T][Hq][128]

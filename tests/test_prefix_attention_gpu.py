@@ -337,3 +337,28 @@ def test_nan_of_keys_without_weight(hq, hkv, q_lens, own, prefix, low):
     assert status == 0
     _compare(w, (out, lse))
     assert torch.isnan(out[-1, -1]).all() and torch.isnan(lse[-1, -1])
+
+
+def test_bound_far_above_the_lengths():
+    # a batch under the largest bound: 32 short requests, 2^23 pages a row of the table
+    w = _batch(16, 2, [1] * 30 + [40, 2], [1 + 20 * i for i in range(30)] + [300, 7], 0, seed=17)
+    want = _run(w)
+    table = torch.full((32, 2 ** 23), -1, dtype=torch.int32, device="cuda")
+    table[:, :w["table"].shape[1]] = w["table"]
+    got = _run(dict(w, table=table, max_k=2 ** 30))
+    assert got[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_long_rows_of_one_page():
+    # 64 requests of 2^21 keys each, all in one page: the softmax over it,
+    # whatever the number of its copies
+    w = _batch(16, 1, [1] * 64, [128] * 64, 0, seed=18)
+    want = _reference(w)
+    pages, P = w["table"][:, 0].clone(), 2 ** 14
+    table = pages[:, None].expand(64, P).contiguous()
+    cu_k = torch.arange(65, dtype=torch.int32, device="cuda") * (128 * P)
+    out, lse, status = _run(dict(w, table=table, cu_k=cu_k, max_k=128 * P))
+    assert status == 0
+    err = (out.double() - want[0]).abs() - (2.0 ** -8 * want[0].abs() + 2.0 ** -10 * want[1])
+    assert not (err > 0).any()
+    assert ((lse.double() - want[2] - np.log(P)).abs() <= 2.0 ** -11).all()
