@@ -298,6 +298,7 @@ constexpr int kOffV = kOffK + kRawK * kTileBytes;
 constexpr int kOffW = kOffV + kRawV * kTileBytes;
 constexpr int kOffBars = kOffW + kWide * kTileBytes;
 constexpr int kThere = 16;  // more than the roles can be apart
+constexpr int kIsThere = 1, kHasNan = 2;
 struct Bars {
   uint64_t q_full, q_free;
   uint64_t k_full[kRawK], k_free[kRawK], v_full[kRawV], v_free[kRawV];
@@ -308,10 +309,11 @@ struct Bars {
   uint64_t mma_done[3];
   uint32_t tmem_base;
   int abort;
-  int nan_seen;      // a NaN among the V codes of valid keys
   int first_tile;
   float2 ml[2][128];  // a solo part's m and l by stream and row
-  uint8_t there[kThere];  // whether a ring position's page is one, by the producer
+  // whether a ring position's page is one, by the producer; kHasNan too where a
+  // NaN lies among the V codes of its keys and not every row sees it whole
+  uint8_t there[kThere];
 };
 constexpr int kSmem = kOffBars + (int)sizeof(Bars) + 1024;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -494,7 +496,6 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
     mbar_init(&bars->read, 256);
     for (int i = 0; i < 3; ++i) mbar_init(&bars->mma_done[i], 1);
     bars->abort = 0;
-    bars->nan_seen = 0;
     bars->first_tile = 0;
     fence_mbar_init();
   }
@@ -705,16 +706,16 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         wb = z.y == 0.f ? kLeftOut : z.x == -INFINITY ? 1.f : ex2_approx((z.x - mt) * c);
         lt = (wa < 0.f ? 0.f : l * wa) + (wb < 0.f ? 0.f : z.y * wb);
       }
-      const bool poison = __any_sync(0xffffffffu, *(volatile int*)&bars->nan_seen != 0);
+      // Where a NaN lies among the V codes of a key in a page that some row
+      // does not see whole, widening wrote it as 0, since a probability of 0
+      // must hide it; now each warp finds, for each column, the first position
+      // that has one (pages of that kind are the last three of a tile at most).
+      bool poison = false;
       int nan_key[4] = {INT_MAX, INT_MAX, INT_MAX, INT_MAX};  // columns 4 lane ..
-      if (poison) {
-        // A NaN lies among the V codes of some valid key.  Widening wrote it
-        // as 0, since a probability of 0 must hide it; now each warp finds,
-        // for each column, the first position of this part that has one (a
-        // rare path: no care is taken of its speed).
-        for (int j = walk.p0; j < walk.p1; ++j) {
+      for (int j = max(walk.p0, (t.pos0 + 1) / kPage - t.page0); j < walk.p1; ++j) {
+        if (bars->there[(g0 + j - walk.p1) % kThere] & kHasNan) {
+          poison = true;
           const int pg = __ldg(table + j);
-          if (pg < 0 || pg >= p.num_pages) continue;
           const uint8_t* v = p.kv + ((int64_t)pg * p.Hkv + walk.cur_h) * kPage * (2 * kD) + kD;
           const int first = (t.page0 + j) * kPage;
           for (int k = 0; k < kPage && first + k < t.seq; ++k) {
@@ -806,7 +807,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
             w[u].x &= ~((x >> 7) * 0xFFu);
             w[u].y &= ~((y >> 7) * 0xFFu);
           }
-          if (bad) *(volatile int*)&bars->nan_seen = 1;
+          if (bad) bars->there[g % kThere] = kIsThere | kHasNan;
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -857,7 +858,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
               const uint32_t v = pair ? i : i >> 1;
               const uint32_t slot = Ring::slot(pair, i & 1, v), ph = ring.phase(pair, slot, v);
               const bool there = page >= 0 && page < p.num_pages;
-              bars->there[g % kThere] = there;
+              bars->there[g % kThere] = there ? kIsThere : 0;
               if (!there && p.status) atomicOr(p.status, (unsigned)MSA_STATUS_BAD_BLOCK);
               const int y = there ? (page * p.Hkv + walk.cur_h) * kPage : 0;
               ok = bounded_wait_long(&bars->k_free[slot], ph ^ 1, abort, p.wait_ns);

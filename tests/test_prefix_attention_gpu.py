@@ -362,3 +362,28 @@ def test_long_rows_of_one_page():
     err = (out.double() - want[0]).abs() - (2.0 ** -8 * want[0].abs() + 2.0 ** -10 * want[1])
     assert not (err > 0).any()
     assert ((lse.double() - want[2] - np.log(P)).abs() <= 2.0 ** -11).all()
+
+
+@pytest.mark.parametrize("n,own", [(8, [40000 + 100 * i for i in range(8)]), (1, [100 + 800 * i // 512 for i in range(512)])])
+def test_a_nan_does_not_slow_the_rest_of_the_batch(n, own):
+    # a NaN among the V of the first request's last page: only the page that
+    # holds it is looked through, not every page that follows
+    w = _batch(16, 2, [n] * len(own), own, 0, seed=19)
+    dirty = dict(w, kv=w["kv"].view(torch.uint8).clone())
+    dirty["kv"][w["table"][0, (w["seqs"][0] - 1) // 128], :, (w["seqs"][0] - 1) % 128, 128 + 9] = 0x7F
+    dirty["kv"] = dirty["kv"].view(torch.float8_e4m3fn)
+    out, lse, status = _run(dirty)
+    assert status == 0 and torch.isnan(out[n - 1, :, 9]).all() and not torch.isnan(out[n:]).any() and not torch.isnan(lse).any()
+    took = {}
+    for name, x in (("clean", w), ("dirty", dirty)):
+        times = []
+        for _ in range(8):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            msa.msa_prefix_attention(x["q"], x["kv"], QS, KS, VS, SM, x["table"], x["cu_q"], x["cu_k"], 0, x["max_q"], x["max_k"])
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        took[name] = min(times)
+    print(took)
+    assert took["dirty"] < 2 * took["clean"] + 0.1, took
