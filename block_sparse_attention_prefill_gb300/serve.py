@@ -282,8 +282,9 @@ def prefix_attention_workspace_bytes(B, T, Hq, Hkv, prefix_pages, max_seqlen_q,
 
 @functools.lru_cache(maxsize=64)
 def _attention_bytes(dev, B, T, Hq, Hkv, prefix_pages, max_q, max_k):
-    """The same; the size depends on these numbers and the device alone, and a
-    decode loop asks for the same one again and again."""
+    """The same for the current device, `dev`; the size depends on these
+    numbers and the device alone, and a decode loop asks for the same one again
+    and again."""
     return prefix_attention_workspace_bytes(B, T, Hq, Hkv, prefix_pages, max_q, max_k)
 
 
@@ -332,7 +333,11 @@ def msa_prefix_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_
         _check_attention(q, kv, block_table, cu_seqlens_q, cu_seqlens_k, workspace, out, lse,
                          status)
     B, Hkv = table[0], pool[1]
-    need = _attention_bytes(dev, B, T, Hq, Hkv, prefix_pages, max_seqlen_q, max_seqlen_k)
+    # the library answers for the current device: nothing is kept for another,
+    # which is refused below
+    here = sound or (dev >= 0 and dev == torch._C._cuda_getDevice())
+    sizes = (B, T, Hq, Hkv, prefix_pages, max_seqlen_q, max_seqlen_k)
+    need = _attention_bytes(dev, *sizes) if here else prefix_attention_workspace_bytes(*sizes)
     if workspace is not None and workspace.numel() < need:
         _fail("workspace too small: %d < %d bytes", workspace.numel(), need)
     if not sound:

@@ -115,3 +115,21 @@ def test_older_calls_take_no_blocks_freed_on_the_current_stream():
     side.synchronize()
     assert got[2].status() == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert all(torch.equal(a, b) for a, b in zip(again, merged))
+
+
+def test_a_workspace_size_is_kept_for_the_current_device_only(monkeypatch):
+    # the library gives the current device's size: tensors of another device
+    # have to be refused, and nothing be kept under theirs
+    class Other(torch.Tensor):
+        def get_device(self):
+            return 3
+
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32).as_subclass(Other)  # noqa: E731
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8).as_subclass(Other)  # noqa: E731
+    asked = []
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(serve, "_attention_bytes", lambda *a: asked.append(a) or 1 << 20)
+    with pytest.raises(msa.MsaError, match="current device is cuda:0"):
+        msa.msa_prefix_attention(u8(6, 4, 128), u8(4, 2, 128, 256), 1.0, 1.0, 1.0, 0.1, i32(2, 3), i32(3), i32(3), 1, 6, 300)
+    assert not asked
