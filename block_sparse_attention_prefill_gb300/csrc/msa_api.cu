@@ -393,7 +393,7 @@ int verify_impl(const VerifyArgs& a, bool greedy, cudaStream_t st) {
 int prefix_shape(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t prefix, int64_t max_q,
                  int64_t max_k, size_t* bytes) {
   if (B < 0 || T < 0 || Hq <= 0 || Hkv <= 0 || prefix < 0 || max_q < 0 || max_k < max_q ||
-      max_k > (1 << 30) || prefix * kPage > max_k || B >= kI32Max / 2)
+      max_k > (1 << 30) || prefix > max_k / kPage || B >= kI32Max / 2)
     return MSA_ERR_SHAPE;
   if (Hq % Hkv != 0 || Hq / Hkv > kTileM || Hkv > 127) return MSA_ERR_UNSUPPORTED;
   if (T >= kI32Max / kTopK || T * Hq >= kI32Max / kTopK) return MSA_ERR_SHAPE;
@@ -702,7 +702,7 @@ int msa_prefix_attention(const uint8_t* q, const uint8_t* kv, int64_t num_pages,
   size_t need = 0;
   int rc = prefix_shape(B, T, Hq, Hkv, prefix_pages, max_seqlen_q, max_seqlen_k, &need);
   if (rc) return rc;
-  if (num_pages < 0 || num_pages * Hkv * kPage >= kI32Max ||
+  if (num_pages < 0 || num_pages >= kI32Max || num_pages * Hkv * kPage >= kI32Max ||
       bt_stride < ceil_div(max_seqlen_k, kPage) || bt_stride > (1 << 24))
     return MSA_ERR_SHAPE;
   // the largest score of E4M3 codes, 128 * 448^2 products, has to be finite

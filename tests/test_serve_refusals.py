@@ -188,3 +188,12 @@ def test_prefix_attention_takes_every_length_that_it_documents():
         if Hkv == 1:  # (a machine without a GPU counts as one SM, whose range of several heads is refused earlier)
             assert size(B, T, Hq, Hkv, prefix, 1, 128 * pages) == 0
         assert size(B, T, Hq, Hkv, prefix, 1, 128 * pages + 1) == 1
+
+
+def test_prefix_attention_sizes_whose_products_wrap():
+    n = ctypes.c_size_t()
+    for prefix in (2 ** 55, 2 ** 57, 2 ** 57 + 1, 2 ** 62):  # times 128: 2^62, 0, 128 and 0 in 64 bits
+        assert msa.load().msa_prefix_attention_workspace_bytes(2, 6, 4, 2, prefix, 6, 300, ctypes.byref(n)) == 1
+    a = ctypes.c_void_p(4096)
+    for pages in (2 ** 56, 2 ** 57, 2 ** 63 - 1):
+        assert msa.load().msa_prefix_attention(a, a, pages, 1.0, 1.0, 1.0, 0.1, a, 3, a, a, 0, 6, 4, 2, 1, 6, 300, a, 1 << 40, a, None, None, None) == 1
