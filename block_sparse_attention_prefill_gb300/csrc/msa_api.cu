@@ -309,6 +309,8 @@ int kv_cache_impl(KvCacheArgs a, int64_t B, int64_t Hkv, const void* lens, cudaS
   if (!(a.k_scale > 0.f) || !(a.v_scale > 0.f) || !std::isfinite(a.k_scale) ||
       !std::isfinite(a.v_scale))
     return MSA_ERR_SHAPE;
+  if (a.write && a.fp4 && (!std::isfinite(6.f * a.k_scale) || !std::isfinite(6.f * a.v_scale)))
+    return MSA_ERR_SHAPE;
   if (B == 0 || a.T == 0) return MSA_OK;
   if (!a.pool || !a.block_table || !a.cu || (a.write && !lens)) return MSA_ERR_NULL;
   const int64_t es = a.dtype == MSA_DTYPE_F32 ? 4 : 2;

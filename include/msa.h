@@ -482,8 +482,8 @@ MSA_API int msa_decode_noalloc(const uint8_t *q, const uint8_t *kv,
  *                elements of a token and a head (multiples of 16 bytes), so
  *                that parts of a fused projection can be passed as they are
  *   kv / kv4     the pool, as in msa_prefill / msa_prefill_nvfp4
- *   k_scale, v_scale  per-tensor scales (NVFP4: the global scales g), finite
- *                and > 0
+ *   k_scale, v_scale  per-tensor scales (NVFP4: the global scales g, with 6 g
+ *                finite too), finite and > 0
  *   block_table, bt_stride, cu_seqlens_q, cu_seqlens_k, B  as in msa_plan
  *   T            rows of k and v; tokens at or behind cu_seqlens_q[B] (the
  *                padding of a captured batch) are left out

@@ -197,3 +197,16 @@ def test_prefix_attention_sizes_whose_products_wrap():
     a = ctypes.c_void_p(4096)
     for pages in (2 ** 56, 2 ** 57, 2 ** 63 - 1):
         assert msa.load().msa_prefix_attention(a, a, pages, 1.0, 1.0, 1.0, 0.1, a, 3, a, a, 0, 6, 4, 2, 1, 6, 300, a, 1 << 40, a, None, None, None) == 1
+
+
+def test_nvfp4_write_refuses_a_scale_whose_block_scales_overflow():
+    # s = amax / (6 g): 6 g has to be finite in fp32, or every code would be 0
+    a = ctypes.c_void_p(4096)
+
+    def run(fn, ks, vs, T=6):
+        return fn(a, 256, 128, a, 256, 128, 1, a, 4, ks, vs, a, 3, a, a, 2, T, 2, None, None)
+
+    for big in (5.7e37, 1e38, 3.4e38):
+        assert run(msa.load().msa_kv_write_nvfp4, big, 1.0) == 1 and run(msa.load().msa_kv_write_nvfp4, 1.0, big) == 1
+        assert run(msa.load().msa_kv_write, big, big, T=0) == 0  # (nothing is launched)
+    assert run(msa.load().msa_kv_write_nvfp4, 5.6e37, 5.6e37, T=0) == 0
