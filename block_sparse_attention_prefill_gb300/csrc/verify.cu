@@ -194,7 +194,7 @@ verify_kernel(const VerifyArgs a, int seg) {
     const int used = __shfl_sync(0xffffffffu, x, acc & 31);
     if (lane == 0) {
       s_acc = min(acc, drafts);
-      s_used = acc < drafts ? used : -1;
+      s_used = acc < drafts && used < V ? max(used, -1) : -1;  // -1: not a token
     }
     if (rank == 0) {  // the drafts that stand, and -1 behind the next token
       if (lane < n && lane != min(acc, drafts))

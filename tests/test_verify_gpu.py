@@ -300,3 +300,12 @@ def test_accepted_in_place_of_num_drafts():
             room = torch.cat((drafts[b], drafts[b, :1]))
             msa.msa_verify(target[b:b + 1], room[:5].view(1, 5), u[b:b + 1], draft_probs=draft[b:b + 1], num_drafts=counts[b:b + 1], tokens=room.view(1, 6))
             assert np.array_equal(room.cpu().numpy(), want[0][b])
+
+
+def test_certain_drafts_that_are_no_tokens():
+    for V in (40, 5003, 200003):
+        target, _, drafts, u = _inputs(8, 2, V, torch.float32, V)
+        drafts[0, 0], drafts[1, 0], drafts[2, 0] = -2 ** 31, 2 ** 31 - 1, -1
+        drafts[3, 0], drafts[4, 0], drafts[5, 0], drafts[6, 1] = V, -2 ** 31 + 1, -2 ** 31 + 4096, -2 ** 31 + V
+        want = _check(target, None, drafts, u)
+        assert not want[1][:6].any()
