@@ -196,13 +196,35 @@ def msa_kv_write_nvfp4(k, v, kv4, k_scale, v_scale, block_table, cu_seqlens_q, c
            cu_seqlens_k, status, stream)
 
 
-def _check_read(fp4, kv, block_table, cu, starts, k, v, status):
-    _pool(kv, fp4)
+def _apart_rows(t, name):
+    """Refuses rows [T, Hkv, 128] of an output that share elements (the larger
+    stride has to step over all rows of the smaller)."""
+    (T, H, _), (token, head, _) = t.shape, t.stride()
+    reach = HEAD_DIM
+    for stride, n in sorted(((token, T), (head, H))):
+        if n > 1 and stride < reach:
+            _fail("rows of %s must not overlap", name)
+        if n > 1:
+            reach += stride * (n - 1)
+
+
+def _check_read(fp4, kv, block_table, cu, T, starts, k, v, status):
+    _, Hkv = _pool(kv, fp4)
     B = _requests(cu, "cu_tokens")
     _table(block_table, B)
     if starts is not None:
         _tensor(starts, "starts", _I32, (B,))
     _status(status)
+    if (k is None) != (v is None):
+        _fail("give both of k and v, or neither")
+    if k is not None:
+        for t, name in ((k, "k"), (v, "v")):
+            _rows(t, name, (T, Hkv, HEAD_DIM))
+            _apart_rows(t, name)
+        if k.dtype != v.dtype:
+            _fail("k and v have different dtypes: %s and %s", k.dtype, v.dtype)
+        if T > 0 and k.data_ptr() == v.data_ptr():
+            _fail("k and v must not share rows")
     _place(kv, block_table, cu, starts, k, v, status)
 
 
@@ -223,26 +245,20 @@ def _read(name, fp4, kv, k_scale, v_scale, block_table, cu, T, starts, dtype, k,
             and dev == block_table.get_device() == cu.get_device() == torch._C._cuda_getDevice())
     except _NOT_SOUND:
         sound = False
-    if not sound:
-        _check_read(fp4, kv, block_table, cu, starts, k, v, status)
-    handle = _handle(stream, dev)
     T = int(T)
     if T < 0:
         _fail("total_tokens must not be negative")
-    if (k is None) != (v is None):
-        _fail("give both of k and v, or neither")
-    shape = (T, pool[1], HEAD_DIM)
+    if not sound:
+        _check_read(fp4, kv, block_table, cu, T, starts, k, v, status)
+    handle = _handle(stream, dev)
     if k is None:
+        shape = (T, pool[1], HEAD_DIM)
         if dtype not in _TYPES:
             _fail("dtype must be one of %s", tuple(_TYPES))
         k, v = _new(shape, dtype, dev, handle), _new(shape, dtype, dev, handle)
         ks = vs = (pool[1] * HEAD_DIM, HEAD_DIM)
     else:
-        ks, vs = _rows(k, "k", shape), _rows(v, "v", shape)
-        if k.dtype != v.dtype:
-            _fail("k and v have different dtypes: %s and %s", k.dtype, v.dtype)
-        if (T > 1 and 0 in (ks[0], vs[0])) or (pool[1] > 1 and 0 in (ks[1], vs[1])):
-            _fail("rows of k and v must not overlap")
+        ks, vs = k.stride(), v.stride()
     rc = getattr(load(), name)(kv.data_ptr(), pool[0], k_scale, v_scale, block_table.data_ptr(),
                                table[1], cu.data_ptr(), _ptr(starts), table[0], T, pool[1],
                                k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],

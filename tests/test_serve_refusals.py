@@ -210,3 +210,16 @@ def test_nvfp4_write_refuses_a_scale_whose_block_scales_overflow():
         assert run(msa.load().msa_kv_write_nvfp4, big, 1.0) == 1 and run(msa.load().msa_kv_write_nvfp4, 1.0, big) == 1
         assert run(msa.load().msa_kv_write, big, big, T=0) == 0  # (nothing is launched)
     assert run(msa.load().msa_kv_write_nvfp4, 5.6e37, 5.6e37, T=0) == 0
+
+
+def test_read_refuses_rows_that_overlap():
+    c = _cache()
+    run = lambda k, v: _err(msa.msa_kv_read, c["kv"], 1.0, 1.0, c["table"], c["cu_q"], 6, k=k, v=v)  # noqa: E731
+    room = torch.zeros(6 * 2 * 256 + 256)
+    rows = lambda at, token, head: room.as_strided((6, 2, 128), (token, head, 1), at)  # noqa: E731
+    good = rows(0, 512, 256)
+    for bad in (rows(0, 0, 128), rows(0, 512, 0), rows(0, 64, 512), rows(0, 128, 128), rows(0, 256, 192), rows(0, 256, 256)):
+        assert "rows of k must not overlap" in run(bad, torch.zeros(6, 2, 128)) and "rows of v must not overlap" in run(torch.zeros(6, 2, 128), bad)
+    assert "k and v must not share rows" in run(good, good)
+    for k, v in ((good, rows(128, 512, 256)), (rows(0, 256, 128), torch.zeros(6, 2, 128)), (rows(0, 128, 768), rows(1536, 128, 768))):
+        assert "CUDA" in run(k, v)
