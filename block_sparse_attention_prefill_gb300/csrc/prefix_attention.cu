@@ -60,8 +60,8 @@ namespace {
 
 // Cost of a tile: its pages by kind, and its start and end (Q, epilogue), in
 // the proportions measured (about 0.9, 1.8 and 4.5 us).
-constexpr int kCostSolo = 1, kCostPair = 2, kCostTile = 5;
-constexpr int kMinShare = 6;  // least cost of a CTA's range
+constexpr int kCostSolo = 2, kCostPair = 4, kCostTile = 10;
+constexpr int kMinShare = 12;  // least cost of a CTA's range
 
 // Behind every key (positions are below 2^30), with room for a tile's tokens.
 constexpr int kNoMask = INT_MAX - 1024;
@@ -72,12 +72,14 @@ struct __align__(16) Tile {
   int ntok;    // tokens
   int page0;   // first logical page
   int npages;
-  int start;   // cost of the head's tiles before this one
+  uint32_t start;  // cost of the head's tiles before this one
   int pos0;    // position of tok0, or kNoMask (the shared pages)
   int seq;     // keys of the request (a page's keys behind it are not read)
 };
 struct PlanHead {
-  int ntiles, cost, shared_tiles;
+  int ntiles;
+  uint32_t cost;  // of all tiles
+  int shared_tiles;
   int bad;  // lengths inconsistent: every output row becomes empty
   int T;    // tokens of the batch
   int pad[3];
@@ -146,30 +148,30 @@ __device__ __forceinline__ RowPlace row_place(int off, int ntok, int C, int G) {
 constexpr int kPlanThreads = 1024;
 
 template <int kThreads>
-__device__ __forceinline__ int block_excl_scan(int v, int* total) {
-  __shared__ int sums[33];
+__device__ __forceinline__ uint32_t block_excl_scan(uint32_t v, uint32_t* total) {
+  __shared__ uint32_t sums[33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = v;
+  uint32_t incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int n = __shfl_up_sync(0xffffffffu, incl, o);
+    const uint32_t n = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += n;
   }
   if (lane == 31) sums[warp] = incl;
   __syncthreads();
   if (warp == 0) {
-    const int s = lane < kThreads / 32 ? sums[lane] : 0;
-    int si = s;
+    const uint32_t s = lane < kThreads / 32 ? sums[lane] : 0;
+    uint32_t si = s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(0xffffffffu, si, o);
+      const uint32_t n = __shfl_up_sync(0xffffffffu, si, o);
       if (lane >= o) si += n;
     }
     sums[lane] = si - s;
     if (lane == 31) sums[32] = si;
   }
   __syncthreads();
-  const int r = sums[warp] + incl - v;
+  const uint32_t r = sums[warp] + incl - v;
   *total = sums[32];
   __syncthreads();
   return r;
@@ -214,10 +216,10 @@ __device__ __forceinline__ PlanHead make_plan(const PlanParams& p, int* req) {
         atomicAdd(&s_rate, rate_of((int)q, p.C));
       }
     }
-    int total;
-    const int before = block_excl_scan<kThreads>(n, &total);
+    uint32_t total;
+    const int before = (int)block_excl_scan<kThreads>(n, &total);
     if (b < p.B) req[b] = run + before;
-    run += total;
+    run += (int)total;
   }
   if (bad) s_bad = 1;
   __syncthreads();  // also makes req visible to this CTA
@@ -237,7 +239,7 @@ __device__ __forceinline__ PlanHead make_plan(const PlanParams& p, int* req) {
     shared_tiles = 0;
   const int prefix = shared_tiles > 0 ? p.prefix : 0;
   const int ntiles = shared_tiles + run;
-  int cost = 0;
+  uint32_t cost = 0;
   for (int i0 = 0; i0 < ntiles; i0 += kThreads) {
     const int i = i0 + tid;
     Tile t = {};
@@ -269,7 +271,7 @@ __device__ __forceinline__ PlanHead make_plan(const PlanParams& p, int* req) {
       }
       c = tile_cost(t.ntok, t.npages, p.C);
     }
-    int total;
+    uint32_t total;
     t.start = cost + block_excl_scan<kThreads>(c, &total);
     cost += total;
     if (i < ntiles)
@@ -365,7 +367,7 @@ struct Walk {
     h = left > 0 ? (int)(x / hd.cost) : 0;
     if (left > 0) {
       ahead = tile_at(tile);
-      at = (int)(x - (int64_t)h * hd.cost) - ahead.start;
+      at = (int)(x - (int64_t)h * hd.cost - ahead.start);
     }
   }
   __device__ __forceinline__ const Tile& tile_at(int i) const {
@@ -530,7 +532,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
     const int64_t total = (int64_t)hd.cost * p.Hkv;
     const int64_t x = blockIdx.x * share_of(total, gridDim.x);
     if (x < total) {
-      const int r = (int)(x % hd.cost);
+      const uint32_t r = (uint32_t)(x % hd.cost);
       auto start = [&](int i) {
         return p.tiles[i < hd.shared_tiles ? i : p.own_base + i - hd.shared_tiles].start;
       };
@@ -1086,7 +1088,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
         t.tok0 = ti * 2 * p.C;
         t.ntok = min(2 * p.C, hd.T - t.tok0);
         t.npages = p.prefix;
-        t.start = ti * tile_cost(2 * p.C, p.prefix, p.C);
+        t.start = (uint32_t)ti * tile_cost(2 * p.C, p.prefix, p.C);
       }
       const int rate = tile_rate(t.ntok, p.C);
       const int64_t share = share_of((int64_t)hd.cost * p.Hkv, p.ctas);
@@ -1248,10 +1250,12 @@ bool layout(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t prefix, int64
   const int64_t G = Hq / Hkv, C = kTileM / G;
   const int64_t tiles = max_tiles(B, T, C, prefix);
   // the cost of a head's tiles, that of a CTA's range and the rows of the
-  // partials in range of their integers (places in 64 bits cost the attention
-  // kernel 1 to 7 %, by its registers)
+  // partials in range of their integers (64-bit places cost the attention
+  // kernel 1 to 7 %, by its registers).  A machine without a GPU, where sizes
+  // are asked too, counts as one SM.
   const double cost = (double)tiles * (double)(ceil_div(max_k, kPage) * kCostPair + kCostTile);
-  if (cost > (double)INT_MAX || cost * (double)Hkv > (double)INT_MAX * ctas) return false;
+  if (cost > (double)UINT32_MAX || cost * (double)Hkv > (double)INT_MAX * (ctas > 1 ? ctas : 152))
+    return false;
   const int64_t rows = 256 * ((int64_t)ctas + 1) + Hkv * (prefix > 0 ? 2 : 1) * T * G;
   if (rows >= INT_MAX || ctas > kMaxParts) return false;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };

@@ -551,10 +551,11 @@ MSA_API int msa_kv_read_nvfp4(const uint8_t *kv4, int64_t num_pages, float k_sca
  *                 tokens: once for all of them, or by each where that is
  *                 less work (one request, long chunks, a page or two)
  *   max_seqlen_q, max_seqlen_k  host-known bounds, max_seqlen_k <= 2^30 and
- *                 n (2 ceil(max_seqlen_k / 128) + 5) < 2^31 for n tiles of t
+ *                 n (4 ceil(max_seqlen_k / 128) + 10) < 2^32 for n tiles of t
  *                 tokens, t = 2 floor(128 Hkv / Hq): n = min(T, ceil(T / t) +
  *                 B), and ceil(T / t) more where prefix_pages > 0 (a million
- *                 tokens of one request with Hq / Hkv = 16 are within it)
+ *                 tokens of one request with Hq / Hkv = 16 are within it);
+ *                 with more than 76 KV heads, this times Hkv < 2^31 SMs
  *   workspace     msa_prefix_attention_workspace_bytes() bytes, 256-byte
  *                 aligned; calls whose work may overlap need one each
  *   out           bf16 [T][Hq][128]

@@ -176,17 +176,16 @@ def test_verify_refuses_outputs_over_inputs():
 def test_prefix_attention_takes_every_length_that_it_documents():
     n = ctypes.c_size_t()
     size = lambda *v: msa.load().msa_prefix_attention_workspace_bytes(*v, ctypes.byref(n))  # noqa: E731
-    for B, T, Hq, Hkv, prefix, max_k in ((32, 32, 8, 1, 0, 2 ** 30), (127, 127, 8, 1, 0, 2 ** 30), (1, 2 ** 20, 16, 1, 0, 2 ** 20), (4, 2 ** 15, 128, 1, 8000, 2 ** 20)):
+    for B, T, Hq, Hkv, prefix, max_k in ((32, 32, 16, 2, 0, 2 ** 30), (127, 127, 16, 2, 0, 2 ** 30), (1, 2 ** 20, 16, 1, 0, 2 ** 20), (4, 2 ** 15, 128, 1, 8000, 2 ** 20)):
         assert size(B, T, Hq, Hkv, prefix, min(T, max_k), max_k) == 0
         rows = Hkv * (2 if prefix else 1) * T * (Hq // Hkv)
         assert rows * 516 < n.value < (rows + 256 * 200) * 516 + 32 * 2 * (T + B) + 4 * B + 2000
-    # either side of n (2 ceil(max_seqlen_k / 128) + 5) < 2^31
+    # either side of n (4 ceil(max_seqlen_k / 128) + 10) < 2^32
     for B, T, Hq, Hkv, prefix in ((128, 128, 16, 2, 0), (5000, 7000, 12, 4, 3), (1, 2 ** 20, 31, 31, 0), (3, 2 ** 18, 128, 1, 1)):
         t = 2 * (128 * Hkv // Hq)
         tiles = min(T, -(-T // t) + B) + (-(-T // t) if prefix else 0)
-        pages = min(2 ** 23, ((2 ** 31 - 1) // tiles - 5) // 2)
-        if Hkv == 1:  # (a machine without a GPU counts as one SM, whose range of several heads is refused earlier)
-            assert size(B, T, Hq, Hkv, prefix, 1, 128 * pages) == 0
+        pages = min(2 ** 23, ((2 ** 32 - 1) // tiles - 10) // 4)
+        assert size(B, T, Hq, Hkv, prefix, 1, 128 * pages) == 0
         assert size(B, T, Hq, Hkv, prefix, 1, 128 * pages + 1) == 1
 
 
