@@ -6,7 +6,7 @@
 // query row, a reference m near the running maximum, l = sum 2^(s_j - m) and
 // O = sum 2^(s_j - m) v_j over a range of pages; ranges are merged by their
 // l and m (combine kernel below).  QK is an E4M3 MMA, exact products with
-// fp32 sums; the probabilities are rounded to f16 (2^-12 of their value at
+// fp32 sums; the probabilities are rounded to f16 (2^-11 of their value at
 // most) and V widened to f16 (exact), so that the bf16 output is limited by
 // its own rounding.
 //
@@ -32,13 +32,14 @@
 // lets QK of one unit, softmax of the next and PV run at the same time within
 // a stream.
 //
-// Bounds and what was measured (whole calls): 512 tokens x 16 heads over 128k
-// shared keys 337 us, 1.65 PFLOP/s; QK at twice and PV at the bf16 rate would
+// Bounds and what was measured (GPU time of a call's launches, replayed from a
+// graph; a call of its own takes 4-8 us more): 512 tokens x 16 heads over 128k
+// shared keys 338 us, 1.64 PFLOP/s; QK at twice and PV at the bf16 rate would
 // take 217.  A unit of both streams takes 1440 cycles, of which the tensor
 // pipes are busy 0.6 (ncu), the issue slots 0.58: what is left is the latency
 // of the hops S -> softmax -> P -> PV -> next QK, with all of tensor memory
-// in use.  16 requests of 8 tokens over 80k keys of their own each: 129 us, 678 MB at
-// 5.25 TB/s.  16 single tokens over 32k shared keys: 21.7 us, latency (plan
+// in use.  16 requests of 8 tokens over 83k keys of their own each: 130 us, 678 MB at
+// 5.2 TB/s.  16 single tokens over 32k shared keys: 21.7 us, latency (plan
 // and first loads 4, 6 units 5, epilogue 3, combine 5 us).
 #include <cuda.h>
 
@@ -324,6 +325,7 @@ constexpr int kHalf = kPage / 2;  // keys of a unit: of one S, and one P
 // 128 s on, O at 256 + 128 s.  P (f16, 32 columns) replaces its S.
 constexpr int kTmemCols = 512, kColO = 256;
 // 512 threads with 128 registers each, shared out anew among the roles
+// (of the launch's 128, 108 bytes are spilled)
 constexpr int kRegsControl = 120, kRegsSoftmax = 144, kRegsWiden = 104;
 static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsWiden <= 512, "registers");
 // P is kept as 2^(s - m + 7): a unit whose P add up to at most 2^15 has none

@@ -21,16 +21,21 @@
 // holds the threshold reads its own few hundred weights once more (from L2)
 // to place it.  Bound: HBM for large batches, else the latency of the
 // dependent steps (gather, row, cluster barrier, placing).
-// Measured: 64 requests, 200003 fp32 values a row 25 us, 102 MB at 4.1 TB/s;
-// one request of 32000 5.3 us.
+// Measured (GPU time, replayed from a graph): 64 requests, 200003 fp32 values
+// a row 24.8 us, 102 MB at 4.1 TB/s, and 200000 (rows on 16 bytes) 21.3; one
+// request of 32000 4.3 us.  64 registers a thread, four CTAs an SM; the odd
+// rows' kernels spill 28 bytes.
 //
 // Greedy: draft i stands iff it is the first of the largest values of its
 // row.  The same cluster scans the request's rows in order, each CTA its
 // eighth, each warp by itself; a warp that has seen a draft beaten tells all
 // CTAs (a minimum in their shared memory, no barrier), and rows behind it
 // are left out: they cannot matter.
-// Measured: 64 requests of 8 rows of 131072 bf16 values, drafts that fall
-// anywhere: 23.5 us (5.7 TB/s counting every row; two thirds of them are read).
+// Measured: 64 requests of 8 rows of 131072 bf16 values, three drafts of ten
+// fall: 23.4 us.  The rows up to each request's first fallen draft are 51 MB
+// (7.5 us at a copy's rate); 61 of 134 MB are read, at 2.6 TB/s: the requests
+// whose drafts stand long are read row after row by their 8 CTAs, with too few
+// bytes in flight for the SMs that are left.
 #include <algorithm>
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -462,8 +467,8 @@ cudaError_t launch_verify_type(const VerifyArgs& a, bool greedy, cudaStream_t st
   constexpr int N = 16 / sizeof(T);
   // 16-byte loads where every row starts on 16 bytes; else one value a load
   // (an odd vocabulary's rows start anywhere).  Greedy, 64 x 8 bf16 rows of
-  // 131072: 23.5 us, by single values 44; one row of 32000 fp32 drawn from:
-  // 5.3 us and 5.7
+  // 131072: 25 us, by single values 48; 64 rows of 200000 fp32 drawn from:
+  // 21.3 us and 25.2, one row of 32000 4.3 either way
   const bool vec = vector_rows<T>(a.target, a.t_req, a.t_row) &&
                    (greedy || !a.draft || vector_rows<T>(a.draft, a.d_req, a.d_row));
   const int seg = (int)(ceil_div(ceil_div(a.V, kCluster), 32 * N) * (32 * N));

@@ -182,7 +182,8 @@ def msa_kv_write(k, v, kv, k_scale, v_scale, block_table, cu_seqlens_q, cu_seqle
     k, v [T, Hkv, 128] in fp32, bf16 or fp16 (any token and head strides that
     keep rows on 16 bytes); they are the last q_len positions of each request,
     as in msa_plan.  Rows behind cu_seqlens_q's last are left out.  status: an
-    int32 [1] tensor that MSA_STATUS_* bits are OR-ed into."""
+    int32 [1] tensor that MSA_STATUS_* bits are OR-ed into; tokens that it
+    would tell of are not written, with it or without."""
     _write("msa_kv_write", False, k, v, kv, k_scale, v_scale, block_table, cu_seqlens_q,
            cu_seqlens_k, status, stream)
 
@@ -274,7 +275,8 @@ def msa_kv_read(kv, k_scale, v_scale, block_table, cu_tokens, total_tokens, star
     positions starts[b] .. (0 without starts) become rows cu_tokens[b] ..
     cu_tokens[b + 1] - 1 of k and v [total_tokens, Hkv, 128].  k and v may be
     given (any of the three types, strided); rows behind cu_tokens' last, and
-    rows whose page is not valid, keep their contents.  Returns (k, v)."""
+    rows whose page is not valid, keep their contents, which in new tensors
+    are undefined.  status as in msa_kv_write.  Returns (k, v)."""
     return _read("msa_kv_read", False, kv, k_scale, v_scale, block_table, cu_tokens,
                  total_tokens, starts, dtype, k, v, status, stream)
 
@@ -329,8 +331,10 @@ def msa_prefix_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_
     share their first prefix_pages pages, whose part is computed once for all
     (0: nothing shared).  q E4M3 [T, Hq, 128]; lengths as in msa_plan, all
     queries behind the shared pages.  status: an int32 [1] tensor that
-    MSA_STATUS_* bits are OR-ed into.  Returns (out bf16 [T, Hq, 128], lse
-    fp32 [T, Hq] or None)."""
+    MSA_STATUS_* bits are OR-ed into; without it nothing tells of lengths that
+    do not fit (all rows 0) or entries that are no pages (left out).  Rows
+    behind cu_seqlens_q's last keep their contents, which in new tensors are
+    undefined.  Returns (out bf16 [T, Hq, 128], lse fp32 [T, Hq] or None)."""
     try:
         pool, table, (T, Hq, dim) = kv.shape, block_table.shape, q.shape
         dev = kv.get_device()

@@ -557,17 +557,22 @@ MSA_API int msa_kv_read_nvfp4(const uint8_t *kv4, int64_t num_pages, float k_sca
  *                 tokens of one request with Hq / Hkv = 16 are within it);
  *                 with more than 76 KV heads, this times Hkv < 2^31 SMs
  *   workspace     msa_prefix_attention_workspace_bytes() bytes, 256-byte
- *                 aligned; calls whose work may overlap need one each
+ *                 aligned; calls whose work may overlap need one each.  Every
+ *                 row's result goes through it in fp32: about 516 T Hq bytes,
+ *                 twice that with a prefix (16 k tokens x 64 heads behind a
+ *                 prefix: 1.1 GB), and 20 MB
  *   out           bf16 [T][Hq][128]
  *   lse           fp32 [T][Hq] natural-log sum of exp(score), or NULL
  *   status        device word that MSA_STATUS_* bits are OR-ed into, or NULL:
  *                 BAD_SEQLENS (lengths inconsistent, past the bounds, or
  *                 queries inside the shared pages: the whole call then gives
  *                 zeros and lse -inf on all T rows), BAD_BLOCK (an entry that
- *                 is not a page: its keys are left out), TIMEOUT
+ *                 is not a page: its keys are left out), TIMEOUT (rows may
+ *                 hold anything).  With NULL nothing tells of these
  * QK runs as E4M3 MMAs, the probabilities are rounded to f16 and V widened to
- * f16 (exactly), sums are fp32: the output is within its bf16 rounding of
- * exact attention for all practical purposes.  A NaN among the K of a key a
+ * f16 (exactly), sums are fp32: each probability has an error of at most 2^-11
+ * of itself or 2^-32 of the row's largest, whichever is more, and the output
+ * is within its bf16 rounding of exact attention for all practical purposes.  A NaN among the K of a key a
  * row attends to makes the row NaN, one among its V that column; codes behind
  * a request's end, or behind a row's position, have no effect on the row.
  * Scores have to be finite: q_scale * k_scale * softmax_scale below about
