@@ -15,6 +15,8 @@ Calls (same names as the C ABI, without the ``msa_`` prefix where noted):
   msa_nvfp4_to_e4m3   NVFP4 pages -> the E4M3 pages those calls read
   msa_kv_write, msa_kv_read (and _nvfp4)   new K/V tokens into the pages, and
                 cached tokens back out of them
+  msa_rope_write (and _nvfp4)   Q and K normalised and rotated, Q quantised,
+                K and V written into the pages; MsaRope says how a model rotates
   msa_prefix_attention   dense attention behind pages that a batch shares
   msa_verify, msa_verify_greedy   which drafted tokens stand, and the next one
 """
@@ -57,6 +59,14 @@ class MsaPlanStruct(ctypes.Structure):
                [(n, ctypes.c_void_p) for n in _PTR]
 
 
+class MsaRopeStruct(ctypes.Structure):
+    """Mirror of ``msa_rope_t``."""
+    _fields_ = [("pairs", ctypes.c_int64), ("interleaved", ctypes.c_int64),
+                ("axes", ctypes.c_int64), ("eps", ctypes.c_double),
+                ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+                ("turns", ctypes.c_uint64 * 64), ("axis", ctypes.c_uint8 * 64)]
+
+
 class MsaError(RuntimeError):
     pass
 
@@ -82,6 +92,9 @@ def load():
                i64, i64, i64, P, P], i32)
     _READ = ([P, i64, f32, f32, P, i64, P, P, i64, i64, i64, P, i64, i64, P,
               i64, i64, i32, P, P], i32)
+    _ROPE = ([ctypes.POINTER(MsaRopeStruct), P, P, i64, i64, P, i64, i64, P, i64,
+              i64, i32, P, i32, f32, P, i64, f32, f32, P, i64, P, P, i64, i64,
+              i64, i64, P, P], i32)
     sigs = {
         "msa_version": ([], i32),
         "msa_status_string": ([i32], ctypes.c_char_p),
@@ -118,6 +131,10 @@ def load():
         "msa_kv_write_nvfp4": _WRITE,
         "msa_kv_read": _READ,
         "msa_kv_read_nvfp4": _READ,
+        "msa_rope_turns": ([ctypes.POINTER(ctypes.c_double), i64,
+                            ctypes.POINTER(ctypes.c_uint64)], i32),
+        "msa_rope_write": _ROPE,
+        "msa_rope_write_nvfp4": _ROPE,
         "msa_prefix_attention_workspace_bytes": ([i64, i64, i64, i64, i64, i64,
                                                   i64, SZ], i32),
         "msa_prefix_attention": ([P, P, i64, f32, f32, f32, f32, P, i64, P, P,
@@ -629,3 +646,5 @@ def run_workload(w, stream=None):
 from .serve import (msa_kv_read, msa_kv_read_nvfp4, msa_kv_write,  # noqa: E402,F401
                     msa_kv_write_nvfp4, msa_prefix_attention,
                     msa_verify, msa_verify_greedy, prefix_attention_workspace_bytes)
+from .tree import (MsaRope, msa_rope_turns, msa_rope_write,  # noqa: E402,F401
+                   msa_rope_write_nvfp4)

@@ -144,6 +144,36 @@ struct KvCacheArgs {
 };
 cudaError_t launch_kv_cache(const KvCacheArgs& a, cudaStream_t stream);
 
+// Rotation, quantisation and cache write of a projection's output
+// (rope_write.cu).  q, k and v are [T][heads][128] with strides in elements.
+struct RopeArgs {
+  const void *q, *k, *v;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+  int dtype;               // MSA_DTYPE_*
+  void* q_out;             // [T][Hq][128] E4M3 codes, or bf16
+  bool q_bf16;
+  float q_scale, k_scale, v_scale;
+  uint8_t* pool;
+  int64_t num_pages;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  const int32_t* cu;       // [B + 1] the new tokens by request
+  const int32_t* cu_k;     // [B + 1] sequence lengths
+  const int32_t* positions;  // [axes][T], or NULL: the cache positions
+  int B;
+  int64_t T;
+  int Hq, Hkv;
+  uint32_t* status;        // or NULL
+  bool fp4;
+  const float *q_norm, *k_norm;  // [128] or NULL
+  float eps;
+  int pairs, axes;
+  bool interleaved;
+  uint64_t turns[MSA_ROPE_MAX_PAIRS];
+  uint8_t axis[MSA_ROPE_MAX_PAIRS];
+};
+cudaError_t launch_rope_write(const RopeArgs& a, cudaStream_t stream);
+
 // Draft verification (verify.cu).  Row (b, i) of target is at b * t_req +
 // i * t_row elements, of draft_probs at b * d_req + i * d_row.
 struct VerifyArgs {

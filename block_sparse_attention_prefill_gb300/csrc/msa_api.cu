@@ -374,6 +374,95 @@ int kv_read_impl(const uint8_t* pool, int64_t num_pages, float k_scale, float v_
   return kv_cache_impl(a, B, Hkv, nullptr, static_cast<cudaStream_t>(stream));
 }
 
+// 1 / (2 pi) modulo 2^-128 as two words of 64 bits behind the point, and the
+// next 64 bits: 1 / 2 pi = 0.28BE60DB9391054A 7F09D5F47D4D3770 36D8A5664F10E410 ...
+// (hexadecimal).
+constexpr uint64_t kTurn[3] = {0x28BE60DB9391054Aull, 0x7F09D5F47D4D3770ull,
+                               0x36D8A5664F10E410ull};
+
+// f / 2 pi modulo 1 in steps of 2^-64, rounded to nearest: f = m 2^e with a
+// whole number m of 53 bits, times the 192 bits above in whole numbers.  The
+// product's error, m 2^(e - 192), is below 2^-100 for |f| < 2^32.
+bool turns_of(double f, uint64_t* out) {
+  if (!std::isfinite(f) || std::fabs(f) >= 4294967296.0) return false;
+  int e;
+  const double frac = std::frexp(std::fabs(f), &e);
+  const uint64_t m = (uint64_t)std::ldexp(frac, 53);
+  e -= 53;  // at most -21
+  // w[0]: whole turns (m's upper part), w[1 .. 3] behind the point
+  uint64_t w[4];
+  unsigned __int128 carry = 0;
+  for (int i = 2; i >= 0; --i) {
+    carry += (unsigned __int128)m * kTurn[i];
+    w[i + 1] = (uint64_t)carry;
+    carry >>= 64;
+  }
+  w[0] = (uint64_t)carry;
+  // shift right by -e bits; what falls off below 2^-64 turns decides the rounding
+  int s = -e;
+  while (s >= 64) {
+    for (int i = 3; i > 0; --i) w[i] = w[i - 1];
+    w[0] = 0;
+    s -= 64;
+    if (-e - s >= 256) break;
+  }
+  if (-e - s >= 256) {
+    for (uint64_t& x : w) x = 0;
+    s = 0;
+  }
+  if (s > 0)
+    for (int i = 3; i >= 0; --i) w[i] = (w[i] >> s) | (i > 0 ? w[i - 1] << (64 - s) : 0);
+  const uint64_t turn = w[1] + (w[2] >> 63);
+  *out = f < 0 ? 0 - turn : turn;
+  return true;
+}
+
+int rope_write_impl(const msa_rope_t* rope, RopeArgs a, int64_t B, int64_t Hq, int64_t Hkv,
+                    cudaStream_t st) {
+  if (!rope) return MSA_ERR_NULL;
+  if (a.dtype != MSA_DTYPE_F32 && a.dtype != MSA_DTYPE_BF16 && a.dtype != MSA_DTYPE_F16)
+    return MSA_ERR_UNSUPPORTED;
+  if (rope->pairs < 0 || rope->pairs > MSA_ROPE_MAX_PAIRS || rope->axes < 1 ||
+      rope->axes > MSA_ROPE_MAX_AXES || !(rope->eps >= 0.0) || !std::isfinite((float)rope->eps))
+    return MSA_ERR_SHAPE;
+  for (int64_t j = 0; j < rope->pairs; ++j)
+    if (rope->axis[j] >= rope->axes) return MSA_ERR_SHAPE;
+  if (B < 0 || B >= kI32Max / 2 || a.T < 0 || a.T >= kI32Max || Hkv < 1 || Hkv > 127 || Hq < 0 ||
+      Hq > 127 * kTileM || a.num_pages < 0 || a.num_pages >= kI32Max || a.bt_stride < 0 ||
+      a.bt_stride > (1 << 24))
+    return MSA_ERR_SHAPE;
+  if (!(a.k_scale > 0.f) || !(a.v_scale > 0.f) || !std::isfinite(a.k_scale) ||
+      !std::isfinite(a.v_scale))
+    return MSA_ERR_SHAPE;
+  if (Hq > 0 && !a.q_bf16 && (!(a.q_scale > 0.f) || !std::isfinite(a.q_scale)))
+    return MSA_ERR_SHAPE;
+  if (a.fp4 && (!std::isfinite(6.f * a.k_scale) || !std::isfinite(6.f * a.v_scale)))
+    return MSA_ERR_SHAPE;
+  if (B == 0 || a.T == 0) return MSA_OK;
+  if (!a.pool || !a.block_table || !a.cu || !a.cu_k || (Hq > 0 && !a.q_out)) return MSA_ERR_NULL;
+  const int64_t es = a.dtype == MSA_DTYPE_F32 ? 4 : 2;
+  int rc = Hq > 0 ? check_rows(a.q, a.q_token, a.q_head, a.T, Hq, es) : MSA_OK;
+  if (!rc) rc = check_rows(a.k, a.k_token, a.k_head, a.T, Hkv, es);
+  if (!rc) rc = check_rows(a.v, a.v_token, a.v_head, a.T, Hkv, es);
+  if (rc) return rc;
+  if (!aligned(a.pool, 16) || !aligned(a.q_out, 16) || !aligned(a.block_table, 4) ||
+      !aligned(a.cu, 4) || !aligned(a.cu_k, 4) || !aligned(a.positions, 4) ||
+      !aligned(a.status, 4) || !aligned(rope->q_norm, 4) || !aligned(rope->k_norm, 4))
+    return MSA_ERR_ALIGN;
+  a.B = (int)B;
+  a.Hq = (int)Hq;
+  a.Hkv = (int)Hkv;
+  a.q_norm = rope->q_norm;
+  a.k_norm = rope->k_norm;
+  a.eps = (float)rope->eps;
+  a.pairs = (int)rope->pairs;
+  a.axes = (int)rope->axes;
+  a.interleaved = rope->interleaved != 0;
+  std::copy_n(rope->turns, MSA_ROPE_MAX_PAIRS, a.turns);
+  std::copy_n(rope->axis, MSA_ROPE_MAX_PAIRS, a.axis);
+  return cuda_rc(launch_rope_write(a, st));
+}
+
 int verify_impl(const VerifyArgs& a, bool greedy, cudaStream_t st) {
   if (a.dtype != MSA_DTYPE_F32 && a.dtype != MSA_DTYPE_BF16 && a.dtype != MSA_DTYPE_F16)
     return MSA_ERR_UNSUPPORTED;
@@ -684,6 +773,70 @@ int msa_kv_read_nvfp4(const uint8_t* kv4, int64_t num_pages, float k_scale, floa
   return kv_read_impl(kv4, num_pages, k_scale, v_scale, block_table, bt_stride, cu_tokens, starts,
                       B, T, Hkv, k, k_token, k_head, v, v_token, v_head, dtype, status, stream,
                       true);
+}
+
+int msa_rope_turns(const double* inv_freq, int64_t n, uint64_t* turns) {
+  if (n < 0) return MSA_ERR_SHAPE;
+  if (n > 0 && (!inv_freq || !turns)) return MSA_ERR_NULL;
+  for (int64_t j = 0; j < n; ++j)
+    if (!turns_of(inv_freq[j], turns + j)) return MSA_ERR_SHAPE;
+  return MSA_OK;
+}
+
+int msa_rope_write(const msa_rope_t* rope, const int32_t* positions, const void* q,
+                   int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+                   int64_t k_head, const void* v, int64_t v_token, int64_t v_head, int dtype,
+                   void* q_out, int q_bf16, float q_scale, uint8_t* kv, int64_t num_pages,
+                   float k_scale, float v_scale, const int32_t* block_table, int64_t bt_stride,
+                   const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int64_t B,
+                   int64_t T, int64_t Hq, int64_t Hkv, uint32_t* status, void* stream) {
+  RopeArgs a = {};
+  a.q = q, a.k = k, a.v = v;
+  a.q_token = q_token, a.q_head = q_head, a.k_token = k_token, a.k_head = k_head;
+  a.v_token = v_token, a.v_head = v_head;
+  a.dtype = dtype;
+  a.q_out = q_out;
+  a.q_bf16 = q_bf16 != 0;
+  a.q_scale = q_scale, a.k_scale = k_scale, a.v_scale = v_scale;
+  a.pool = kv;
+  a.num_pages = num_pages;
+  a.block_table = block_table;
+  a.bt_stride = bt_stride;
+  a.cu = cu_seqlens_q;
+  a.cu_k = cu_seqlens_k;
+  a.positions = positions;
+  a.T = T;
+  a.status = status;
+  a.fp4 = false;
+  return rope_write_impl(rope, a, B, Hq, Hkv, static_cast<cudaStream_t>(stream));
+}
+
+int msa_rope_write_nvfp4(const msa_rope_t* rope, const int32_t* positions, const void* q,
+                         int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+                         int64_t k_head, const void* v, int64_t v_token, int64_t v_head, int dtype,
+                         void* q_out, int q_bf16, float q_scale, uint8_t* kv4, int64_t num_pages,
+                         float k_scale, float v_scale, const int32_t* block_table, int64_t bt_stride,
+                         const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int64_t B,
+                         int64_t T, int64_t Hq, int64_t Hkv, uint32_t* status, void* stream) {
+  RopeArgs a = {};
+  a.q = q, a.k = k, a.v = v;
+  a.q_token = q_token, a.q_head = q_head, a.k_token = k_token, a.k_head = k_head;
+  a.v_token = v_token, a.v_head = v_head;
+  a.dtype = dtype;
+  a.q_out = q_out;
+  a.q_bf16 = q_bf16 != 0;
+  a.q_scale = q_scale, a.k_scale = k_scale, a.v_scale = v_scale;
+  a.pool = kv4;
+  a.num_pages = num_pages;
+  a.block_table = block_table;
+  a.bt_stride = bt_stride;
+  a.cu = cu_seqlens_q;
+  a.cu_k = cu_seqlens_k;
+  a.positions = positions;
+  a.T = T;
+  a.status = status;
+  a.fp4 = true;
+  return rope_write_impl(rope, a, B, Hq, Hkv, static_cast<cudaStream_t>(stream));
 }
 
 int msa_prefix_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv,

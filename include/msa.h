@@ -533,6 +533,77 @@ MSA_API int msa_kv_read_nvfp4(const uint8_t *kv4, int64_t num_pages, float k_sca
                       void *stream);
 
 /*
+ * From a projection's output to what the attention reads, in one pass: Q and K
+ * are normalised by head (where weights are given) and rotated to their
+ * positions; Q is quantised to E4M3 (or rounded to bf16) for the attention
+ * calls; K and V are quantised and written into their pages as msa_kv_write /
+ * msa_kv_write_nvfp4 write them.  (The pages name such a producer of the E4M3
+ * query and the cache, a fused QK-norm / RoPE / KV-insert.)
+ *   y = x / sqrt(mean of the head's x^2 + eps) * norm
+ *   pair j turned by positions[axis[j]][t] * inv_freq[j]:
+ *     (a, b) -> (a cos - b sin, a sin + b cos)
+ * in fp32 with one rounding at the end; the angle is exact to 2^-32 turns at
+ * any position.  V is neither normalised nor rotated.
+ *
+ * msa_rope_t (on the host, read during the call): how a model rotates.
+ *   pairs        rotated pairs of a head, 0 .. 64; the other values of Q and K
+ *                are left as they are (but for the norm)
+ *   interleaved  nonzero: pair j is values 2j and 2j + 1; 0: j and j + pairs
+ *   axes         rows of `positions`, 1 .. MSA_ROPE_MAX_AXES (several: time,
+ *                height and width of images and video)
+ *   eps          added to the mean square, finite and >= 0
+ *   q_norm, k_norm  device fp32 [128] weights, or NULL: no normalisation
+ *   turns        inv_freq[j] / 2 pi modulo 1 in steps of 2^-64, from
+ *                msa_rope_turns
+ *   axis         the axis of each pair, < axes
+ *
+ *   positions    int32 [axes][T], or NULL: a token's place in its sequence on
+ *                every axis.  Of any size and sign; they need not be the places
+ *                in the cache (a drafted tree's tokens, images, a cache whose
+ *                first tokens were dropped)
+ *   q, k, v      [T][heads][128] in `dtype`, strided as in msa_kv_write; q may
+ *                be NULL with Hq = 0
+ *   q_out        [T][Hq][128]: E4M3(y / q_scale), nearest even, saturating at
+ *                448, or bf16 where q_bf16 is nonzero (q_scale is then unused);
+ *                16-byte aligned
+ *   kv / kv4, scales, block_table, lengths, status  as in msa_kv_write.  Tokens
+ *                that status would tell of, and rows at or behind
+ *                cu_seqlens_q[B], are left out: their q_out rows too keep their
+ *                contents
+ * q_out shares no memory with the inputs.  One kernel on `stream`.
+ */
+#define MSA_ROPE_MAX_PAIRS 64
+#define MSA_ROPE_MAX_AXES 8
+typedef struct msa_rope {
+  int64_t pairs, interleaved, axes;
+  double eps;
+  const float *q_norm, *k_norm;
+  uint64_t turns[MSA_ROPE_MAX_PAIRS];
+  uint8_t axis[MSA_ROPE_MAX_PAIRS];
+} msa_rope_t;
+
+/* turns[j] of n finite frequencies in radians a position, on the host:
+ * |inv_freq| < 2^32, rounded to nearest.  MSA_ERR_SHAPE for others. */
+MSA_API int msa_rope_turns(const double *inv_freq, int64_t n, uint64_t *turns);
+
+MSA_API int msa_rope_write(const msa_rope_t *rope, const int32_t *positions, const void *q,
+                   int64_t q_token, int64_t q_head, const void *k, int64_t k_token,
+                   int64_t k_head, const void *v, int64_t v_token, int64_t v_head, int dtype,
+                   void *q_out, int q_bf16, float q_scale, uint8_t *kv, int64_t num_pages,
+                   float k_scale, float v_scale, const int32_t *block_table,
+                   int64_t bt_stride, const int32_t *cu_seqlens_q,
+                   const int32_t *cu_seqlens_k, int64_t B, int64_t T, int64_t Hq, int64_t Hkv,
+                   uint32_t *status, void *stream);
+MSA_API int msa_rope_write_nvfp4(const msa_rope_t *rope, const int32_t *positions, const void *q,
+                   int64_t q_token, int64_t q_head, const void *k, int64_t k_token,
+                   int64_t k_head, const void *v, int64_t v_token, int64_t v_head, int dtype,
+                   void *q_out, int q_bf16, float q_scale, uint8_t *kv4, int64_t num_pages,
+                   float k_scale, float v_scale, const int32_t *block_table,
+                   int64_t bt_stride, const int32_t *cu_seqlens_q,
+                   const int32_t *cu_seqlens_k, int64_t B, int64_t T, int64_t Hq, int64_t Hkv,
+                   uint32_t *status, void *stream);
+
+/*
  * Dense causal attention over the paged E4M3 cache for a batch whose requests
  * share their first pages (a system prompt, a document): every query token
  * attends to all keys up to its own position, the part over the shared pages
