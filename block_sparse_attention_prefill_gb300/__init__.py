@@ -17,6 +17,10 @@ Calls (same names as the C ABI, without the ``msa_`` prefix where noted):
                 cached tokens back out of them
   msa_rope_write (and _nvfp4)   Q and K normalised and rotated, Q quantised,
                 K and V written into the pages; MsaRope says how a model rotates
+  msa_tree_mask, msa_tree_attention, msa_tree_accept (and _nvfp4)   trees of
+                drafted tokens: masks and positions, dense attention, the path
+                that stands with its rows of the cache
+  msa_logprobs  log probabilities, ranks, entropies, best alternatives
   msa_prefix_attention   dense attention behind pages that a batch shares
   msa_verify, msa_verify_greedy   which drafted tokens stand, and the next one
 """
@@ -44,6 +48,7 @@ STATUS_BAD_SEQLENS = 1 << 2
 STATUS_ROWS_OVERFLOW = 1 << 3
 STATUS_TIMEOUT = 1 << 4
 STATUS_BAD_WORK = 1 << 5
+STATUS_BAD_TREE = 1 << 6
 
 _I64 = ("B", "T", "Hq", "Hkv", "total_rows", "max_seqlen_q", "max_seqlen_k",
         "num_pages", "bt_stride", "bitmap_words", "chunk_tokens", "max_nnz",
@@ -95,6 +100,8 @@ def load():
     _ROPE = ([ctypes.POINTER(MsaRopeStruct), P, P, i64, i64, P, i64, i64, P, i64,
               i64, i32, P, i32, f32, P, i64, f32, f32, P, i64, P, P, i64, i64,
               i64, i64, P, P], i32)
+    _ACCEPT = ([P, P, P, P, P, i64, i64, i64, ctypes.POINTER(P), i64, i64, i64, P,
+                i64, P, P, P, P, P], i32)
     sigs = {
         "msa_version": ([], i32),
         "msa_status_string": ([i32], ctypes.c_char_p),
@@ -140,6 +147,13 @@ def load():
         "msa_prefix_attention": ([P, P, i64, f32, f32, f32, f32, P, i64, P, P,
                                   i64, i64, i64, i64, i64, i64, i64, P,
                                   ctypes.c_size_t, P, P, P, P], i32),
+        "msa_tree_mask": ([P, P, P, i64, i64, i64, P, P, P, P], i32),
+        "msa_tree_attention": ([P, P, i64, f32, f32, f32, f32, P, i64, P, P, P,
+                                i64, i64, i64, i64, i64, i64, i64, i64, P,
+                                ctypes.c_size_t, P, P, P, P], i32),
+        "msa_tree_accept": _ACCEPT,
+        "msa_tree_accept_nvfp4": _ACCEPT,
+        "msa_logprobs": ([P, i64, i32, P, i64, i64, i64, P, P, P, P, P, P], i32),
         "msa_verify": ([P, i64, i64, P, i64, i64, i32, P, P, P, i64, i64, i64,
                         P, P, P], i32),
         "msa_verify_greedy": ([P, i64, i64, i32, P, P, i64, i64, i64, P, P, P],
@@ -646,5 +660,6 @@ def run_workload(w, stream=None):
 from .serve import (msa_kv_read, msa_kv_read_nvfp4, msa_kv_write,  # noqa: E402,F401
                     msa_kv_write_nvfp4, msa_prefix_attention,
                     msa_verify, msa_verify_greedy, prefix_attention_workspace_bytes)
-from .tree import (MsaRope, msa_rope_turns, msa_rope_write,  # noqa: E402,F401
-                   msa_rope_write_nvfp4)
+from .tree import (MsaRope, msa_logprobs, msa_rope_turns, msa_rope_write,  # noqa: E402,F401
+                   msa_rope_write_nvfp4, msa_tree_accept, msa_tree_accept_nvfp4,
+                   msa_tree_attention, msa_tree_mask)

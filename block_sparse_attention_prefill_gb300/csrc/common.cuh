@@ -174,6 +174,51 @@ struct RopeArgs {
 };
 cudaError_t launch_rope_write(const RopeArgs& a, cudaStream_t stream);
 
+// Trees of drafted tokens (tree.cu).  A request's nodes are its new tokens.
+struct TreeMaskArgs {
+  const int32_t* parents;  // [T]
+  const int32_t *cu_q, *cu_k;
+  int B;
+  int64_t T;
+  int max_q, words;
+  uint32_t* mask;          // [T][words] or NULL
+  int32_t* positions;      // [T] or NULL
+  uint32_t* status;        // or NULL
+};
+cudaError_t launch_tree_mask(const TreeMaskArgs& a, cudaStream_t stream);
+
+struct TreeAcceptArgs {
+  const int32_t *drafts, *parents, *chosen;  // [T]
+  const int32_t *cu_q, *cu_k;
+  int B;
+  int64_t T;
+  int max_q;
+  const int32_t* block_table;
+  int64_t bt_stride, num_pages;
+  int Hkv, layers;
+  bool fp4;
+  int32_t *tokens, *accepted, *path;  // path may be NULL
+  uint32_t* status;                   // or NULL
+  uint8_t* pools[MSA_TREE_MAX_LAYERS];
+};
+cudaError_t launch_tree_accept(const TreeAcceptArgs& a, cudaStream_t stream);
+
+// Log probabilities from logits (logprobs.cu); outputs may be NULL.
+struct LogprobsArgs {
+  const void* logits;      // row t at t * row elements
+  int64_t row;
+  int dtype;
+  const int32_t* tokens;   // [T] or NULL
+  int64_t T;
+  int V, top;
+  float* logprobs;         // [T]
+  int32_t* ranks;          // [T]
+  float* entropy;          // [T]
+  int32_t* top_tokens;     // [T][top]
+  float* top_logprobs;     // [T][top]
+};
+cudaError_t launch_logprobs(const LogprobsArgs& a, cudaStream_t stream);
+
 // Draft verification (verify.cu).  Row (b, i) of target is at b * t_req +
 // i * t_row elements, of draft_probs at b * d_req + i * d_row.
 struct VerifyArgs {
@@ -209,6 +254,10 @@ struct PrefixArgs {
   uint16_t* out;         // bf16 [T][Hq][128]
   float* lse;            // [T][Hq] or NULL
   uint32_t* status;      // or NULL
+  // trees: bit j of a token's words: it attends to its request's new token j;
+  // NULL: causal
+  const uint32_t* mask;  // [T][mask_words]
+  int mask_words;
 };
 // Bytes of workspace, or 0 where the sizes are out of range.
 size_t prefix_workspace(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t prefix_pages,

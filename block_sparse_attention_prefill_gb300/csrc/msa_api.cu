@@ -492,6 +492,77 @@ int prefix_shape(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t prefix, 
   return *bytes ? MSA_OK : MSA_ERR_SHAPE;
 }
 
+// The calls of the shared-prefix attention, causal or (mask) of trees.
+int prefix_attention_impl(PrefixArgs a, float q_scale, float k_scale, float softmax_scale,
+                          void* workspace, size_t workspace_bytes, cudaStream_t st) {
+  size_t need = 0;
+  int rc = prefix_shape(a.B, a.T, a.Hq, a.Hkv, a.prefix_pages, a.max_q, a.max_k, &need);
+  if (rc) return rc;
+  if (a.num_pages < 0 || a.num_pages >= kI32Max || a.num_pages * a.Hkv * kPage >= kI32Max ||
+      a.bt_stride < ceil_div(a.max_k, kPage) || a.bt_stride > (1 << 24))
+    return MSA_ERR_SHAPE;
+  // the largest score of E4M3 codes, 128 * 448^2 products, has to be finite
+  const double score = (double)q_scale * (double)k_scale * (double)softmax_scale *
+                       1.4426950408889634074;
+  if (!(q_scale > 0.f) || !(k_scale > 0.f) || !(a.v_scale > 0.f) || !(softmax_scale > 0.f) ||
+      !(score * kD * 448.0 * 448.0 < FLT_MAX) || !std::isfinite(a.v_scale))
+    return MSA_ERR_SHAPE;
+  if (a.B == 0 || a.T == 0) return MSA_OK;
+  if (!a.q || !a.kv || !a.block_table || !a.cu_q || !a.cu_k || !a.out) return MSA_ERR_NULL;
+  if (!aligned(a.q, 16) || !aligned(a.kv, 16) || !aligned(a.block_table, 4) ||
+      !aligned(a.cu_q, 4) || !aligned(a.cu_k, 4) || !aligned(a.out, 8) || !aligned(a.lse, 4) ||
+      !aligned(a.mask, 4) || !aligned(a.status, 4))
+    return MSA_ERR_ALIGN;
+  if (!workspace || workspace_bytes < need) return MSA_ERR_WORKSPACE;
+  if (!aligned(workspace, kAlign)) return MSA_ERR_ALIGN;
+  // never 0, by which a masked score of -inf would become NaN
+  a.score_log2 = std::max((float)score, FLT_MIN);
+  return cuda_rc(launch_prefix_attention(a, workspace, st));
+}
+
+int tree_lengths(int64_t B, int64_t T, int64_t max_q) {
+  return B < 0 || B >= kI32Max / 2 || T < 0 || T >= kI32Max / kTopK || max_q < 0 ||
+                 max_q > MSA_TREE_MAX_TOKENS
+             ? MSA_ERR_SHAPE
+             : MSA_OK;
+}
+
+int tree_accept_impl(TreeAcceptArgs a, uint8_t* const* pools, int64_t layers, int64_t Hkv,
+                     int64_t B, int64_t max_q, cudaStream_t st) {
+  int rc = tree_lengths(B, a.T, max_q);
+  if (rc) return rc;
+  if (layers < 0 || layers > MSA_TREE_MAX_LAYERS || (layers > 0 && (Hkv < 1 || Hkv > 127)) ||
+      a.num_pages < 0 || a.num_pages >= kI32Max || a.bt_stride < 0 || a.bt_stride > (1 << 24))
+    return MSA_ERR_SHAPE;
+  if (B == 0) return MSA_OK;
+  if (!a.accepted || (max_q > 0 && !a.tokens) || !a.cu_q || !a.cu_k) return MSA_ERR_NULL;
+  if (a.T > 0 && (!a.drafts || !a.parents || !a.chosen)) return MSA_ERR_NULL;
+  if (layers > 0 && (!pools || !a.block_table)) return MSA_ERR_NULL;
+  if (!aligned(a.drafts, 4) || !aligned(a.parents, 4) || !aligned(a.chosen, 4) ||
+      !aligned(a.cu_q, 4) || !aligned(a.cu_k, 4) || !aligned(a.block_table, 4) ||
+      !aligned(a.tokens, 4) || !aligned(a.accepted, 4) || !aligned(a.path, 4) ||
+      !aligned(a.status, 4))
+    return MSA_ERR_ALIGN;
+  uintptr_t at[MSA_TREE_MAX_LAYERS];
+  for (int64_t i = 0; i < layers; ++i) {
+    if (!pools[i]) return MSA_ERR_NULL;
+    if (!aligned(pools[i], 16)) return MSA_ERR_ALIGN;
+    a.pools[i] = pools[i];
+    at[i] = reinterpret_cast<uintptr_t>(pools[i]);
+  }
+  // rows of a pool given twice would be moved by two at once
+  std::sort(at, at + layers);
+  const uint64_t bytes = (uint64_t)a.num_pages * (uint64_t)Hkv *
+                         (a.fp4 ? kFp4PageBytes : kPage * 2 * kD);
+  for (int64_t i = 1; i < layers; ++i)
+    if (at[i] - at[i - 1] < std::max<uint64_t>(bytes, 1)) return MSA_ERR_SHAPE;
+  a.B = (int)B;
+  a.max_q = (int)max_q;
+  a.Hkv = (int)Hkv;
+  a.layers = (int)layers;
+  return cuda_rc(launch_tree_accept(a, st));
+}
+
 struct DecodeLayout {
   int64_t R;
   size_t cu_bytes, plan_bytes, prefill_bytes, total;
@@ -854,32 +925,10 @@ int msa_prefix_attention(const uint8_t* q, const uint8_t* kv, int64_t num_pages,
                          int64_t max_seqlen_q, int64_t max_seqlen_k, void* workspace,
                          size_t workspace_bytes, uint16_t* out, float* lse, uint32_t* status,
                          void* stream) {
-  size_t need = 0;
-  int rc = prefix_shape(B, T, Hq, Hkv, prefix_pages, max_seqlen_q, max_seqlen_k, &need);
-  if (rc) return rc;
-  if (num_pages < 0 || num_pages >= kI32Max || num_pages * Hkv * kPage >= kI32Max ||
-      bt_stride < ceil_div(max_seqlen_k, kPage) || bt_stride > (1 << 24))
-    return MSA_ERR_SHAPE;
-  // the largest score of E4M3 codes, 128 * 448^2 products, has to be finite
-  const double score = (double)q_scale * (double)k_scale * (double)softmax_scale *
-                       1.4426950408889634074;
-  if (!(q_scale > 0.f) || !(k_scale > 0.f) || !(v_scale > 0.f) || !(softmax_scale > 0.f) ||
-      !(score * kD * 448.0 * 448.0 < FLT_MAX) || !std::isfinite(v_scale))
-    return MSA_ERR_SHAPE;
-  if (B == 0 || T == 0) return MSA_OK;
-  if (!q || !kv || !block_table || !cu_seqlens_q || !cu_seqlens_k || !out) return MSA_ERR_NULL;
-  if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(block_table, 4) ||
-      !aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4) || !aligned(out, 8) ||
-      !aligned(lse, 4) || !aligned(status, 4))
-    return MSA_ERR_ALIGN;
-  if (!workspace || workspace_bytes < need) return MSA_ERR_WORKSPACE;
-  if (!aligned(workspace, kAlign)) return MSA_ERR_ALIGN;
   PrefixArgs a = {};
   a.q = q;
   a.kv = kv;
   a.num_pages = num_pages;
-  // never 0, by which a masked score of -inf would become NaN
-  a.score_log2 = std::max((float)score, FLT_MIN);
   a.v_scale = v_scale;
   a.block_table = block_table;
   a.bt_stride = bt_stride;
@@ -891,7 +940,56 @@ int msa_prefix_attention(const uint8_t* q, const uint8_t* kv, int64_t num_pages,
   a.out = out;
   a.lse = lse;
   a.status = status;
-  return cuda_rc(launch_prefix_attention(a, workspace, static_cast<cudaStream_t>(stream)));
+  return prefix_attention_impl(a, q_scale, k_scale, softmax_scale, workspace, workspace_bytes,
+                               static_cast<cudaStream_t>(stream));
+}
+
+int msa_tree_mask(const int32_t* parents, const int32_t* cu_seqlens_q,
+                  const int32_t* cu_seqlens_k, int64_t B, int64_t T, int64_t max_seqlen_q,
+                  uint32_t* mask, int32_t* positions, uint32_t* status, void* stream) {
+  int rc = tree_lengths(B, T, max_seqlen_q);
+  if (rc) return rc;
+  if (B == 0 || T == 0) return MSA_OK;
+  if (!parents || !cu_seqlens_q || !cu_seqlens_k) return MSA_ERR_NULL;
+  if (!aligned(parents, 4) || !aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4) ||
+      !aligned(mask, 4) || !aligned(positions, 4) || !aligned(status, 4))
+    return MSA_ERR_ALIGN;
+  const TreeMaskArgs a = {parents, cu_seqlens_q, cu_seqlens_k, (int)B, T, (int)max_seqlen_q,
+                          (int)ceil_div(max_seqlen_q, 32), mask, positions, status};
+  return cuda_rc(launch_tree_mask(a, static_cast<cudaStream_t>(stream)));
+}
+
+int msa_tree_attention(const uint8_t* q, const uint8_t* kv, int64_t num_pages, float q_scale,
+                       float k_scale, float v_scale, float softmax_scale,
+                       const int32_t* block_table, int64_t bt_stride,
+                       const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                       const uint32_t* mask, int64_t mask_words, int64_t B, int64_t T,
+                       int64_t Hq, int64_t Hkv, int64_t prefix_pages, int64_t max_seqlen_q,
+                       int64_t max_seqlen_k, void* workspace, size_t workspace_bytes,
+                       uint16_t* out, float* lse, uint32_t* status, void* stream) {
+  int rc = tree_lengths(B, T, max_seqlen_q);
+  if (rc) return rc;
+  if (mask_words < ceil_div(max_seqlen_q, 32) || mask_words > (1 << 20)) return MSA_ERR_SHAPE;
+  if (B > 0 && T > 0 && max_seqlen_q > 0 && !mask) return MSA_ERR_NULL;
+  PrefixArgs a = {};
+  a.q = q;
+  a.kv = kv;
+  a.num_pages = num_pages;
+  a.v_scale = v_scale;
+  a.block_table = block_table;
+  a.bt_stride = bt_stride;
+  a.cu_q = cu_seqlens_q;
+  a.cu_k = cu_seqlens_k;
+  a.B = B, a.T = T, a.Hq = Hq, a.Hkv = Hkv;
+  a.prefix_pages = prefix_pages;
+  a.max_q = max_seqlen_q, a.max_k = max_seqlen_k;
+  a.out = out;
+  a.lse = lse;
+  a.status = status;
+  a.mask = mask;
+  a.mask_words = (int)mask_words;
+  return prefix_attention_impl(a, q_scale, k_scale, softmax_scale, workspace, workspace_bytes,
+                               static_cast<cudaStream_t>(stream));
 }
 
 int msa_verify(const void* target_probs, int64_t target_req, int64_t target_row,
@@ -913,6 +1011,62 @@ int msa_verify_greedy(const void* target, int64_t target_req, int64_t target_row
   VerifyArgs a = {target, target_req, target_row, nullptr, 0, 0, dtype, draft_tokens, nullptr,
                   num_drafts, B, (int)n, V, tokens, accepted};
   return verify_impl(a, true, static_cast<cudaStream_t>(stream));
+}
+
+int msa_tree_accept(const int32_t* draft_tokens, const int32_t* parents,
+                    const int32_t* chosen, const int32_t* cu_seqlens_q,
+                    const int32_t* cu_seqlens_k, int64_t B, int64_t T, int64_t max_seqlen_q,
+                    uint8_t* const* kv, int64_t layers, int64_t num_pages, int64_t Hkv,
+                    const int32_t* block_table, int64_t bt_stride, int32_t* tokens,
+                    int32_t* accepted, int32_t* path, uint32_t* status, void* stream) {
+  TreeAcceptArgs a = {};
+  a.drafts = draft_tokens, a.parents = parents, a.chosen = chosen;
+  a.cu_q = cu_seqlens_q, a.cu_k = cu_seqlens_k;
+  a.T = T;
+  a.block_table = block_table;
+  a.bt_stride = bt_stride, a.num_pages = num_pages;
+  a.fp4 = false;
+  a.tokens = tokens, a.accepted = accepted, a.path = path;
+  a.status = status;
+  return tree_accept_impl(a, kv, layers, Hkv, B, max_seqlen_q, static_cast<cudaStream_t>(stream));
+}
+
+int msa_tree_accept_nvfp4(const int32_t* draft_tokens, const int32_t* parents,
+                          const int32_t* chosen, const int32_t* cu_seqlens_q,
+                          const int32_t* cu_seqlens_k, int64_t B, int64_t T, int64_t max_seqlen_q,
+                          uint8_t* const* kv4, int64_t layers, int64_t num_pages, int64_t Hkv,
+                          const int32_t* block_table, int64_t bt_stride, int32_t* tokens,
+                          int32_t* accepted, int32_t* path, uint32_t* status, void* stream) {
+  TreeAcceptArgs a = {};
+  a.drafts = draft_tokens, a.parents = parents, a.chosen = chosen;
+  a.cu_q = cu_seqlens_q, a.cu_k = cu_seqlens_k;
+  a.T = T;
+  a.block_table = block_table;
+  a.bt_stride = bt_stride, a.num_pages = num_pages;
+  a.fp4 = true;
+  a.tokens = tokens, a.accepted = accepted, a.path = path;
+  a.status = status;
+  return tree_accept_impl(a, kv4, layers, Hkv, B, max_seqlen_q, static_cast<cudaStream_t>(stream));
+}
+
+int msa_logprobs(const void* logits, int64_t row_stride, int dtype, const int32_t* tokens,
+                 int64_t T, int64_t V, int64_t top, float* logprobs, int32_t* ranks,
+                 float* entropy, int32_t* top_tokens, float* top_logprobs, void* stream) {
+  if (dtype != MSA_DTYPE_F32 && dtype != MSA_DTYPE_BF16 && dtype != MSA_DTYPE_F16)
+    return MSA_ERR_UNSUPPORTED;
+  if (T < 0 || T > kI32Max / 64 || V < 1 || V >= MSA_VERIFY_MAX_VOCAB || row_stride < 0 ||
+      top < 0 || top > MSA_LOGPROBS_MAX_TOP)
+    return MSA_ERR_SHAPE;
+  if (T == 0) return MSA_OK;
+  if (!logits || (top > 0 && (!top_tokens || !top_logprobs)) || (!tokens && (logprobs || ranks)))
+    return MSA_ERR_NULL;
+  if (!aligned(logits, dtype == MSA_DTYPE_F32 ? 4 : 2) || !aligned(tokens, 4) ||
+      !aligned(logprobs, 4) || !aligned(ranks, 4) || !aligned(entropy, 4) ||
+      !aligned(top_tokens, 4) || !aligned(top_logprobs, 4))
+    return MSA_ERR_ALIGN;
+  const LogprobsArgs a = {logits, row_stride, dtype, tokens, T, (int)V, (int)top, logprobs, ranks,
+                          entropy, top_tokens, top_logprobs};
+  return cuda_rc(launch_logprobs(a, static_cast<cudaStream_t>(stream)));
 }
 
 int msa_decode_workspace_bytes(int64_t B, int64_t n, int64_t Hq, int64_t Hkv,

@@ -1,6 +1,9 @@
 // Dense causal attention over the paged E4M3 cache for a batch whose requests
 // share their first pages: the part over the shared pages is computed once
-// for all requests.  sm_103a: TMA, tcgen05, TMEM.
+// for all requests.  sm_103a: TMA, tcgen05, TMEM.  The same for trees of
+// drafted tokens, which see the keys before the tree and, of the tree, those
+// whose bits are set in a token's mask words (kTree): the last few units of a
+// request's keys are masked by 64 bits a row in place of a last position.
 //
 // With s_j = (q . k_j) c (c: the scales times log2 e) the kernel keeps, per
 // query row, a reference m near the running maximum, l = sum 2^(s_j - m) and
@@ -74,7 +77,8 @@ struct __align__(16) Tile {
   int page0;   // first logical page
   int npages;
   uint32_t start;  // cost of the head's tiles before this one
-  int pos0;    // position of tok0, or kNoMask (the shared pages)
+  int pos0;    // position of tok0 (trees: of the last key before the tree), or
+               // kNoMask (the shared pages)
   int seq;     // keys of the request (a page's keys behind it are not read)
 };
 struct PlanHead {
@@ -193,7 +197,7 @@ struct PlanParams {
 // Lists the tiles of one head (every head has the same): first those over the
 // shared pages, then each request's own.  Run by a whole CTA; req is room for
 // B ints that it can see.  Every thread gets the plan's head.
-template <int kThreads>
+template <int kThreads, bool kTree>
 __device__ __forceinline__ PlanHead make_plan(const PlanParams& p, int* req) {
   __shared__ int s_bad, s_first, s_rate;
   const int tid = threadIdx.x;
@@ -266,8 +270,8 @@ __device__ __forceinline__ PlanHead make_plan(const PlanParams& p, int* req) {
         t.tok0 = p.cu_q[lo] + o;
         t.ntok = min(2 * p.C, q - o);
         t.page0 = prefix;
-        t.pos0 = k - q + o;
-        t.npages = (t.pos0 + t.ntok - 1) / kPage + 1 - prefix;
+        t.pos0 = kTree ? k - q - 1 : k - q + o;
+        t.npages = (kTree ? k - 1 : t.pos0 + t.ntok - 1) / kPage + 1 - prefix;
         t.seq = k;
       }
       c = tile_cost(t.ntok, t.npages, p.C);
@@ -283,10 +287,11 @@ __device__ __forceinline__ PlanHead make_plan(const PlanParams& p, int* req) {
   return hd;
 }
 
+template <bool kTree>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
   pdl_wait();
   pdl_trigger();
-  make_plan<kPlanThreads>(p, p.req);
+  make_plan<kPlanThreads, kTree>(p, p.req);
 }
 
 // ------------------------------------------------------------------ attend
@@ -349,6 +354,8 @@ struct AttendParams {
   float* part_lse;  // base-2 log-sum-exp of the row's part
   uint32_t* status;
   uint32_t wait_ns;
+  const uint32_t* mask;  // trees: [T][mask_words]
+  int mask_words;
 };
 
 // One CTA's range of the line, tile by tile; each role walks it for itself.
@@ -465,6 +472,13 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
+// The words of a tree's token: word i, and what lies before and behind them (all
+// keys before the tree are seen, none behind it).
+__device__ __forceinline__ uint32_t mask_word(const uint32_t* words, int n, int i) {
+  return i < 0 ? 0xFFFFFFFFu : i < n ? __ldg(words + i) : 0u;
+}
+
+template <bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
 attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
               const AttendParams p) {
@@ -522,7 +536,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
   // same places, and each reads what it has written itself.
   PlanHead hd;
   if (p.plan_here)
-    hd = make_plan<kThreads>(p.plan, reinterpret_cast<int*>(smem + kOffW));
+    hd = make_plan<kThreads, kTree>(p.plan, reinterpret_cast<int*>(smem + kOffW));
   else
     hd = *p.plan.head;
   tc_fence_before();
@@ -564,7 +578,11 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
       const int ntok = pair ? (s ? t.ntok - p.C : p.C) : t.ntok;
       const bool valid = i_tok < ntok;
       const int tok = i_tok + (pair && s ? p.C : 0);  // within the tile
-      const int pos = t.pos0 + tok;
+      // the last key that the row sees, but for its tree's
+      const int pos = kTree ? t.pos0 : t.pos0 + tok;
+      // (a row of no token has no words)
+      const uint32_t* words =
+          kTree && valid ? p.mask + (int64_t)(t.tok0 + tok) * p.mask_words : nullptr;
       const int32_t* table = p.block_table + t.b * p.bt_stride + t.page0;
       // the first position of the warp's rows: pages before it need no mask
       const int least = __reduce_min_sync(0xffffffffu, pos);
@@ -590,12 +608,33 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
         tmem_wait_ld();
         const bool there = bars->there[(g0 + walk.stream_page(s, i >> 1)) % kThere];
         if (!there || key0 + kHalf - 1 > least) {
-          const int lim = there ? pos - key0 : -1;  // the last key this row attends to
+          if constexpr (kTree) {
+            // a bit for each key of the unit: the row's words from the node of
+            // its first key on, up to the request's last key
+            const int node = key0 - t.pos0 - 1, left = there ? t.seq - key0 : 0;
+            uint32_t bits[2] = {0u, 0u};
+            if (words && left > 0) {
+              const uint32_t w0 = mask_word(words, p.mask_words, node >> 5);
+              const uint32_t w1 = mask_word(words, p.mask_words, (node >> 5) + 1);
+              const uint32_t w2 = mask_word(words, p.mask_words, (node >> 5) + 2);
+              bits[0] = __funnelshift_r(w0, w1, node & 31);
+              bits[1] = __funnelshift_r(w1, w2, node & 31);
+              if (left < 32) bits[0] &= (1u << left) - 1u;
+              if (left < 64) bits[1] &= left > 32 ? (1u << (left - 32)) - 1u : 0u;
+            }
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (q * 32 + e > lim) r[q][e] = 0xFF800000u;  // -inf
+              for (int e = 0; e < 32; ++e)
+                if (!(bits[q] >> e & 1u)) r[q][e] = 0xFF800000u;  // -inf
+          } else {
+            const int lim = there ? pos - key0 : -1;  // the last key this row attends to
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (q * 32 + e > lim) r[q][e] = 0xFF800000u;  // -inf
+          }
         }
         const float2 c2 = make_float2(c, c);
         // The reference m is the maximum of the row's first unit.  Later
@@ -714,8 +753,10 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
       // does not see whole, widening wrote it as 0, since a probability of 0
       // must hide it; now each warp finds, for each column, the first position
       // that has one (pages of that kind are the last three of a tile at most).
+      // Of trees each row notes the columns in which a key that it sees has one.
       bool poison = false;
       int nan_key[4] = {INT_MAX, INT_MAX, INT_MAX, INT_MAX};  // columns 4 lane ..
+      uint32_t nan_cols[4] = {0u, 0u, 0u, 0u};  // [e], bit c: column 4 c + e
       for (int j = max(walk.p0, (t.pos0 + 1) / kPage - t.page0); j < walk.p1; ++j) {
         if (bars->there[(g0 + j - walk.p1) % kThere] & kHasNan) {
           poison = true;
@@ -725,9 +766,20 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
           for (int k = 0; k < kPage && first + k < t.seq; ++k) {
             const uint32_t bad = nan_bytes(
                 __ldg(reinterpret_cast<const uint32_t*>(v + k * (2 * kD)) + lane));
+            if constexpr (kTree) {
+              const int node = first + k - t.pos0 - 1;
+              const bool seen = node < 0 || (words && (mask_word(words, p.mask_words, node >> 5) >>
+                                                       (node & 31) & 1u));
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if ((bad >> (8 * e)) & 0x80u) nan_key[e] = min(nan_key[e], first + k);
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t cols = __ballot_sync(0xffffffffu, (bad >> (8 * e)) & 0x80u);
+                if (seen) nan_cols[e] |= cols;
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if ((bad >> (8 * e)) & 0x80u) nan_key[e] = min(nan_key[e], first + k);
+            }
           }
         }
       }
@@ -748,9 +800,14 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
                                  (fb < 0.f ? 0.f : __uint_as_float(x[e]) * fb));
         if (poison) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (__shfl_sync(0xffffffffu, nan_key[e & 3], q * 4 + (e >> 2)) <= pos)
-              o[e] = 0x7FFFFFFFu;
+          for (int e = 0; e < 16; ++e) {
+            if constexpr (kTree) {
+              if (nan_cols[e & 3] >> (q * 4 + (e >> 2)) & 1u) o[e] = 0x7FFFFFFFu;
+            } else {
+              if (__shfl_sync(0xffffffffu, nan_key[e & 3], q * 4 + (e >> 2)) <= pos)
+                o[e] = 0x7FFFFFFFu;
+            }
+          }
         }
         if (valid) {
 #pragma unroll
@@ -1297,15 +1354,8 @@ bool encode(EncodeTiledFn enc, CUtensorMap* map, const void* base, int dims, con
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace
-
-size_t prefix_workspace(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t prefix_pages,
-                        int64_t max_k) {
-  Layout l;
-  return layout(B, T, Hq, Hkv, prefix_pages, max_k, num_sms(), &l) ? l.total : 0;
-}
-
-cudaError_t launch_prefix_attention(const PrefixArgs& a, void* ws, cudaStream_t stream) {
+template <bool kTree>
+cudaError_t launch(const PrefixArgs& a, void* ws, cudaStream_t stream) {
   const int ctas = num_sms();
   const int G = (int)(a.Hq / a.Hkv), C = kTileM / G;
   Layout l;
@@ -1340,7 +1390,7 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, void* ws, cudaStream_t 
   const bool plan_here =
       a.B <= kThreads && max_tiles(a.B, a.T, C, a.prefix_pages) <= kThreads;
   if (!plan_here) {
-    e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pp);
+    e = launch_pdl(plan_kernel<kTree>, dim3(1), dim3(kPlanThreads), 0, stream, pp);
     if (e != cudaSuccess) return e;
   }
 
@@ -1350,14 +1400,15 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, void* ws, cudaStream_t 
   e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices || !attr_set[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(attend_kernel<kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) attr_set[dev].store(true, std::memory_order_release);
   }
   const AttendParams ap = {pp, plan_here, tiles, own0, a.block_table, a.bt_stride, a.kv, (int)a.num_pages,
                            (int)a.T, G, C, (int)a.Hkv, a.score_log2, part_o, part_lse, a.status,
-                           (uint32_t)std::min<uint64_t>(pipeline_wait_limit_ns(), kWaitLimitNs)};
-  e = launch_pdl(attend_kernel, dim3((unsigned)ctas), dim3(kThreads), (size_t)kSmem, stream, kv_map,
+                           (uint32_t)std::min<uint64_t>(pipeline_wait_limit_ns(), kWaitLimitNs),
+                           a.mask, a.mask_words};
+  e = launch_pdl(attend_kernel<kTree>, dim3((unsigned)ctas), dim3(kThreads), (size_t)kSmem, stream, kv_map,
                  q_map, ap);
   if (e != cudaSuccess) return e;
 
@@ -1381,6 +1432,18 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, void* ws, cudaStream_t 
   if (team == 8) return launch_pdl(combine_kernel<8>, grid, block, 0, stream, cp);
   if (team == 2) return launch_pdl(combine_kernel<2>, grid, block, 0, stream, cp);
   return launch_pdl(combine_kernel<1>, grid, block, 0, stream, cp);
+}
+
+}  // namespace
+
+size_t prefix_workspace(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t prefix_pages,
+                        int64_t max_k) {
+  Layout l;
+  return layout(B, T, Hq, Hkv, prefix_pages, max_k, num_sms(), &l) ? l.total : 0;
+}
+
+cudaError_t launch_prefix_attention(const PrefixArgs& a, void* ws, cudaStream_t stream) {
+  return a.mask ? launch<true>(a, ws, stream) : launch<false>(a, ws, stream);
 }
 
 }  // namespace msa

@@ -323,18 +323,11 @@ def _check_attention(q, kv, block_table, cu_q, cu_k, workspace, out, lse, status
         _tensor(workspace, "workspace", (torch.uint8,))
 
 
-def msa_prefix_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_table,
-                         cu_seqlens_q, cu_seqlens_k, prefix_pages, max_seqlen_q, max_seqlen_k,
-                         workspace=None, out=None, lse=None, want_lse=True, status=None,
-                         stream=None):
-    """Dense causal attention over the E4M3 pool for a batch whose requests
-    share their first prefix_pages pages, whose part is computed once for all
-    (0: nothing shared).  q E4M3 [T, Hq, 128]; lengths as in msa_plan, all
-    queries behind the shared pages.  status: an int32 [1] tensor that
-    MSA_STATUS_* bits are OR-ed into; without it nothing tells of lengths that
-    do not fit (all rows 0) or entries that are no pages (left out).  Rows
-    behind cu_seqlens_q's last keep their contents, which in new tensors are
-    undefined.  Returns (out bf16 [T, Hq, 128], lse fp32 [T, Hq] or None)."""
+def _attend(name, q, kv, q_scale, k_scale, v_scale, softmax_scale, block_table, cu_seqlens_q,
+            cu_seqlens_k, mask, prefix_pages, max_seqlen_q, max_seqlen_k, workspace, out, lse,
+            want_lse, status, stream):
+    """msa_prefix_attention, or with the mask words of trees msa_tree_attention
+    (whose check of them is the caller's)."""
     try:
         pool, table, (T, Hq, dim) = kv.shape, block_table.shape, q.shape
         dev = kv.get_device()
@@ -346,7 +339,8 @@ def msa_prefix_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_
             and cu_seqlens_q.is_contiguous() and cu_seqlens_k.is_contiguous()
             and out is None and lse is None and workspace is None and status is None and dev >= 0
             and dev == q.get_device() == block_table.get_device() == cu_seqlens_q.get_device()
-            == cu_seqlens_k.get_device() == torch._C._cuda_getDevice())
+            == cu_seqlens_k.get_device() == torch._C._cuda_getDevice()
+            and (mask is None or mask.get_device() == dev))
     except _NOT_SOUND:
         sound = False
     if not sound:
@@ -361,7 +355,7 @@ def msa_prefix_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_
     if workspace is not None and workspace.numel() < need:
         _fail("workspace too small: %d < %d bytes", workspace.numel(), need)
     if not sound:
-        _place(q, kv, block_table, cu_seqlens_q, cu_seqlens_k, workspace, out, lse, status)
+        _place(q, kv, block_table, cu_seqlens_q, cu_seqlens_k, mask, workspace, out, lse, status)
     handle = _handle(stream, dev)
     if workspace is None:
         workspace = _new(need, torch.uint8, dev, handle)
@@ -369,14 +363,32 @@ def msa_prefix_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_
         out = _new((T, Hq, HEAD_DIM), torch.bfloat16, dev, handle)
     if lse is None and want_lse:
         lse = _new((T, Hq), torch.float32, dev, handle)
-    rc = load().msa_prefix_attention(
+    words = () if mask is None else (mask.data_ptr(), mask.shape[1])
+    rc = getattr(load(), name)(
         q.data_ptr(), kv.data_ptr(), pool[0], q_scale, k_scale, v_scale, softmax_scale,
-        block_table.data_ptr(), table[1], cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, T,
-        Hq, Hkv, prefix_pages, max_seqlen_q, max_seqlen_k, workspace.data_ptr(),
+        block_table.data_ptr(), table[1], cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), *words,
+        B, T, Hq, Hkv, prefix_pages, max_seqlen_q, max_seqlen_k, workspace.data_ptr(),
         workspace.numel(), out.data_ptr(), _ptr(lse), _ptr(status), handle)
     if rc:
-        _check(rc, "msa_prefix_attention")
+        _check(rc, name)
     return out, lse
+
+
+def msa_prefix_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_table,
+                         cu_seqlens_q, cu_seqlens_k, prefix_pages, max_seqlen_q, max_seqlen_k,
+                         workspace=None, out=None, lse=None, want_lse=True, status=None,
+                         stream=None):
+    """Dense causal attention over the E4M3 pool for a batch whose requests
+    share their first prefix_pages pages, whose part is computed once for all
+    (0: nothing shared).  q E4M3 [T, Hq, 128]; lengths as in msa_plan, all
+    queries behind the shared pages.  status: an int32 [1] tensor that
+    MSA_STATUS_* bits are OR-ed into; without it nothing tells of lengths that
+    do not fit (all rows 0) or entries that are no pages (left out).  Rows
+    behind cu_seqlens_q's last keep their contents, which in new tensors are
+    undefined.  Returns (out bf16 [T, Hq, 128], lse fp32 [T, Hq] or None)."""
+    return _attend("msa_prefix_attention", q, kv, q_scale, k_scale, v_scale, softmax_scale,
+                   block_table, cu_seqlens_q, cu_seqlens_k, None, prefix_pages, max_seqlen_q,
+                   max_seqlen_k, workspace, out, lse, want_lse, status, stream)
 
 
 def _probs(t, name, dtypes):

@@ -13,11 +13,15 @@ import ctypes
 import torch
 
 from . import HEAD_DIM, MsaError, MsaRopeStruct, load
-from .serve import (_E4M3, _I32, _NOT_SOUND, _PAGE, _PAGE4, _TYPES, _check, _fail, _handle, _new,
-                    _place, _pool, _ptr, _requests, _rows, _status, _table, _tensor)
+from .serve import (_E4M3, _F32, _I32, _NOT_SOUND, _PAGE, _PAGE4, _TYPES, _WORD, _attend, _check,
+                    _fail, _handle, _new, _place, _pool, _ptr, _requests, _rows, _status, _table,
+                    _tensor)
 
 ROPE_MAX_PAIRS = 64
 ROPE_MAX_AXES = 8
+TREE_MAX_TOKENS = 256
+TREE_MAX_LAYERS = 128
+LOGPROBS_MAX_TOP = 32
 
 
 def msa_rope_turns(inv_freq):
@@ -78,6 +82,17 @@ def _reach(t):
     return at, at + n * t.element_size()
 
 
+def _apart(outs, inputs):
+    """Refuses outputs that share memory with inputs or with one another (by
+    name; None: not there)."""
+    reach = [(name, *_reach(t)) for name, t in outs.items() if t is not None]
+    rest = [(name, *_reach(t)) for name, t in inputs.items() if t is not None]
+    for i, (name, lo, hi) in enumerate(reach):
+        for other, a, b in reach[:i] + rest:
+            if a < hi and lo < b:
+                _fail("%s must not share memory with %s", name, other)
+
+
 def _fits(shape, axes, T):
     """Whether positions have a row of T for each axis (further rows are not
     read)."""
@@ -117,14 +132,9 @@ def _check_rope(fp4, rope, q, k, v, kv, q_scale, block_table, cu_q, cu_k, positi
     _status(status)
     dev = _place(kv, k, v, q, block_table, cu_q, cu_k, positions, q_out, status, rope.q_norm,
                  rope.k_norm)
-    if q_out is not None:
-        lo, hi = _reach(q_out)
-        for name, t in (("q", q), ("k", k), ("v", v), ("kv", kv), ("positions", positions),
-                        ("block_table", block_table)):
-            if t is not None:
-                a, b = _reach(t)
-                if a < hi and lo < b:
-                    _fail("q_out must not share memory with %s", name)
+    _apart({"q_out": q_out}, {"q": q, "k": k, "v": v, "kv": kv, "positions": positions,
+                              "block_table": block_table, "cu_seqlens_q": cu_q,
+                              "cu_seqlens_k": cu_k})
     return dev
 
 
@@ -197,3 +207,273 @@ def msa_rope_write_nvfp4(rope, q, k, v, kv4, q_scale, k_scale, v_scale, block_ta
     as msa_kv_write_nvfp4 writes it."""
     return _rope_write("msa_rope_write_nvfp4", True, rope, q, k, v, kv4, q_scale, k_scale, v_scale,
                        block_table, cu_seqlens_q, cu_seqlens_k, positions, q_out, status, stream)
+
+
+def _check_tree(flat, cu_q, cu_k, outs, status):
+    """Tensors [T] by name, the lengths, and the outputs' types and shapes."""
+    B = _requests(cu_q, "cu_seqlens_q")
+    _tensor(cu_k, "cu_seqlens_k", _I32, (B + 1,))
+    first = None
+    for name, t in flat.items():
+        _tensor(t, name, _I32, first)
+        if first is None:
+            if t.dim() != 1:
+                _fail("%s must be [T], got %s", name, tuple(t.shape))
+            first = t.shape
+    for name, (t, dtypes, shape) in outs.items():
+        if t is not None:
+            _tensor(t, name, dtypes, shape)
+    _status(status)
+
+
+def _tree_limit(max_seqlen_q):
+    n = int(max_seqlen_q)
+    if not 0 <= n <= TREE_MAX_TOKENS:
+        _fail("max_seqlen_q must be 0 .. %d, got %d", TREE_MAX_TOKENS, n)
+    return n
+
+
+def msa_tree_mask(parents, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, mask=None, positions=None,
+                  status=None, stream=None):
+    """Ancestor masks and positions of a batch's trees of drafted tokens.
+    parents int32 [T]: each token's parent by its place among its request's
+    new tokens (at most max_seqlen_q <= 256), parents first, -1 for a root.
+    Returns (mask int32 [T, ceil(max_seqlen_q / 32)], positions int32 [T]) for
+    msa_tree_attention and msa_rope_write; rows behind cu_seqlens_q's last and
+    of requests whose lengths do not fit keep their contents, which in new
+    tensors are undefined.  status: an int32 [1] tensor that MSA_STATUS_* bits
+    are OR-ed into; without it nothing tells of lengths that do not fit or of
+    parents that are no earlier tokens (taken for -1)."""
+    n = _tree_limit(max_seqlen_q)
+    words = (n + 31) // 32
+    try:
+        (T,), dev = parents.shape, parents.get_device()
+        sound = (
+            parents.dtype is cu_seqlens_q.dtype is cu_seqlens_k.dtype is torch.int32
+            and cu_seqlens_q.shape == cu_seqlens_k.shape and cu_seqlens_q.dim() == 1
+            and cu_seqlens_q.shape[0] > 0 and parents.is_contiguous()
+            and cu_seqlens_q.is_contiguous() and cu_seqlens_k.is_contiguous()
+            and mask is None and positions is None and status is None and dev >= 0
+            and dev == cu_seqlens_q.get_device() == cu_seqlens_k.get_device()
+            == torch._C._cuda_getDevice())
+    except _NOT_SOUND:
+        sound = False
+    if not sound:
+        _check_tree({"parents": parents}, cu_seqlens_q, cu_seqlens_k,
+                    {"mask": (mask, _WORD, (T, words)), "positions": (positions, _I32, (T,))}
+                    if parents is not None and parents.dim() == 1 else {}, status)
+        _place(parents, cu_seqlens_q, cu_seqlens_k, mask, positions, status)
+        _apart({"mask": mask, "positions": positions},
+               {"parents": parents, "cu_seqlens_q": cu_seqlens_q, "cu_seqlens_k": cu_seqlens_k})
+    handle = _handle(stream, dev)
+    if mask is None:
+        mask = _new((T, words), torch.int32, dev, handle)
+    if positions is None:
+        positions = _new((T,), torch.int32, dev, handle)
+    rc = load().msa_tree_mask(parents.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(),
+                              cu_seqlens_q.shape[0] - 1, T, n, mask.data_ptr(),
+                              positions.data_ptr(), _ptr(status), handle)
+    if rc:
+        _check(rc, "msa_tree_mask")
+    return mask, positions
+
+
+def msa_tree_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_table, cu_seqlens_q,
+                       cu_seqlens_k, mask, prefix_pages, max_seqlen_q, max_seqlen_k,
+                       workspace=None, out=None, lse=None, want_lse=True, status=None,
+                       stream=None):
+    """Dense attention of trees of drafted tokens over the E4M3 pool: as
+    msa_prefix_attention (whose arguments, workspace and returns these are),
+    with each token attending to all keys before its request's new ones, and of
+    these to those whose bits are set in its words of mask, int32 [T, at least
+    ceil(max_seqlen_q / 32)] (msa_tree_mask's, or any others); max_seqlen_q at
+    most 256.  A token that sees no key gets zeros and lse -inf."""
+    n = _tree_limit(max_seqlen_q)
+    _tensor(mask, "mask", _WORD)
+    shape = mask.shape
+    if q is None or q.dim() != 3 or len(shape) != 2 or shape[0] != q.shape[0] or shape[1] * 32 < n:
+        _fail("mask must be [%s, %d or more], got %s",
+              "T" if q is None or q.dim() != 3 else q.shape[0], (n + 31) // 32, tuple(shape))
+    return _attend("msa_tree_attention", q, kv, q_scale, k_scale, v_scale, softmax_scale,
+                   block_table, cu_seqlens_q, cu_seqlens_k, mask, prefix_pages, max_seqlen_q,
+                   max_seqlen_k, workspace, out, lse, want_lse, status, stream)
+
+
+def _pools(kv, fp4):
+    """The layers' pools of a call, as a list of tensors of one shape."""
+    if kv is None:
+        return []
+    if isinstance(kv, torch.Tensor):
+        return list(kv.unbind(0)) if kv.dim() == 5 else [kv]
+    return list(kv)
+
+
+def _check_accept(fp4, drafts, parents, chosen, cu_q, cu_k, n, pools, table, tokens, accepted,
+                  path, status):
+    B = _requests(cu_q, "cu_seqlens_q")
+    _check_tree({"draft_tokens": drafts, "parents": parents, "chosen": chosen}, cu_q, cu_k,
+                {"tokens": (tokens, _I32, (B, n)), "accepted": (accepted, _I32, (B,)),
+                 "path": (path, _I32, (B, n))}, status)
+    if len(pools) > TREE_MAX_LAYERS:
+        _fail("at most %d layers, got %d", TREE_MAX_LAYERS, len(pools))
+    for p in pools:
+        _pool(p, fp4)
+        if p.shape != pools[0].shape:
+            _fail("the layers' pools differ: %s and %s", tuple(pools[0].shape), tuple(p.shape))
+    if pools:
+        _table(table, B)
+    dev = _place(drafts, parents, chosen, cu_q, cu_k, tokens, accepted, path, status, *pools,
+                 table if pools else None)
+    spans = sorted(_reach(p) for p in pools)
+    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+        _fail("the layers' pools must not share memory")
+    _apart({"tokens": tokens, "accepted": accepted, "path": path},
+           {"draft_tokens": drafts, "parents": parents, "chosen": chosen, "cu_seqlens_q": cu_q,
+            "cu_seqlens_k": cu_k})
+    return dev
+
+
+def _accept(name, fp4, drafts, parents, chosen, cu_q, cu_k, max_q, kv, table, tokens, accepted,
+            path, status, stream):
+    n = _tree_limit(max_q)
+    pools = _pools(kv, fp4)
+    dev = -1
+    try:
+        shape = pools[0].shape if pools else None
+        page = _PAGE4 if fp4 else _PAGE
+        B, dev = cu_q.shape[0] - 1, drafts.get_device()
+        sound = (
+            drafts.dtype is parents.dtype is chosen.dtype is cu_q.dtype is cu_k.dtype
+            is torch.int32 and drafts.dim() == 1 == cu_q.dim() and B >= 0
+            and drafts.shape == parents.shape == chosen.shape and cu_q.shape == cu_k.shape
+            and drafts.is_contiguous() and parents.is_contiguous() and chosen.is_contiguous()
+            and cu_q.is_contiguous() and cu_k.is_contiguous() and len(pools) <= TREE_MAX_LAYERS
+            and tokens is None and accepted is None and path is None and status is None
+            and dev >= 0 and dev == parents.get_device() == chosen.get_device()
+            == cu_q.get_device() == cu_k.get_device() == torch._C._cuda_getDevice()
+            and (not pools or (
+                shape[2:] == page and len(shape) == 4 and table.dtype is torch.int32
+                and table.dim() == 2 and table.shape[0] == B and table.is_contiguous()
+                and table.get_device() == dev))
+            and all((p.dtype is torch.uint8 or (p.dtype in _E4M3 and not fp4)) and p.shape == shape
+                    and p.is_contiguous() and p.get_device() == dev for p in pools))
+    except _NOT_SOUND + (IndexError,):
+        sound = False
+    if not sound:
+        dev = _check_accept(fp4, drafts, parents, chosen, cu_q, cu_k, n, pools, table, tokens,
+                            accepted, path, status)
+    handle = _handle(stream, dev)
+    if tokens is None:
+        tokens = _new((B, n), torch.int32, dev, handle)
+    if accepted is None:
+        accepted = _new((B,), torch.int32, dev, handle)
+    if path is None:
+        path = _new((B, n), torch.int32, dev, handle)
+    L = len(pools)
+    at = (ctypes.c_void_p * L)(*[p.data_ptr() for p in pools]) if L else None
+    rc = getattr(load(), name)(
+        drafts.data_ptr(), parents.data_ptr(), chosen.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),
+        B, drafts.shape[0], n, at, L, shape[0] if L else 0, shape[1] if L else 0,
+        table.data_ptr() if L else None, table.shape[1] if L else 0, tokens.data_ptr(),
+        accepted.data_ptr(), path.data_ptr(), _ptr(status), handle)
+    if rc:
+        _check(rc, name)
+    return tokens, accepted, path
+
+
+def msa_tree_accept(draft_tokens, parents, chosen, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                    kv=None, block_table=None, tokens=None, accepted=None, path=None, status=None,
+                    stream=None):
+    """Which drafted tokens of each request's tree stand, and their rows moved in
+    the cache.  draft_tokens, parents, chosen int32 [T]: each node's token, its
+    parent (as in msa_tree_mask) and the target's own token after it (the best,
+    as msa_logprobs gives it, or a drawn one).  The path starts at a request's
+    first token and follows the target's choices.  kv: the pools of all layers,
+    a sequence of E4M3 pools [num_pages, Hkv, 128, 256] (at most 128, which
+    share no memory), one pool, a tensor [layers, ...] of them, or None: the
+    rows of the path are moved to follow the context directly, so that the
+    sequence goes on at length seq_len - q_len + 1 + accepted.  Returns (tokens
+    int32 [B, max_seqlen_q]: the drafts that stand, the next token, -1; accepted
+    int32 [B]; path int32 [B, max_seqlen_q]: the nodes, the first with them,
+    then -1).  status as in msa_tree_mask."""
+    return _accept("msa_tree_accept", False, draft_tokens, parents, chosen, cu_seqlens_q,
+                   cu_seqlens_k, max_seqlen_q, kv, block_table, tokens, accepted, path, status,
+                   stream)
+
+
+def msa_tree_accept_nvfp4(draft_tokens, parents, chosen, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                          kv=None, block_table=None, tokens=None, accepted=None, path=None,
+                          status=None, stream=None):
+    """msa_tree_accept with NVFP4 pools uint8 [num_pages, Hkv, 2, 9216]."""
+    return _accept("msa_tree_accept_nvfp4", True, draft_tokens, parents, chosen, cu_seqlens_q,
+                   cu_seqlens_k, max_seqlen_q, kv, block_table, tokens, accepted, path, status,
+                   stream)
+
+
+def _check_logprobs(logits, tokens, top, outs):
+    _tensor(logits, "logits", _TYPES, None, False)
+    if logits.dim() != 2:
+        _fail("logits must be [T, V], got %s", tuple(logits.shape))
+    T, V = logits.shape
+    if V > 1 and logits.stride(1) != 1:
+        _fail("logits' rows must be contiguous")
+    if tokens is not None:
+        _tensor(tokens, "tokens", _I32, (T,))
+    elif outs["logprobs"] is not None or outs["ranks"] is not None:
+        _fail("logprobs and ranks need tokens")
+    for name, dtypes, shape in (("logprobs", _F32, (T,)), ("ranks", _I32, (T,)),
+                                ("entropy", _F32, (T,)), ("top_tokens", _I32, (T, top)),
+                                ("top_logprobs", _F32, (T, top))):
+        if outs[name] is not None:
+            _tensor(outs[name], name, dtypes, shape)
+    dev = _place(logits, tokens, *outs.values())
+    _apart(outs, {"logits": logits, "tokens": tokens})
+    return dev
+
+
+def msa_logprobs(logits, tokens=None, top=0, logprobs=None, ranks=None, entropy=None,
+                 top_tokens=None, top_logprobs=None, stream=None):
+    """Log probabilities from logits [T, V] (fp32, bf16 or fp16; rows may be
+    strided; -inf: a probability of 0) of the given tokens int32 [T], with their
+    ranks, and each row's entropy and best alternatives (top <= 32).  Returns
+    (logprobs fp32 [T], ranks int32 [T] (0: the best), entropy fp32 [T] in nats,
+    top_tokens int32 [T, top], top_logprobs fp32 [T, top]); the first two are
+    None without tokens.  Of equal logits the lower index comes first.  A token
+    outside [0, V) has -inf and rank -1; a row with a NaN has NaN, but for the
+    tokens and ranks."""
+    top = int(top)
+    if not 0 <= top <= LOGPROBS_MAX_TOP:
+        _fail("top must be 0 .. %d, got %d", LOGPROBS_MAX_TOP, top)
+    dev = -1
+    try:
+        (T, V), (row, one) = logits.shape, logits.stride()
+        dev = logits.get_device()
+        sound = (
+            logits.dtype in _TYPES and (one == 1 or V == 1)
+            and (tokens is None or (tokens.dtype is torch.int32 and tokens.shape == (T,)
+                                    and tokens.is_contiguous() and tokens.get_device() == dev))
+            and logprobs is None and ranks is None and entropy is None and top_tokens is None
+            and top_logprobs is None and dev >= 0 and dev == torch._C._cuda_getDevice())
+    except _NOT_SOUND:
+        sound = False
+    if not sound:
+        dev = _check_logprobs(logits, tokens, top,
+                              {"logprobs": logprobs, "ranks": ranks, "entropy": entropy,
+                               "top_tokens": top_tokens, "top_logprobs": top_logprobs})
+    handle = _handle(stream, dev)
+    if tokens is not None and logprobs is None:
+        logprobs = _new((T,), torch.float32, dev, handle)
+    if tokens is not None and ranks is None:
+        ranks = _new((T,), torch.int32, dev, handle)
+    if entropy is None:
+        entropy = _new((T,), torch.float32, dev, handle)
+    if top_tokens is None:
+        top_tokens = _new((T, top), torch.int32, dev, handle)
+    if top_logprobs is None:
+        top_logprobs = _new((T, top), torch.float32, dev, handle)
+    rc = load().msa_logprobs(logits.data_ptr(), row, _TYPES[logits.dtype], _ptr(tokens), T, V, top,
+                             _ptr(logprobs), _ptr(ranks), entropy.data_ptr(), top_tokens.data_ptr(),
+                             top_logprobs.data_ptr(), handle)
+    if rc:
+        _check(rc, "msa_logprobs")
+    return logprobs, ranks, entropy, top_tokens, top_logprobs

@@ -79,6 +79,7 @@ extern "C" {
 #define MSA_STATUS_ROWS_OVERFLOW (1u << 3)/* sum of page counts > total_rows */
 #define MSA_STATUS_TIMEOUT (1u << 4)      /* a bounded device wait expired   */
 #define MSA_STATUS_BAD_WORK (1u << 5)     /* inconsistent work item skipped  */
+#define MSA_STATUS_BAD_TREE (1u << 6)     /* a parent that is no earlier node */
 
 /* element types (split partials of msa_combine: F32 or BF16) */
 #define MSA_DTYPE_F32 0
@@ -663,6 +664,99 @@ MSA_API int msa_prefix_attention(const uint8_t *q, const uint8_t *kv, int64_t nu
                          void *stream);
 
 /*
+ * Trees of drafted tokens.  A request's new tokens (cu_seqlens_q) are the nodes
+ * of its tree, at most MSA_TREE_MAX_TOKENS, parents before their children;
+ * parents[t] is a node's parent by its place among the request's tokens, -1 for
+ * a root.  Node 0 is the request's last known token.  In the cache the nodes
+ * are the last q_len places of their request, in their order (as msa_kv_write
+ * and msa_rope_write put them); their positions follow from their depth.
+ *
+ * msa_tree_mask: for each token the words that msa_tree_attention takes, bit j
+ * % 32 of word j / 32 set where node j is the token itself or an ancestor, and
+ * its position seq_len - q_len + depth, as msa_rope_write takes it.
+ *   parents      int32 [T]; one that is no earlier node sets
+ *                MSA_STATUS_BAD_TREE, and its token is taken for a root
+ *   cu_seqlens_q, cu_seqlens_k  int32 [B + 1] as in msa_plan; the last of
+ *                cu_seqlens_q may be less than T
+ *   max_seqlen_q 0 .. MSA_TREE_MAX_TOKENS; a request with more tokens, or with
+ *                more than its length, sets MSA_STATUS_BAD_SEQLENS and its rows
+ *                are left as they are, as are those behind cu_seqlens_q[B]
+ *   mask         uint32 [T][ceil(max_seqlen_q / 32)], or NULL
+ *   positions    int32 [T], or NULL
+ * The outputs share no memory with the inputs.  One kernel on `stream`.
+ */
+#define MSA_TREE_MAX_TOKENS 256
+#define MSA_TREE_MAX_LAYERS 128
+MSA_API int msa_tree_mask(const int32_t *parents, const int32_t *cu_seqlens_q,
+                  const int32_t *cu_seqlens_k, int64_t B, int64_t T, int64_t max_seqlen_q,
+                  uint32_t *mask, int32_t *positions, uint32_t *status, void *stream);
+
+/*
+ * Dense attention of drafted trees over the paged cache: msa_prefix_attention
+ * (whose arguments, workspace, numerics, limits and status these are) with
+ * another mask: a token attends to all keys before its request's new ones, and
+ * of these to those whose bit is set in its words.
+ *   mask         uint32 [T][mask_words], mask_words >= ceil(max_seqlen_q / 32);
+ *                any bits (a token need not see itself; bits at or behind the
+ *                request's q_len have no effect).  A token without any key gets
+ *                zeros and lse -inf
+ *   max_seqlen_q at most MSA_TREE_MAX_TOKENS
+ * Codes of keys that a row does not attend to, NaN among them, have no effect
+ * on it.
+ */
+MSA_API int msa_tree_attention(const uint8_t *q, const uint8_t *kv, int64_t num_pages,
+                       float q_scale, float k_scale, float v_scale, float softmax_scale,
+                       const int32_t *block_table, int64_t bt_stride,
+                       const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                       const uint32_t *mask, int64_t mask_words, int64_t B, int64_t T,
+                       int64_t Hq, int64_t Hkv, int64_t prefix_pages, int64_t max_seqlen_q,
+                       int64_t max_seqlen_k, void *workspace, size_t workspace_bytes,
+                       uint16_t *out, float *lse, uint32_t *status, void *stream);
+
+/*
+ * Acceptance of drafted trees, the step after the target has run on them: with
+ * chosen[t] the target's own token after token t (its best, as
+ * msa_logprobs gives it, or one drawn from its distribution, which keeps that
+ * distribution), the path starts at node 0 and goes on to the first child whose
+ * draft token is the choice after the node before it, as long as there is one.
+ * The rows of the path are then moved in the cache to where a sequence of those
+ * tokens has them: row seq_len - q_len + path[j] becomes row seq_len - q_len +
+ * j, in every layer's pool (K was rotated to the node's depth, which is j), so
+ * that the sequence goes on at length seq_len - q_len + 1 + accepted.
+ *   draft_tokens int32 [T]: the token of each node (node 0's is not looked at)
+ *   parents      as in msa_tree_mask; a node whose parent is no earlier node
+ *                (other than -1) sets MSA_STATUS_BAD_TREE and is on no path
+ *   chosen       int32 [T]
+ *   kv / kv4     host array of `layers` pools (0 .. MSA_TREE_MAX_LAYERS) in
+ *                device memory, each as in msa_kv_write and of num_pages pages;
+ *                they share no memory with one another (MSA_ERR_SHAPE)
+ *   block_table  as in msa_plan; pages that rows are moved in belong to one
+ *                request each.  Rows whose place is no page (MSA_STATUS_BAD_BLOCK)
+ *                or lies behind the table (BAD_SEQLENS) are not moved.  With
+ *                layers = 0 neither is needed
+ *   tokens       int32 [B][max_seqlen_q]: the drafts that stand, the target's
+ *                token after them, -1
+ *   accepted     int32 [B]: how many drafts stand
+ *   path         int32 [B][max_seqlen_q]: the path's nodes, 0 first, then -1; or
+ *                NULL
+ * A request without tokens, or whose lengths do not fit (BAD_SEQLENS, as in
+ * msa_tree_mask), gets -1 in all places and accepted 0.  The outputs share no
+ * memory with the inputs or each other.  One kernel on `stream`.
+ */
+MSA_API int msa_tree_accept(const int32_t *draft_tokens, const int32_t *parents,
+                    const int32_t *chosen, const int32_t *cu_seqlens_q,
+                    const int32_t *cu_seqlens_k, int64_t B, int64_t T, int64_t max_seqlen_q,
+                    uint8_t *const *kv, int64_t layers, int64_t num_pages, int64_t Hkv,
+                    const int32_t *block_table, int64_t bt_stride, int32_t *tokens,
+                    int32_t *accepted, int32_t *path, uint32_t *status, void *stream);
+MSA_API int msa_tree_accept_nvfp4(const int32_t *draft_tokens, const int32_t *parents,
+                    const int32_t *chosen, const int32_t *cu_seqlens_q,
+                    const int32_t *cu_seqlens_k, int64_t B, int64_t T, int64_t max_seqlen_q,
+                    uint8_t *const *kv4, int64_t layers, int64_t num_pages, int64_t Hkv,
+                    const int32_t *block_table, int64_t bt_stride, int32_t *tokens,
+                    int32_t *accepted, int32_t *path, uint32_t *status, void *stream);
+
+/*
  * Verification of drafted tokens, the step after a speculative-verify decode:
  * which of a request's drafts stand, and the token that follows them.  With
  * p_i the target's and q_i the draft model's probabilities at draft i and
@@ -710,6 +804,32 @@ MSA_API int msa_verify_greedy(const void *target, int64_t target_req, int64_t ta
                       int dtype, const int32_t *draft_tokens, const int32_t *num_drafts,
                       int64_t B, int64_t n, int64_t V, int32_t *tokens, int32_t *accepted,
                       void *stream);
+
+/*
+ * Log probabilities from logits: of given tokens, with their ranks, and each
+ * row's entropy and best alternatives, with p = softmax of the row.
+ *   logits       [T][V] in `dtype`, row t at t * row_stride elements, aligned to
+ *                its elements; -inf is a probability of 0
+ *   tokens       int32 [T], or NULL (then logprobs and ranks are NULL)
+ *   logprobs     fp32 [T] log p of the row's token; -inf for a token outside
+ *                [0, V)
+ *   ranks        int32 [T] how many tokens come before it, by larger logit, of
+ *                equal ones by lower index (0: the best); -1 for a token outside
+ *                [0, V) or with a NaN logit
+ *   entropy      fp32 [T] -sum p log p in nats
+ *   top_tokens   int32 [T][top] the best tokens in that order (NaN is never
+ *                among them; -1 where there are no more values)
+ *   top_logprobs fp32 [T][top] their log p; -inf beside -1
+ * 0 <= top <= MSA_LOGPROBS_MAX_TOP; each output but those of `top` may be NULL.
+ * A row whose logits are all -inf has no probabilities: log p -inf, entropy 0.
+ * NaN or +inf in a row makes its log p and entropy NaN (not those of no token).
+ * Sums are fp32, 1 <= V < MSA_VERIFY_MAX_VOCAB.  The outputs share no memory
+ * with the inputs or each other.  One kernel on `stream`.
+ */
+#define MSA_LOGPROBS_MAX_TOP 32
+MSA_API int msa_logprobs(const void *logits, int64_t row_stride, int dtype, const int32_t *tokens,
+                 int64_t T, int64_t V, int64_t top, float *logprobs, int32_t *ranks,
+                 float *entropy, int32_t *top_tokens, float *top_logprobs, void *stream);
 
 /*
  * For tests of the expiry path only: sets the wall-time limit, in
