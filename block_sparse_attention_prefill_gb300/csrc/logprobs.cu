@@ -3,18 +3,20 @@
 //
 // With m near the row's maximum, l = sum e^(x - m) and s = sum e^(x - m) (x - m):
 //   log p(t) = (x_t - m) - log l,   H = log l - s / l
-// m, l and s are kept by each thread in fp32, m raised when a larger value is
-// met, and merged at the end by their m.  x - m is taken before it is multiplied
-// by log2 e, so that large logits cost no accuracy.
+// m, l and s are kept by each thread in fp32 (as powers of 2), m raised for a
+// whole warp when a larger value is met, and merged at the end by their m.
 //
 // The k best are found without a list kept on the way: the pass notes the
 // largest value of every chunk of 512 bytes (a warp's load).  The k best values
 // lie in the k chunks whose largest come first (of equal ones those with lower
-// indices): any other chunk has k values before all of its own.  These chunks
-// are read again, from L2, and the k-th best of their values is found by
-// bisection on keys (value, index) that are all different, so that the work
-// is bounded whatever the row holds (all equal, ascending, masked).  Bisection
-// ends as soon as few enough keys are left; they are put in order by counting.
+// indices): any other chunk has k values before all of its own.  The chunks are
+// dealt out to 64 buckets, and the k-th largest of the buckets' largest values is
+// a bound that the k best pass, and few more chunks (24 for k = 20, were they in
+// random order); these are read again, from L2, and their values that pass it,
+// 512 at most, are put in order by counting.  Where more than that pass (rows
+// that are all equal, ascending, masked) bounds are found by bisection on keys
+// (value, index) that are all different, so that the work is bounded whatever
+// the row holds.
 //
 // A cluster of 1 to 8 CTAs takes a row (as many as fill the GPU when there are
 // few rows): each finds its own k best, and the first merges them through
@@ -35,24 +37,45 @@ namespace cg = cooperative_groups;
 namespace msa {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kMaxCluster = 8;
 constexpr int kTop = MSA_LOGPROBS_MAX_TOP;
 constexpr int kBatch = 4;        // chunks of a warp in flight
 constexpr int kVocabBits = 19;   // V < 2^19
 constexpr int kChunkBits = 13;   // chunks of a row: at most 4097
+constexpr int kVecBits = 18;     // vectors of a row: at most 2^17 + 1
 constexpr int kMaxChunks = (MSA_VERIFY_MAX_VOCAB * 4) / 512 + 1;
-constexpr int kMostChunks = 48;  // chunks that are read again (at least k)
-constexpr int kFew = 64;         // keys that are put in order by counting
+constexpr int kMostChunks = 48;  // chunks that are read again
+constexpr int kMine = kMostChunks / kWarps;  // vectors of a thread among them
+constexpr int kMostVecs = 64;    // vectors whose values are looked at
+constexpr int kFew = kMostVecs * 8;
+constexpr int kBuckets = 64;     // a CTA's whole chunks, dealt out in turn
 static_assert(MSA_VERIFY_MAX_VOCAB == 1 << kVocabBits && kMaxChunks < 1 << kChunkBits, "keys");
-static_assert(kMostChunks % kWarps == 0 && kTop <= kMostChunks && kTop <= kFew, "selection");
+static_assert(kMostChunks % kWarps == 0 && kTop == 32 && kTop <= kMostChunks && kTop <= kMostVecs &&
+                  kMaxCluster * kTop == kThreads && kThreads % kBuckets == 0,
+              "selection");
 constexpr float kLowest = -FLT_MAX;  // m before any value (finite: x - m is no NaN)
-constexpr float kFar = -200.f;       // e^d is 0 in fp32 at and below this, and 0 times it 0
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kFar = -200.f;       // 2^t is 0 in fp32 at and below this, and 0 times it 0
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309f;
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float x) {
+  if constexpr (sizeof(T) == 4) return x;
+  else if constexpr (std::is_same<T, __half>::value) return __float2half(x);
+  else return __float2bfloat16(x);
+}
+// The next larger number of the type (NaN above infinity).
+template <typename T>
+__device__ __forceinline__ T next_above(T x) {
+  using U = typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type;
+  constexpr U kSign = (U)1 << (8 * sizeof(T) - 1);
+  U u = *reinterpret_cast<const U*>(&x);
+  u = (U)(u << 1) == 0 ? (U)1 : u & kSign ? (U)(u - 1) : (U)(u + 1);
+  return *reinterpret_cast<const T*>(&u);
+}
 
 // An integer whose order is that of the values; +0 and -0 are equal, NaN is
 // below all (0).
@@ -63,10 +86,22 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 __device__ __forceinline__ float value_of(uint32_t k) {
   return __uint_as_float((k >> 31) ? k & 0x7FFFFFFFu : ~k);
 }
+// A value and its place; keys of one row are all different.
+__device__ __forceinline__ uint64_t value_key(float x, int place) {
+  const uint32_t o = order_of(x);
+  return o ? ((uint64_t)o << kVocabBits) | (uint32_t)((1 << kVocabBits) - 1 - place) : 0ull;
+}
 
 __device__ __forceinline__ float max_or_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float largest(float a, float b) { return fmaxf(a, b); }  // leaves NaN out
+// The largest of the warp's values, NaN left out.
+__device__ __forceinline__ float warp_max(float x) {
+  float d;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(x));
   return d;
 }
 
@@ -82,52 +117,124 @@ struct Row {
 template <typename T>
 struct Vec {
   static constexpr int N = 16 / sizeof(T);
+  static constexpr bool k16 = sizeof(T) == 2;
+  using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
   uint32_t w[4];
+  __device__ __forceinline__ T2 two(int i) const { return *reinterpret_cast<const T2*>(&w[i]); }
   __device__ __forceinline__ float at(int i) const {
-    if constexpr (sizeof(T) == 4) {
+    if constexpr (!k16) {
       return __uint_as_float(w[i]);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      return __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
     } else {
-      const uint16_t h = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-      return to_f32(*reinterpret_cast<const T*>(&h));
+      return i & 1 ? __high2float(two(i >> 1)) : __low2float(two(i >> 1));
     }
   }
+  __device__ __forceinline__ void load(const Row<T>& r, int v) {  // wholly inside the row
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(r.base) + v);
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  }
   // -inf in places outside the row
-  __device__ __forceinline__ void load(const Row<T>& r, int v) {
+  __device__ __forceinline__ void load_edge(const Row<T>& r, int v) {
     const int first = v * N - r.shift;
-    if (first >= 0 && first + N <= r.V) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(r.base) + v);
-      w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-    } else {
-      const uint32_t inf = sizeof(T) == 4 ? 0xFF800000u
-                           : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+    if (first >= 0 && first + N <= r.V) return load(r, v);
+    const uint32_t inf = !k16 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = inf;
+    for (int i = 0; i < 4; ++i) w[i] = inf;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (first + i >= 0 && first + i < r.V) {
-          if constexpr (sizeof(T) == 4) {
-            w[i] = __ldg(reinterpret_cast<const uint32_t*>(r.base) + v * N + i);
-          } else {
-            const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(r.base) + v * N + i);
-            w[i >> 1] = i & 1 ? (w[i >> 1] & 0xFFFFu) | (h << 16) : (w[i >> 1] & 0xFFFF0000u) | h;
-          }
+    for (int i = 0; i < N; ++i) {
+      if (first + i >= 0 && first + i < r.V) {
+        if constexpr (!k16) {
+          w[i] = __ldg(reinterpret_cast<const uint32_t*>(r.base) + v * N + i);
+        } else {
+          const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(r.base) + v * N + i);
+          w[i >> 1] = i & 1 ? (w[i >> 1] & 0xFFFFu) | (h << 16) : (w[i >> 1] & 0xFFFF0000u) | h;
         }
       }
     }
   }
-  // the order of its largest value in the row
-  __device__ __forceinline__ uint32_t top(const Row<T>& r, int v) const {
-    const int first = v * N - r.shift;
-    float x = __uint_as_float(0x7FFFFFFFu);  // fmaxf leaves NaN out
-    if (first >= 0 && first + N <= r.V) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) x = fmaxf(x, at(i));
+  // its largest value, NaN if it has none
+  __device__ __forceinline__ float top() const {
+    if constexpr (k16) {
+      const T2 x = __hmax2(__hmax2(two(0), two(1)), __hmax2(two(2), two(3)));
+      return largest(__low2float(x), __high2float(x));
     } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (first + i >= 0 && first + i < r.V) x = fmaxf(x, at(i));
+      return largest(largest(at(0), at(1)), largest(at(2), at(3)));
     }
-    return order_of(x);
+  }
+  // the same of a vector that may reach over the row's ends
+  __device__ __forceinline__ float top_edge(const Row<T>& r, int v) const {
+    float x = __uint_as_float(0x7FFFFFFFu);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int place = v * N - r.shift + i;
+      if (place >= 0 && place < r.V) x = largest(x, at(i));
+    }
+    return x;
+  }
+};
+
+// Whether m log2 e may leave fp32's range (m = -FLT_MAX: no value yet).
+__device__ __forceinline__ bool huge(float m) { return !(fabsf(m) < 2e38f); }
+enum { kPlain, kBounded, kHuge };
+
+// What a thread gathers on its way, in powers of 2: with r the reference m log2
+// e rounded to fp32, l = sum 2^t and s = sum 2^t t of t = x log2 e - r, a fused
+// operation.  What log2 e and r lack of exactness is the same in all terms and
+// in the token's own t, so that large logits cost no accuracy.
+template <typename T>
+struct Sums {
+  using V = Vec<T>;
+  float m, r;
+  float2 l, s;  // (of the even and the odd values)
+  int before;   // values that come before the token
+  // What is far below m counts as that far: -inf would give 0 times -inf.  Of 16
+  // bits two values at once before they are widened, by a number `low` that lies
+  // at least 200 below m whichever way it is rounded; where the type has none,
+  // and of fp32, t is bounded.  Where r would not be finite t is (x - m) log2 e.
+  typename V::T2 low;
+  int mode;
+
+  __device__ __forceinline__ void raise(float to) {
+    const float r2 = to * kLog2e;
+    const float d = max_or_nan(huge(to) ? (m - to) * kLog2e : r - r2, kFar), f = ex2_approx(d);
+    s = make_float2(f * fmaf(l.x, d, s.x), f * fmaf(l.y, d, s.y));
+    l = make_float2(l.x * f, l.y * f);
+    m = to, r = r2;
+    mode = huge(to) ? kHuge : kBounded;
+    if constexpr (V::k16) {
+      constexpr bool kHalf = std::is_same<T, __half>::value;
+      const float least = m + kFar - fabsf(m) * 0.015625f;
+      if (least > (kHalf ? -64000.f : -3.3e38f) && mode == kBounded) mode = kPlain;
+      if constexpr (kHalf) low = __float2half2_rn(least);
+      else low = __float2bfloat162_rn(least);
+    }
+  }
+  template <int kMode>
+  __device__ __forceinline__ void add_as(const V& v) {
+    const float2 r2 = make_float2(-r, -r), c2 = make_float2(kLog2e, kLog2e);
+#pragma unroll
+    for (int i = 0; i < 4; i += V::k16 ? 1 : 2) {
+      float2 t;
+      if constexpr (V::k16) {
+        V x = v;
+        if constexpr (kMode == kPlain) {
+          const typename V::T2 y = __hmax2_nan(v.two(i), low);
+          x.w[i] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+        t = make_float2(x.at(2 * i), x.at(2 * i + 1));
+      } else {
+        t = make_float2(v.at(i), v.at(i + 1));
+      }
+      if constexpr (kMode == kHuge)
+        t = mul2(add2(t, make_float2(-m, -m)), c2);
+      else
+        t = fma2(t, c2, r2);
+      if constexpr (kMode != kPlain) t.x = max_or_nan(t.x, kFar), t.y = max_or_nan(t.y, kFar);
+      const float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+      l = add2(l, p);
+      s = fma2(p, t, s);
+    }
   }
 };
 
@@ -149,27 +256,30 @@ __device__ __forceinline__ uint64_t pick(uint64_t lo, uint64_t hi, int n_lo, int
     int all = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) all += s_sum[turn][i];
-    if (all >= k) lo = mid, n_lo = all, step = ~0ull; else hi = mid, step = step > ~0ull / 4 ? ~0ull : 4 * step;
+    if (all >= k) lo = mid, n_lo = all, step = ~0ull;
+    else hi = mid, step = step > ~0ull / 4 ? ~0ull : 4 * step;
   }
   __syncthreads();
   return lo;
 }
 
 struct Part {  // of a warp
-  float m, l, s;
-  int before;  // values that come before the token
+  float m, r, l, s;
+  int before;
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArgs a, int cluster_size) {
-  constexpr int N = Vec<T>::N;
-  __shared__ uint32_t s_key[kMaxChunks];
-  __shared__ uint32_t s_top[kWarps];
-  __shared__ Part s_part[kMaxCluster * kWarps];            // rank 0's is complete
-  __shared__ uint64_t s_all[kMaxCluster][kTop];            // likewise
+__global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobsArgs a, int cluster_size) {
+  using V = Vec<T>;
+  constexpr int N = V::N;
+  extern __shared__ float s_max[];  // the largest value of each chunk
+  __shared__ float s_top[kWarps], s_bound;
+  __shared__ __align__(16) float s_bucket[kBuckets];
+  __shared__ Part s_part[kMaxCluster * kWarps];  // rank 0's is complete
+  __shared__ uint64_t s_all[kMaxCluster][kTop];  // likewise; in order, 0 behind the last
   __shared__ uint64_t s_cand[kFew], s_best[kTop];
   __shared__ int s_list[kMostChunks];
-  __shared__ int s_n[2];
+  __shared__ int s_n[2];  // chunks listed, values gathered
   cg::cluster_group cluster = cg::this_cluster();
   // a CTA's shared memory may be written from outside once it has started
   if (cluster_size > 1) cluster.barrier_arrive();
@@ -178,185 +288,314 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = cluster_size > 1 ? (int)cluster.block_rank() : 0;
   const int64_t t = blockIdx.x / cluster_size;
-  const int V = a.V;
   Row<T> row;
   {
     const T* first = static_cast<const T*>(a.logits) + t * a.row;
     row.shift = (int)(reinterpret_cast<uintptr_t>(first) % 16 / sizeof(T));
     row.base = first - row.shift;
-    row.V = V;
+    row.V = a.V;
   }
-  const int chunks = (row.shift + V + 32 * N - 1) / (32 * N);
+  const int chunks = (row.shift + a.V + 32 * N - 1) / (32 * N);
   const int per = (chunks + cluster_size - 1) / cluster_size;
   const int c0 = min(chunks, rank * per), nch = min(chunks, c0 + per) - c0;  // this CTA's
-  Vec<T> x[2][kBatch];
-  auto load = [&](Vec<T> (&to)[kBatch], int i) {
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      // a chunk behind the CTA's last is one behind the row
-      const int c = i + k * kWarps < nch ? c0 + i + k * kWarps : chunks;
-      to[k].load(row, c * 32 + lane);
-    }
-  };
-  load(x[0], warp);
-  const int token = a.tokens ? __ldg(a.tokens + t) : -1;
-  const bool is_token = token >= 0 && token < V;
-  const float mine = is_token ? to_f32(row.base[row.shift + token]) : __uint_as_float(0x7FFFFFFFu);
-  const uint32_t mine_key = order_of(mine);  // 0: none
-
-  Part p = {kLowest, 0.f, 0.f, 0};
-  float2 l2 = make_float2(0.f, 0.f), s2 = l2;
-  uint32_t warp_top = 0;
-  auto add = [&](const Vec<T> (&v)[kBatch], int i) {
-    uint32_t key[kBatch], top = 0;
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int c = i + k * kWarps < nch ? c0 + i + k * kWarps : chunks;
-      key[k] = __reduce_max_sync(0xffffffffu, v[k].top(row, c * 32 + lane));
-      top = max(top, key[k]);
-    }
+  // its chunks that lie wholly inside the row: in0 .. in1 - 1
+  const int in0 = c0 == 0 && row.shift > 0 ? 1 : 0;
+  const int in1 = min(nch, (row.shift + a.V) / (32 * N) - c0);
+  V x[2][kBatch];
+  auto load = [&](V (&to)[kBatch], int c) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
-      if (lane == k && i + k * kWarps < nch) s_key[i + k * kWarps] = key[k];
-    if (top > warp_top) {
-      warp_top = top;
-      const float m = value_of(top);
-      if (m > p.m) {
-        const float d = max_or_nan(p.m - m, kFar), f = ex2_approx(d * kLog2e);
-        s2 = make_float2(f * fmaf(l2.x, d, s2.x), f * fmaf(l2.y, d, s2.y));
-        l2 = make_float2(l2.x * f, l2.y * f);
-        p.m = m;
-      }
-    }
-    const float2 m2 = make_float2(-p.m, -p.m), c2 = make_float2(kLog2e, kLog2e);
+      if (c + k * kWarps < in1) to[k].load(row, (c0 + c + k * kWarps) * 32 + lane);
+  };
+  load(x[0], in0 + warp);
+  const int token = a.tokens ? __ldg(a.tokens + t) : -1;
+  const bool is_token = token >= 0 && token < a.V;
+  const float mine = is_token ? to_f32(row.base[row.shift + token]) : __uint_as_float(0x7FFFFFFFu);
+  const int token_chunk = is_token ? (row.shift + token) / (32 * N) - c0 : -1;
+
+  Sums<T> sum;
+  sum.m = sum.r = kLowest;
+  sum.l = sum.s = make_float2(0.f, 0.f);
+  sum.before = 0;
+  sum.mode = kHuge;
+  // values before the token in a chunk that it lies in, or at an end of the row
+  auto count_places = [&](const V& v, int c) {
+    const int first = ((c0 + c) * 32 + lane) * N - row.shift;
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-#pragma unroll
-      for (int e = 0; e < N; e += 2) {
-        float2 d = add2(make_float2(v[k].at(e), v[k].at(e + 1)), m2);
-        d.x = max_or_nan(d.x, kFar), d.y = max_or_nan(d.y, kFar);
-        float2 w = mul2(d, c2);
-        w.x = ex2_approx(w.x), w.y = ex2_approx(w.y);
-        l2 = add2(l2, w);
-        s2 = fma2(w, d, s2);
-      }
-      if (key[k] >= mine_key && mine_key) {
-        const int first = ((c0 + i + k * kWarps) * 32 + lane) * N - row.shift;
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float y = v[k].at(e);
-          p.before += y > mine || (y == mine && first + e >= 0 && first + e < token);
-        }
-      }
+    for (int e = 0; e < N; ++e) {
+      const float y = v.at(e);
+      sum.before += y > mine || (y == mine && first + e >= 0 && first + e < token);
     }
   };
-  for (int i = warp; i < nch; i += 2 * kBatch * kWarps) {
-    load(x[1], i + kBatch * kWarps);
-    add(x[0], i);
-    if (i + kBatch * kWarps >= nch) break;
-    load(x[0], i + 2 * kBatch * kWarps);
-    add(x[1], i + kBatch * kWarps);
+  // the chunks that the row ends in
+  auto edge = [&](int c) {
+    V v;
+    const int at = (c0 + c) * 32 + lane;
+    v.load_edge(row, at);
+    const float top = warp_max(v.top_edge(row, at));
+    if (lane == 0) s_max[c] = top;
+    if (top > sum.m) sum.raise(top);
+    if (sum.mode == kHuge) sum.template add_as<kHuge>(v); else sum.template add_as<kBounded>(v);
+    count_places(v, c);
+  };
+  // In the chunks before the token's values as large come before it, in those
+  // behind it larger ones: values at or above the next larger number.
+  const T mine1 = from_f32<T>(mine), above1 = next_above(mine1);
+  const float above_mine = to_f32(above1);
+  const typename V::T2 mine2 = {mine1, mine1}, above2 = {above1, above1};
+  float bucket = -INFINITY;
+  int turn = 0;
+  auto add_some = [&](auto full, const V (&v)[kBatch], int c) {
+    float top[kBatch], most = kLowest;
+    auto there = [&](int k) { return decltype(full)::value || c + k * kWarps < in1; };
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (!there(k)) continue;
+      top[k] = warp_max(v[k].top());
+      most = largest(most, top[k]);
+    }
+    // lanes k, k + 4, ... take the k-th; one of them, another each time, keeps it
+    float kept = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (there(k) && lane % kBatch == k) kept = top[k];
+    if (lane / kBatch == turn % (32 / kBatch)) bucket = largest(bucket, kept);
+    ++turn;
+    if (lane < kBatch && (decltype(full)::value || c + lane * kWarps < in1)) s_max[c + lane * kWarps] = kept;
+    if (most > sum.m) sum.raise(most);
+    constexpr int kUsual = V::k16 ? kPlain : kBounded;
+    if (sum.mode == kUsual) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (there(k)) sum.template add_as<kUsual>(v[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (!there(k)) continue;
+        if (sum.mode == kHuge) sum.template add_as<kHuge>(v[k]); else sum.template add_as<kBounded>(v[k]);
+      }
+    }
+    if (!(most >= mine)) return;  // (no token: mine is NaN)
+    if (token_chunk >= c && token_chunk <= c + (kBatch - 1) * kWarps && (token_chunk - c) % kWarps == 0) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (there(k)) count_places(v[k], c + k * kWarps);
+      return;
+    }
+    using T2 = typename V::T2;
+    T2 n2 = T2{T(0.f), T(0.f)};
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (!there(k)) continue;
+      const bool before = c + k * kWarps < token_chunk;
+      if constexpr (V::k16) {
+        const T2 bound = before ? mine2 : above2;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n2 = __hadd2(n2, __hge2(v[k].two(i), bound));
+      } else {
+        const float bound = before ? mine : above_mine;
+#pragma unroll
+        for (int e = 0; e < N; ++e) sum.before += v[k].at(e) >= bound;
+      }
+    }
+    if constexpr (V::k16) sum.before += (int)(__low2float(n2) + __high2float(n2));  // at most 32
+  };
+  auto add = [&](const V (&v)[kBatch], int c) {
+    if (c + (kBatch - 1) * kWarps < in1) add_some(std::true_type(), v, c);
+    else add_some(std::false_type(), v, c);
+  };
+  constexpr int kStep = kBatch * kWarps;
+  if (in0 > 0 && warp == kWarps - 1) edge(0);
+  for (int c = max(in1, in0) + warp; c < nch; c += kWarps) edge(c);
+  for (int c = in0 + warp; c < in1; c += 2 * kStep) {
+    load(x[1], c + kStep);
+    add(x[0], c);
+    if (c + kStep >= in1) break;
+    load(x[0], c + 2 * kStep);
+    add(x[1], c + kStep);
   }
-  p.l = l2.x + l2.y, p.s = s2.x + s2.y;
+  Part p = {sum.m, sum.r, sum.l.x + sum.l.y, sum.s.x + sum.s.y, sum.before};
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     p.l += __shfl_xor_sync(0xffffffffu, p.l, o);
     p.s += __shfl_xor_sync(0xffffffffu, p.s, o);
     p.before += __shfl_xor_sync(0xffffffffu, p.before, o);
   }
-  if (lane == 0) s_top[warp] = warp_top;
+  if (lane == 0) s_top[warp] = sum.m;
+  // 64 buckets of the CTA: a warp's 32 lanes by as many together as make 64
+  constexpr int kOfWarp = kBuckets / kWarps;
+#pragma unroll
+  for (int o = 16; o >= kOfWarp; o >>= 1) bucket = largest(bucket, __shfl_xor_sync(0xffffffffu, bucket, o));
+  if (lane < kOfWarp) s_bucket[warp * kOfWarp + lane] = bucket;
   if (tid < 2) s_n[tid] = 0;
   if (tid < kTop) s_best[tid] = 0;
   __syncthreads();
 
   const int k = a.top;
   if (k > 0 && nch > 0) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) top = max(top, s_top[i]);
-    // the chunks that the k best lie in
-    auto chunk_key = [&](int c) {
-      return ((uint64_t)s_key[c] << kChunkBits) | (uint32_t)((1 << kChunkBits) - 1 - c);
-    };
-    const uint64_t from = pick(0, (uint64_t)(top + 1ull) << kChunkBits, nch, min(k, nch), kMostChunks,
-                               1ull << (20 + kChunkBits), [&](uint64_t key) {
-                                 int n = 0;
-                                 for (int c = tid; c < nch; c += kThreads) n += chunk_key(c) >= key;
-                                 return n;
-                               });
-    for (int c = tid; c < nch; c += kThreads)
-      if (chunk_key(c) >= from) s_list[atomicAdd(&s_n[0], 1)] = c0 + c;
-    __syncthreads();
-    const int listed = s_n[0];
-    constexpr int kMine = kMostChunks / kWarps;
-    Vec<T> y[kMine];
+    // this thread's vectors of the listed chunks, -1: none
+    V y[kMine];
     int at[kMine];
+    auto read = [&](int listed) {
 #pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-      const int c = j * kWarps + warp < listed ? s_list[j * kWarps + warp] : chunks;
-      at[j] = c * 32 + lane;
-      y[j].load(row, at[j]);
-    }
-    auto value_key = [&](int j, int e) {
-      const int i = at[j] * N - row.shift + e;
-      const uint32_t o = i >= 0 && i < V ? order_of(y[j].at(e)) : 0u;
-      return o ? ((uint64_t)o << kVocabBits) | (uint32_t)((1 << kVocabBits) - 1 - i) : 0ull;
+      for (int j = 0; j < kMine; ++j) {
+        at[j] = j * kWarps + warp < listed ? s_list[j * kWarps + warp] * 32 + lane : -1;
+        if (at[j] >= 0) y[j].load_edge(row, at[j]);
+      }
     };
-    auto count = [&](uint64_t key) {
+    // The places of the values at or above a bound above -inf, of the vectors of
+    // which `take` says so; few lanes have any.
+    auto gather = [&](float bound, auto take) {
+      uint32_t hits[kMine];
       int n = 0;
 #pragma unroll
-      for (int j = 0; j < kMine; ++j)
+      for (int j = 0; j < kMine; ++j) {
+        hits[j] = 0;
 #pragma unroll
-        for (int e = 0; e < N; ++e) n += value_key(j, e) >= key;
-      return n;
-    };
-    // every listed chunk has a value at or above the least of their largest
-    const uint64_t least = max((uint64_t)1, (from >> kChunkBits) << kVocabBits);
-    const int some = __reduce_add_sync(0xffffffffu, count(least));
-    if (lane == 0 && some) atomicAdd(&s_n[1], some);
-    __syncthreads();
-    const int n = s_n[1];
-    if (tid == 0) s_n[0] = 0;
-    const uint64_t low = pick(least, (uint64_t)(top + 1ull) << kVocabBits, n, min(k, n), kFew,
-                              1ull << (20 + kVocabBits), count);
-    // (pick's last barrier stands behind s_n[0] = 0)
-#pragma unroll
-    for (int j = 0; j < kMine; ++j)
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const uint64_t key = value_key(j, e);
-        if (key >= low) s_cand[atomicAdd(&s_n[0], 1)] = key;
+        for (int e = 0; e < N; ++e) hits[j] |= y[j].at(e) >= bound ? 1u << e : 0u;
+        if (at[j] < 0 || !take(j)) hits[j] = 0;
+        n += __popc(hits[j]);
       }
-    __syncthreads();
-    const int cands = s_n[0];
-    if (tid < cands) {
-      const uint64_t key = s_cand[tid];
+      if (n > 0) {
+        int to = atomicAdd(&s_n[1], n);
+#pragma unroll
+        for (int j = 0; j < kMine; ++j)
+          for (uint32_t h = hits[j]; h; h &= h - 1, ++to)
+            if (to < kFew) s_cand[to] = (uint64_t)(at[j] * N - row.shift + __ffs(h) - 1);
+      }
+    };
+    // A bound for the k-th best: the k-th largest of the buckets' largest values,
+    // whose place is the number of those before it (some threads a value)
+    {
+      constexpr int kShare = kThreads / kBuckets;
+      const int j = tid / kShare, i0 = tid % kShare * (kBuckets / kShare);
+      const float u = s_bucket[j];
       int place = 0;
-      for (int i = 0; i < cands; ++i) place += s_cand[i] > key;
-      if (place < k) s_best[place] = key;
+#pragma unroll
+      for (int i = 0; i < kBuckets / kShare; i += 4) {
+        const float4 other = *reinterpret_cast<const float4*>(s_bucket + i0 + i);
+        place += other.x > u || (other.x == u && i0 + i < j);
+        place += other.y > u || (other.y == u && i0 + i + 1 < j);
+        place += other.z > u || (other.z == u && i0 + i + 2 < j);
+        place += other.w > u || (other.w == u && i0 + i + 3 < j);
+      }
+#pragma unroll
+      for (int o = 1; o < kShare; o <<= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
+      if (place == k - 1) s_bound = u;
+    }
+    __syncthreads();
+    const float bound = s_bound;
+    if (bound > -INFINITY) {
+      for (int c = tid; c < nch; c += kThreads) {
+        if (s_max[c] >= bound) {
+          const int to = atomicAdd(&s_n[0], 1);
+          if (to < kMostChunks) s_list[to] = c0 + c;
+        }
+      }
+    } else if (tid == 0) {
+      s_n[0] = kMostChunks + 1;
+    }
+    __syncthreads();
+    const int passed = s_n[0];
+    if (passed <= kMostChunks) {
+      read(passed);
+      gather(bound, [](int) { return true; });
+    }
+    __syncthreads();
+    int cands = s_n[1];
+    if (passed > kMostChunks || cands > kFew) {
+      // Too many pass (values that are alike, few chunks): bounds by bisection,
+      // of the chunks first, then of their vectors, on keys that are all different
+      __syncthreads();
+      if (tid < 2) s_n[tid] = 0;
+      float most = s_top[0];
+#pragma unroll
+      for (int i = 1; i < kWarps; ++i) most = largest(most, s_top[i]);
+      const uint64_t above = (uint64_t)order_of(most) + 1;
+      auto chunk_key = [&](int c) {
+        return ((uint64_t)order_of(s_max[c]) << kChunkBits) | (uint32_t)((1 << kChunkBits) - 1 - c);
+      };
+      const uint64_t from = pick(0, above << kChunkBits, nch, min(k, nch), min(kMostChunks, max(2 * k, 8)),
+                                 1ull << (20 + kChunkBits), [&](uint64_t key) {
+                                   int n = 0;
+                                   for (int c = tid; c < nch; c += kThreads) n += chunk_key(c) >= key;
+                                   return n;
+                                 });
+      // (pick ends with a barrier)
+      for (int c = tid; c < nch; c += kThreads)
+        if (chunk_key(c) >= from) s_list[atomicAdd(&s_n[0], 1)] = c0 + c;
+      __syncthreads();
+      read(s_n[0]);
+      uint64_t key[kMine];
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        const uint32_t o = at[j] < 0 ? 0u : order_of(y[j].top_edge(row, at[j]));
+        key[j] = o ? ((uint64_t)o << kVecBits) | (uint32_t)((1 << kVecBits) - 1 - at[j]) : 0ull;
+      }
+      auto count = [&](uint64_t of) {
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) n += key[j] >= of;
+        return n;
+      };
+      const int some = __reduce_add_sync(0xffffffffu, count(1));
+      if (lane == 0) atomicAdd(&s_n[1], some);
+      __syncthreads();
+      const int n = s_n[1];
+      __syncthreads();
+      if (tid == 0) s_n[1] = 0;
+      const uint64_t low = pick(1, above << kVecBits, n, min(k, n), min(kMostVecs, max(2 * k, 16)),
+                                1ull << (20 + kVecBits), count);
+      // (here -inf may be among the best: places outside the row are told apart)
+      const uint32_t least = max(1u, (uint32_t)(low >> kVecBits));
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        if (key[j] < low) continue;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const int i = at[j] * N - row.shift + e;
+          if (i >= 0 && i < a.V && order_of(y[j].at(e)) >= least) s_cand[atomicAdd(&s_n[1], 1)] = (uint64_t)i;
+        }
+      }
+      __syncthreads();
+      cands = s_n[1];
+    }
+    // the values at these places, and their order
+    for (int c = tid; c < cands; c += kThreads) {
+      const int place = (int)s_cand[c];
+      s_cand[c] = value_key(to_f32(row.base[row.shift + place]), place);
+    }
+    __syncthreads();
+    for (int c = tid; c < cands; c += kThreads) {
+      const uint64_t one = s_cand[c];
+      int place = 0;
+#pragma unroll 4
+      for (int i = 0; i < cands; ++i) place += s_cand[i] > one;
+      if (place < k) s_best[place] = one;
     }
     __syncthreads();
   }
 
   // to rank 0
-  if (cluster_size > 1) cluster.barrier_wait();
-  if (lane == 0)
-    *(cluster_size > 1 ? cluster.map_shared_rank(&s_part[rank * kWarps + warp], 0)
-                       : &s_part[warp]) = p;
-  if (cluster_size > 1 && tid < k) *cluster.map_shared_rank(&s_all[rank][tid], 0) = s_best[tid];
-  if (cluster_size > 1) cluster.sync(); else __syncthreads();
-  if (rank != 0) return;
+  if (cluster_size > 1) {
+    cluster.barrier_wait();
+    if (lane == 0) *cluster.map_shared_rank(&s_part[rank * kWarps + warp], 0) = p;
+    if (tid < kTop) *cluster.map_shared_rank(&s_all[rank][tid], 0) = s_best[tid];
+    cluster.sync();
+    if (rank != 0) return;
+  } else {
+    if (lane == 0) s_part[warp] = p;
+    __syncthreads();
+  }
   // every warp merges the sums for itself
   const int parts = cluster_size * kWarps;  // at most 64
-  const Part none = {kLowest, 0.f, 0.f, 0};
+  const Part none = {kLowest, kLowest, 0.f, 0.f, 0};
   const Part u = lane < parts ? s_part[lane] : none, v = lane + 32 < parts ? s_part[lane + 32] : none;
-  float m = fmaxf(u.m, v.m);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float m = warp_max(largest(u.m, v.m)), ref = m * kLog2e;
   float l = 0.f, s = 0.f;
   int before = u.before + v.before;
   auto join = [&](const Part& q) {
-    const float d = max_or_nan(q.m - m, kFar), f = exp2f(d * kLog2e);
+    const float d = max_or_nan(huge(m) ? (q.m - m) * kLog2e : q.r - ref, kFar), f = ex2_approx(d);
     l += f * q.l;
     s += f * fmaf(q.l, d, q.s);
   };
@@ -367,45 +606,56 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
     s += __shfl_xor_sync(0xffffffffu, s, o);
     before += __shfl_xor_sync(0xffffffffu, before, o);
   }
-  const float norm = logf(l);
-  auto logprob = [&](float value) { return l == 0.f ? -INFINITY : (value - m) - norm; };
+  const float norm = log2f(l);
+  auto logprob = [&](float value) {
+    if (l == 0.f) return -INFINITY;
+    return huge(m) || huge(value) ? (value - m) - kLn2 * norm : kLn2 * (fmaf(value, kLog2e, -ref) - norm);
+  };
   if (tid == 0) {
     if (a.logprobs) a.logprobs[t] = is_token ? logprob(mine) : -INFINITY;
-    if (a.ranks) a.ranks[t] = mine_key ? before : -1;
-    if (a.entropy) a.entropy[t] = l == 0.f ? 0.f : norm - s / l;
+    if (a.ranks) a.ranks[t] = mine == mine ? before : -1;
+    if (a.entropy) a.entropy[t] = l == 0.f ? 0.f : kLn2 * (norm - s / l);
   }
   if (k == 0) return;
   auto put = [&](int place, uint64_t key) {
-    a.top_tokens[t * k + place] = key ? (int)((1 << kVocabBits) - 1 - (uint32_t)(key & ((1 << kVocabBits) - 1))) : -1;
+    a.top_tokens[t * k + place] = key ? (1 << kVocabBits) - 1 - (int)(key & ((1 << kVocabBits) - 1)) : -1;
     a.top_logprobs[t * k + place] = key ? logprob(value_of((uint32_t)(key >> kVocabBits))) : -INFINITY;
   };
   if (cluster_size == 1) {
     if (tid < k) put(tid, s_best[tid]);
     return;
   }
-  // one candidate a thread: its place among all
+  // one candidate a thread: its place among all is the sum of its places in the
+  // CTAs' lists, found by bisection in all at once
   const int of = tid / kTop, pos = tid % kTop;
-  uint64_t key = of < cluster_size && pos < k ? s_all[of][pos] : 0;
-  int place = 0, some = 0;
-  for (int r = 0; r < cluster_size; ++r)
-    for (int i = 0; i < k; ++i) {
-      const uint64_t other = s_all[r][i];
-      place += other > key;
-      some += other != 0;
-    }
-  if (key && place < k) put(place, key);
+  const uint64_t key = of < cluster_size && pos < k ? s_all[of][pos] : 0;
+  int place[kMaxCluster];
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) place[r] = 0;
+#pragma unroll
+  for (int step = kTop / 2; step > 0; step /= 2)
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      if (r < cluster_size && s_all[r][place[r] + step - 1] > key) place[r] += step;
+  int sum_of = 0;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r)
+    if (r < cluster_size) sum_of += place[r] + (s_all[r][place[r]] > key);
+  const int some = __syncthreads_count(key != 0);
+  if (key && sum_of < k) put(sum_of, key);
   if (tid >= some && tid < k) put(tid, 0);  // fewer than k values
 }
 
 template <typename T>
 cudaError_t launch_type(const LogprobsArgs& a, cudaStream_t stream) {
-  // CTAs of a row: as many as keep about four an SM, each with 16 chunks or more
-  const int64_t chunks = ceil_div((int64_t)a.V * sizeof(T), 512);
+  // CTAs of a row: as many as stay at three an SM, each with 16 chunks or more
+  const int64_t chunks = ceil_div((int64_t)a.V * sizeof(T), 512) + 1;
   int c = kMaxCluster;
-  while (c > 1 && (a.T * c > (int64_t)num_sms() * 4 || chunks < 16 * c)) c /= 2;
+  while (c > 1 && (a.T * c > (int64_t)num_sms() * 3 || chunks < 16 * c)) c /= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.T * c));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)ceil_div(chunks, c) * sizeof(float);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
