@@ -18,6 +18,13 @@
 // (value, index) that are all different, so that the work is bounded whatever
 // the row holds.
 //
+// Bounds and what was measured (GPU time, replayed from a graph): 2048 rows of
+// 131072 bf16, 5 best: 117 us, 4.6 TB/s; without tokens and best 89 (6.0 TB/s).
+// Ranks cost a packed comparison and a sum for every two values (13 us), the
+// selection about 4 us a row and CTA, in which its warps load little.  16 rows of
+// 200003 fp32, 20 best: 11.5 us, latency (the row 4.5, the selection 3, exchange
+// and merge of the cluster 3).
+//
 // A cluster of 1 to 8 CTAs takes a row (as many as fill the GPU when there are
 // few rows): each finds its own k best, and the first merges them through
 // distributed shared memory.  Rows may start anywhere: whole 16-byte vectors
@@ -37,7 +44,8 @@ namespace cg = cooperative_groups;
 namespace msa {
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kMaxWarps = 8;     // of a CTA
+constexpr int kWarpsOfSm = 24;   // (80 registers a thread)
 constexpr int kMaxCluster = 8;
 constexpr int kTop = MSA_LOGPROBS_MAX_TOP;
 constexpr int kBatch = 4;        // chunks of a warp in flight
@@ -46,14 +54,12 @@ constexpr int kChunkBits = 13;   // chunks of a row: at most 4097
 constexpr int kVecBits = 18;     // vectors of a row: at most 2^17 + 1
 constexpr int kMaxChunks = (MSA_VERIFY_MAX_VOCAB * 4) / 512 + 1;
 constexpr int kMostChunks = 48;  // chunks that are read again
-constexpr int kMine = kMostChunks / kWarps;  // vectors of a thread among them
+constexpr int kRound = 6;        // of a thread's vectors among them, in flight
 constexpr int kMostVecs = 64;    // vectors whose values are looked at
 constexpr int kFew = kMostVecs * 8;
 constexpr int kBuckets = 64;     // a CTA's whole chunks, dealt out in turn
 static_assert(MSA_VERIFY_MAX_VOCAB == 1 << kVocabBits && kMaxChunks < 1 << kChunkBits, "keys");
-static_assert(kMostChunks % kWarps == 0 && kTop == 32 && kTop <= kMostChunks && kTop <= kMostVecs &&
-                  kMaxCluster * kTop == kThreads && kThreads % kBuckets == 0,
-              "selection");
+static_assert(kTop == 32 && kTop <= kMostChunks && kTop <= kMostVecs, "selection");
 constexpr float kLowest = -FLT_MAX;  // m before any value (finite: x - m is no NaN)
 constexpr float kFar = -200.f;       // 2^t is 0 in fp32 at and below this, and 0 times it 0
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309f;
@@ -243,7 +249,7 @@ struct Sums {
 // at or above `lo` (n_lo of them), fewer than k at or above `hi`; all keys are
 // different, so that there is such a key.  Steps down from hi first, a step
 // four times the last, since the k largest often lie close together.
-template <typename F>
+template <int kWarps, typename F>
 __device__ __forceinline__ uint64_t pick(uint64_t lo, uint64_t hi, int n_lo, int k, int most,
                                          uint64_t step, F count) {
   __shared__ int s_sum[2][kWarps];
@@ -268,10 +274,13 @@ struct Part {  // of a warp
   int before;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobsArgs a, int cluster_size) {
+template <typename T, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, kWarpsOfSm / kWarps)
+logprobs_kernel(const LogprobsArgs a, int cluster_size) {
   using V = Vec<T>;
-  constexpr int N = V::N;
+  constexpr int N = V::N, kThreads = kWarps * 32;
+  constexpr int kMine = kMostChunks / kWarps;  // vectors of a thread among the chunks read again
+  static_assert(kMine % kRound == 0 && kThreads % kBuckets == 0, "selection");
   extern __shared__ float s_max[];  // the largest value of each chunk
   __shared__ float s_top[kWarps], s_bound;
   __shared__ __align__(16) float s_bucket[kBuckets];
@@ -433,35 +442,13 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobsArg
 
   const int k = a.top;
   if (k > 0 && nch > 0) {
-    // this thread's vectors of the listed chunks, -1: none
-    V y[kMine];
-    int at[kMine];
-    auto read = [&](int listed) {
+    // this thread's vectors of the listed chunks from the j0-th on, -1: none
+    auto read = [&](V (&y)[kRound], int (&at)[kRound], int j0, int listed) {
 #pragma unroll
-      for (int j = 0; j < kMine; ++j) {
-        at[j] = j * kWarps + warp < listed ? s_list[j * kWarps + warp] * 32 + lane : -1;
+      for (int j = 0; j < kRound; ++j) {
+        const int of = (j0 + j) * kWarps + warp;
+        at[j] = of < listed ? s_list[of] * 32 + lane : -1;
         if (at[j] >= 0) y[j].load_edge(row, at[j]);
-      }
-    };
-    // The places of the values at or above a bound above -inf, of the vectors of
-    // which `take` says so; few lanes have any.
-    auto gather = [&](float bound, auto take) {
-      uint32_t hits[kMine];
-      int n = 0;
-#pragma unroll
-      for (int j = 0; j < kMine; ++j) {
-        hits[j] = 0;
-#pragma unroll
-        for (int e = 0; e < N; ++e) hits[j] |= y[j].at(e) >= bound ? 1u << e : 0u;
-        if (at[j] < 0 || !take(j)) hits[j] = 0;
-        n += __popc(hits[j]);
-      }
-      if (n > 0) {
-        int to = atomicAdd(&s_n[1], n);
-#pragma unroll
-        for (int j = 0; j < kMine; ++j)
-          for (uint32_t h = hits[j]; h; h &= h - 1, ++to)
-            if (to < kFew) s_cand[to] = (uint64_t)(at[j] * N - row.shift + __ffs(h) - 1);
       }
     };
     // A bound for the k-th best: the k-th largest of the buckets' largest values,
@@ -498,8 +485,30 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobsArg
     __syncthreads();
     const int passed = s_n[0];
     if (passed <= kMostChunks) {
-      read(passed);
-      gather(bound, [](int) { return true; });
+      // the places of the values that pass the bound (above -inf); few lanes have any
+#pragma unroll 1
+      for (int j0 = 0; j0 * kWarps < passed; j0 += kRound) {
+        V y[kRound];
+        int at[kRound];
+        read(y, at, j0, passed);
+        uint32_t hits[kRound];
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < kRound; ++j) {
+          hits[j] = 0;
+#pragma unroll
+          for (int e = 0; e < N; ++e) hits[j] |= y[j].at(e) >= bound ? 1u << e : 0u;
+          if (at[j] < 0) hits[j] = 0;
+          n += __popc(hits[j]);
+        }
+        if (n > 0) {
+          int to = atomicAdd(&s_n[1], n);
+#pragma unroll
+          for (int j = 0; j < kRound; ++j)
+            for (uint32_t h = hits[j]; h; h &= h - 1, ++to)
+              if (to < kFew) s_cand[to] = (uint64_t)(at[j] * N - row.shift + __ffs(h) - 1);
+        }
+      }
     }
     __syncthreads();
     int cands = s_n[1];
@@ -515,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobsArg
       auto chunk_key = [&](int c) {
         return ((uint64_t)order_of(s_max[c]) << kChunkBits) | (uint32_t)((1 << kChunkBits) - 1 - c);
       };
-      const uint64_t from = pick(0, above << kChunkBits, nch, min(k, nch), min(kMostChunks, max(2 * k, 8)),
+      const uint64_t from = pick<kWarps>(0, above << kChunkBits, nch, min(k, nch), min(kMostChunks, max(2 * k, 8)),
                                  1ull << (20 + kChunkBits), [&](uint64_t key) {
                                    int n = 0;
                                    for (int c = tid; c < nch; c += kThreads) n += chunk_key(c) >= key;
@@ -525,12 +534,18 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobsArg
       for (int c = tid; c < nch; c += kThreads)
         if (chunk_key(c) >= from) s_list[atomicAdd(&s_n[0], 1)] = c0 + c;
       __syncthreads();
-      read(s_n[0]);
+      const int listed = s_n[0];
       uint64_t key[kMine];
 #pragma unroll
-      for (int j = 0; j < kMine; ++j) {
-        const uint32_t o = at[j] < 0 ? 0u : order_of(y[j].top_edge(row, at[j]));
-        key[j] = o ? ((uint64_t)o << kVecBits) | (uint32_t)((1 << kVecBits) - 1 - at[j]) : 0ull;
+      for (int j0 = 0; j0 < kMine; j0 += kRound) {
+        V y[kRound];
+        int at[kRound];
+        read(y, at, j0, listed);
+#pragma unroll
+        for (int j = 0; j < kRound; ++j) {
+          const uint32_t o = at[j] < 0 ? 0u : order_of(y[j].top_edge(row, at[j]));
+          key[j0 + j] = o ? ((uint64_t)o << kVecBits) | (uint32_t)((1 << kVecBits) - 1 - at[j]) : 0ull;
+        }
       }
       auto count = [&](uint64_t of) {
         int n = 0;
@@ -544,18 +559,16 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobsArg
       const int n = s_n[1];
       __syncthreads();
       if (tid == 0) s_n[1] = 0;
-      const uint64_t low = pick(1, above << kVecBits, n, min(k, n), min(kMostVecs, max(2 * k, 16)),
+      const uint64_t low = pick<kWarps>(1, above << kVecBits, n, min(k, n), min(kMostVecs, max(2 * k, 16)),
                                 1ull << (20 + kVecBits), count);
       // (here -inf may be among the best: places outside the row are told apart)
       const uint32_t least = max(1u, (uint32_t)(low >> kVecBits));
 #pragma unroll
       for (int j = 0; j < kMine; ++j) {
         if (key[j] < low) continue;
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const int i = at[j] * N - row.shift + e;
-          if (i >= 0 && i < a.V && order_of(y[j].at(e)) >= least) s_cand[atomicAdd(&s_n[1], 1)] = (uint64_t)i;
-        }
+        const int first = ((1 << kVecBits) - 1 - (int)(key[j] & ((1 << kVecBits) - 1))) * N - row.shift;
+        for (int i = max(first, 0); i < min(first + N, a.V); ++i)
+          if (order_of(to_f32(row.base[row.shift + i])) >= least) s_cand[atomicAdd(&s_n[1], 1)] = (uint64_t)i;
       }
       __syncthreads();
       cands = s_n[1];
@@ -625,47 +638,65 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobsArg
     if (tid < k) put(tid, s_best[tid]);
     return;
   }
-  // one candidate a thread: its place among all is the sum of its places in the
-  // CTAs' lists, found by bisection in all at once
-  const int of = tid / kTop, pos = tid % kTop;
-  const uint64_t key = of < cluster_size && pos < k ? s_all[of][pos] : 0;
-  int place[kMaxCluster];
+  // A candidate's place among all is the sum of its places in the CTAs' lists:
+  // a thread looks for one candidate in one list, by bisection.
+  const int most = cluster_size * k;
+  int* s_place = reinterpret_cast<int*>(s_cand);  // (no longer needed)
+  for (int c = tid; c < most; c += kThreads) s_place[c] = 0;
+  __syncthreads();
+  for (int w = tid; w < most * cluster_size; w += kThreads) {
+    const int in = w / most, c = w - in * most, of = c / k;
+    const uint64_t key = s_all[of][c - of * k];
+    int place = 0;
 #pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r) place[r] = 0;
-#pragma unroll
-  for (int step = kTop / 2; step > 0; step /= 2)
-#pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r)
-      if (r < cluster_size && s_all[r][place[r] + step - 1] > key) place[r] += step;
-  int sum_of = 0;
-#pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r)
-    if (r < cluster_size) sum_of += place[r] + (s_all[r][place[r]] > key);
-  const int some = __syncthreads_count(key != 0);
-  if (key && sum_of < k) put(sum_of, key);
+    for (int step = kTop / 2; step > 0; step /= 2)
+      if (s_all[in][place + step - 1] > key) place += step;
+    place += s_all[in][place] > key;
+    if (place) atomicAdd(&s_place[c], place);
+  }
+  __syncthreads();
+  int some = 0;
+  for (int c0 = 0; c0 < most; c0 += kThreads) {
+    const int c = c0 + tid, of = c / k;
+    const uint64_t key = c < most ? s_all[of][c - of * k] : 0;
+    if (key && s_place[c] < k) put(s_place[c], key);
+    some += __syncthreads_count(key != 0);
+  }
   if (tid >= some && tid < k) put(tid, 0);  // fewer than k values
 }
 
-template <typename T>
-cudaError_t launch_type(const LogprobsArgs& a, cudaStream_t stream) {
-  // CTAs of a row: as many as stay at three an SM, each with 16 chunks or more
-  const int64_t chunks = ceil_div((int64_t)a.V * sizeof(T), 512) + 1;
-  int c = kMaxCluster;
-  while (c > 1 && (a.T * c > (int64_t)num_sms() * 3 || chunks < 16 * c)) c /= 2;
+template <typename T, int kWarps>
+cudaError_t launch_as(const LogprobsArgs& a, int cluster, int64_t chunks, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.T * c));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)ceil_div(chunks, c) * sizeof(float);
+  cfg.gridDim = dim3((unsigned)(a.T * cluster));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = (size_t)ceil_div(chunks, cluster) * sizeof(float);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)c;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T>, a, c);
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kWarps>, a, cluster);
+}
+
+template <typename T>
+cudaError_t launch_type(const LogprobsArgs& a, cudaStream_t stream) {
+  // CTAs of a row: as many as stay at three an SM, each with 16 chunks or more
+  // (64 rows of 131072 bf16 by clusters of 4, 256 CTAs: 13 us; by 8, in two
+  // waves: 20)
+  const int64_t chunks = ceil_div((int64_t)a.V * sizeof(T), 512) + 1;
+  int c = kMaxCluster;
+  while (c > 1 && (a.T * c > (int64_t)num_sms() * 3 || chunks < 16 * c)) c /= 2;
+  // Many short rows: twice as many CTAs of half the warps, whose selections
+  // overlap more rows' loads (8192 rows of 32000 bf16, 5 best: 167 us, with 8
+  // warps 208; 2048 of 131072: 118 and 117; 456 of 131072: 35 and 29)
+  if (a.T >= (int64_t)num_sms() * (kWarpsOfSm / 4) && chunks <= 256)
+    return launch_as<T, 4>(a, c, chunks, stream);
+  return launch_as<T, kMaxWarps>(a, c, chunks, stream);
 }
 
 }  // namespace
