@@ -16,10 +16,12 @@
 //
 // One pass over the data, bound by HBM for long chunks and by latency for
 // decode steps.  A slot of 8 lanes (16 for fp32: 32 bytes a lane) takes a token
-// and a run of its heads, Q's then K's then V's: a lane's places in the row stay
-// the same, so its cosines and sines are found once for all of them and stay in
-// registers.
+// and a run of its heads, Q's then K's then V's, with the same heads in all of a
+// warp's slots: a lane's places in the row stay the same, so its cosines and
+// sines (times the norm's weights) are found once for all heads of Q and stay in
+// registers, and no branch divides a warp.
 #include <algorithm>
+#include <cfloat>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -32,75 +34,85 @@
 namespace msa {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256, kRopeWarps = kRopeThreads / 32;
 constexpr int kStaged = 512;  // requests whose lengths a CTA keeps in shared memory
-constexpr int kInFlight = 2;  // rows of a slot loaded together
+constexpr int kInFlight = 4;  // rows of a slot loaded together
 
-// Which values make a pair: neighbours; values half of the rotated part apart,
-// in whole lanes; the same where the half is no whole number of lanes.
-enum { kNeighbours = 0, kHalvesByLane = 1, kHalves = 2 };
+// Where a lane's two pieces of 16 bytes lie and how its pairs are formed.
+//   kNeighbours  side by side; pairs of neighbouring values
+//   kSplit       half of the rotated part apart (or, behind it, half of the
+//                rest): a lane has both values of its pairs
+//   kHalves      side by side; a pair's other value comes through shared memory
+//                (a half that is no whole number of pieces)
+enum { kNeighbours, kSplit, kHalves };
 
 struct RopeParams {
-  Recip q, k, v;
+  float q_inverse, k_inverse;
+  Recip v;
   float k6, v6;   // 6 g, NVFP4
   int chunks;     // of a token's rows
   int run;        // rows of a chunk
   bool q_wide, kv_wide;  // rows lie on 32 bytes
 };
 
-// 16-byte chunks of 8 kept apart by rows of 8, so that lanes that read chunks
-// a power of two apart meet in no bank.
-__device__ __forceinline__ int spread(int chunk) { return chunk ^ ((chunk >> 3) & 7); }
-
 template <typename T, bool kFp4, int kPairing>
 __global__ void __launch_bounds__(kRopeThreads, 2)
 rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopeParams p) {
-  constexpr int kV = kVals<T>;               // values of a lane
-  constexpr int N = kV / 2;
-  constexpr int kLanes = kD / kV;            // of a slot
-  constexpr int kSlots = kRopeThreads / kLanes;
-  constexpr int kAngles = kPairing == kNeighbours ? N : kV;
+  constexpr int kV = kVals<T>, kPiece = kV / 2;  // values of a lane, and of a piece
+  constexpr int N = kV / 2, H = N / 2;           // pairs of values: of a lane, of a piece
+  constexpr int kLanes = kD / kV;                // of a slot
+  constexpr int kTokens = 32 / kLanes;           // of a warp
+  constexpr int kCtaTokens = kRopeWarps * kTokens;
+  constexpr bool kIsSplit = kPairing == kSplit;
+  static_assert(kCtaTokens <= 32, "looked up by one warp");
   __shared__ uint64_t s_turns[MSA_ROPE_MAX_PAIRS];
   __shared__ uint8_t s_axis[MSA_ROPE_MAX_PAIRS];
   __shared__ __align__(16) float s_norm[2][kD];
   __shared__ int64_t s_page[32];
   __shared__ int s_off[32], s_pos[32];
   __shared__ int s_cu[kStaged + 1], s_cuk[kStaged + 1];
-  __shared__ float s_row[kPairing == kHalves ? kSlots : 1][kD + 4];
+  __shared__ float s_row[kPairing == kHalves ? kCtaTokens : 1][kD + 4];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31;
-  const int64_t unit0 = (int64_t)blockIdx.x * kSlots;
-  const int64_t t0 = unit0 / p.chunks;
-  const int slot = tid / kLanes, cc = tid % kLanes;
-  const uint32_t peers = (kLanes == 32 ? 0xffffffffu : (1u << kLanes) - 1u) << (lane & ~(kLanes - 1));
-  const int64_t unit = unit0 + slot;
-  const int64_t t = unit / p.chunks;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (the same for all lanes)
+  // a warp takes kTokens tokens and a run of their heads: its rows are all of Q,
+  // all of K or all of V at a time
+  const int64_t unit0 = (int64_t)blockIdx.x * kRopeWarps, unit = unit0 + warp;
+  const int64_t t0 = unit0 / p.chunks * kTokens, group = unit / p.chunks;
+  const int slot = lane / kLanes, cc = lane % kLanes;
+  const int64_t t = group * kTokens + slot;
   const int i = (int)(t - t0);  // the token within the CTA's
-  const int rows = a.Hq + 2 * a.Hkv;
-  const int r_first = (int)(unit - t * p.chunks) * p.run;
-  const int r_end = t < a.T ? min(rows, r_first + p.run) : r_first;
-  // a row's first byte of this lane
-  auto source = [&](int r) {
-    const T* x = static_cast<const T*>(r < a.Hq ? a.q : r < a.Hq + a.Hkv ? a.k : a.v);
-    const int64_t token = r < a.Hq ? a.q_token : r < a.Hq + a.Hkv ? a.k_token : a.v_token;
-    const int64_t head = r < a.Hq ? a.q_head : r < a.Hq + a.Hkv ? a.k_head : a.v_head;
-    const int h = r < a.Hq ? r : r < a.Hq + a.Hkv ? r - a.Hq : r - a.Hq - a.Hkv;
-    return x + t * token + h * head + cc * kV;
-  };
+  const int k0 = a.Hq, v0 = a.Hq + a.Hkv, rows = v0 + a.Hkv;  // first rows of K and V
+  const int r_first = (int)(unit - group * p.chunks) * p.run;
+  const int r_end = group * kTokens < a.T ? min(rows, r_first + p.run) : r_first;
+  const bool in_batch = t < a.T;
+  // the first values of the lane's pieces
+  const int turned = a.pairs / kPiece;  // (kSplit) lanes with pairs
+  const int d0 = !kIsSplit ? cc * kV : cc < turned ? cc * kPiece : a.pairs + cc * kPiece;
+  const int d1 = !kIsSplit ? d0 + kPiece : cc < turned ? d0 + a.pairs : kD / 2 + cc * kPiece;
+  const T* const q_row = static_cast<const T*>(a.q) + t * a.q_token + d0;
+  const T* const k_row = static_cast<const T*>(a.k) + t * a.k_token + d0;
+  const T* const v_row = static_cast<const T*>(a.v) + t * a.v_token + d0;
   uint32_t w[kInFlight][8];
-  auto load = [&](int r0) {
-#pragma unroll
-    for (int k = 0; k < kInFlight; ++k) {
-      if (r0 + k < r_end) {
-        load32(source(r0 + k), r0 + k < a.Hq ? p.q_wide : p.kv_wide, w[k]);
+  auto load = [&](uint32_t (&to)[8], int r) {
+    if (r < r_end && in_batch) {
+      const T* x = r < k0 ? q_row + r * a.q_head : r < v0 ? k_row + (r - k0) * a.k_head : v_row + (r - v0) * a.v_head;
+      if constexpr (kIsSplit) {
+        const uint4 lo = __ldg(reinterpret_cast<const uint4*>(x));
+        const uint4 hi = __ldg(reinterpret_cast<const uint4*>(x + (d1 - d0)));
+        to[0] = lo.x, to[1] = lo.y, to[2] = lo.z, to[3] = lo.w;
+        to[4] = hi.x, to[5] = hi.y, to[6] = hi.z, to[7] = hi.w;
       } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[k][e] = 0u;
+        load32(x, r < k0 ? p.q_wide : p.kv_wide, to);
       }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) to[e] = 0u;
     }
   };
-  load(r_first);  // does not wait for the look-up
+#pragma unroll
+  for (int k = 0; k < kInFlight; ++k) load(w[k], r_first + k);  // does not wait for the look-up
   for (int j = tid; j < a.pairs; j += kRopeThreads) {
     s_turns[j] = a.turns[j];
     s_axis[j] = a.axis[j];
@@ -109,7 +121,7 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopePara
     const float* n = tid < kD / 4 ? a.q_norm : a.k_norm;
     const int c = tid % (kD / 4);
     if (n)
-      reinterpret_cast<float4*>(s_norm[tid / (kD / 4)])[spread(c)] =
+      reinterpret_cast<float4*>(s_norm[tid / (kD / 4)])[c] =
           make_float4(__ldg(n + 4 * c), __ldg(n + 4 * c + 1), __ldg(n + 4 * c + 2), __ldg(n + 4 * c + 3));
   }
   const bool staged = a.B <= kStaged;
@@ -120,10 +132,10 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopePara
     }
     __syncthreads();
   }
-  // the CTA's tokens (at most one a slot): their places in the pool
-  if (tid < 32) {
+  // the CTA's tokens: their places in the pool
+  if (warp == 0) {
     const int64_t tt = t0 + lane;
-    const bool used = lane < kSlots && tt < a.T;
+    const bool used = lane < kCtaTokens && tt < a.T;
     int b;
     if (staged) {
       int lo = 0, hi = a.B;  // the number of requests that end at or before tt
@@ -151,140 +163,204 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopePara
     s_pos[lane] = (int)pos;
   }
   __syncthreads();
-  if (r_first >= r_end) return;
+  if (r_first >= r_end) return;  // (whole warps)
   const int off = s_off[i];
-  if (off < 0) return;
+  const bool live = off >= 0;  // what is written of this slot's token
 
-  // cosines and sines of this lane's pairs (or of its values' pairs)
+  // Cosines and sines of the lane's pairs (kHalves: of its values' pairs, the
+  // sine with its sign), 1 and 0 where there is none.
+  constexpr int kAngles = kPairing == kHalves ? kV : kPiece;
   float cs[kAngles], sn[kAngles];
-  if (r_first < a.Hq + a.Hkv) {
-    int pos = a.positions && a.axes == 1 ? __ldg(a.positions + t) : s_pos[i];
+  auto pair_of = [&](int e) {  // -1: none
+    if (kPairing == kNeighbours) return cc * N + e < a.pairs ? cc * N + e : -1;
+    if (kIsSplit) return cc < turned ? d0 + e : -1;
+    return d0 + e < a.pairs ? d0 + e : d0 + e < 2 * a.pairs ? d0 + e - a.pairs : -1;
+  };
+  if (r_first < v0) {
+    int pos = a.positions && a.axes == 1 && in_batch ? __ldg(a.positions + t) : s_pos[i];
 #pragma unroll
     for (int e = 0; e < kAngles; ++e) {
-      const int at = cc * kAngles + e;
-      const int j = kPairing == kNeighbours || at < a.pairs ? at : at - a.pairs;
+      const int j = pair_of(e);
       cs[e] = 1.f, sn[e] = 0.f;
-      if (j < a.pairs) {
-        if (a.axes > 1 && a.positions) pos = __ldg(a.positions + s_axis[j] * a.T + t);
+      if (j >= 0) {
+        if (a.axes > 1 && a.positions && in_batch) pos = __ldg(a.positions + s_axis[j] * a.T + t);
         const uint64_t turn = s_turns[j] * (uint64_t)(int64_t)pos;
         const int32_t signed_turn = (int32_t)(uint32_t)((turn + 0x80000000u) >> 32);
         sincospif((float)signed_turn * 0x1p-31f, &sn[e], &cs[e]);
-        if (kPairing != kNeighbours && at < a.pairs) sn[e] = -sn[e];
+        if (kPairing == kHalves && d0 + e < a.pairs) sn[e] = -sn[e];
       }
     }
   }
+  // the norm's weights, of Q and then of K
+  float2 g[N];
+  auto weights = [&](const float* of) {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      const float4 y = *reinterpret_cast<const float4*>(of + (e < H ? d0 + 2 * e : d1 + 2 * (e - H)));
+      g[e] = make_float2(y.x, y.y), g[e + 1] = make_float2(y.z, y.w);
+    }
+  };
+  if (a.q_norm && r_first < k0) weights(s_norm[0]);
+  if (a.k_norm && r_first >= k0) weights(s_norm[1]);
 
+  // x normalised and turned
+  auto turn = [&](float2 (&x)[N], bool normed) {
+    if (normed) {
+      float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < N; ++e) ss = fma2(x[e], x[e], ss);
+      float sum = ss.x + ss.y;
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const float f = 1.f / sqrtf(sum * (1.f / kD) + a.eps);
+#pragma unroll
+      for (int e = 0; e < N; ++e) x[e] = mul2(mul2(x[e], make_float2(f, f)), g[e]);
+    }
+    if constexpr (kPairing == kNeighbours) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float2 y = make_float2(fmaf(x[e].x, cs[e], -x[e].y * sn[e]), fmaf(x[e].x, sn[e], x[e].y * cs[e]));
+        if (pair_of(e) >= 0) x[e] = y;
+      }
+    } else if constexpr (kIsSplit) {
+      if (cc < turned) {
+#pragma unroll
+        for (int e = 0; e < H; ++e) {
+          const float2 c = make_float2(cs[2 * e], cs[2 * e + 1]), s = make_float2(sn[2 * e], sn[2 * e + 1]);
+          const float2 lo = x[e], hi = x[e + H];
+          x[e] = fma2(lo, c, mul2(hi, make_float2(-s.x, -s.y)));
+          x[e + H] = fma2(lo, s, mul2(hi, c));
+        }
+      }
+    } else {
+      float* row = s_row[warp * kTokens + slot];
+#pragma unroll
+      for (int e = 0; e < N; ++e) *reinterpret_cast<float2*>(row + d0 + 2 * e) = x[e];
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < kV; ++e) {
+        const int d = d0 + e;
+        if (d < 2 * a.pairs) {
+          float& mine = e & 1 ? x[e / 2].y : x[e / 2].x;
+          mine = fmaf(mine, cs[e], row[d < a.pairs ? d + a.pairs : d - a.pairs] * sn[e]);
+        }
+      }
+      __syncwarp();
+    }
+  };
+  // one byte a value, at the row's first byte
+  auto store8 = [&](uint8_t* to, const uint32_t (&code)[N / 2]) {
+    if constexpr (!kIsSplit) {
+      store_words<N / 2>(to + d0, code);
+    } else {
+      uint32_t lo[N / 4], hi[N / 4];
+#pragma unroll
+      for (int e = 0; e < N / 4; ++e) lo[e] = code[e], hi[e] = code[N / 4 + e];
+      store_words<N / 4>(to + d0, lo);
+      store_words<N / 4>(to + d1, hi);
+    }
+  };
+  // NVFP4 codes and scales of a row, from its slot's first byte
+  auto store4 = [&](uint8_t* to, const float2 (&x)[N], float scale, float scale6) {
+    if constexpr (!kIsSplit) {
+      uint32_t code[N / 4], s;
+      encode_nvfp4<N>(x, scale, scale6, code, &s);
+      if (live) {
+        store_words<N / 4>(to + off * (kD / 2) + d0 / 2, code);
+        if (d0 % 16 == 0) to[kFp4Codes + off * 8 + d0 / 16] = (uint8_t)s;
+      }
+    } else {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float2 y[H];
+#pragma unroll
+        for (int e = 0; e < H; ++e) y[e] = x[half * H + e];
+        const int d = half ? d1 : d0;
+        uint32_t code[1], s;
+        encode_nvfp4<H>(y, scale, scale6, code, &s);
+        if (live) {
+          if constexpr (H == 4) *reinterpret_cast<uint32_t*>(to + off * (kD / 2) + d / 2) = code[0];
+          else *reinterpret_cast<uint16_t*>(to + off * (kD / 2) + d / 2) = (uint16_t)code[0];
+          if (d % 16 == 0) to[kFp4Codes + off * 8 + d / 16] = (uint8_t)s;
+        }
+      }
+    }
+  };
+  uint8_t* const k_page = a.pool + s_page[i] + (kFp4 ? 0 : off * (2 * kD));
+  const int64_t head_bytes = kFp4 ? kFp4PageHead : kPage * 2 * kD;
   auto handle = [&](int r, const uint32_t (&raw)[8]) {
     float2 x[N];
     unpack<T>(raw, x);
-    const bool is_q = r < a.Hq, turned = r < a.Hq + a.Hkv;
-    if (turned) {
-      if (is_q ? a.q_norm != nullptr : a.k_norm != nullptr) {
-        float2 ss = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int e = 0; e < N; ++e) ss = fma2(x[e], x[e], ss);
-        float sum = ss.x + ss.y;
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(peers, sum, o);
-        const float f = 1.f / sqrtf(sum * (1.f / kD) + a.eps);
-        const float4* weight = reinterpret_cast<const float4*>(s_norm[is_q ? 0 : 1]);
-#pragma unroll
-        for (int c = 0; c < kV / 4; ++c) {
-          const float4 g = weight[spread(cc * (kV / 4) + c)];
-          x[2 * c] = mul2(mul2(x[2 * c], make_float2(f, f)), make_float2(g.x, g.y));
-          x[2 * c + 1] = mul2(mul2(x[2 * c + 1], make_float2(f, f)), make_float2(g.z, g.w));
-        }
-      }
-      if constexpr (kPairing == kNeighbours) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float2 y = make_float2(fmaf(x[e].x, cs[e], -x[e].y * sn[e]),
-                                       fmaf(x[e].x, sn[e], x[e].y * cs[e]));
-          if (cc * N + e < a.pairs) x[e] = y;
-        }
-      } else if constexpr (kPairing == kHalvesByLane) {
-        const int step = a.pairs / kV;  // lanes of a half
-        const int other = cc < step ? cc + step : cc < 2 * step ? cc - step : cc;
-        const int from = (lane & ~(kLanes - 1)) + other;
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float2 y = make_float2(__shfl_sync(peers, x[e].x, from),
-                                       __shfl_sync(peers, x[e].y, from));
-          if (cc < 2 * step)
-            x[e] = make_float2(fmaf(x[e].x, cs[2 * e], y.x * sn[2 * e]),
-                               fmaf(x[e].y, cs[2 * e + 1], y.y * sn[2 * e + 1]));
-        }
+    if (r >= v0) {
+      uint8_t* to = k_page + (r - v0) * head_bytes;
+      if constexpr (kFp4) {
+        store4(to + kFp4Slot, x, a.v_scale, p.v6);
       } else {
-        float* row = s_row[slot];
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-          *reinterpret_cast<float2*>(row + cc * kV + 2 * e) = x[e];
-        __syncwarp(peers);
-#pragma unroll
-        for (int e = 0; e < kV; ++e) {
-          const int d = cc * kV + e;
-          if (d < 2 * a.pairs) {
-            const float y = row[d < a.pairs ? d + a.pairs : d - a.pairs];
-            float& mine = e & 1 ? x[e / 2].y : x[e / 2].x;
-            mine = fmaf(mine, cs[e], y * sn[e]);
-          }
-        }
-        __syncwarp(peers);
+        uint32_t code[N / 2];
+        encode_e4m3<N>(x, p.v, code);
+        if (live) store8(to + kD, code);
       }
+      return;
     }
-    if (is_q) {
-      uint8_t* out = static_cast<uint8_t*>(a.q_out) +
-                     ((t * a.Hq + r) * kD + cc * kV) * (a.q_bf16 ? 2 : 1);
-      if (a.q_bf16) {
+    const bool is_q = r < k0;
+    if (r == k0 && a.k_norm) weights(s_norm[1]);
+    turn(x, (is_q ? a.q_norm : a.k_norm) != nullptr);
+    if ((is_q && a.q_bf16) || (!is_q && kFp4)) {
+      if (!is_q) {
+        store4(k_page + (r - k0) * head_bytes, x, a.k_scale, p.k6);
+      } else {
         uint32_t o[N];
 #pragma unroll
         for (int e = 0; e < N; ++e) {
           const __nv_bfloat162 h = __floats2bfloat162_rn(x[e].x, x[e].y);
           o[e] = *reinterpret_cast<const uint32_t*>(&h);
         }
+        uint16_t* to = static_cast<uint16_t*>(a.q_out) + (t * a.Hq + r) * kD;
+        if (live) {
 #pragma unroll
-        for (int e = 0; e < N; e += 4)
-          reinterpret_cast<uint4*>(out)[e / 4] = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-      } else {
-        uint32_t code[N / 2];
-        encode_e4m3<N>(x, p.q, code);
-        store_words<N / 2>(out, code);
+          for (int e = 0; e < N; e += H) {
+            uint32_t* at = reinterpret_cast<uint32_t*>(to + (e ? d1 : d0));
+            if constexpr (H == 4) *reinterpret_cast<uint4*>(at) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            else *reinterpret_cast<uint2*>(at) = make_uint2(o[e], o[e + 1]);
+          }
+        }
       }
       return;
     }
-    const int half = turned ? 0 : 1;
-    const int h = r - a.Hq - half * a.Hkv;
-    if constexpr (kFp4) {
-      uint8_t* base = a.pool + s_page[i] + (int64_t)h * kFp4PageHead + half * kFp4Slot;
-      uint32_t code[N / 4], s;
-      encode_nvfp4<N>(x, half ? a.v_scale : a.k_scale, half ? p.v6 : p.k6, code, &s, peers);
-      store_words<N / 4>(base + off * (kD / 2) + cc * N, code);
-      if (N == 8 || (cc & 1) == 0) base[kFp4Codes + off * 8 + cc * N / 8] = (uint8_t)s;
-    } else {
-      uint32_t code[N / 2];
-      encode_e4m3<N>(x, half ? p.v : p.k, code);
-      store_words<N / 2>(a.pool + s_page[i] + ((int64_t)h * kPage + off) * (2 * kD) + half * kD + cc * kV,
-                         code);
+    // E4M3 of Q, or of K.  The values have been rounded on their way: the
+    // reciprocal's rounding is one more of them.
+    const float m = is_q ? p.q_inverse : p.k_inverse;
+    uint32_t code[N / 2];
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(mul2(x[2 * e], make_float2(m, m)), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(mul2(x[2 * e + 1], make_float2(m, m)), __NV_SATFINITE, __NV_E4M3);
+      code[e] = lo | (hi << 16);
     }
+    uint8_t* to = is_q ? static_cast<uint8_t*>(a.q_out) + (t * a.Hq + r) * kD : k_page + (r - k0) * head_bytes;
+    if (live) store8(to, code);
   };
   for (int r = r_first; r < r_end; r += kInFlight) {
 #pragma unroll
-    for (int k = 0; k < kInFlight; ++k)
+    for (int k = 0; k < kInFlight; ++k) {
       if (r + k < r_end) handle(r + k, w[k]);
-    load(r + kInFlight);
+      load(w[k], r + k + kInFlight);
+    }
   }
 }
 
 template <typename T, bool kFp4>
 cudaError_t launch_type(const RopeArgs& a, cudaStream_t stream) {
-  constexpr int kSlots = kRopeThreads * kVals<T> / kD;
-  const int64_t rows = a.Hq + 2 * a.Hkv;
+  constexpr int kTokens = 32 * kVals<T> / kD;  // of a warp
+  const int64_t rows = a.Hq + 2 * a.Hkv, groups = ceil_div(a.T, kTokens);
   RopeParams p;
-  p.q = recip_of(a.q_bf16 ? 1.f : a.q_scale), p.k = recip_of(a.k_scale), p.v = recip_of(a.v_scale);
+  p.q_inverse = std::min(1.f / a.q_scale, FLT_MAX);
+  p.k_inverse = std::min(1.f / a.k_scale, FLT_MAX);
+  p.v = recip_of(a.v_scale);
   p.k6 = 6.f * a.k_scale, p.v6 = 6.f * a.v_scale;
   // rows of a slot: all of a token's where there are tokens for two CTAs an SM
-  const int64_t slots = (int64_t)num_sms() * 2 * kSlots;
-  const int64_t run = std::min<int64_t>(rows, ceil_div(ceil_div(a.T * rows, slots), kInFlight) * kInFlight);
+  const int64_t warps = (int64_t)num_sms() * 2 * kRopeWarps;
+  const int64_t run = std::min<int64_t>(rows, ceil_div(groups * rows, warps));
   p.chunks = (int)ceil_div(rows, run);
   p.run = (int)ceil_div(rows, p.chunks);
   const int64_t es = sizeof(T);
@@ -293,12 +369,13 @@ cudaError_t launch_type(const RopeArgs& a, cudaStream_t stream) {
   };
   p.q_wide = on32(a.q, a.q_token, a.q_head);
   p.kv_wide = on32(a.k, a.k_token, a.k_head) && on32(a.v, a.v_token, a.v_head);
-  const int64_t grid = ceil_div(a.T * p.chunks, kSlots);
+  const int64_t grid = ceil_div(groups * p.chunks, kRopeWarps);
   auto run_it = [&](auto kernel) {
     return launch_pdl(kernel, dim3((unsigned)grid), dim3(kRopeThreads), 0, stream, a, p);
   };
   if (a.interleaved || a.pairs == 0) return run_it(rope_kernel<T, kFp4, kNeighbours>);
-  if (a.pairs % kVals<T> == 0) return run_it(rope_kernel<T, kFp4, kHalvesByLane>);
+  // whole pieces, and for NVFP4 whole blocks of 16 in a lane and its neighbours
+  if (a.pairs % std::max<int>(kVals<T> / 2, kFp4 ? 16 : 0) == 0) return run_it(rope_kernel<T, kFp4, kSplit>);
   return run_it(rope_kernel<T, kFp4, kHalves>);
 }
 
