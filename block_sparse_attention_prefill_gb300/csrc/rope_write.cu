@@ -55,6 +55,17 @@ struct RopeParams {
   bool q_wide, kv_wide;  // rows lie on 32 bytes
 };
 
+// Four E4M3 codes, nearest even, saturating.
+__device__ __forceinline__ uint32_t four_e4m3(float2 a, float2 b) {
+  uint32_t w;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}\n"
+      : "=r"(w)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return w;
+}
+
 template <typename T, bool kFp4, int kPairing>
 __global__ void __launch_bounds__(kRopeThreads, 2)
 rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopeParams p) {
@@ -91,28 +102,40 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopePara
   const int turned = a.pairs / kPiece;  // (kSplit) lanes with pairs
   const int d0 = !kIsSplit ? cc * kV : cc < turned ? cc * kPiece : a.pairs + cc * kPiece;
   const int d1 = !kIsSplit ? d0 + kPiece : cc < turned ? d0 + a.pairs : kD / 2 + cc * kPiece;
-  const T* const q_row = static_cast<const T*>(a.q) + t * a.q_token + d0;
-  const T* const k_row = static_cast<const T*>(a.k) + t * a.k_token + d0;
-  const T* const v_row = static_cast<const T*>(a.v) + t * a.v_token + d0;
+  // Rows in order, Q's, K's, V's: the next one to load, its kind's next.
+  struct Walk {
+    const T* at;
+    int64_t head;
+    int row;
+  } next;
+  auto enter = [&](Walk& x, int r) {  // row r is the first of a kind, or of the run
+    const bool q = r < k0, k = r < v0;
+    x.head = q ? a.q_head : k ? a.k_head : a.v_head;
+    x.at = static_cast<const T*>(q ? a.q : k ? a.k : a.v) +
+           t * (q ? a.q_token : k ? a.k_token : a.v_token) + (r - (q ? 0 : k ? k0 : v0)) * x.head + d0;
+    x.row = r;
+  };
+  enter(next, r_first);
   uint32_t w[kInFlight][8];
-  auto load = [&](uint32_t (&to)[8], int r) {
-    if (r < r_end && in_batch) {
-      const T* x = r < k0 ? q_row + r * a.q_head : r < v0 ? k_row + (r - k0) * a.k_head : v_row + (r - v0) * a.v_head;
+  auto load = [&](uint32_t (&to)[8]) {  // the next row, zeros behind the last
+    if (next.row < r_end && in_batch) {
       if constexpr (kIsSplit) {
-        const uint4 lo = __ldg(reinterpret_cast<const uint4*>(x));
-        const uint4 hi = __ldg(reinterpret_cast<const uint4*>(x + (d1 - d0)));
+        const uint4 lo = __ldg(reinterpret_cast<const uint4*>(next.at));
+        const uint4 hi = __ldg(reinterpret_cast<const uint4*>(next.at + (d1 - d0)));
         to[0] = lo.x, to[1] = lo.y, to[2] = lo.z, to[3] = lo.w;
         to[4] = hi.x, to[5] = hi.y, to[6] = hi.z, to[7] = hi.w;
       } else {
-        load32(x, r < k0 ? p.q_wide : p.kv_wide, to);
+        load32(next.at, next.row < k0 ? p.q_wide : p.kv_wide, to);
       }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) to[e] = 0u;
     }
+    next.at += next.head;
+    if (++next.row == k0 || next.row == v0) enter(next, next.row);
   };
 #pragma unroll
-  for (int k = 0; k < kInFlight; ++k) load(w[k], r_first + k);  // does not wait for the look-up
+  for (int k = 0; k < kInFlight; ++k) load(w[k]);  // does not wait for the look-up
   for (int j = tid; j < a.pairs; j += kRopeThreads) {
     s_turns[j] = a.turns[j];
     s_axis[j] = a.axis[j];
@@ -170,7 +193,7 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopePara
   // Cosines and sines of the lane's pairs (kHalves: of its values' pairs, the
   // sine with its sign), 1 and 0 where there is none.
   constexpr int kAngles = kPairing == kHalves ? kV : kPiece;
-  float cs[kAngles], sn[kAngles];
+  float cs[kAngles], sn[kAngles], ms[kIsSplit ? kAngles : 1];
   auto pair_of = [&](int e) {  // -1: none
     if (kPairing == kNeighbours) return cc * N + e < a.pairs ? cc * N + e : -1;
     if (kIsSplit) return cc < turned ? d0 + e : -1;
@@ -189,6 +212,7 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopePara
         sincospif((float)signed_turn * 0x1p-31f, &sn[e], &cs[e]);
         if (kPairing == kHalves && d0 + e < a.pairs) sn[e] = -sn[e];
       }
+      if (kIsSplit) ms[e] = -sn[e];  // (a packed product takes no sign)
     }
   }
   // the norm's weights, of Q and then of K
@@ -227,8 +251,9 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopePara
 #pragma unroll
         for (int e = 0; e < H; ++e) {
           const float2 c = make_float2(cs[2 * e], cs[2 * e + 1]), s = make_float2(sn[2 * e], sn[2 * e + 1]);
+          const float2 minus = make_float2(ms[2 * e], ms[2 * e + 1]);
           const float2 lo = x[e], hi = x[e + H];
-          x[e] = fma2(lo, c, mul2(hi, make_float2(-s.x, -s.y)));
+          x[e] = fma2(lo, c, mul2(hi, minus));
           x[e + H] = fma2(lo, s, mul2(hi, c));
         }
       }
@@ -286,6 +311,7 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopePara
       }
     }
   };
+  uint8_t* const q_to = static_cast<uint8_t*>(a.q_out) + t * a.Hq * (a.q_bf16 ? 2 * kD : kD);
   uint8_t* const k_page = a.pool + s_page[i] + (kFp4 ? 0 : off * (2 * kD));
   const int64_t head_bytes = kFp4 ? kFp4PageHead : kPage * 2 * kD;
   auto handle = [&](int r, const uint32_t (&raw)[8]) {
@@ -315,7 +341,7 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopePara
           const __nv_bfloat162 h = __floats2bfloat162_rn(x[e].x, x[e].y);
           o[e] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        uint16_t* to = static_cast<uint16_t*>(a.q_out) + (t * a.Hq + r) * kD;
+        uint16_t* to = reinterpret_cast<uint16_t*>(q_to) + r * kD;
         if (live) {
 #pragma unroll
           for (int e = 0; e < N; e += H) {
@@ -332,19 +358,15 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopePara
     const float m = is_q ? p.q_inverse : p.k_inverse;
     uint32_t code[N / 2];
 #pragma unroll
-    for (int e = 0; e < N / 2; ++e) {
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(mul2(x[2 * e], make_float2(m, m)), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(mul2(x[2 * e + 1], make_float2(m, m)), __NV_SATFINITE, __NV_E4M3);
-      code[e] = lo | (hi << 16);
-    }
-    uint8_t* to = is_q ? static_cast<uint8_t*>(a.q_out) + (t * a.Hq + r) * kD : k_page + (r - k0) * head_bytes;
-    if (live) store8(to, code);
+    for (int e = 0; e < N / 2; ++e)
+      code[e] = four_e4m3(mul2(x[2 * e], make_float2(m, m)), mul2(x[2 * e + 1], make_float2(m, m)));
+    if (live) store8(is_q ? q_to + r * kD : k_page + (r - k0) * head_bytes, code);
   };
   for (int r = r_first; r < r_end; r += kInFlight) {
 #pragma unroll
     for (int k = 0; k < kInFlight; ++k) {
       if (r + k < r_end) handle(r + k, w[k]);
-      load(w[k], r + k + kInFlight);
+      load(w[k]);
     }
   }
 }
