@@ -1417,12 +1417,14 @@ cudaError_t launch(const PrefixArgs& a, void* ws, cudaStream_t stream) {
   // 256 rows: 22.0 us in all, with two warps 27.1, with one 40.9).  Some parts
   // of more rows: 2 (4 parts of 2048 rows: 128.1, with 8 warps 130.5, with one
   // 134.0).  Two parts of 25 thousand rows: 1 (105, with two warps 168).
+  // Trees, whose rows are more and parts fewer than those of single tokens: 8 from
+  // 3 parts on (19 parts of 1024 rows: 24.2 us, with two warps 28.9).
   const int64_t tile_rows = std::min<int64_t>(2 * C, a.max_q) * G;
   const int64_t tiles_n =
       a.prefix_pages > 0 ? ceil_div(a.T, 2 * C) : std::min(a.T, ceil_div(a.T, 2 * C) + a.B);
   const int64_t parts = (int64_t)ctas / (a.Hkv * tiles_n);  // of a row, about
   const int64_t all_rows = a.T * a.Hq;
-  const int team = parts >= 24 && all_rows <= 4096 ? 8 : parts >= 3 && all_rows <= 16384 ? 2 : 1;
+  const int team = parts >= (kTree ? 3 : 24) && all_rows <= 4096 ? 8 : parts >= 3 && all_rows <= 16384 ? 2 : 1;
   const int cta_rows = kCombineWarps / team * 4;
   const CombineParams cp = {head, tiles + own0, (int)a.T, (int)a.Hq, (int)a.Hkv, G, C, ctas,
                             (int)a.prefix_pages, cta_rows, part_o, part_lse, a.v_scale, a.out, a.lse};

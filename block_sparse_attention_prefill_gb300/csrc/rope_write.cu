@@ -136,6 +136,7 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopePara
   };
 #pragma unroll
   for (int k = 0; k < kInFlight; ++k) load(w[k]);  // does not wait for the look-up
+  int pos = a.positions && a.axes == 1 && in_batch ? __ldg(a.positions + t) : 0;
   for (int j = tid; j < a.pairs; j += kRopeThreads) {
     s_turns[j] = a.turns[j];
     s_axis[j] = a.axis[j];
@@ -153,12 +154,15 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopePara
       s_cu[b] = __ldg(a.cu + b);
       s_cuk[b] = __ldg(a.cu_k + b);
     }
-    __syncthreads();
   }
-  // the CTA's tokens: their places in the pool
+  __syncthreads();
+  // the CTA's tokens: their places in the pool, found by warp 0; the page's number
+  // is on its way while the angles are found
+  int64_t place = -1;
+  int page = 0;
+  uint32_t bad = 0;
   if (warp == 0) {
     const int64_t tt = t0 + lane;
-    const bool used = lane < kCtaTokens && tt < a.T;
     int b;
     if (staged) {
       int lo = 0, hi = a.B;  // the number of requests that end at or before tt
@@ -170,26 +174,32 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopePara
     } else {
       b = lane_request_of(a.cu, a.B, (int)t0);
     }
-    int64_t row = -1, pos = 0;
-    if (used && b < a.B) {
+    if (lane < kCtaTokens && tt < a.T && b < a.B) {
       const int* cu = staged ? s_cu : a.cu;
       const int* cu_k = staged ? s_cuk : a.cu_k;
       const int first = cu[b];
       const int64_t q_len = (int64_t)cu[b + 1] - first, seq = (int64_t)cu_k[b + 1] - cu_k[b];
-      pos = seq - q_len + (tt - first);
-      uint32_t bad = q_len > seq || first > tt ? MSA_STATUS_BAD_SEQLENS : 0;
-      if (!bad) row = pool_row(a.block_table, a.bt_stride, a.num_pages, b, pos, &bad);
-      if (bad && a.status) atomicOr(a.status, bad);
+      place = seq - q_len + (tt - first);
+      if (q_len > seq || first > tt || place < 0 || place / kPage >= a.bt_stride) {
+        bad = MSA_STATUS_BAD_SEQLENS;
+        place = -1;
+      } else {
+        page = __ldg(a.block_table + b * a.bt_stride + place / kPage);
+      }
     }
-    s_page[lane] = row < 0 ? 0 : row / kPage * ((int64_t)a.Hkv * (kFp4 ? kFp4PageHead : kPage * 2 * kD));
-    s_off[lane] = row < 0 ? -1 : (int)(row % kPage);
-    s_pos[lane] = (int)pos;
   }
-  __syncthreads();
-  if (r_first >= r_end) return;  // (whole warps)
-  const int off = s_off[i];
-  const bool live = off >= 0;  // what is written of this slot's token
-
+  auto finish = [&] {
+    if (warp == 0) {
+      if (place >= 0 && (page < 0 || page >= a.num_pages)) bad = MSA_STATUS_BAD_BLOCK;
+      if (bad && a.status) atomicOr(a.status, bad);
+      const bool there = place >= 0 && !bad;
+      s_page[lane] = there ? (int64_t)page * a.Hkv * (kFp4 ? kFp4PageHead : kPage * 2 * kD) : 0;
+      s_off[lane] = there ? (int)(place % kPage) : -1;
+      s_pos[lane] = (int)place;
+    }
+    __syncthreads();
+  };
+  if (!a.positions) finish();
   // Cosines and sines of the lane's pairs (kHalves: of its values' pairs, the
   // sine with its sign), 1 and 0 where there is none.
   constexpr int kAngles = kPairing == kHalves ? kV : kPiece;
@@ -199,8 +209,8 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopePara
     if (kIsSplit) return cc < turned ? d0 + e : -1;
     return d0 + e < a.pairs ? d0 + e : d0 + e < 2 * a.pairs ? d0 + e - a.pairs : -1;
   };
-  if (r_first < v0) {
-    int pos = a.positions && a.axes == 1 && in_batch ? __ldg(a.positions + t) : s_pos[i];
+  if (r_first < min(v0, r_end)) {
+    if (!a.positions) pos = s_pos[i];
 #pragma unroll
     for (int e = 0; e < kAngles; ++e) {
       const int j = pair_of(e);
@@ -215,6 +225,10 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopePara
       if (kIsSplit) ms[e] = -sn[e];  // (a packed product takes no sign)
     }
   }
+  if (a.positions) finish();
+  if (r_first >= r_end) return;  // (whole warps)
+  const int off = s_off[i];
+  const bool live = off >= 0;  // what is written of this slot's token
   // the norm's weights, of Q and then of K
   float2 g[N];
   auto weights = [&](const float* of) {
