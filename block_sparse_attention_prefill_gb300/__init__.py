@@ -100,7 +100,7 @@ def load():
     _ROPE = ([ctypes.POINTER(MsaRopeStruct), P, P, i64, i64, P, i64, i64, P, i64,
               i64, i32, P, i32, f32, P, i64, f32, f32, P, i64, P, P, i64, i64,
               i64, i64, P, P], i32)
-    _ACCEPT = ([P, P, P, P, P, i64, i64, i64, ctypes.POINTER(P), i64, i64, i64, P,
+    _ACCEPT = ([P, P, P, P, P, i64, i64, i64, P, i64, i64, i64, P,
                 i64, P, P, P, P, P], i32)
     sigs = {
         "msa_version": ([], i32),

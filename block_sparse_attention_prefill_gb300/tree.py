@@ -8,14 +8,23 @@ the current device.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+from operator import attrgetter
 
 import torch
 
-from . import HEAD_DIM, MsaError, MsaRopeStruct, load
-from .serve import (_E4M3, _F32, _I32, _NOT_SOUND, _PAGE, _PAGE4, _TYPES, _WORD, _attend, _check,
-                    _fail, _handle, _new, _place, _pool, _ptr, _requests, _rows, _status, _table,
-                    _tensor)
+from . import HEAD_DIM, MsaRopeStruct, load
+from .serve import (_DEVICES, _E4M3, _F32, _I32, _NOT_SOUND, _PAGE, _PAGE4, _TYPES, _WORD, _attend,
+                    _check, _fail, _handle, _new, _place, _pool, _ptr, _requests, _rows, _status,
+                    _table, _tensor)
+
+# Names that a decode step looks up often.
+_int32, _float32, _e4m3, _u8 = torch.int32, torch.float32, torch.float8_e4m3fn, torch.uint8
+_empty, _current, _raw = torch.empty, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_data_ptr, _contiguous, _device = (torch.Tensor.data_ptr, torch.Tensor.is_contiguous,
+                                   torch.Tensor.get_device)
+_dtype, _shape = attrgetter("dtype"), attrgetter("shape")
 
 ROPE_MAX_PAIRS = 64
 ROPE_MAX_AXES = 8
@@ -140,46 +149,49 @@ def _check_rope(fp4, rope, q, k, v, kv, q_scale, block_table, cu_q, cu_k, positi
 
 def _rope_write(name, fp4, rope, q, k, v, kv, q_scale, k_scale, v_scale, block_table, cu_q, cu_k,
                 positions, q_out, status, stream):
+    dev = -1
     try:
         shape, pool, table, (T, Hq, dim) = k.shape, kv.shape, block_table.shape, q.shape
         ks, vs, qs = k.stride(), v.stride(), q.stride()
-        dev = kv.get_device()
+        dev, type_, pos = kv.get_device(), k.dtype, positions
+        q_norm, k_norm, kv_type = rope.q_norm, rope.k_norm, kv.dtype
         sound = (
-            type(rope) is MsaRope and (kv.dtype is torch.uint8 or (kv.dtype in _E4M3 and not fp4))
-            and pool[2:] == (_PAGE4 if fp4 else _PAGE) and shape[1:] == (pool[1], HEAD_DIM)
-            and len(table) == 2 and cu_q.shape == cu_k.shape == (table[0] + 1,)
-            and v.shape == shape and ks[2] == 1 == vs[2] and k.dtype is v.dtype is q.dtype
-            and k.dtype in _TYPES and T == shape[0] and dim == HEAD_DIM and qs[2] == 1
-            and cu_q.dtype is cu_k.dtype is block_table.dtype is torch.int32
-            and (positions is None
-                 or (positions.dtype is torch.int32 and positions.is_contiguous()
-                     and positions.get_device() == dev
-                     and _fits(positions.shape, rope.axes, T)))
-            and kv.is_contiguous() and block_table.is_contiguous() and cu_q.is_contiguous()
-            and cu_k.is_contiguous() and q_out is None and status is None and dev >= 0
-            and (rope.q_norm is None or rope.q_norm.get_device() == dev)
-            and (rope.k_norm is None or rope.k_norm.get_device() == dev)
+            type(rope) is MsaRope and (kv_type is _u8 or (kv_type is _e4m3 and not fp4))
+            and pool[2:] == (_PAGE4 if fp4 else _PAGE) and shape == (T, pool[1], dim) == v.shape
+            and dim == HEAD_DIM and len(table) == 2
+            and cu_q.shape == cu_k.shape == (table[0] + 1,)
+            and ks[2] == vs[2] == qs[2] == 1 and type_ in _TYPES
+            and type_ is v.dtype is q.dtype and cu_q.dtype is cu_k.dtype is block_table.dtype
+            is _int32 and kv.is_contiguous() and block_table.is_contiguous()
+            and cu_q.is_contiguous() and cu_k.is_contiguous()
+            and (pos is None or (pos.dtype is _int32 and _fits(pos.shape, rope.axes, T)
+                                 and pos.is_contiguous() and pos.get_device() == dev))
+            and q_out is None and status is None and dev >= 0
+            and (q_norm is None or q_norm.get_device() == dev)
+            and (k_norm is None or k_norm.get_device() == dev)
             and dev == k.get_device() == v.get_device() == q.get_device()
-            == block_table.get_device() == cu_q.get_device() == cu_k.get_device()
-            == torch._C._cuda_getDevice())
+            == block_table.get_device() == cu_q.get_device() == cu_k.get_device() == _current())
     except _NOT_SOUND:
         sound = False
     if not sound:
         dev = _check_rope(fp4, rope, q, k, v, kv, q_scale, block_table, cu_q, cu_k, positions, q_out,
-                    status)
-    handle = _handle(stream, dev)
+                          status)
+    handle = _raw(dev) if stream is None else _handle(stream, dev)
     if q is None:
-        shape, pool, table = k.shape, kv.shape, block_table.shape
+        shape, pool, table, type_ = k.shape, kv.shape, block_table.shape, k.dtype
         ks, vs, qs, Hq = k.stride(), v.stride(), (0, 0), 0
     elif q_out is None:
-        q_out = _new((T, Hq, HEAD_DIM), torch.bfloat16 if q_scale is None else torch.float8_e4m3fn,
-                     dev, handle)
-    rc = getattr(load(), name)(
-        rope._at, _ptr(positions), _ptr(q), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(),
-        vs[0], vs[1], _TYPES[k.dtype], _ptr(q_out), q_scale is None,
+        out = torch.bfloat16 if q_scale is None else _e4m3
+        q_out = (_empty((T, Hq, HEAD_DIM), dtype=out, device=_DEVICES[dev]) if stream is None
+                 else _new((T, Hq, HEAD_DIM), out, dev, handle))
+    lib = load()
+    rc = (lib.msa_rope_write_nvfp4 if fp4 else lib.msa_rope_write)(
+        rope._at, None if positions is None else positions.data_ptr(),
+        None if q is None else q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(),
+        vs[0], vs[1], _TYPES[type_], None if q is None else q_out.data_ptr(), q_scale is None,
         1.0 if q_scale is None else q_scale, kv.data_ptr(), pool[0], k_scale, v_scale,
         block_table.data_ptr(), table[1], cu_q.data_ptr(), cu_k.data_ptr(), table[0], shape[0], Hq,
-        pool[1], _ptr(status), handle)
+        pool[1], None if status is None else status.data_ptr(), handle)
     if rc:
         _check(rc, name)
     return q_out
@@ -227,10 +239,9 @@ def _check_tree(flat, cu_q, cu_k, outs, status):
 
 
 def _tree_limit(max_seqlen_q):
-    n = int(max_seqlen_q)
-    if not 0 <= n <= TREE_MAX_TOKENS:
-        _fail("max_seqlen_q must be 0 .. %d, got %d", TREE_MAX_TOKENS, n)
-    return n
+    if not 0 <= max_seqlen_q <= TREE_MAX_TOKENS:
+        _fail("max_seqlen_q must be 0 .. %d, got %d", TREE_MAX_TOKENS, max_seqlen_q)
+    return int(max_seqlen_q)
 
 
 def msa_tree_mask(parents, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, mask=None, positions=None,
@@ -247,32 +258,37 @@ def msa_tree_mask(parents, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, mask=None, 
     n = _tree_limit(max_seqlen_q)
     words = (n + 31) // 32
     try:
-        (T,), dev = parents.shape, parents.get_device()
+        (T,), (B1,), dev = parents.shape, cu_seqlens_q.shape, parents.get_device()
         sound = (
-            parents.dtype is cu_seqlens_q.dtype is cu_seqlens_k.dtype is torch.int32
-            and cu_seqlens_q.shape == cu_seqlens_k.shape and cu_seqlens_q.dim() == 1
-            and cu_seqlens_q.shape[0] > 0 and parents.is_contiguous()
+            parents.dtype is cu_seqlens_q.dtype is cu_seqlens_k.dtype is _int32 and B1 > 0
+            and cu_seqlens_k.shape == (B1,) and parents.is_contiguous()
             and cu_seqlens_q.is_contiguous() and cu_seqlens_k.is_contiguous()
             and mask is None and positions is None and status is None and dev >= 0
-            and dev == cu_seqlens_q.get_device() == cu_seqlens_k.get_device()
-            == torch._C._cuda_getDevice())
+            and dev == cu_seqlens_q.get_device() == cu_seqlens_k.get_device() == _current())
     except _NOT_SOUND:
         sound = False
     if not sound:
         _check_tree({"parents": parents}, cu_seqlens_q, cu_seqlens_k,
                     {"mask": (mask, _WORD, (T, words)), "positions": (positions, _I32, (T,))}
                     if parents is not None and parents.dim() == 1 else {}, status)
-        _place(parents, cu_seqlens_q, cu_seqlens_k, mask, positions, status)
+        dev = _place(parents, cu_seqlens_q, cu_seqlens_k, mask, positions, status)
         _apart({"mask": mask, "positions": positions},
                {"parents": parents, "cu_seqlens_q": cu_seqlens_q, "cu_seqlens_k": cu_seqlens_k})
-    handle = _handle(stream, dev)
-    if mask is None:
-        mask = _new((T, words), torch.int32, dev, handle)
-    if positions is None:
-        positions = _new((T,), torch.int32, dev, handle)
+    if stream is None:
+        handle, on = _raw(dev), _DEVICES[dev]
+        if mask is None:
+            mask = _empty((T, words), dtype=_int32, device=on)
+        if positions is None:
+            positions = _empty((T,), dtype=_int32, device=on)
+    else:
+        handle = _handle(stream, dev)
+        if mask is None:
+            mask = _new((T, words), _int32, dev, handle)
+        if positions is None:
+            positions = _new((T,), _int32, dev, handle)
     rc = load().msa_tree_mask(parents.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(),
-                              cu_seqlens_q.shape[0] - 1, T, n, mask.data_ptr(),
-                              positions.data_ptr(), _ptr(status), handle)
+                              B1 - 1, T, n, mask.data_ptr(), positions.data_ptr(),
+                              None if status is None else status.data_ptr(), handle)
     if rc:
         _check(rc, "msa_tree_mask")
     return mask, positions
@@ -299,7 +315,7 @@ def msa_tree_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_ta
                    max_seqlen_k, workspace, out, lse, want_lse, status, stream)
 
 
-def _pools(kv, fp4):
+def _pools(kv):
     """The layers' pools of a call, as a list of tensors of one shape."""
     if kv is None:
         return []
@@ -336,46 +352,56 @@ def _check_accept(fp4, drafts, parents, chosen, cu_q, cu_k, n, pools, table, tok
 def _accept(name, fp4, drafts, parents, chosen, cu_q, cu_k, max_q, kv, table, tokens, accepted,
             path, status, stream):
     n = _tree_limit(max_q)
-    pools = _pools(kv, fp4)
-    dev = -1
+    pools = _pools(kv)
+    L, dev, shape, at = len(pools), -1, (0, 0), None
     try:
-        shape = pools[0].shape if pools else None
-        page = _PAGE4 if fp4 else _PAGE
-        B, dev = cu_q.shape[0] - 1, drafts.get_device()
+        (T,), (B1,), dev = drafts.shape, cu_q.shape, drafts.get_device()
         sound = (
-            drafts.dtype is parents.dtype is chosen.dtype is cu_q.dtype is cu_k.dtype
-            is torch.int32 and drafts.dim() == 1 == cu_q.dim() and B >= 0
-            and drafts.shape == parents.shape == chosen.shape and cu_q.shape == cu_k.shape
+            drafts.dtype is parents.dtype is chosen.dtype is cu_q.dtype is cu_k.dtype is _int32
+            and B1 > 0 and parents.shape == chosen.shape == (T,) and cu_k.shape == (B1,)
             and drafts.is_contiguous() and parents.is_contiguous() and chosen.is_contiguous()
-            and cu_q.is_contiguous() and cu_k.is_contiguous() and len(pools) <= TREE_MAX_LAYERS
+            and cu_q.is_contiguous() and cu_k.is_contiguous() and L <= TREE_MAX_LAYERS
             and tokens is None and accepted is None and path is None and status is None
             and dev >= 0 and dev == parents.get_device() == chosen.get_device()
-            == cu_q.get_device() == cu_k.get_device() == torch._C._cuda_getDevice()
-            and (not pools or (
-                shape[2:] == page and len(shape) == 4 and table.dtype is torch.int32
-                and table.dim() == 2 and table.shape[0] == B and table.is_contiguous()
-                and table.get_device() == dev))
-            and all((p.dtype is torch.uint8 or (p.dtype in _E4M3 and not fp4)) and p.shape == shape
-                    and p.is_contiguous() and p.get_device() == dev for p in pools))
-    except _NOT_SOUND + (IndexError,):
+            == cu_q.get_device() == cu_k.get_device() == _current())
+        if sound and L:
+            # all pools alike: what they have in common is looked at once
+            (shape,), (type_,), (on,) = (set(map(_shape, pools)), set(map(_dtype, pools)),
+                                         set(map(_device, pools)))
+            sound = (
+                shape[2:] == (_PAGE4 if fp4 else _PAGE) and len(shape) == 4 and on == dev
+                and (type_ is _u8 or (type_ is _e4m3 and not fp4))
+                and all(map(_contiguous, pools)) and table.dtype is _int32 and table.dim() == 2
+                and table.shape[0] == B1 - 1 and table.is_contiguous()
+                and table.get_device() == dev)
+    except _NOT_SOUND:
         sound = False
     if not sound:
         dev = _check_accept(fp4, drafts, parents, chosen, cu_q, cu_k, n, pools, table, tokens,
                             accepted, path, status)
-    handle = _handle(stream, dev)
-    if tokens is None:
-        tokens = _new((B, n), torch.int32, dev, handle)
-    if accepted is None:
-        accepted = _new((B,), torch.int32, dev, handle)
-    if path is None:
-        path = _new((B, n), torch.int32, dev, handle)
-    L = len(pools)
-    at = (ctypes.c_void_p * L)(*[p.data_ptr() for p in pools]) if L else None
-    rc = getattr(load(), name)(
+        shape = pools[0].shape if L else shape
+    B = B1 - 1
+    if stream is None:
+        handle, on = _raw(dev), _DEVICES[dev]
+        if tokens is None:
+            tokens = _empty((B, n), dtype=_int32, device=on)
+        if accepted is None:
+            accepted = _empty((B,), dtype=_int32, device=on)
+        if path is None:
+            path = _empty((B, n), dtype=_int32, device=on)
+    else:
+        handle = _handle(stream, dev)
+        tokens = _new((B, n), _int32, dev, handle) if tokens is None else tokens
+        accepted = _new((B,), _int32, dev, handle) if accepted is None else accepted
+        path = _new((B, n), _int32, dev, handle) if path is None else path
+    if L:
+        at = array.array("Q", map(_data_ptr, pools))  # (kept until the call has read it)
+    lib = load()
+    rc = (lib.msa_tree_accept_nvfp4 if fp4 else lib.msa_tree_accept)(
         drafts.data_ptr(), parents.data_ptr(), chosen.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),
-        B, drafts.shape[0], n, at, L, shape[0] if L else 0, shape[1] if L else 0,
+        B, T, n, at.buffer_info()[0] if L else None, L, shape[0], shape[1],
         table.data_ptr() if L else None, table.shape[1] if L else 0, tokens.data_ptr(),
-        accepted.data_ptr(), path.data_ptr(), _ptr(status), handle)
+        accepted.data_ptr(), path.data_ptr(), None if status is None else status.data_ptr(), handle)
     if rc:
         _check(rc, name)
     return tokens, accepted, path
@@ -441,39 +467,49 @@ def msa_logprobs(logits, tokens=None, top=0, logprobs=None, ranks=None, entropy=
     None without tokens.  Of equal logits the lower index comes first.  A token
     outside [0, V) has -inf and rank -1; a row with a NaN has NaN, but for the
     tokens and ranks."""
-    top = int(top)
     if not 0 <= top <= LOGPROBS_MAX_TOP:
         _fail("top must be 0 .. %d, got %d", LOGPROBS_MAX_TOP, top)
     dev = -1
     try:
-        (T, V), (row, one) = logits.shape, logits.stride()
-        dev = logits.get_device()
+        (T, V), (row, one), dev, type_ = (logits.shape, logits.stride(), logits.get_device(),
+                                          logits.dtype)
         sound = (
-            logits.dtype in _TYPES and (one == 1 or V == 1)
-            and (tokens is None or (tokens.dtype is torch.int32 and tokens.shape == (T,)
+            type_ in _TYPES and (one == 1 or V == 1)
+            and (tokens is None or (tokens.dtype is _int32 and tokens.shape == (T,)
                                     and tokens.is_contiguous() and tokens.get_device() == dev))
             and logprobs is None and ranks is None and entropy is None and top_tokens is None
-            and top_logprobs is None and dev >= 0 and dev == torch._C._cuda_getDevice())
+            and top_logprobs is None and dev >= 0 and dev == _current())
     except _NOT_SOUND:
         sound = False
     if not sound:
         dev = _check_logprobs(logits, tokens, top,
                               {"logprobs": logprobs, "ranks": ranks, "entropy": entropy,
                                "top_tokens": top_tokens, "top_logprobs": top_logprobs})
-    handle = _handle(stream, dev)
-    if tokens is not None and logprobs is None:
-        logprobs = _new((T,), torch.float32, dev, handle)
-    if tokens is not None and ranks is None:
-        ranks = _new((T,), torch.int32, dev, handle)
-    if entropy is None:
-        entropy = _new((T,), torch.float32, dev, handle)
-    if top_tokens is None:
-        top_tokens = _new((T, top), torch.int32, dev, handle)
-    if top_logprobs is None:
-        top_logprobs = _new((T, top), torch.float32, dev, handle)
-    rc = load().msa_logprobs(logits.data_ptr(), row, _TYPES[logits.dtype], _ptr(tokens), T, V, top,
-                             _ptr(logprobs), _ptr(ranks), entropy.data_ptr(), top_tokens.data_ptr(),
-                             top_logprobs.data_ptr(), handle)
+    given = tokens is not None
+    if stream is None and sound:
+        handle, on = _raw(dev), _DEVICES[dev]
+        if given:
+            logprobs = _empty((T,), dtype=_float32, device=on)
+            ranks = _empty((T,), dtype=_int32, device=on)
+        entropy = _empty((T,), dtype=_float32, device=on)
+        top_tokens = _empty((T, top), dtype=_int32, device=on)
+        top_logprobs = _empty((T, top), dtype=_float32, device=on)
+    else:
+        handle = _handle(stream, dev)
+        if given and logprobs is None:
+            logprobs = _new((T,), _float32, dev, handle)
+        if given and ranks is None:
+            ranks = _new((T,), _int32, dev, handle)
+        if entropy is None:
+            entropy = _new((T,), _float32, dev, handle)
+        if top_tokens is None:
+            top_tokens = _new((T, top), _int32, dev, handle)
+        if top_logprobs is None:
+            top_logprobs = _new((T, top), _float32, dev, handle)
+    rc = load().msa_logprobs(
+        logits.data_ptr(), row, _TYPES[type_], tokens.data_ptr() if given else None, T, V, top,
+        logprobs.data_ptr() if given else None, ranks.data_ptr() if given else None,
+        entropy.data_ptr(), top_tokens.data_ptr(), top_logprobs.data_ptr(), handle)
     if rc:
         _check(rc, "msa_logprobs")
     return logprobs, ranks, entropy, top_tokens, top_logprobs
