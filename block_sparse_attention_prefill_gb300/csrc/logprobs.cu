@@ -45,16 +45,14 @@ namespace msa {
 namespace {
 
 constexpr int kMaxWarps = 8;     // of a CTA
-constexpr int kWarpsOfSm = 24;   // (80 registers a thread)
 constexpr int kMaxCluster = 8;
 constexpr int kTop = MSA_LOGPROBS_MAX_TOP;
-constexpr int kBatch = 4;        // chunks of a warp in flight
 constexpr int kVocabBits = 19;   // V < 2^19
 constexpr int kChunkBits = 13;   // chunks of a row: at most 4097
 constexpr int kVecBits = 18;     // vectors of a row: at most 2^17 + 1
 constexpr int kMaxChunks = (MSA_VERIFY_MAX_VOCAB * 4) / 512 + 1;
-constexpr int kMostChunks = 48;  // chunks that are read again
-constexpr int kRound = 6;        // of a thread's vectors among them, in flight
+constexpr int kMostChunks = 64;  // chunks that are read again
+constexpr int kRound = 4;        // of a thread's vectors among them, in flight
 constexpr int kMostVecs = 64;    // vectors whose values are looked at
 constexpr int kFew = kMostVecs * 8;
 constexpr int kBuckets = 64;     // a CTA's whole chunks, dealt out in turn
@@ -274,8 +272,12 @@ struct Part {  // of a warp
   int before;
 };
 
-template <typename T, int kWarps>
-__global__ void __launch_bounds__(kWarps * 32, kWarpsOfSm / kWarps)
+// kBatch: chunks of a warp that are worked on together, with as many more in
+// flight: 4 with 24 warps an SM (80 registers a thread), 2 with 32.
+constexpr int warps_of_sm(int batch) { return batch == 4 ? 24 : 32; }
+
+template <typename T, int kWarps, int kBatch>
+__global__ void __launch_bounds__(kWarps * 32, warps_of_sm(kBatch) / kWarps)
 logprobs_kernel(const LogprobsArgs a, int cluster_size) {
   using V = Vec<T>;
   constexpr int N = V::N, kThreads = kWarps * 32;
@@ -665,7 +667,7 @@ logprobs_kernel(const LogprobsArgs a, int cluster_size) {
   if (tid >= some && tid < k) put(tid, 0);  // fewer than k values
 }
 
-template <typename T, int kWarps>
+template <typename T, int kWarps, int kBatch>
 cudaError_t launch_as(const LogprobsArgs& a, int cluster, int64_t chunks, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.T * cluster));
@@ -680,7 +682,7 @@ cudaError_t launch_as(const LogprobsArgs& a, int cluster, int64_t chunks, cudaSt
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kWarps>, a, cluster);
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kWarps, kBatch>, a, cluster);
 }
 
 template <typename T>
@@ -691,12 +693,12 @@ cudaError_t launch_type(const LogprobsArgs& a, cudaStream_t stream) {
   const int64_t chunks = ceil_div((int64_t)a.V * sizeof(T), 512) + 1;
   int c = kMaxCluster;
   while (c > 1 && (a.T * c > (int64_t)num_sms() * 3 || chunks < 16 * c)) c /= 2;
-  // Many short rows: twice as many CTAs of half the warps, whose selections
-  // overlap more rows' loads (8192 rows of 32000 bf16, 5 best: 167 us, with 8
-  // warps 208; 2048 of 131072: 118 and 117; 456 of 131072: 35 and 29)
-  if (a.T >= (int64_t)num_sms() * (kWarpsOfSm / 4) && chunks <= 256)
-    return launch_as<T, 4>(a, c, chunks, stream);
-  return launch_as<T, kMaxWarps>(a, c, chunks, stream);
+  // Many short rows: more CTAs of half the warps, whose selections overlap more
+  // rows' loads (5 best, 8192 rows of 32000 bf16: 144 us, with 8 warps 208; but
+  // 2048 of 131072: 122 and 117; 456 of 131072: 35 and 29)
+  if (a.T >= (int64_t)num_sms() * (warps_of_sm(2) / 4) && chunks <= 256)
+    return launch_as<T, 4, 2>(a, c, chunks, stream);
+  return launch_as<T, kMaxWarps, 4>(a, c, chunks, stream);
 }
 
 }  // namespace
