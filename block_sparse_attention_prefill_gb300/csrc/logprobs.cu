@@ -7,16 +7,16 @@
 // whole warp when a larger value is met, and merged at the end by their m.
 //
 // The k best are found without a list kept on the way: the pass notes the
-// largest value of every chunk of 512 bytes (a warp's load).  The k best values
-// lie in the k chunks whose largest come first (of equal ones those with lower
-// indices): any other chunk has k values before all of its own.  The chunks are
-// dealt out to 64 buckets, and the k-th largest of the buckets' largest values is
-// a bound that the k best pass, and few more chunks (24 for k = 20, were they in
-// random order); these are read again, from L2, and their values that pass it,
-// 512 at most, are put in order by counting.  Where more than that pass (rows
-// that are all equal, ascending, masked) bounds are found by bisection on keys
-// (value, index) that are all different, so that the work is bounded whatever
-// the row holds.
+// largest value of every chunk of 512 bytes (a warp's load), and of each lane.
+// The k-th largest of 64 groups of lanes' is a bound that k values pass, and few
+// more (24 for k = 20, were they in random order); the chunks whose largest pass
+// it are read again, from L2, and their values that do, 512 at most, are put in
+// order by counting.  Where more than that pass (rows that are all equal,
+// ascending, masked) bounds are found by bisection on keys (value, index) that
+// are all different: the k best lie in the k chunks whose largest come first (of
+// equal ones those with lower indices, as any other chunk has k values before
+// all of its own), and in the k of their vectors for which the same holds.  So
+// the work is bounded whatever the row holds.
 //
 // Bounds and what was measured (GPU time, replayed from a graph): 2048 rows of
 // 131072 bf16, 5 best: 117 us, 4.6 TB/s; without tokens and best 89 (6.0 TB/s).
@@ -55,7 +55,7 @@ constexpr int kMostChunks = 64;  // chunks that are read again
 constexpr int kRound = 4;        // of a thread's vectors among them, in flight
 constexpr int kMostVecs = 64;    // vectors whose values are looked at
 constexpr int kFew = kMostVecs * 8;
-constexpr int kBuckets = 64;     // a CTA's whole chunks, dealt out in turn
+constexpr int kBuckets = 64;     // of a CTA's lanes
 static_assert(MSA_VERIFY_MAX_VOCAB == 1 << kVocabBits && kMaxChunks < 1 << kChunkBits, "keys");
 static_assert(kTop == 32 && kTop <= kMostChunks && kTop <= kMostVecs, "selection");
 constexpr float kLowest = -FLT_MAX;  // m before any value (finite: x - m is no NaN)
@@ -354,24 +354,22 @@ logprobs_kernel(const LogprobsArgs a, int cluster_size) {
   const T mine1 = from_f32<T>(mine), above1 = next_above(mine1);
   const float above_mine = to_f32(above1);
   const typename V::T2 mine2 = {mine1, mine1}, above2 = {above1, above1};
-  float bucket = -INFINITY;
-  int turn = 0;
+  float bucket = -INFINITY;  // the lane's largest value
   auto add_some = [&](auto full, const V (&v)[kBatch], int c) {
     float top[kBatch], most = kLowest;
     auto there = [&](int k) { return decltype(full)::value || c + k * kWarps < in1; };
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       if (!there(k)) continue;
-      top[k] = warp_max(v[k].top());
+      const float own = v[k].top();
+      bucket = largest(bucket, own);
+      top[k] = warp_max(own);
       most = largest(most, top[k]);
     }
-    // lanes k, k + 4, ... take the k-th; one of them, another each time, keeps it
     float kept = -INFINITY;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
-      if (there(k) && lane % kBatch == k) kept = top[k];
-    if (lane / kBatch == turn % (32 / kBatch)) bucket = largest(bucket, kept);
-    ++turn;
+      if (there(k) && lane == k) kept = top[k];
     if (lane < kBatch && (decltype(full)::value || c + lane * kWarps < in1)) s_max[c + lane * kWarps] = kept;
     if (most > sum.m) sum.raise(most);
     constexpr int kUsual = V::k16 ? kPlain : kBounded;
@@ -433,7 +431,7 @@ logprobs_kernel(const LogprobsArgs a, int cluster_size) {
     p.before += __shfl_xor_sync(0xffffffffu, p.before, o);
   }
   if (lane == 0) s_top[warp] = sum.m;
-  // 64 buckets of the CTA: a warp's 32 lanes by as many together as make 64
+  // 64 buckets of the CTA: its lanes by as many together as make 64
   constexpr int kOfWarp = kBuckets / kWarps;
 #pragma unroll
   for (int o = 16; o >= kOfWarp; o >>= 1) bucket = largest(bucket, __shfl_xor_sync(0xffffffffu, bucket, o));
@@ -453,7 +451,7 @@ logprobs_kernel(const LogprobsArgs a, int cluster_size) {
         if (at[j] >= 0) y[j].load_edge(row, at[j]);
       }
     };
-    // A bound for the k-th best: the k-th largest of the buckets' largest values,
+    // A bound that k values pass: the k-th largest of the buckets' largest values,
     // whose place is the number of those before it (some threads a value)
     {
       constexpr int kShare = kThreads / kBuckets;
