@@ -1099,9 +1099,9 @@ struct CombineParams {
 // KV head (.y): first the parts of that tile and of the shared tiles (two at
 // most) that its tokens lie in are listed, then each warp merges the parts of
 // four neighbouring rows, 8 lanes a row, or kTeam warps together: weights
-// 2^(lse - m), fp32 sums, eight or more 16-byte loads in flight per lane.  A
+// 2^(lse - m), fp32 sums, kFlight parts, of four 16-byte loads a lane, in flight.  A
 // batch that was refused gives empty rows.
-template <int kTeam>
+template <int kTeam, int kFlight>
 __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const CombineParams p) {
   // per listed tile: its parts' first rows (of the tile's first token and
   // head), in line order
@@ -1110,7 +1110,6 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
   __shared__ Tile s_tile[3];
   constexpr int kLanes = 8;
   constexpr int kQ = 32 / kLanes;             // float4 of a row per lane
-  constexpr int kFlight = kTeam == 8 ? 8 : 2;  // parts in flight
   __shared__ __align__(16) float s_acc[kTeam > 1 ? kCombineWarps * 4 : 1][kD];  // (as float4)
   __shared__ float s_m[kCombineWarps * 4], s_l[kCombineWarps * 4];
   pdl_wait();
@@ -1417,23 +1416,40 @@ cudaError_t launch(const PrefixArgs& a, void* ws, cudaStream_t stream) {
   // 256 rows: 22.0 us in all, with two warps 27.1, with one 40.9).  Some parts
   // of more rows: 2 (4 parts of 2048 rows: 128.1, with 8 warps 130.5, with one
   // 134.0).  Two parts of 25 thousand rows: 1 (105, with two warps 168).
-  // Trees, whose rows are more and parts fewer than those of single tokens: 8 from
-  // 3 parts on (19 parts of 1024 rows: 24.2 us, with two warps 28.9).
   const int64_t tile_rows = std::min<int64_t>(2 * C, a.max_q) * G;
   const int64_t tiles_n =
       a.prefix_pages > 0 ? ceil_div(a.T, 2 * C) : std::min(a.T, ceil_div(a.T, 2 * C) + a.B);
   const int64_t parts = (int64_t)ctas / (a.Hkv * tiles_n);  // of a row, about
   const int64_t all_rows = a.T * a.Hq;
-  const int team = parts >= (kTree ? 3 : 24) && all_rows <= 4096 ? 8 : parts >= 3 && all_rows <= 16384 ? 2 : 1;
-  const int cta_rows = kCombineWarps / team * 4;
+  const int team = parts >= 24 && all_rows <= 4096 ? 8 : parts >= 3 && all_rows <= 16384 ? 2 : 1;
   const CombineParams cp = {head, tiles + own0, (int)a.T, (int)a.Hq, (int)a.Hkv, G, C, ctas,
-                            (int)a.prefix_pages, cta_rows, part_o, part_lse, a.v_scale, a.out, a.lse};
+                            (int)a.prefix_pages, 0, part_o, part_lse, a.v_scale, a.out, a.lse};
   const int64_t own = std::min<int64_t>(a.T, ceil_div(a.T, 2 * C) + a.B);
-  const dim3 grid((unsigned)own, (unsigned)a.Hkv, (unsigned)std::max<int64_t>(1, ceil_div(tile_rows, cta_rows)));
-  const dim3 block(kCombineWarps * 32);
-  if (team == 8) return launch_pdl(combine_kernel<8>, grid, block, 0, stream, cp);
-  if (team == 2) return launch_pdl(combine_kernel<2>, grid, block, 0, stream, cp);
-  return launch_pdl(combine_kernel<1>, grid, block, 0, stream, cp);
+  auto combine = [&](auto kernel, int warps) {  // that many warps share four rows
+    CombineParams p = cp;
+    p.rows = kCombineWarps / warps * 4;
+    const dim3 grid((unsigned)own, (unsigned)a.Hkv,
+                    (unsigned)std::max<int64_t>(1, ceil_div(tile_rows, p.rows)));
+    return launch_pdl(kernel, grid, dim3(kCombineWarps * 32), 0, stream, p);
+  };
+  if constexpr (kTree) {
+    // Trees: the fewer rows, the more warps a row and parts in flight; the more,
+    // the fewer registers, by which more CTAs fit an SM (with 8 parts in flight
+    // one).  128 rows of 76 parts: 8 warps, 8 parts 19.6 us in all, 4 parts 20.8.
+    // 1024 of 19: 8 and 4 20.4, 8 and 8 24.1, 4 and 4 21.9.  2048 of 9: 4 and 4
+    // 23.5, 8 and 8 33.8, 4 and 2 25.3.  4096 of 10: 4 and 2 54.8, 4 and 4 57.4,
+    // 8 and 8 77, 2 and 2 57.0.
+    if (parts >= 3 && all_rows <= 16384) {
+      if (all_rows <= 256) return combine(combine_kernel<8, 8>, 8);
+      if (all_rows <= 1024) return combine(combine_kernel<8, 4>, 8);
+      if (all_rows <= 2048) return combine(combine_kernel<4, 4>, 4);
+      return combine(combine_kernel<4, 2>, 4);
+    }
+    return combine(combine_kernel<1, 2>, 1);
+  }
+  if (team == 8) return combine(combine_kernel<8, 8>, 8);
+  if (team == 2) return combine(combine_kernel<2, 2>, 2);
+  return combine(combine_kernel<1, 2>, 1);
 }
 
 }  // namespace
