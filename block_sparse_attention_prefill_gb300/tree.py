@@ -21,7 +21,9 @@ from .serve import (_DEVICES, _E4M3, _F32, _I32, _NOT_SOUND, _PAGE, _PAGE4, _TYP
 
 # Names that a decode step looks up often.
 _int32, _float32, _e4m3, _u8 = torch.int32, torch.float32, torch.float8_e4m3fn, torch.uint8
-_empty, _current, _raw = torch.empty, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_empty = torch.empty
+_current = getattr(torch._C, "_cuda_getDevice", None)
+_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _data_ptr, _contiguous, _device = (torch.Tensor.data_ptr, torch.Tensor.is_contiguous,
                                    torch.Tensor.get_device)
 _dtype, _shape = attrgetter("dtype"), attrgetter("shape")

@@ -221,3 +221,26 @@ def test_tree_library_refusals():
     for bad in (dict(T=-1), dict(T=2 ** 31), dict(V=0), dict(V=2 ** 19), dict(row=-1), dict(top=33), dict(top=-1)):
         assert logprobs(**bad) == 1
     assert logprobs(x=P(4098)) == 3 and logprobs(x=P(4097), dtype=1) == 3 and logprobs(t=P(4097)) == 3 and logprobs(e=P(4097)) == 3
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    from block_sparse_attention_prefill_gb300 import tree
+
+    class Other(torch.Tensor):
+        def get_device(self):
+            return 3
+
+    on = lambda t: t.as_subclass(Other)  # noqa: E731
+    z = lambda *s: on(torch.zeros(s, dtype=torch.int32))  # noqa: E731
+    u8 = lambda *s: on(torch.zeros(s, dtype=torch.uint8))  # noqa: E731
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(tree, "_current", lambda: 0)
+    kv = u8(4, 2, 128, 256)
+    x = on(torch.zeros((6, 2, 128)))
+    for call in (lambda: msa.msa_rope_write(msa.MsaRope([1.0]), x, x, x, kv, 1.0, 1.0, 1.0, z(2, 3), z(3), z(3)),
+                 lambda: msa.msa_tree_mask(z(6), z(3), z(3), 6),
+                 lambda: msa.msa_tree_attention(u8(6, 4, 128), kv, 1.0, 1.0, 1.0, 0.1, z(2, 3), z(3), z(3), z(6, 1), 1, 6, 300),
+                 lambda: msa.msa_tree_accept(z(6), z(6), z(6), z(3), z(3), 6, kv=[kv], block_table=z(2, 3)),
+                 lambda: msa.msa_logprobs(on(torch.zeros((6, 50))), z(6), top=2)):
+        assert "the current device is cuda:0" in _err(call)
