@@ -1442,12 +1442,19 @@ cudaError_t launch(const PrefixArgs& a, void* ws, cudaStream_t stream) {
     // one).  128 rows of 76 parts: 8 warps, 8 parts 19.6 us in all, 4 parts 20.8.
     // 1024 of 19: 8 and 4 20.4, 8 and 8 24.1, 4 and 4 21.9.  2048 of 9: 4 and 4
     // 23.5, 8 and 8 33.8, 4 and 2 25.3.  4096 of 10: 4 and 2 54.8, 4 and 4 57.4,
-    // 8 and 8 77, 2 and 2 57.0.
-    if (parts >= 3 && all_rows <= 16384) {
+    // 8 and 8 77, 2 and 2 57.0.  9600 of 4: 2 and 2 119.9, 4 and 2 125.4, one warp
+    // 121.5; of two parts of 16 thousand: one warp 54.4, 2 and 2 58.1.
+    // (parts of a row, about: tiles are whole requests, or hold 2 C tokens each)
+    const int64_t tiles_lo =
+        a.prefix_pages > 0 ? ceil_div(a.T, 2 * C)
+                           : std::max(ceil_div(a.T, 2 * C), std::min(a.T, a.B));
+    const int64_t parts_lo = (int64_t)ctas / (a.Hkv * tiles_lo);
+    if (parts_lo >= 3 && all_rows <= 16384) {
       if (all_rows <= 256) return combine(combine_kernel<8, 8>, 8);
       if (all_rows <= 1024) return combine(combine_kernel<8, 4>, 8);
       if (all_rows <= 2048) return combine(combine_kernel<4, 4>, 4);
-      return combine(combine_kernel<4, 2>, 4);
+      if (all_rows <= 4096) return combine(combine_kernel<4, 2>, 4);
+      return combine(combine_kernel<2, 2>, 2);
     }
     return combine(combine_kernel<1, 2>, 1);
   }
