@@ -19,11 +19,11 @@
 // the work is bounded whatever the row holds.
 //
 // Bounds and what was measured (GPU time, replayed from a graph): 2048 rows of
-// 131072 bf16, 5 best: 117 us, 4.6 TB/s; without tokens and best 89 (6.0 TB/s).
-// Ranks cost a packed comparison and a sum for every two values (13 us), the
-// selection about 4 us a row and CTA, in which its warps load little.  16 rows of
-// 200003 fp32, 20 best: 11.5 us, latency (the row 4.5, the selection 3, exchange
-// and merge of the cluster 3).
+// 131072 bf16, 5 best: 112 us, 4.8 TB/s; without tokens and best 87 (6.2 TB/s).
+// Ranks cost a packed comparison and a sum for every two values (14 us), the
+// selection about 4 us a row and CTA, in which its warps load little (12 us).
+// 16 rows of 200003 fp32, 20 best: 11.5 us, latency (the pass 6, bound and
+// selection 3, exchange and merge of the cluster 2.5).
 //
 // A cluster of 1 to 8 CTAs takes a row (as many as fill the GPU when there are
 // few rows): each finds its own k best, and the first merges them through
@@ -692,8 +692,8 @@ cudaError_t launch_type(const LogprobsArgs& a, cudaStream_t stream) {
   int c = kMaxCluster;
   while (c > 1 && (a.T * c > (int64_t)num_sms() * 3 || chunks < 16 * c)) c /= 2;
   // Many short rows: more CTAs of half the warps, whose selections overlap more
-  // rows' loads (5 best, 8192 rows of 32000 bf16: 144 us, with 8 warps 208; but
-  // 2048 of 131072: 122 and 117; 456 of 131072: 35 and 29)
+  // rows' loads (5 best, 8192 rows of 32000 bf16: 133 us, with 8 warps about 200;
+  // but 2048 of 131072: 122 and 117; 456 of 131072: 35 and 29)
   if (a.T >= (int64_t)num_sms() * (warps_of_sm(2) / 4) && chunks <= 256)
     return launch_as<T, 4, 2>(a, c, chunks, stream);
   return launch_as<T, kMaxWarps, 4>(a, c, chunks, stream);

@@ -11,7 +11,8 @@
 //            becomes row context + j, in every layer
 //
 // Both are bound by latency: a few dependent loads and a few rounds in shared
-// memory.  A CTA takes a request.  Ancestors are found by doubling: every round
+// memory (GPU time, replayed from a graph: masks of one tree of 16 2.3 us, of 256
+// of up to 255 4.5; acceptance of one tree in 4 layers 1.9 us, of 64 in 32 3.4).  A CTA takes a request.  Ancestors are found by doubling: every round
 // a node takes over what its farthest known ancestor knows, so that a chain of
 // 256 takes 8 rounds and not 255.  An accepting CTA finds the path for itself
 // and then moves rows of some (layer, head)s: 16 lanes a row, 16 bytes each.
