@@ -97,7 +97,7 @@ def load():
                i64, i64, i64, P, P], i32)
     _READ = ([P, i64, f32, f32, P, i64, P, P, i64, i64, i64, P, i64, i64, P,
               i64, i64, i32, P, P], i32)
-    _ROPE = ([ctypes.POINTER(MsaRopeStruct), P, P, i64, i64, P, i64, i64, P, i64,
+    _ROPE = ([P, P, P, i64, i64, P, i64, i64, P, i64,
               i64, i32, P, i32, f32, P, i64, f32, f32, P, i64, P, P, i64, i64,
               i64, i64, P, P], i32)
     _ACCEPT = ([P, P, P, P, P, i64, i64, i64, P, i64, i64, i64, P,
@@ -660,6 +660,6 @@ def run_workload(w, stream=None):
 from .serve import (msa_kv_read, msa_kv_read_nvfp4, msa_kv_write,  # noqa: E402,F401
                     msa_kv_write_nvfp4, msa_prefix_attention,
                     msa_verify, msa_verify_greedy, prefix_attention_workspace_bytes)
-from .tree import (MsaRope, msa_logprobs, msa_rope_turns, msa_rope_write,  # noqa: E402,F401
+from .tree import (MsaRope, load_binding, msa_logprobs, msa_rope_turns, msa_rope_write,  # noqa: E402,F401
                    msa_rope_write_nvfp4, msa_tree_accept, msa_tree_accept_nvfp4,
                    msa_tree_attention, msa_tree_mask)

@@ -5,13 +5,20 @@ Each .cu file is compiled to an object in parallel, then linked into
 runtime linked statically (the library needs only the driver at run time).
 The driver entry point for TMA descriptors is looked up at run time, so the
 library also loads on a machine without a GPU.
+
+``csrc/binding.cpp``, the tree calls' way from Python to the library, is
+compiled beside it with the C++ compiler against the installed PyTorch, into a
+module of its own: the library itself does not know PyTorch.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -49,6 +56,39 @@ def _stale(target, deps):
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _cuda_include() -> str:
+    nvcc = _nvcc()
+    home = os.path.dirname(os.path.dirname(nvcc)) if os.path.isabs(nvcc) else "/usr/local/cuda"
+    return os.path.join(home, "include")
+
+
+def binding_path() -> str:
+    """The binding's module for this interpreter and PyTorch."""
+    return os.path.join(OUT, "msa_binding-torch%s%s" % (importlib.metadata.version("torch"),
+                                                        sysconfig.get_config_var("EXT_SUFFIX")))
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the Python module if its source or the header is newer."""
+    os.makedirs(OUT, exist_ok=True)
+    path, src = binding_path(), os.path.join(CSRC, "binding.cpp")
+    if not force and not _stale(path, [src, os.path.join(INCLUDE, "msa.h"), __file__]):
+        return path
+    root = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch, libs = os.path.join(root, "include"), os.path.join(root, "lib")
+    tmp = path + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", torch,
+           "-I", os.path.join(torch, "torch", "csrc", "api", "include"), "-I", _cuda_include(), src,
+           "-o", tmp, "-L", libs, "-Wl,-rpath," + libs, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("the C++ compiler failed for %s:\n%s\n%s" % (src, r.stdout, r.stderr))
+    os.replace(tmp, path)
+    return path
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info=False) -> str:

@@ -2,37 +2,52 @@
 (and around any step): rotation with the cache write, tree masks and attention,
 acceptance, log probabilities.
 
-Argument marshalling only, as in ``serve.py``, whose way of checking these
-calls share; ``include/msa.h`` has each call's meaning.  Tensors have to be on
-the current device.
+Argument marshalling only, as in ``serve.py``, whose checks these calls share;
+``include/msa.h`` has each call's meaning.  Tensors have to be on the current
+device.
+
+A decode step waits for the host's way to each launch, so the form that it uses
+(outputs to be made, the current stream, no status) is checked and called by the
+compiled module of ``csrc/binding.cpp``; what that does not take, other forms and
+arguments that are not sound, is looked at here one by one, with its messages.
 """
 from __future__ import annotations
 
-import array
 import ctypes
-from operator import attrgetter
+import importlib.machinery
+import importlib.util
 
 import torch
 
-from . import HEAD_DIM, MsaRopeStruct, load
-from .serve import (_DEVICES, _E4M3, _F32, _I32, _NOT_SOUND, _PAGE, _PAGE4, _TYPES, _WORD, _attend,
-                    _check, _fail, _handle, _new, _place, _pool, _ptr, _requests, _rows, _status,
-                    _table, _tensor)
-
-# Names that a decode step looks up often.
-_int32, _float32, _e4m3, _u8 = torch.int32, torch.float32, torch.float8_e4m3fn, torch.uint8
-_empty = torch.empty
-_current = getattr(torch._C, "_cuda_getDevice", None)
-_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_data_ptr, _contiguous, _device = (torch.Tensor.data_ptr, torch.Tensor.is_contiguous,
-                                   torch.Tensor.get_device)
-_dtype, _shape = attrgetter("dtype"), attrgetter("shape")
+from . import HEAD_DIM, MsaRopeStruct, _build, load
+from .serve import (_E4M3, _F32, _I32, _TYPES, _WORD, _attend, _check, _fail, _handle, _new, _place,
+                    _pool, _ptr, _requests, _rows, _status, _table, _tensor)
 
 ROPE_MAX_PAIRS = 64
 ROPE_MAX_AXES = 8
 TREE_MAX_TOKENS = 256
 TREE_MAX_LAYERS = 128
 LOGPROBS_MAX_TOP = 32
+
+
+_binding = None
+
+
+def load_binding():
+    """The compiled module (building it first if it is missing)."""
+    global _binding
+    if _binding is None:
+        lib, path = load(), _build.build_binding()
+        loader = importlib.machinery.ExtensionFileLoader("msa_binding", path)
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_file_location("msa_binding", path, loader=loader))
+        loader.exec_module(module)
+        module.connect(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.msa_rope_write, lib.msa_rope_write_nvfp4, lib.msa_tree_mask, lib.msa_tree_accept,
+            lib.msa_tree_accept_nvfp4, lib.msa_logprobs, lib.msa_tree_attention,
+            lib.msa_prefix_attention_workspace_bytes)])
+        _binding = module
+    return _binding
 
 
 def msa_rope_turns(inv_freq):
@@ -81,7 +96,11 @@ class MsaRope:
         s.q_norm, s.k_norm = _ptr(self.q_norm), _ptr(self.k_norm)
         s.turns[:len(freq)] = msa_rope_turns(freq)
         s.axis[:len(freq)] = axis
-        self._at = ctypes.byref(s)
+        self._address = ctypes.addressof(s)
+        weights = [w.get_device() for w in (self.q_norm, self.k_norm) if w is not None]
+        if len(set(weights)) > 1:
+            _fail("q_norm and k_norm are on different devices")
+        self._device = weights[0] if weights else -1
 
 
 def _reach(t):
@@ -151,51 +170,28 @@ def _check_rope(fp4, rope, q, k, v, kv, q_scale, block_table, cu_q, cu_k, positi
 
 def _rope_write(name, fp4, rope, q, k, v, kv, q_scale, k_scale, v_scale, block_table, cu_q, cu_k,
                 positions, q_out, status, stream):
-    dev = -1
-    try:
-        shape, pool, table, (T, Hq, dim) = k.shape, kv.shape, block_table.shape, q.shape
-        ks, vs, qs = k.stride(), v.stride(), q.stride()
-        dev, type_, pos = kv.get_device(), k.dtype, positions
-        q_norm, k_norm, kv_type = rope.q_norm, rope.k_norm, kv.dtype
-        sound = (
-            type(rope) is MsaRope and (kv_type is _u8 or (kv_type is _e4m3 and not fp4))
-            and pool[2:] == (_PAGE4 if fp4 else _PAGE) and shape == (T, pool[1], dim) == v.shape
-            and dim == HEAD_DIM and len(table) == 2
-            and cu_q.shape == cu_k.shape == (table[0] + 1,)
-            and ks[2] == vs[2] == qs[2] == 1 and type_ in _TYPES
-            and type_ is v.dtype is q.dtype and cu_q.dtype is cu_k.dtype is block_table.dtype
-            is _int32 and kv.is_contiguous() and block_table.is_contiguous()
-            and cu_q.is_contiguous() and cu_k.is_contiguous()
-            and (pos is None or (pos.dtype is _int32 and _fits(pos.shape, rope.axes, T)
-                                 and pos.is_contiguous() and pos.get_device() == dev))
-            and q_out is None and status is None and dev >= 0
-            and (q_norm is None or q_norm.get_device() == dev)
-            and (k_norm is None or k_norm.get_device() == dev)
-            and dev == k.get_device() == v.get_device() == q.get_device()
-            == block_table.get_device() == cu_q.get_device() == cu_k.get_device() == _current())
-    except _NOT_SOUND:
-        sound = False
-    if not sound:
-        dev = _check_rope(fp4, rope, q, k, v, kv, q_scale, block_table, cu_q, cu_k, positions, q_out,
-                          status)
-    handle = _raw(dev) if stream is None else _handle(stream, dev)
-    if q is None:
-        shape, pool, table, type_ = k.shape, kv.shape, block_table.shape, k.dtype
-        ks, vs, qs, Hq = k.stride(), v.stride(), (0, 0), 0
-    elif q_out is None:
-        out = torch.bfloat16 if q_scale is None else _e4m3
-        q_out = (_empty((T, Hq, HEAD_DIM), dtype=out, device=_DEVICES[dev]) if stream is None
-                 else _new((T, Hq, HEAD_DIM), out, dev, handle))
-    lib = load()
-    rc = (lib.msa_rope_write_nvfp4 if fp4 else lib.msa_rope_write)(
-        rope._at, None if positions is None else positions.data_ptr(),
-        None if q is None else q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(),
-        vs[0], vs[1], _TYPES[type_], None if q is None else q_out.data_ptr(), q_scale is None,
-        1.0 if q_scale is None else q_scale, kv.data_ptr(), pool[0], k_scale, v_scale,
-        block_table.data_ptr(), table[1], cu_q.data_ptr(), cu_k.data_ptr(), table[0], shape[0], Hq,
-        pool[1], None if status is None else status.data_ptr(), handle)
-    if rc:
-        _check(rc, name)
+    if type(rope) is MsaRope and q_out is status is stream is None:
+        r = (_binding or load_binding()).rope_write(
+            rope._address, rope.axes, rope._device, fp4, q, k, v, kv, q_scale, k_scale, v_scale,
+            block_table, cu_q, cu_k, positions)
+        if r.__class__ is int:
+            _check(r, name)
+        if r is not None:
+            return r
+    dev = _check_rope(fp4, rope, q, k, v, kv, q_scale, block_table, cu_q, cu_k, positions, q_out,
+                      status)
+    T, Hkv, _ = k.shape
+    ks, vs, table, handle = k.stride(), v.stride(), block_table.shape, _handle(stream, dev)
+    Hq, qs = (0, (0, 0)) if q is None else (q.shape[1], q.stride())
+    if q is not None and q_out is None:
+        q_out = _new((T, Hq, HEAD_DIM), torch.bfloat16 if q_scale is None else torch.float8_e4m3fn,
+                     dev, handle)
+    _check(getattr(load(), name)(
+        rope._address, _ptr(positions), _ptr(q), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
+        v.data_ptr(), vs[0], vs[1], _TYPES[k.dtype], _ptr(q_out), q_scale is None,
+        1.0 if q_scale is None else q_scale, kv.data_ptr(), kv.shape[0], k_scale, v_scale,
+        block_table.data_ptr(), table[1], cu_q.data_ptr(), cu_k.data_ptr(), table[0], T, Hq, Hkv,
+        _ptr(status), handle), name)
     return q_out
 
 
@@ -257,42 +253,28 @@ def msa_tree_mask(parents, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, mask=None, 
     tensors are undefined.  status: an int32 [1] tensor that MSA_STATUS_* bits
     are OR-ed into; without it nothing tells of lengths that do not fit or of
     parents that are no earlier tokens (taken for -1)."""
+    if mask is positions is status is stream is None:
+        r = (_binding or load_binding()).tree_mask(parents, cu_seqlens_q, cu_seqlens_k,
+                                                   max_seqlen_q)
+        if r.__class__ is int:
+            _check(r, "msa_tree_mask")
+        if r is not None:
+            return r
     n = _tree_limit(max_seqlen_q)
     words = (n + 31) // 32
-    try:
-        (T,), (B1,), dev = parents.shape, cu_seqlens_q.shape, parents.get_device()
-        sound = (
-            parents.dtype is cu_seqlens_q.dtype is cu_seqlens_k.dtype is _int32 and B1 > 0
-            and cu_seqlens_k.shape == (B1,) and parents.is_contiguous()
-            and cu_seqlens_q.is_contiguous() and cu_seqlens_k.is_contiguous()
-            and mask is None and positions is None and status is None and dev >= 0
-            and dev == cu_seqlens_q.get_device() == cu_seqlens_k.get_device() == _current())
-    except _NOT_SOUND:
-        sound = False
-    if not sound:
-        _check_tree({"parents": parents}, cu_seqlens_q, cu_seqlens_k,
-                    {"mask": (mask, _WORD, (T, words)), "positions": (positions, _I32, (T,))}
-                    if parents is not None and parents.dim() == 1 else {}, status)
-        dev = _place(parents, cu_seqlens_q, cu_seqlens_k, mask, positions, status)
-        _apart({"mask": mask, "positions": positions},
-               {"parents": parents, "cu_seqlens_q": cu_seqlens_q, "cu_seqlens_k": cu_seqlens_k})
-    if stream is None:
-        handle, on = _raw(dev), _DEVICES[dev]
-        if mask is None:
-            mask = _empty((T, words), dtype=_int32, device=on)
-        if positions is None:
-            positions = _empty((T,), dtype=_int32, device=on)
-    else:
-        handle = _handle(stream, dev)
-        if mask is None:
-            mask = _new((T, words), _int32, dev, handle)
-        if positions is None:
-            positions = _new((T,), _int32, dev, handle)
-    rc = load().msa_tree_mask(parents.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(),
-                              B1 - 1, T, n, mask.data_ptr(), positions.data_ptr(),
-                              None if status is None else status.data_ptr(), handle)
-    if rc:
-        _check(rc, "msa_tree_mask")
+    T = parents.shape[0] if parents is not None and parents.dim() == 1 else 0
+    _check_tree({"parents": parents}, cu_seqlens_q, cu_seqlens_k,
+                {"mask": (mask, _WORD, (T, words)), "positions": (positions, _I32, (T,))}, status)
+    dev = _place(parents, cu_seqlens_q, cu_seqlens_k, mask, positions, status)
+    _apart({"mask": mask, "positions": positions},
+           {"parents": parents, "cu_seqlens_q": cu_seqlens_q, "cu_seqlens_k": cu_seqlens_k})
+    handle = _handle(stream, dev)
+    mask = _new((T, words), torch.int32, dev, handle) if mask is None else mask
+    positions = _new((T,), torch.int32, dev, handle) if positions is None else positions
+    _check(load().msa_tree_mask(parents.data_ptr(), cu_seqlens_q.data_ptr(),
+                                cu_seqlens_k.data_ptr(), cu_seqlens_q.shape[0] - 1, T, n,
+                                mask.data_ptr(), positions.data_ptr(), _ptr(status), handle),
+           "msa_tree_mask")
     return mask, positions
 
 
@@ -306,6 +288,14 @@ def msa_tree_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_ta
     these to those whose bits are set in its words of mask, int32 [T, at least
     ceil(max_seqlen_q / 32)] (msa_tree_mask's, or any others); max_seqlen_q at
     most 256.  A token that sees no key gets zeros and lse -inf."""
+    if workspace is out is lse is status is stream is None:
+        r = (_binding or load_binding()).tree_attention(
+            q, kv, q_scale, k_scale, v_scale, softmax_scale, block_table, cu_seqlens_q,
+            cu_seqlens_k, mask, prefix_pages, max_seqlen_q, max_seqlen_k, want_lse)
+        if r.__class__ is int:
+            _check(r, "msa_tree_attention")
+        if r is not None:
+            return r
     n = _tree_limit(max_seqlen_q)
     _tensor(mask, "mask", _WORD)
     shape = mask.shape
@@ -353,59 +343,28 @@ def _check_accept(fp4, drafts, parents, chosen, cu_q, cu_k, n, pools, table, tok
 
 def _accept(name, fp4, drafts, parents, chosen, cu_q, cu_k, max_q, kv, table, tokens, accepted,
             path, status, stream):
+    if tokens is accepted is path is status is stream is None:
+        r = (_binding or load_binding()).tree_accept(fp4, drafts, parents, chosen, cu_q, cu_k, max_q,
+                                                     kv, table)
+        if r.__class__ is int:
+            _check(r, name)
+        if r is not None:
+            return r
     n = _tree_limit(max_q)
     pools = _pools(kv)
-    L, dev, shape, at = len(pools), -1, (0, 0), None
-    try:
-        (T,), (B1,), dev = drafts.shape, cu_q.shape, drafts.get_device()
-        sound = (
-            drafts.dtype is parents.dtype is chosen.dtype is cu_q.dtype is cu_k.dtype is _int32
-            and B1 > 0 and parents.shape == chosen.shape == (T,) and cu_k.shape == (B1,)
-            and drafts.is_contiguous() and parents.is_contiguous() and chosen.is_contiguous()
-            and cu_q.is_contiguous() and cu_k.is_contiguous() and L <= TREE_MAX_LAYERS
-            and tokens is None and accepted is None and path is None and status is None
-            and dev >= 0 and dev == parents.get_device() == chosen.get_device()
-            == cu_q.get_device() == cu_k.get_device() == _current())
-        if sound and L:
-            # all pools alike: what they have in common is looked at once
-            (shape,), (type_,), (on,) = (set(map(_shape, pools)), set(map(_dtype, pools)),
-                                         set(map(_device, pools)))
-            sound = (
-                shape[2:] == (_PAGE4 if fp4 else _PAGE) and len(shape) == 4 and on == dev
-                and (type_ is _u8 or (type_ is _e4m3 and not fp4))
-                and all(map(_contiguous, pools)) and table.dtype is _int32 and table.dim() == 2
-                and table.shape[0] == B1 - 1 and table.is_contiguous()
-                and table.get_device() == dev)
-    except _NOT_SOUND:
-        sound = False
-    if not sound:
-        dev = _check_accept(fp4, drafts, parents, chosen, cu_q, cu_k, n, pools, table, tokens,
-                            accepted, path, status)
-        shape = pools[0].shape if L else shape
-    B = B1 - 1
-    if stream is None:
-        handle, on = _raw(dev), _DEVICES[dev]
-        if tokens is None:
-            tokens = _empty((B, n), dtype=_int32, device=on)
-        if accepted is None:
-            accepted = _empty((B,), dtype=_int32, device=on)
-        if path is None:
-            path = _empty((B, n), dtype=_int32, device=on)
-    else:
-        handle = _handle(stream, dev)
-        tokens = _new((B, n), _int32, dev, handle) if tokens is None else tokens
-        accepted = _new((B,), _int32, dev, handle) if accepted is None else accepted
-        path = _new((B, n), _int32, dev, handle) if path is None else path
-    if L:
-        at = array.array("Q", map(_data_ptr, pools))  # (kept until the call has read it)
-    lib = load()
-    rc = (lib.msa_tree_accept_nvfp4 if fp4 else lib.msa_tree_accept)(
+    dev = _check_accept(fp4, drafts, parents, chosen, cu_q, cu_k, n, pools, table, tokens, accepted,
+                        path, status)
+    B, L, handle = cu_q.shape[0] - 1, len(pools), _handle(stream, dev)
+    tokens = _new((B, n), torch.int32, dev, handle) if tokens is None else tokens
+    accepted = _new((B,), torch.int32, dev, handle) if accepted is None else accepted
+    path = _new((B, n), torch.int32, dev, handle) if path is None else path
+    at = (ctypes.c_void_p * max(L, 1))(*[p.data_ptr() for p in pools])
+    pages, Hkv = pools[0].shape[:2] if L else (0, 0)
+    _check(getattr(load(), name)(
         drafts.data_ptr(), parents.data_ptr(), chosen.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),
-        B, T, n, at.buffer_info()[0] if L else None, L, shape[0], shape[1],
-        table.data_ptr() if L else None, table.shape[1] if L else 0, tokens.data_ptr(),
-        accepted.data_ptr(), path.data_ptr(), None if status is None else status.data_ptr(), handle)
-    if rc:
-        _check(rc, name)
+        B, drafts.shape[0], n, ctypes.addressof(at), L, pages, Hkv, table.data_ptr() if L else None,
+        table.shape[1] if L else 0, tokens.data_ptr(), accepted.data_ptr(), path.data_ptr(),
+        _ptr(status), handle), name)
     return tokens, accepted, path
 
 
@@ -469,49 +428,31 @@ def msa_logprobs(logits, tokens=None, top=0, logprobs=None, ranks=None, entropy=
     None without tokens.  Of equal logits the lower index comes first.  A token
     outside [0, V) has -inf and rank -1; a row with a NaN has NaN, but for the
     tokens and ranks."""
+    if logprobs is ranks is entropy is top_tokens is top_logprobs is stream is None:
+        r = (_binding or load_binding()).logprobs(logits, tokens, top)
+        if r.__class__ is int:
+            _check(r, "msa_logprobs")
+        if r is not None:
+            return r
     if not 0 <= top <= LOGPROBS_MAX_TOP:
         _fail("top must be 0 .. %d, got %d", LOGPROBS_MAX_TOP, top)
-    dev = -1
-    try:
-        (T, V), (row, one), dev, type_ = (logits.shape, logits.stride(), logits.get_device(),
-                                          logits.dtype)
-        sound = (
-            type_ in _TYPES and (one == 1 or V == 1)
-            and (tokens is None or (tokens.dtype is _int32 and tokens.shape == (T,)
-                                    and tokens.is_contiguous() and tokens.get_device() == dev))
-            and logprobs is None and ranks is None and entropy is None and top_tokens is None
-            and top_logprobs is None and dev >= 0 and dev == _current())
-    except _NOT_SOUND:
-        sound = False
-    if not sound:
-        dev = _check_logprobs(logits, tokens, top,
-                              {"logprobs": logprobs, "ranks": ranks, "entropy": entropy,
-                               "top_tokens": top_tokens, "top_logprobs": top_logprobs})
-    given = tokens is not None
-    if stream is None and sound:
-        handle, on = _raw(dev), _DEVICES[dev]
-        if given:
-            logprobs = _empty((T,), dtype=_float32, device=on)
-            ranks = _empty((T,), dtype=_int32, device=on)
-        entropy = _empty((T,), dtype=_float32, device=on)
-        top_tokens = _empty((T, top), dtype=_int32, device=on)
-        top_logprobs = _empty((T, top), dtype=_float32, device=on)
-    else:
-        handle = _handle(stream, dev)
-        if given and logprobs is None:
-            logprobs = _new((T,), _float32, dev, handle)
-        if given and ranks is None:
-            ranks = _new((T,), _int32, dev, handle)
-        if entropy is None:
-            entropy = _new((T,), _float32, dev, handle)
-        if top_tokens is None:
-            top_tokens = _new((T, top), _int32, dev, handle)
-        if top_logprobs is None:
-            top_logprobs = _new((T, top), _float32, dev, handle)
-    rc = load().msa_logprobs(
-        logits.data_ptr(), row, _TYPES[type_], tokens.data_ptr() if given else None, T, V, top,
-        logprobs.data_ptr() if given else None, ranks.data_ptr() if given else None,
-        entropy.data_ptr(), top_tokens.data_ptr(), top_logprobs.data_ptr(), handle)
-    if rc:
-        _check(rc, "msa_logprobs")
+    top = int(top)
+    dev = _check_logprobs(logits, tokens, top,
+                          {"logprobs": logprobs, "ranks": ranks, "entropy": entropy,
+                           "top_tokens": top_tokens, "top_logprobs": top_logprobs})
+    T, V = logits.shape
+    handle = _handle(stream, dev)
+
+    def new(t, shape, dtype):
+        return _new(shape, dtype, dev, handle) if t is None else t
+
+    if tokens is not None:
+        logprobs, ranks = new(logprobs, (T,), torch.float32), new(ranks, (T,), torch.int32)
+    entropy = new(entropy, (T,), torch.float32)
+    top_tokens = new(top_tokens, (T, top), torch.int32)
+    top_logprobs = new(top_logprobs, (T, top), torch.float32)
+    _check(load().msa_logprobs(
+        logits.data_ptr(), logits.stride(0), _TYPES[logits.dtype], _ptr(tokens), T, V, top,
+        _ptr(logprobs), _ptr(ranks), entropy.data_ptr(), top_tokens.data_ptr(),
+        top_logprobs.data_ptr(), handle), "msa_logprobs")
     return logprobs, ranks, entropy, top_tokens, top_logprobs

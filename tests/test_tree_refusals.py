@@ -59,12 +59,14 @@ def test_rope_refusals():
 def test_rope_library_refusals():
     lib, P = msa.load(), ctypes.c_void_p
     a = P(4096)  # never dereferenced: every call below ends on the host
+    keep = []
 
     def struct(pairs=2, axes=1, eps=1e-6, axis=0, norm=None):
         s = msa.MsaRopeStruct()
         s.pairs, s.axes, s.eps, s.q_norm = pairs, axes, eps, norm
         s.axis[1] = axis
-        return ctypes.byref(s)
+        keep.append(s)
+        return ctypes.addressof(s)
 
     def run(rope=struct(), pos=None, q=a, qt=512, qh=128, k=a, dtype=1, out=a, bf16=0, qs=1.0, kv=a, pages=4, s=1.0, table=a, width=3, cu=a, cu_k=a, B=2, T=6,
             Hq=4, H=2, status=None, fn=lib.msa_rope_write):
@@ -224,8 +226,6 @@ def test_tree_library_refusals():
 
 
 def test_tensors_of_another_device_are_refused(monkeypatch):
-    from block_sparse_attention_prefill_gb300 import tree
-
     class Other(torch.Tensor):
         def get_device(self):
             return 3
@@ -235,7 +235,6 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     u8 = lambda *s: on(torch.zeros(s, dtype=torch.uint8))  # noqa: E731
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(tree, "_current", lambda: 0)
     kv = u8(4, 2, 128, 256)
     x = on(torch.zeros((6, 2, 128)))
     for call in (lambda: msa.msa_rope_write(msa.MsaRope([1.0]), x, x, x, kv, 1.0, 1.0, 1.0, z(2, 3), z(3), z(3)),
