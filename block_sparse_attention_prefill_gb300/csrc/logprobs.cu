@@ -22,8 +22,8 @@
 // 131072 bf16, 5 best: 112 us, 4.8 TB/s; without tokens and best 87 (6.2 TB/s).
 // Ranks cost a packed comparison and a sum for every two values (14 us), the
 // selection about 4 us a row and CTA, in which its warps load little (12 us).
-// 16 rows of 200003 fp32, 20 best: 11.5 us, latency (the pass 6, bound and
-// selection 3, exchange and merge of the cluster 2.5).
+// 16 rows of 200003 fp32, 20 best: 10.1 us, latency (the pass 5, bound and
+// selection 2.5, exchange and merge of the cluster 2.5).
 //
 // A cluster of 1 to 8 CTAs takes a row (as many as fill the GPU when there are
 // few rows): each finds its own k best, and the first merges them through
@@ -44,7 +44,6 @@ namespace cg = cooperative_groups;
 namespace msa {
 namespace {
 
-constexpr int kMaxWarps = 8;     // of a CTA
 constexpr int kMaxCluster = 8;
 constexpr int kTop = MSA_LOGPROBS_MAX_TOP;
 constexpr int kVocabBits = 19;   // V < 2^19
@@ -275,9 +274,10 @@ struct Part {  // of a warp
 // kBatch: chunks of a warp that are worked on together, with as many more in
 // flight: 4 with 24 warps an SM (80 registers a thread), 2 with 32.
 constexpr int warps_of_sm(int batch) { return batch == 4 ? 24 : 32; }
+constexpr int ctas_of_sm(int warps, int batch) { return warps_of_sm(batch) / warps; }
 
 template <typename T, int kWarps, int kBatch>
-__global__ void __launch_bounds__(kWarps * 32, warps_of_sm(kBatch) / kWarps)
+__global__ void __launch_bounds__(kWarps * 32, ctas_of_sm(kWarps, kBatch))
 logprobs_kernel(const LogprobsArgs a, int cluster_size) {
   using V = Vec<T>;
   constexpr int N = V::N, kThreads = kWarps * 32;
@@ -601,18 +601,28 @@ logprobs_kernel(const LogprobsArgs a, int cluster_size) {
     __syncthreads();
   }
   // every warp merges the sums for itself
-  const int parts = cluster_size * kWarps;  // at most 64
-  const Part none = {kLowest, kLowest, 0.f, 0.f, 0};
-  const Part u = lane < parts ? s_part[lane] : none, v = lane + 32 < parts ? s_part[lane + 32] : none;
-  const float m = warp_max(largest(u.m, v.m)), ref = m * kLog2e;
+  const int parts = cluster_size * kWarps;
+  constexpr int kParts = kMaxCluster * kWarps / 32;  // of a lane
+  Part part[kParts];
+  float m = kLowest;
+  int before = 0;
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) {
+    part[i] = {kLowest, kLowest, 0.f, 0.f, 0};
+    if (lane + 32 * i < parts) part[i] = s_part[lane + 32 * i];
+    m = largest(m, part[i].m);
+    before += part[i].before;
+  }
+  m = warp_max(m);
+  const float ref = m * kLog2e;
   float l = 0.f, s = 0.f;
-  int before = u.before + v.before;
   auto join = [&](const Part& q) {
     const float d = max_or_nan(huge(m) ? (q.m - m) * kLog2e : q.r - ref, kFar), f = ex2_approx(d);
     l += f * q.l;
     s += f * fmaf(q.l, d, q.s);
   };
-  join(u), join(v);
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) join(part[i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -638,31 +648,23 @@ logprobs_kernel(const LogprobsArgs a, int cluster_size) {
     if (tid < k) put(tid, s_best[tid]);
     return;
   }
-  // A candidate's place among all is the sum of its places in the CTAs' lists:
-  // a thread looks for one candidate in one list, by bisection.
-  const int most = cluster_size * k;
-  int* s_place = reinterpret_cast<int*>(s_cand);  // (no longer needed)
-  for (int c = tid; c < most; c += kThreads) s_place[c] = 0;
-  __syncthreads();
-  for (int w = tid; w < most * cluster_size; w += kThreads) {
-    const int in = w / most, c = w - in * most, of = c / k;
-    const uint64_t key = s_all[of][c - of * k];
-    int place = 0;
+  // Two lists in order at a time into one, by a warp: of the first's i-th and the
+  // second's i-th from the end the larger ones are the 32 best, first ascending
+  // or descending and then the other way, and five exchanges put them in order.
+  for (int lists = cluster_size / 2; lists > 0; lists /= 2) {
+    if (warp < lists) {
+      const uint64_t one = s_all[warp][lane], other = s_all[warp + lists][kTop - 1 - lane];
+      uint64_t key = one > other ? one : other;
 #pragma unroll
-    for (int step = kTop / 2; step > 0; step /= 2)
-      if (s_all[in][place + step - 1] > key) place += step;
-    place += s_all[in][place] > key;
-    if (place) atomicAdd(&s_place[c], place);
+      for (int o = kTop / 2; o > 0; o /= 2) {
+        const uint64_t far = __shfl_xor_sync(0xffffffffu, key, o);
+        key = ((lane & o) == 0) == (key > far) ? key : far;
+      }
+      s_all[warp][lane] = key;
+      if (lists == 1 && lane < k) put(lane, key);
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  int some = 0;
-  for (int c0 = 0; c0 < most; c0 += kThreads) {
-    const int c = c0 + tid, of = c / k;
-    const uint64_t key = c < most ? s_all[of][c - of * k] : 0;
-    if (key && s_place[c] < k) put(s_place[c], key);
-    some += __syncthreads_count(key != 0);
-  }
-  if (tid >= some && tid < k) put(tid, 0);  // fewer than k values
 }
 
 template <typename T, int kWarps, int kBatch>
@@ -696,7 +698,13 @@ cudaError_t launch_type(const LogprobsArgs& a, cudaStream_t stream) {
   // but 2048 of 131072: 122 and 117; 456 of 131072: 35 and 29)
   if (a.T >= (int64_t)num_sms() * (warps_of_sm(2) / 4) && chunks <= 256)
     return launch_as<T, 4, 2>(a, c, chunks, stream);
-  return launch_as<T, kMaxWarps, 4>(a, c, chunks, stream);
+  // Few long rows: twice the warps a CTA, for the bytes in flight, as long as all
+  // clusters find room at one CTA an SM (20 best of 200003 fp32: 8 or 12 rows
+  // 8.1 us, with 8 warps 9.2 and 9.7; but 16 rows, whose clusters of 8 do not all
+  // fit at once, 13.5 and 10.1)
+  if (a.T * c * 3 <= (int64_t)num_sms() * 2 && chunks >= 64 * c)
+    return launch_as<T, 16, 4>(a, c, chunks, stream);
+  return launch_as<T, 8, 4>(a, c, chunks, stream);
 }
 
 }  // namespace
