@@ -116,8 +116,13 @@ __device__ __forceinline__ int rate_of(int tokens, int C) {
 // Pages of a tile in front of cost y of its own.
 __device__ __forceinline__ int pages_before(int64_t y, int npages, int rate) {
   if (y <= kCostTile) return 0;
-  const int64_t p = (y - kCostTile + rate - 1) / rate;
+  static_assert(kCostSolo == 2 && kCostPair == 4, "rates are powers of 2");
+  const int64_t p = (y - kCostTile + rate - 1) >> (rate == kCostPair ? 2 : 1);
   return p < npages ? (int)p : npages;
+}
+// a / b of numbers >= 0 (64-bit divisions are slow, and costs rarely need them)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 31) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 __device__ __forceinline__ int64_t share_of(int64_t total, int ctas) {
   const int64_t s = total <= INT_MAX - ctas ? ((int)total + ctas - 1) / ctas
@@ -199,22 +204,27 @@ struct PlanParams {
 
 // Lists the tiles of one head (every head has the same): first those over the
 // shared pages, then each request's own.  Run by a whole CTA; req is room for
-// B ints that it can see.  Every thread gets the plan's head.
+// B ints that it can see.  Every thread gets the plan's head and, if there is
+// one round of tiles, in `mine` its own tile, of cost `mine_cost` (else 0).
 template <int kThreads, bool kTree>
-__device__ __forceinline__ PlanHead make_plan(const PlanParams& p, int* req) {
+__device__ __forceinline__ PlanHead make_plan(const PlanParams& p, int* req, Tile* mine, int* mine_cost) {
   __shared__ int s_bad, s_first, s_rate;
   const int tid = threadIdx.x;
+  // all loads of the first round at once
+  const int T = p.cu_q[p.B], first = p.cu_q[0];
+  int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+  if (tid < p.B) q0 = p.cu_q[tid], q1 = p.cu_q[tid + 1], k0 = p.cu_k[tid], k1 = p.cu_k[tid + 1];
   if (tid == 0) s_bad = 0, s_first = INT_MAX, s_rate = 0;
+  *mine_cost = 0;
   __syncthreads();
-  const int T = p.cu_q[p.B];
-  bool bad = p.cu_q[0] != 0 || T < 0 || T > p.T;
+  bool bad = first != 0 || T < 0 || T > p.T;
   int run = 0;  // tiles of the requests before this round's
   for (int b0 = 0; b0 < p.B; b0 += kThreads) {
     const int b = b0 + tid;
     int n = 0;
     if (b < p.B) {
-      const int64_t q = (int64_t)p.cu_q[b + 1] - p.cu_q[b];
-      const int64_t k = (int64_t)p.cu_k[b + 1] - p.cu_k[b];
+      if (b0 > 0) q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
+      const int64_t q = (int64_t)q1 - q0, k = (int64_t)k1 - k0;
       if (q < 0 || k < q || q > p.max_q || k > p.max_k ||
           (q > 0 && k - q < (int64_t)p.prefix * kPage))
         bad = true;
@@ -284,6 +294,7 @@ __device__ __forceinline__ PlanHead make_plan(const PlanParams& p, int* req) {
     cost += total;
     if (i < ntiles)
       p.tiles[i < shared_tiles ? i : p.own_base + i - shared_tiles] = t;
+    if (ntiles <= kThreads) *mine = t, *mine_cost = c;
   }
   const PlanHead hd = {ntiles, cost, shared_tiles, 0, T, {0, 0, 0}};
   if (tid == 0) *p.head = hd;
@@ -294,7 +305,9 @@ template <bool kTree>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
   pdl_wait();
   pdl_trigger();
-  make_plan<kPlanThreads, kTree>(p, p.req);
+  Tile mine;
+  int mine_cost;
+  make_plan<kPlanThreads, kTree>(p, p.req, &mine, &mine_cost);
 }
 
 // ------------------------------------------------------------------ attend
@@ -320,7 +333,8 @@ struct Bars {
   uint64_t mma_done[3];
   uint32_t tmem_base;
   int abort;
-  int first_tile;
+  int first_tile;  // that the CTA's range starts in
+  Tile first;
   float2 ml[2][128];  // a solo part's m and l by stream and row
   // whether a ring position's page is one, by the producer; kHasNan too where a
   // NaN lies among the V codes of its keys and not every row sees it whole
@@ -371,14 +385,14 @@ struct Walk {
   Tile t, ahead;
   int p0, p1;        // pages of the tile in this range
   int cur_h, cur_tile;
-  __device__ Walk(const AttendParams& prm, const PlanHead& hd, int first_tile)
-      : p(prm), ntiles(hd.ntiles), shared_tiles(hd.shared_tiles), tile(first_tile) {
+  __device__ Walk(const AttendParams& prm, const PlanHead& hd, const Bars& bars)
+      : p(prm), ntiles(hd.ntiles), shared_tiles(hd.shared_tiles), tile(bars.first_tile) {
     const int64_t total = (int64_t)hd.cost * p.Hkv, share = share_of(total, gridDim.x);
     const int64_t x = blockIdx.x * share;
     left = x < total ? (int)min(share, total - x) : 0;
-    h = left > 0 ? (int)(x / hd.cost) : 0;
+    h = left > 0 ? (int)quotient(x, hd.cost) : 0;
     if (left > 0) {
-      ahead = tile_at(tile);
+      ahead = bars.first;
       at = (int)(x - (int64_t)h * hd.cost - ahead.start);
     }
   }
@@ -517,8 +531,9 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
     mbar_init(&bars->read, 256);
     for (int i = 0; i < 3; ++i) mbar_init(&bars->mma_done[i], 1);
     bars->abort = 0;
-    bars->first_tile = 0;
     fence_mbar_init();
+    prefetch_tensormap(&kv_map);
+    prefetch_tensormap(&q_map);
   }
   if (warp == 1) {
     __syncwarp();
@@ -538,29 +553,36 @@ attend_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant_
   // round of this CTA's threads, here: the CTAs write the same values to the
   // same places, and each reads what it has written itself.
   PlanHead hd;
+  Tile mine;
+  int mine_cost = 0;
   if (p.plan_here)
-    hd = make_plan<kThreads, kTree>(p.plan, reinterpret_cast<int*>(smem + kOffW));
+    hd = make_plan<kThreads, kTree>(p.plan, reinterpret_cast<int*>(smem + kOffW), &mine, &mine_cost);
   else
     hd = *p.plan.head;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = bars->tmem_base;
   // the tile that this CTA's range starts in
   {
     const int64_t total = (int64_t)hd.cost * p.Hkv;
     const int64_t x = blockIdx.x * share_of(total, gridDim.x);
     if (x < total) {
-      const uint32_t r = (uint32_t)(x % hd.cost);
-      auto start = [&](int i) {
-        return p.tiles[i < hd.shared_tiles ? i : p.own_base + i - hd.shared_tiles].start;
-      };
-      for (int i = tid; i < hd.ntiles; i += kThreads)
-        if (start(i) <= r && (i + 1 == hd.ntiles || start(i + 1) > r)) bars->first_tile = i;
+      const uint32_t r = (uint32_t)(x - quotient(x, hd.cost) * hd.cost);
+      if (p.plan_here) {
+        if (mine.start <= r && r - mine.start < (uint32_t)mine_cost)
+          bars->first_tile = tid, bars->first = mine;
+      } else {
+        auto tile = [&](int i) -> const Tile& {
+          return p.tiles[i < hd.shared_tiles ? i : p.own_base + i - hd.shared_tiles];
+        };
+        for (int i = tid; i < hd.ntiles; i += kThreads)
+          if (tile(i).start <= r && (i + 1 == hd.ntiles || tile(i + 1).start > r))
+            bars->first_tile = i, bars->first = tile(i);
+      }
     }
   }
+  tc_fence_before();
   __syncthreads();
-  Walk walk(p, hd, bars->first_tile);
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  Walk walk(p, hd, *bars);
 
   if (warp >= 4 && warp < 12) {
     setmaxnreg_inc<kRegsSoftmax>();
@@ -1159,10 +1181,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
       const int64_t share = share_of((int64_t)hd.cost * p.Hkv, p.ctas);
       const int64_t t0 = (int64_t)h * hd.cost + t.start;
       const int64_t t1 = t0 + tile_cost(t.ntok, t.npages, p.C);
-      // (64-bit divisions are slow; costs rarely need them)
-      const bool small = t1 <= INT_MAX && share <= INT_MAX;
-      const int i0 = small ? (int)t0 / (int)share : (int)(t0 / share);
-      const int i1 = small ? (int)(t1 - 1) / (int)share : (int)((t1 - 1) / share);
+      const int i0 = (int)quotient(t0, share), i1 = (int)quotient(t1 - 1, share);
       for (int c0 = i0; c0 <= i1; c0 += 32) {
         const int cta = c0 + lane;
         int pa = 0, pb = 0;

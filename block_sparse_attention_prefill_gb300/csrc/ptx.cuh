@@ -130,6 +130,11 @@ __device__ __forceinline__ bool bounded_wait_long(uint64_t* bar, uint32_t parity
 
 // ---------------------------------------------------------------- TMA
 
+// Fetches a tensor map (a __grid_constant__ parameter) ahead of its first copy.
+__device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // 2-D tiled bulk tensor load global -> shared, completion counted in bytes
 // on `bar`.  x is the innermost (byte) coordinate and must be a multiple of
 // 16; y is the row.
