@@ -183,7 +183,7 @@ PyObject* tree_mask(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // cu_seqlens_k, mask, prefix_pages, max_seqlen_q, max_seqlen_k, want_lse)
 PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    if (n != 14) Py_RETURN_NONE;
+    if (n != 14 || !PyBool_Check(a[13])) Py_RETURN_NONE;
     const at::Tensor *q = tensor(a[0]), *kv = tensor(a[1]), *table = tensor(a[6]), *cu_q = tensor(a[7]);
     const at::Tensor *cu_k = tensor(a[8]), *mask = tensor(a[9]);
     double scale[4];
