@@ -3,6 +3,8 @@
 Argument marshalling only.  Every step of the computation runs in the CUDA
 kernels of ``libmsa.so`` (see ``include/msa.h`` for the C ABI); PyTorch is
 used here for device memory (tensors, workspaces) and the current stream.
+Calls go through ctypes, the usual form of the tree calls through the
+compiled module of ``csrc/binding.cpp``.
 There is no fallback: if the library cannot be built or loaded, every call
 raises.
 

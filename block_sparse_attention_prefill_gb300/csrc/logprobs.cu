@@ -26,9 +26,10 @@
 // selection 2.5, exchange and merge of the cluster 2.5).
 //
 // A cluster of 1 to 8 CTAs takes a row (as many as fill the GPU when there are
-// few rows): each finds its own k best, and the first merges them through
-// distributed shared memory.  Rows may start anywhere: whole 16-byte vectors
-// are loaded, the first and last of a row value by value.
+// few rows): each finds its own k best and hands them to the first through
+// distributed shared memory, whose warps merge them by twos (bitonic merges).
+// Rows may start anywhere: whole 16-byte vectors are loaded, the first and last
+// of a row value by value.
 #include <algorithm>
 #include <cfloat>
 #include <cooperative_groups.h>

@@ -45,8 +45,8 @@
 // 5.2 TB/s.  16 single tokens over 32k shared keys: 21.7 us, latency (plan
 // and first loads 4, 6 units 5, epilogue 3, combine 5 us).
 // Trees: 32 of 33-64 tokens over 32k shared keys 278 us, 1.48 PFLOP/s; 16 of 24
-// over 83k keys of their own each 219 us, 1.19 (192 of a pair's 256 rows are
-// used); 4 of 16 over 12k each 20.1 us, latency.
+// over 83k keys of their own each 218 us, 1.19 (192 of a pair's 256 rows are
+// used); 4 of 16 over 12k each 19.9 us, latency.
 #include <cuda.h>
 
 #include <algorithm>
