@@ -24,7 +24,7 @@
 // bytes and exchanges between lanes: 243 us instead of 180).
 //
 // Measured (GPU time, replayed from a graph): 59 k tokens x (32 + 2 x 4) heads
-// bf16 -> E4M3 162 us, 5.6 TB/s; 512 tokens x (16 + 2 x 2) heads 6.1 us, of which
+// bf16 -> E4M3 163 us, 5.6 TB/s; 512 tokens x (16 + 2 x 2) heads 6.1 us, of which
 // the launch, the look-up's dependent loads and the angles are most.
 #include <algorithm>
 #include <cfloat>
@@ -43,8 +43,8 @@ namespace {
 constexpr int kRopeThreads = 128, kRopeWarps = kRopeThreads / 32;
 constexpr int kStaged = 512;  // requests whose lengths a CTA keeps in shared memory
 // Rows of a slot in flight, and CTAs an SM, by the registers that a format needs
-// (8 chunks of 8k tokens to E4M3: 162 us, by 4 and 4: 170; 10 k tokens to NVFP4
-// and back 28.9 us, by 3 and 5: 30.3)
+// (before rounds were told apart, see launch_type: 8 chunks of 8k tokens to E4M3
+// 162 us, by 4 and 4: 170; 10 k tokens to NVFP4 and back 28.9 us, by 3 and 5: 30.3)
 constexpr int in_flight(bool fp4) { return fp4 ? 4 : 3; }
 constexpr int ctas_of_sm(bool fp4) { return fp4 ? 4 : 5; }
 
@@ -60,8 +60,11 @@ struct RopeParams {
   float q_inverse, k_inverse;
   Recip v;
   float k6, v6;   // 6 g, NVFP4
-  int chunks;     // of a token's rows
-  int run;        // rows of a chunk
+  struct Part {   // CTAs of one kind, from the first on
+    int cta, group;  // first CTA and group of a warp's tokens
+    int chunks;      // of a token's rows
+    int run;         // rows of a chunk
+  } part[2];
   bool q_wide, kv_wide;  // rows lie on 32 bytes
 };
 
@@ -100,14 +103,15 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopePara
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (the same for all lanes)
   // a warp takes kTokens tokens and a run of their heads: its rows are all of Q,
   // all of K or all of V at a time
-  const int64_t unit0 = (int64_t)blockIdx.x * kRopeWarps, unit = unit0 + warp;
-  const int64_t t0 = unit0 / p.chunks * kTokens, group = unit / p.chunks;
+  const RopeParams::Part& m = p.part[(int)blockIdx.x >= p.part[1].cta];
+  const int64_t unit0 = (int64_t)((int)blockIdx.x - m.cta) * kRopeWarps, unit = unit0 + warp;
+  const int64_t t0 = (m.group + unit0 / m.chunks) * kTokens, group = m.group + unit / m.chunks;
   const int slot = lane / kLanes, cc = lane % kLanes;
   const int64_t t = group * kTokens + slot;
   const int i = (int)(t - t0);  // the token within the CTA's
   const int k0 = a.Hq, v0 = a.Hq + a.Hkv, rows = v0 + a.Hkv;  // first rows of K and V
-  const int r_first = (int)(unit - group * p.chunks) * p.run;
-  const int r_end = group * kTokens < a.T ? min(rows, r_first + p.run) : r_first;
+  const int r_first = (int)(unit - (group - m.group) * m.chunks) * m.run;
+  const int r_end = group * kTokens < a.T ? min(rows, r_first + m.run) : r_first;
   const bool in_batch = t < a.T;
   // the first values of the lane's pieces
   const int turned = a.pairs / kPiece;  // (kSplit) lanes with pairs
@@ -405,18 +409,22 @@ cudaError_t launch_type(const RopeArgs& a, cudaStream_t stream) {
   p.k_inverse = std::min(1.f / a.k_scale, FLT_MAX);
   p.v = recip_of(a.v_scale);
   p.k6 = 6.f * a.k_scale, p.v6 = 6.f * a.v_scale;
-  // rows of a slot: all of a token's where there are tokens for every CTA
-  const int64_t warps = (int64_t)num_sms() * ctas_of_sm(kFp4) * kRopeWarps;
-  const int64_t run = std::min<int64_t>(rows, ceil_div(groups * rows, warps));
-  p.chunks = (int)ceil_div(rows, run);
-  p.run = (int)ceil_div(rows, p.chunks);
+  // Whole rounds of the GPU's places take all rows of their tokens; the tokens of
+  // the last round share its places, so that it is one round (16 k tokens x (32 +
+  // 2 x 8) heads to E4M3, 1.35 rounds: 78 us, by one chunk a token 89; 4096
+  // tokens, 0.34: 28, by chunks that come to just over one round 34).
+  const int64_t places = (int64_t)num_sms() * ctas_of_sm(kFp4) * kRopeWarps;
+  const int64_t whole = groups / places * places, rest = groups - whole;
+  const int run = (int)ceil_div(rows, std::min(rows, rest > 0 ? places / rest : 1));
+  p.part[0] = {0, 0, 1, (int)rows};
+  p.part[1] = {(int)(whole / kRopeWarps), (int)whole, (int)ceil_div(rows, run), run};
   const int64_t es = sizeof(T);
   auto on32 = [&](const void* x, int64_t token, int64_t head) {
     return reinterpret_cast<uintptr_t>(x) % 32 == 0 && token * es % 32 == 0 && head * es % 32 == 0;
   };
   p.q_wide = on32(a.q, a.q_token, a.q_head);
   p.kv_wide = on32(a.k, a.k_token, a.k_head) && on32(a.v, a.v_token, a.v_head);
-  const int64_t grid = ceil_div(groups * p.chunks, kRopeWarps);
+  const int64_t grid = p.part[1].cta + ceil_div(rest * p.part[1].chunks, kRopeWarps);
   auto run_it = [&](auto kernel) {
     return launch_pdl(kernel, dim3((unsigned)grid), dim3(kRopeThreads), 0, stream, a, p);
   };

@@ -222,3 +222,45 @@ def test_graph_and_other_stream():
     s.kv.fill_(0x5A)
     graph.replay()
     assert torch.equal(out.view(torch.uint8), want.view(torch.uint8)) and torch.equal(s.kv, pool)
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rounds_of_ctas(dtype, fp4):
+    """Numbers of tokens around whole rounds of the GPU's places, whose last round is split another way: the same bytes as in small calls."""
+    tokens = torch.cuda.get_device_properties(0).multi_processor_count * 4 * (4 if fp4 else 5) * (2 if dtype == torch.float32 else 4)
+    heads, most = (3, 2), 2 * tokens + tokens // 3 + 1
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    x = torch.randn((most, heads[0] + 2 * heads[1], 128), generator=g, device="cuda").to(dtype)
+    q, k, v = x[:, :3], x[:, 3:5], x[:, 5:]
+    pages = -(-most // 128)
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)[None]
+    rope = msa.MsaRope([0.8 ** j for j in range(64)], q_norm=torch.rand(128, generator=g, device="cuda"), k_norm=torch.rand(128, generator=g, device="cuda"))
+    write = msa.msa_rope_write_nvfp4 if fp4 else msa.msa_rope_write
+    new = lambda: torch.zeros((pages, 2, 2, 9216) if fp4 else (pages, 2, 128, 256), dtype=torch.uint8, device="cuda")  # noqa: E731
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    pool, parts = new(), []
+    for a in range(0, most, 1000):
+        b = min(a + 1000, most)
+        parts.append(write(rope, q[a:b], k[a:b], v[a:b], pool, QS, KS, VS, table, i32([0, b - a]), i32([0, b])))
+    parts = torch.cat(parts).view(torch.uint8)
+    for T in (tokens // 7 + 1, tokens // 2 + 2, tokens - 1, tokens, tokens + 1, tokens + tokens // 2, 2 * tokens - 3, most):
+        got, status = new(), i32([0])
+        out = write(rope, q[:T], k[:T], v[:T], got, QS, KS, VS, table, i32([0, T]), i32([0, T]), status=status)
+        assert status.item() == 0 and torch.equal(out.view(torch.uint8), parts[:T])
+        want = pool.clone()
+        if T < most:  # rows behind the last stay as they were
+            page, off = T // 128, T % 128
+            keep = table[0, :page].long()
+            clean = new()
+            clean[keep] = pool[keep]
+            if off:
+                last = int(table[0, page])
+                if fp4:
+                    clean[last, :, :, :off * 64] = pool[last, :, :, :off * 64]
+                    clean[last, :, :, 8192:8192 + off * 8] = pool[last, :, :, 8192:8192 + off * 8]
+                else:
+                    clean[last, :, :off] = pool[last, :, :off]
+            want = clean
+        assert torch.equal(got, want)
