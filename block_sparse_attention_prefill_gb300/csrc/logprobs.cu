@@ -19,7 +19,7 @@
 // the work is bounded whatever the row holds.
 //
 // Bounds and what was measured (GPU time, replayed from a graph): 2048 rows of
-// 131072 bf16, 5 best: 112 us, 4.8 TB/s; without tokens and best 87 (6.2 TB/s).
+// 131072 bf16, 5 best: 111 us, 4.8 TB/s; without tokens and best 87 (6.2 TB/s).
 // Ranks cost a packed comparison and a sum for every two values (14 us), the
 // selection about 4 us a row and CTA, in which its warps load little (12 us).
 // 16 rows of 200003 fp32, 20 best: 10.1 us, latency (the pass 5, bound and
@@ -32,6 +32,7 @@
 // of a row value by value.
 #include <algorithm>
 #include <cfloat>
+#include <cmath>
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -688,24 +689,51 @@ cudaError_t launch_as(const LogprobsArgs& a, int cluster, int64_t chunks, cudaSt
 
 template <typename T>
 cudaError_t launch_type(const LogprobsArgs& a, cudaStream_t stream) {
-  // CTAs of a row: as many as stay at three an SM, each with 16 chunks or more
-  // (64 rows of 131072 bf16 by clusters of 4, 256 CTAs: 13 us; by 8, in two
-  // waves: 20)
+  // Which CTAs and how many a row: the least of an estimate in microseconds.  A
+  // round of CTAs takes what is fixed (launch, selection, outputs: 6, half a one
+  // more in clusters, up to `crowd` more where an SM has all its CTAs; later
+  // rounds' half overlaps the rows still read) and its share of the bytes at
+  // 6 TB/s, of a round that is not full at least `least`.
+  // 10 best, measured (and estimated), with 16, 8 or 4 warps a CTA x CTAs a row:
+  //   131072 bf16:   64 rows 16x2 9.9 (10), 8x4 10.5 (11), 4x8 10.9
+  //     190 rows 8x2 17.0 (17), 8x1 18.8 (19); 304 rows 8x1 19.7 (23), 16x1 23.1
+  //     512 rows 4x2 35.2 (34), 8x1 40.6 (40), 4x1 45.7 (42)
+  //     912 rows 8x1 53.8 (51), 4x1 55.0 (54); 1024 rows 4x1 60.0 (58), 8x1 64.1 (65)
+  //    1500 rows 8x1 86.6 (90), 4x1 95.8 (94); 2048 rows 4x1 111 (110), 8x1 115 (116)
+  //   32000 bf16: 152 rows 16x1 7.9 (8), 8x1 8.4 (9); 512 rows 4x1 13.7 (16), 8x1 16.8 (18)
+  //   200003 fp32: 12 rows 16x8 7.9 (11), 8x8 9.2 (11); 16 rows 8x8 9.8 (11), 16x8, whose
+  //     clusters do not all find room at once, 13.2; 100 rows 8x4 18.6 (22), 16x1 19.4 (25)
   const int64_t chunks = ceil_div((int64_t)a.V * sizeof(T), 512) + 1;
-  int c = kMaxCluster;
-  while (c > 1 && (a.T * c > (int64_t)num_sms() * 3 || chunks < 16 * c)) c /= 2;
-  // Many short rows: more CTAs of half the warps, whose selections overlap more
-  // rows' loads (5 best, 8192 rows of 32000 bf16: 133 us, with 8 warps about 200;
-  // but 2048 of 131072: 122 and 117; 456 of 131072: 35 and 29)
-  if (a.T >= (int64_t)num_sms() * (warps_of_sm(2) / 4) && chunks <= 256)
-    return launch_as<T, 4, 2>(a, c, chunks, stream);
-  // Few long rows: twice the warps a CTA, for the bytes in flight, as long as all
-  // clusters find room at one CTA an SM (20 best of 200003 fp32: 8 or 12 rows
-  // 8.1 us, with 8 warps 9.2 and 9.7; but 16 rows, whose clusters of 8 do not all
-  // fit at once, 13.5 and 10.1)
-  if (a.T * c * 3 <= (int64_t)num_sms() * 2 && chunks >= 64 * c)
-    return launch_as<T, 16, 4>(a, c, chunks, stream);
-  return launch_as<T, 8, 4>(a, c, chunks, stream);
+  const double sms = num_sms();
+  constexpr double kFixed = 6.0, kCluster = 0.5, kChunk = 0.013;  // (512 bytes on every SM)
+  struct Kind {
+    int warps, ctas;  // of a CTA, of an SM
+    double crowd, least;
+    int chunks, most; // of a CTA at least, where a row has several; of a row's CTAs
+  };
+  static_assert(kMaxCluster == 8, "kinds");
+  constexpr Kind kinds[] = {{16, 1, 0.5, 0.88, 64, 8}, {8, 3, 1.5, 0.35, 12, 8}, {4, 8, 4.0, 0.32, 64, 2}};
+  static_assert(ctas_of_sm(16, 4) == 1 && ctas_of_sm(8, 4) == 3 && ctas_of_sm(4, 2) == 8, "kinds");
+  int warps = 8, cluster = 1;
+  double best = DBL_MAX;
+  for (const Kind& kind : kinds) {
+    for (int c = 1; c <= kind.most && (c == 1 || chunks >= (int64_t)kind.chunks * c); c *= 2) {
+      const double rounds = (double)a.T * c / (sms * kind.ctas);
+      // one CTA an SM: clusters have to find room in what is left of a GPC
+      if (kind.ctas == 1 && (chunks < kind.chunks || rounds > (c == 8 ? 0.66 : c == 4 ? 0.85 : 1.0))) continue;
+      const double whole = std::floor(rounds), rest = rounds - whole;
+      const double fixed = kFixed + (c > 1 ? kCluster : 0.0) + kind.crowd * std::min(rounds, 1.0);
+      const double t = fixed * (std::ceil(rounds) + 1.0) / 2.0 +
+                       kChunk * kind.ctas * (double)chunks / c *
+                           (whole + (rest > 0 ? kind.least + (1.0 - kind.least) * rest : 0.0));
+      if (t < best) best = t, warps = kind.warps, cluster = c;
+    }
+  }
+  switch (warps) {
+    case 16: return launch_as<T, 16, 4>(a, cluster, chunks, stream);
+    case 8: return launch_as<T, 8, 4>(a, cluster, chunks, stream);
+    default: return launch_as<T, 4, 2>(a, cluster, chunks, stream);
+  }
 }
 
 }  // namespace

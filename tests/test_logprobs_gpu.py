@@ -175,3 +175,17 @@ def test_graph_and_other_stream():
         t.zero_()
     graph.replay()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T,V,dtype", [(24, 70001, torch.float32), (100, 40000, torch.float16), (64, 131072, torch.bfloat16), (152, 65535, torch.float16),
+                                       (200, 131071, torch.bfloat16), (300, 50000, torch.float32), (500, 50001, torch.float32), (600, 70000, torch.bfloat16),
+                                       (513, 33000, torch.float16), (1000, 65537, torch.bfloat16), (1300, 40001, torch.float32), (2500, 5001, torch.bfloat16)])
+def test_numbers_of_rows(T, V, dtype):
+    """Rows from a few to many rounds of the GPU's places: other CTAs, and other numbers of them a row."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T + V)
+    x = torch.randn((T, V), generator=g, device="cuda").to(dtype)
+    x[T // 2] = 1.0  # equal values are chosen another way
+    tokens = torch.randint(-1, V + 1, (T,), generator=g, device="cuda", dtype=torch.int32)
+    for top in (3, 32):
+        _check(x, tokens, top)
