@@ -234,7 +234,7 @@ kv_cache_kernel(const KvCacheArgs a, const CacheScales sc) {
             if (off[k] >= 0 && (N == 8 || (cc & 1) == 0))
               page[k][half * kFp4Slot + kFp4Codes + off[k] * 8 + cc * N / 8] = (uint8_t)s;
           } else {
-            encode_e4m3<N>(x, r, code);
+            encode_e4m3<N, false>(x, r, code);
           }
           if (off[k] >= 0) store_words<NW>(page[k] + code0 + off[k] * kRow, code);
         } else if (off[k] >= 0) {

@@ -7,6 +7,16 @@
 // quotient; if both round to the same code, so does the quotient.  The few
 // values near the middle of two codes are divided (a scale that is a power
 // of two, whose ties are many, has an exact reciprocal).
+//
+// Scales like 0.01 bring many bf16 values there (its powers of 2).  Residuals
+// make their division cheap: with the correctly rounded reciprocal y, q = x y and
+// twice q += (x - s q) y, whose residuals are exact; the last gives the rounded
+// quotient (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990).  The rotation's V takes them (59 k tokens x 40
+// rows, 4 of them V's, by 0.01: 167 us, by division 180; by 0.0127 163 both
+// ways), the plain write does not (59 k tokens x 16 rows by 0.01: 88 instead of
+// 101, but 75 instead of 59 by 0.0127: the code of a path that is hardly taken
+// costs it more than its division).
 #pragma once
 
 #include <cmath>
@@ -74,16 +84,18 @@ __device__ __forceinline__ void pack(const float2 (&x)[kVals<T> / 2], uint32_t (
 // How codes are found for a scale (see the top): 1 / scale rounded down and
 // up by more than the errors of the reciprocal, the product and the quotient
 // together (3 * 2^-24 of it); equal for a power of two; not used where the
-// scale is so small or large that these could leave fp32's range.
+// scale is so small or large that these, or a residual's last bit (2^-47 of the
+// value, 2^-11 scales at least where codes differ), could leave fp32's range.
 struct Recip {
-  float scale, lo, hi;
+  float scale, inverse, lo, hi;
   bool use;
 };
 __host__ __device__ inline Recip recip_of(float scale) {
   Recip r;
   r.scale = scale;
-  r.use = scale > 1e-30f && scale < 1e30f;
+  r.use = scale > 1e-25f && scale < 1e25f;
   const float inv = 1.f / scale;
+  r.inverse = inv;
 #ifdef __CUDA_ARCH__
   const bool two = (__float_as_uint(scale) & 0x7FFFFFu) == 0;
 #else
@@ -96,7 +108,7 @@ __host__ __device__ inline Recip recip_of(float scale) {
 }
 
 // N pairs -> N / 2 words of four E4M3 codes.
-template <int N>
+template <int N, bool kResiduals>
 __device__ __forceinline__ void encode_e4m3(const float2 (&x)[N], const Recip& r,
                                             uint32_t (&w)[N / 2]) {
   uint32_t differ = r.use ? 0u : 1u;
@@ -113,7 +125,25 @@ __device__ __forceinline__ void encode_e4m3(const float2 (&x)[N], const Recip& r
     w[i] = lo[0] | (lo[1] << 16);
     differ |= w[i] ^ (hi[0] | (hi[1] << 16));
   }
-  if (differ) {
+  if (kResiduals && r.use && differ) {
+    const float2 y = make_float2(r.inverse, r.inverse), minus = make_float2(-r.scale, -r.scale);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      uint32_t hi[2], code[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float2 v = x[2 * i + k];
+        hi[k] = __nv_cvt_float2_to_fp8x2(mul2(v, make_float2(r.hi, r.hi)), __NV_SATFINITE, __NV_E4M3);
+        float2 q = mul2(v, y);
+        q = fma2(fma2(q, minus, v), y, q);
+        q = fma2(fma2(q, minus, v), y, q);
+        code[k] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+      }
+      // only codes that differ (the others' quotients may be infinite)
+      const uint32_t those = __vcmpne4(w[i], hi[0] | (hi[1] << 16));
+      w[i] = (w[i] & ~those) | ((code[0] | (code[1] << 16)) & those);
+    }
+  } else if (differ) {
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
       const uint32_t a = __nv_cvt_float2_to_fp8x2(

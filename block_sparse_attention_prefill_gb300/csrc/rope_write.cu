@@ -265,7 +265,7 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopePara
       float sum = ss.x + ss.y;
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const float f = 1.f / sqrtf(sum * (1.f / kD) + a.eps);
+      const float f = rsqrtf(sum * (1.f / kD) + a.eps);
 #pragma unroll
       for (int e = 0; e < N; ++e) x[e] = mul2(mul2(x[e], make_float2(f, f)), g[e]);
     }
@@ -352,7 +352,7 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopePara
         store4(to + kFp4Slot, x, a.v_scale, p.v6);
       } else {
         uint32_t code[N / 2];
-        encode_e4m3<N>(x, p.v, code);
+        encode_e4m3<N, true>(x, p.v, code);
         if (live) store8(to + kD, code);
       }
       return;

@@ -264,3 +264,27 @@ def test_rounds_of_ctas(dtype, fp4):
                     clean[last, :, :off] = pool[last, :, :off]
             want = clean
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("scale", [0.01, 0.02, 0.05, 0.1, 1 / 3, 0.7, 1.9999999, 3.0, 1e-8, 1.1e-25, 1e-27, 1e20, 0.25, 0.0131])
+def test_codes_are_of_the_rounded_quotient(scale):
+    """Codes of values near the middle of two codes: V's, and K's of msa_kv_write, are E4M3 of the fp32 quotient."""
+    s32 = float(np.float32(scale))
+    codes = torch.arange(127, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).float()
+    mid = ((codes[1:] + codes[:-1]) / 2).double() * s32
+    near = mid.float().view(torch.int32)[:, None] + torch.arange(-40, 41, device="cuda", dtype=torch.int32)
+    every = torch.arange(65536, device="cuda", dtype=torch.int32).to(torch.uint16)
+    for x in (near.flatten().view(torch.float32), every.view(torch.bfloat16), every.view(torch.float16)):
+        x = torch.cat([x, -x])
+        T = -(-x.numel() // 128)
+        v = torch.nn.functional.pad(x, (0, T * 128 - x.numel())).view(T, 1, 128)
+        want = (v.float() / torch.full_like(v, s32, dtype=torch.float32)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        pages = T // 128 + 1
+        table, cu = torch.arange(pages, dtype=torch.int32, device="cuda")[None], torch.tensor([0, T], dtype=torch.int32, device="cuda")
+        nan = torch.isnan(v.float())
+        for write in (lambda kv: msa.msa_rope_write(msa.MsaRope([]), None, torch.zeros_like(v), v, kv, 1.0, 1.0, s32, table, cu, cu),
+                      lambda kv: msa.msa_kv_write(v, v, kv, s32, s32, table, cu, cu)):
+            kv = torch.zeros((pages, 1, 128, 256), dtype=torch.uint8, device="cuda")
+            write(kv)
+            got = kv.view(-1, 256)[:T, 128:].reshape(T, 1, 128)
+            assert torch.equal(got[~nan], want[~nan]) and ((got[nan] & 0x7F) == 0x7F).all()
