@@ -104,6 +104,22 @@ def test_both_ways_give_the_same(form):
     assert _same(*got)
 
 
+@pytest.mark.parametrize("name", ["mask", "accept", "logprobs"])
+def test_outputs_of_one_allocation_lie_apart(name):
+    outs = _call(name, _arguments(name))
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in outs)
+    assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:])) and all(t.is_contiguous() and t.data_ptr() % 256 == 0 for t in outs)
+    want = [t.clone() for t in outs]
+    for i, t in enumerate(outs):
+        t.add_(1)
+        assert all(torch.equal(o, w) for o, w in zip(outs[i + 1:], want[i + 1:]))
+    last, value = outs[-1], outs[-1].clone()
+    del outs, t
+    torch.cuda.synchronize()
+    other = [torch.zeros(1 << 16, device="cuda") for _ in range(8)]  # noqa: F841
+    assert torch.equal(last, value)
+
+
 @pytest.mark.parametrize("name", ORDER)
 def test_both_ways_refuse_the_same(name):
     """Every tensor of a call as another type, shape, order, place or nothing; every number out of range."""
