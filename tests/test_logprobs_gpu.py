@@ -189,3 +189,28 @@ def test_numbers_of_rows(T, V, dtype):
     tokens = torch.randint(-1, V + 1, (T,), generator=g, device="cuda", dtype=torch.int32)
     for top in (3, 32):
         _check(x, tokens, top)
+
+
+@pytest.mark.parametrize("T,V,dtype", [(500, 200003, torch.float32), (1100, 200003, torch.float32), (600, 2 ** 19 - 1, torch.bfloat16)])
+def test_many_long_rows(T, V, dtype):
+    """Long rows in CTAs of few warps, two of them a row or one; some rows in order, equal or masked."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T + V)
+    x = torch.randn((T, V), generator=g, device="cuda").to(dtype)
+    x[3] = torch.linspace(-4, 4, V, device="cuda").to(dtype)
+    x[5] = 0.5
+    x[7, 100:] = -torch.inf
+    x[9, :-20] = torch.finfo(dtype).min
+    tokens = torch.randint(-1, V + 1, (T,), generator=g, device="cuda", dtype=torch.int32)
+    some = torch.arange(0, T, 37, device="cuda")
+    some = torch.cat([torch.arange(11, device="cuda"), some[some > 10], torch.tensor([T - 1], device="cuda")])
+    got = msa.msa_logprobs(x, tokens, top=20)
+    few = msa.msa_logprobs(x[some].contiguous(), tokens[some].contiguous(), top=20)
+    _check(x[some].contiguous(), tokens[some].contiguous(), 20)
+    assert torch.equal(got[1][some], few[1]) and torch.equal(got[3][some], few[3])  # ranks and best
+    H = np.log(V) + 1
+    tol = 2 * (1 + H) * ((V / 512 + 17) * 2.0 ** -24 + 2.0 ** -20)  # both off by one such
+    for a, b in ((got[0][some], few[0]), (got[2][some] / (2 * (1 + H)), few[2] / (2 * (1 + H))), (got[4][some], few[4])):
+        assert torch.equal(torch.isinf(a), torch.isinf(b))
+        fine = ~torch.isinf(a)
+        assert not ((a - b).abs()[fine].double() > tol + 2.0 ** -21 * a[fine].abs().double()).any()
