@@ -44,7 +44,7 @@ constexpr int kRopeThreads = 128, kRopeWarps = kRopeThreads / 32;
 constexpr int kStaged = 512;  // requests whose lengths a CTA keeps in shared memory
 // Rows of a slot in flight, and CTAs an SM, by the registers that a format needs
 // (before rounds were told apart, see launch_type: 8 chunks of 8k tokens to E4M3
-// 162 us, by 4 and 4: 170; 10 k tokens to NVFP4 and back 28.9 us, by 3 and 5: 30.3)
+// 162 us, by 4 and 4: 170; 8 k tokens to NVFP4 and back 28.9 us, by 3 and 5: 30.3)
 constexpr int in_flight(bool fp4) { return fp4 ? 4 : 3; }
 constexpr int ctas_of_sm(bool fp4) { return fp4 ? 4 : 5; }
 
