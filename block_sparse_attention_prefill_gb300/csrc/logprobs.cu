@@ -179,14 +179,28 @@ struct Vec {
   }
 };
 
-// Whether m log2 e may leave fp32's range (m = -FLT_MAX: no value yet).
-__device__ __forceinline__ bool huge(float m) { return !(fabsf(m) < 2e38f); }
-enum { kPlain, kBounded, kHuge };
+// A reference m has sums in powers of 2 of one of two kinds.  Near 0, of x log2 e
+// - r with r = m log2 e rounded to fp32, whose rounding, at most 2^-4 here, is the
+// same in all terms.  Far from 0 that rounding would grow (to 64 at 1e9: powers
+// out of fp32's range), and they are of (x - m) log2 e.  (m = -FLT_MAX: no value yet.)
+__device__ __forceinline__ bool is_far(float m) { return !(fabsf(m) < 1e6f); }
+enum { kPlain, kBounded, kFarM };
+// r of m: a rounded product, wherever it is used (never fused with a sum: the terms
+// and what they are joined by would then not be by the same r)
+__device__ __forceinline__ float ref_of(float m) { return __fmul_rn(m, kLog2e); }
 
-// What a thread gathers on its way, in powers of 2: with r the reference m log2
-// e rounded to fp32, l = sum 2^t and s = sum 2^t t of t = x log2 e - r, a fused
-// operation.  What log2 e and r lack of exactness is the same in all terms and
-// in the token's own t, so that large logits cost no accuracy.
+// What sums by the reference (m, r) have to be multiplied by, as a power of 2, to
+// be by (m2, r2); kFar and less count as kFar.
+__device__ __forceinline__ float shift_of(float m, float r, float m2, float r2) {
+  const float d = !is_far(m2) ? (!is_far(m) ? r - r2 : fmaf(m, kLog2e, -r2))
+                  : !is_far(m) ? -fmaf(m2, kLog2e, -r) : (m - m2) * kLog2e;
+  return max_or_nan(d, kFar);
+}
+
+// What a thread gathers on its way, in powers of 2: l = sum 2^t and s = sum 2^t t
+// of t = x log2 e - r, a fused operation (far from 0: of (x - m) log2 e, two).
+// What log2 e and r lack of exactness is the same in all terms and in the token's
+// own t, so that large logits cost no accuracy.
 template <typename T>
 struct Sums {
   using V = Vec<T>;
@@ -196,17 +210,17 @@ struct Sums {
   // What is far below m counts as that far: -inf would give 0 times -inf.  Of 16
   // bits two values at once before they are widened, by a number `low` that lies
   // at least 200 below m whichever way it is rounded; where the type has none,
-  // and of fp32, t is bounded.  Where r would not be finite t is (x - m) log2 e.
+  // and of fp32, t is bounded.
   typename V::T2 low;
   int mode;
 
   __device__ __forceinline__ void raise(float to) {
-    const float r2 = to * kLog2e;
-    const float d = max_or_nan(huge(to) ? (m - to) * kLog2e : r - r2, kFar), f = ex2_approx(d);
+    const float r2 = ref_of(to);
+    const float d = shift_of(m, r, to, r2), f = ex2_approx(d);
     s = make_float2(f * fmaf(l.x, d, s.x), f * fmaf(l.y, d, s.y));
     l = make_float2(l.x * f, l.y * f);
     m = to, r = r2;
-    mode = huge(to) ? kHuge : kBounded;
+    mode = is_far(to) ? kFarM : kBounded;
     if constexpr (V::k16) {
       constexpr bool kHalf = std::is_same<T, __half>::value;
       const float least = m + kFar - fabsf(m) * 0.015625f;
@@ -231,7 +245,7 @@ struct Sums {
       } else {
         t = make_float2(v.at(i), v.at(i + 1));
       }
-      if constexpr (kMode == kHuge)
+      if constexpr (kMode == kFarM)
         t = mul2(add2(t, make_float2(-m, -m)), c2);
       else
         t = fma2(t, c2, r2);
@@ -330,7 +344,7 @@ logprobs_kernel(const LogprobsArgs a, int cluster_size) {
   sum.m = sum.r = kLowest;
   sum.l = sum.s = make_float2(0.f, 0.f);
   sum.before = 0;
-  sum.mode = kHuge;
+  sum.mode = kFarM;
   // values before the token in a chunk that it lies in, or at an end of the row
   auto count_places = [&](const V& v, int c) {
     const int first = ((c0 + c) * 32 + lane) * N - row.shift;
@@ -348,7 +362,7 @@ logprobs_kernel(const LogprobsArgs a, int cluster_size) {
     const float top = warp_max(v.top_edge(row, at));
     if (lane == 0) s_max[c] = top;
     if (top > sum.m) sum.raise(top);
-    if (sum.mode == kHuge) sum.template add_as<kHuge>(v); else sum.template add_as<kBounded>(v);
+    if (sum.mode == kFarM) sum.template add_as<kFarM>(v); else sum.template add_as<kBounded>(v);
     count_places(v, c);
   };
   // In the chunks before the token's values as large come before it, in those
@@ -383,7 +397,7 @@ logprobs_kernel(const LogprobsArgs a, int cluster_size) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         if (!there(k)) continue;
-        if (sum.mode == kHuge) sum.template add_as<kHuge>(v[k]); else sum.template add_as<kBounded>(v[k]);
+        if (sum.mode == kFarM) sum.template add_as<kFarM>(v[k]); else sum.template add_as<kBounded>(v[k]);
       }
     }
     if (!(most >= mine)) return;  // (no token: mine is NaN)
@@ -616,10 +630,10 @@ logprobs_kernel(const LogprobsArgs a, int cluster_size) {
     before += part[i].before;
   }
   m = warp_max(m);
-  const float ref = m * kLog2e;
+  const float ref = ref_of(m);
   float l = 0.f, s = 0.f;
   auto join = [&](const Part& q) {
-    const float d = max_or_nan(huge(m) ? (q.m - m) * kLog2e : q.r - ref, kFar), f = ex2_approx(d);
+    const float d = shift_of(q.m, q.r, m, ref), f = ex2_approx(d);
     l += f * q.l;
     s += f * fmaf(q.l, d, q.s);
   };
@@ -634,7 +648,8 @@ logprobs_kernel(const LogprobsArgs a, int cluster_size) {
   const float norm = log2f(l);
   auto logprob = [&](float value) {
     if (l == 0.f) return -INFINITY;
-    return huge(m) || huge(value) ? (value - m) - kLn2 * norm : kLn2 * (fmaf(value, kLog2e, -ref) - norm);
+    // (beside a value whose product with log2 e is not finite ref's rounding vanishes)
+    return is_far(m) || !(fabsf(value) < 2e38f) ? (value - m) - kLn2 * norm : kLn2 * (fmaf(value, kLog2e, -ref) - norm);
   };
   if (tid == 0) {
     if (a.logprobs) a.logprobs[t] = is_token ? logprob(mine) : -INFINITY;
