@@ -438,6 +438,10 @@ int rope_write_impl(const msa_rope_t* rope, RopeArgs a, int64_t B, int64_t Hq, i
     return MSA_ERR_SHAPE;
   if (a.fp4 && (!std::isfinite(6.f * a.k_scale) || !std::isfinite(6.f * a.v_scale)))
     return MSA_ERR_SHAPE;
+  // E4M3 codes of Q and K are of products with these
+  if ((Hq > 0 && !a.q_bf16 && !std::isfinite(1.f / a.q_scale)) ||
+      (!a.fp4 && !std::isfinite(1.f / a.k_scale)))
+    return MSA_ERR_SHAPE;
   if (B == 0 || a.T == 0) return MSA_OK;
   if (!a.pool || !a.block_table || !a.cu || !a.cu_k || (Hq > 0 && !a.q_out)) return MSA_ERR_NULL;
   const int64_t es = a.dtype == MSA_DTYPE_F32 ? 4 : 2;

@@ -538,9 +538,12 @@ MSA_API int msa_kv_read_nvfp4(const uint8_t *kv4, int64_t num_pages, float k_sca
  * are normalised by head (where weights are given) and rotated to their
  * positions; Q is quantised to E4M3 (or rounded to bf16) for the attention
  * calls; K and V are quantised and written into their pages as msa_kv_write /
- * msa_kv_write_nvfp4 write them (E4M3 codes of K and Q from the product with
- * the scale's reciprocal: y itself is rounded).  (The pages name such a producer of the E4M3
- * query and the cache, a fused QK-norm / RoPE / KV-insert.)
+ * msa_kv_write_nvfp4 write them, but that E4M3 codes of K and Q are those of the
+ * product with the scale's rounded reciprocal: within 2^-23 of the quotient,
+ * whose code is the neighbour's where that lies so near to the middle of two,
+ * also of values that are neither normalised nor rotated.  These scales have
+ * to have a finite reciprocal (2.94e-39 and up).  (The pages name such a
+ * producer of the E4M3 query and the cache, a fused QK-norm / RoPE / KV-insert.)
  *   y = x / sqrt(mean of the head's x^2 + eps) * norm
  *   pair j turned by positions[axis[j]][t] * inv_freq[j]:
  *     (a, b) -> (a cos - b sin, a sin + b cos)
