@@ -8,7 +8,8 @@
 // one by one, with its messages, and makes the call itself.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -46,34 +47,13 @@ struct Place {
   bool i32(const at::Tensor* t, int64_t dims) const {
     return t && t->scalar_type() == at::kInt && t->dim() == dims && t->is_contiguous() && has(*t);
   }
-  at::Tensor empty(at::IntArrayRef size, at::ScalarType type) const {
-    return at::empty(size, at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)dev));
+  // A new tensor on the current device, with storage of its own: what a caller does
+  // with one output (resize_, out=) cannot reach another.
+  static at::Tensor empty(at::IntArrayRef size, at::ScalarType type) {
+    return at::Tensor(at::detail::empty_generic(size, c10::cuda::CUDACachingAllocator::get(),
+                                                c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt));
   }
   void* stream() const { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
-};
-
-// A call's outputs as parts of one allocation, each on 256 bytes (an allocation
-// takes 0.8 us, a part 0.2: log probabilities 5.5-6.2 us a call instead of 8.6-9.3).
-class Outputs {
- public:
-  Outputs(const Place& here, std::initializer_list<int64_t> values) {  // of 4 bytes
-    int64_t n = 0;
-    for (int64_t v : values) n += padded(v);
-    block_ = here.empty({n}, at::kInt);
-  }
-  at::Tensor part(at::IntArrayRef size, at::ScalarType type) {
-    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(block_.storage()), block_.key_set(),
-                                                            caffe2::TypeMeta::fromScalarType(type));
-    t.unsafeGetTensorImpl()->set_storage_offset(at_);
-    t.unsafeGetTensorImpl()->set_sizes_contiguous(size);
-    at_ += padded(t.numel());
-    return t;
-  }
-
- private:
-  static int64_t padded(int64_t n) { return (n + 63) / 64 * 64; }
-  at::Tensor block_;
-  int64_t at_ = 0;
 };
 
 // A page pool [num_pages, Hkv, ...] of a format.
@@ -196,8 +176,7 @@ PyObject* tree_mask(PyObject*, PyObject* const* a, Py_ssize_t n) {
       Py_RETURN_NONE;
     const int64_t T = parents->size(0);
     const int64_t words = (most + 31) / 32;
-    Outputs out(here, {T * words, T});
-    const at::Tensor mask = out.part({T, words}, at::kInt), positions = out.part({T}, at::kInt);
+    const at::Tensor mask = here.empty({T, words}, at::kInt), positions = here.empty({T}, at::kInt);
     const int rc = calls.tree_mask(data<int32_t>(parents), data<int32_t>(cu_q), data<int32_t>(cu_k),
                                    cu_q->size(0) - 1, T, most, data<uint32_t>(mask), data<int32_t>(positions),
                                    nullptr, here.stream());
@@ -286,9 +265,8 @@ PyObject* tree_accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const at::Tensor* table = layers ? tensor(a[8]) : nullptr;
     if (layers && (!here.i32(table, 2) || table->size(0) != B)) Py_RETURN_NONE;
-    Outputs out(here, {B * most, B, B * most});
-    const at::Tensor tokens = out.part({B, most}, at::kInt), accepted = out.part({B}, at::kInt),
-                     path = out.part({B, most}, at::kInt);
+    const at::Tensor tokens = here.empty({B, most}, at::kInt), accepted = here.empty({B}, at::kInt),
+                     path = here.empty({B, most}, at::kInt);
     const int rc = (fp4 ? calls.tree_accept_nvfp4 : calls.tree_accept)(
         data<int32_t>(drafts), data<int32_t>(parents), data<int32_t>(chosen), data<int32_t>(cu_q),
         data<int32_t>(cu_k), B, T, most, pools, layers, pages, heads, data<int32_t>(table),
@@ -311,11 +289,10 @@ PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
         (a[1] != Py_None && (!here.i32(tokens, 1) || tokens->size(0) != logits->size(0))))
       Py_RETURN_NONE;
     const int64_t T = logits->size(0);
-    Outputs out(here, {tokens ? T : 0, tokens ? T : 0, T, T * top, T * top});
     at::Tensor logprob, rank;
-    if (tokens) logprob = out.part({T}, at::kFloat), rank = out.part({T}, at::kInt);
-    const at::Tensor entropy = out.part({T}, at::kFloat), best = out.part({T, top}, at::kInt),
-                     value = out.part({T, top}, at::kFloat);
+    if (tokens) logprob = here.empty({T}, at::kFloat), rank = here.empty({T}, at::kInt);
+    const at::Tensor entropy = here.empty({T}, at::kFloat), best = here.empty({T, top}, at::kInt),
+                     value = here.empty({T, top}, at::kFloat);
     const int rc = calls.logprobs(logits->data_ptr(), logits->stride(0), type, data<int32_t>(tokens), T,
                                   logits->size(1), top, tokens ? data<float>(logprob) : nullptr,
                                   tokens ? data<int32_t>(rank) : nullptr, data<float>(entropy), data<int32_t>(best),

@@ -10,8 +10,6 @@ A decode step waits for the host's way to each launch, so the form that it uses
 (outputs to be made, the current stream, no status) is checked and called by the
 compiled module of ``csrc/binding.cpp``; what that does not take, other forms and
 arguments that are not sound, is looked at here one by one, with its messages.
-The outputs that it makes of msa_tree_mask, msa_tree_accept and msa_logprobs are
-parts of one allocation, which lives as long as any of them.
 """
 from __future__ import annotations
 
