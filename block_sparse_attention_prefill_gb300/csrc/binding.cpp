@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
 
 #include "msa.h"
 
@@ -120,6 +121,24 @@ PyObject* guarded(F body) {
   return nullptr;
 }
 
+// The interpreter's lock given up while the library launches: a launch waits where
+// the device's queue is full, and other threads must not wait with it.
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+template <typename F, typename... A>
+int launch(F* f, A... a) {
+  const Unlocked now;
+  return f(a...);
+}
+
 // (address of the msa_rope_t, its axes, its weights' device or -1, fp4, q, k, v,
 // kv, q_scale, k_scale, v_scale, block_table, cu_seqlens_q, cu_seqlens_k,
 // positions)
@@ -155,8 +174,8 @@ PyObject* rope_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
     double q_scale = 1.0, k_scale, v_scale;
     if ((!bf16 && !number(a[8], &q_scale)) || !number(a[9], &k_scale) || !number(a[10], &v_scale)) Py_RETURN_NONE;
     const at::Tensor out = here.empty({T, q->size(1), MSA_HEAD_DIM}, bf16 ? at::kBFloat16 : at::kFloat8_e4m3fn);
-    const int rc = (fp4 ? calls.rope_write_nvfp4 : calls.rope_write)(
-        rope, data<int32_t>(pos), q->data_ptr(), q->stride(0), q->stride(1), k->data_ptr(), k->stride(0),
+    const int rc = launch(
+        fp4 ? calls.rope_write_nvfp4 : calls.rope_write, rope, data<int32_t>(pos), q->data_ptr(), q->stride(0), q->stride(1), k->data_ptr(), k->stride(0),
         k->stride(1), v->data_ptr(), v->stride(0), v->stride(1), type, out.data_ptr(), bf16, (float)q_scale,
         data<uint8_t>(kv), kv->size(0), (float)k_scale, (float)v_scale, data<int32_t>(table), table->size(1),
         data<int32_t>(cu_q), data<int32_t>(cu_k), B, T, q->size(1), Hkv, nullptr, here.stream());
@@ -177,9 +196,9 @@ PyObject* tree_mask(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t T = parents->size(0);
     const int64_t words = (most + 31) / 32;
     const at::Tensor mask = here.empty({T, words}, at::kInt), positions = here.empty({T}, at::kInt);
-    const int rc = calls.tree_mask(data<int32_t>(parents), data<int32_t>(cu_q), data<int32_t>(cu_k),
-                                   cu_q->size(0) - 1, T, most, data<uint32_t>(mask), data<int32_t>(positions),
-                                   nullptr, here.stream());
+    const int rc = launch(calls.tree_mask, data<int32_t>(parents), data<int32_t>(cu_q), data<int32_t>(cu_k),
+                          cu_q->size(0) - 1, T, most, data<uint32_t>(mask), data<int32_t>(positions), nullptr,
+                          here.stream());
     return rc ? PyLong_FromLong(rc) : outputs({mask, positions});
   });
 }
@@ -214,11 +233,11 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor out = here.empty({T, Hq, MSA_HEAD_DIM}, at::kBFloat16);
     at::Tensor lse;
     if (a[13] == Py_True) lse = here.empty({T, Hq}, at::kFloat);
-    rc = calls.tree_attention(data<uint8_t>(q), data<uint8_t>(kv), kv->size(0), (float)scale[0], (float)scale[1],
-                              (float)scale[2], (float)scale[3], data<int32_t>(table), table->size(1),
-                              data<int32_t>(cu_q), data<int32_t>(cu_k), data<uint32_t>(mask), mask->size(1), B, T,
-                              Hq, Hkv, prefix, max_q, max_k, workspace.data_ptr(), bytes, data<uint16_t>(out),
-                              lse.defined() ? data<float>(lse) : nullptr, nullptr, here.stream());
+    rc = launch(calls.tree_attention, data<uint8_t>(q), data<uint8_t>(kv), kv->size(0), (float)scale[0],
+                (float)scale[1], (float)scale[2], (float)scale[3], data<int32_t>(table), table->size(1),
+                data<int32_t>(cu_q), data<int32_t>(cu_k), data<uint32_t>(mask), mask->size(1), B, T, Hq, Hkv, prefix,
+                max_q, max_k, workspace.data_ptr(), bytes, data<uint16_t>(out),
+                lse.defined() ? data<float>(lse) : nullptr, nullptr, here.stream());
     return rc ? PyLong_FromLong(rc) : outputs({out, lse});
   });
 }
@@ -247,10 +266,12 @@ PyObject* tree_accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
       pools[layers++] = data<uint8_t>(t);
       return t->size(0) == pages && t->size(1) == heads;
     };
+    THPObjectPtr held;  // (another thread may change a list during the launch)
     if (PyList_CheckExact(a[7]) || PyTuple_CheckExact(a[7])) {
-      PyObject** items = PySequence_Fast_ITEMS(a[7]);
-      for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(a[7]); ++i)
-        if (!add(tensor(items[i]))) Py_RETURN_NONE;
+      held = PySequence_Tuple(a[7]);
+      if (!held) return nullptr;
+      for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(held.get()); ++i)
+        if (!add(tensor(PyTuple_GET_ITEM(held.get(), i)))) Py_RETURN_NONE;
     } else if (const at::Tensor* t = a[7] == Py_None ? nullptr : tensor(a[7])) {
       if (t->dim() != 5) {
         if (!add(t)) Py_RETURN_NONE;
@@ -267,8 +288,8 @@ PyObject* tree_accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (layers && (!here.i32(table, 2) || table->size(0) != B)) Py_RETURN_NONE;
     const at::Tensor tokens = here.empty({B, most}, at::kInt), accepted = here.empty({B}, at::kInt),
                      path = here.empty({B, most}, at::kInt);
-    const int rc = (fp4 ? calls.tree_accept_nvfp4 : calls.tree_accept)(
-        data<int32_t>(drafts), data<int32_t>(parents), data<int32_t>(chosen), data<int32_t>(cu_q),
+    const int rc = launch(
+        fp4 ? calls.tree_accept_nvfp4 : calls.tree_accept, data<int32_t>(drafts), data<int32_t>(parents), data<int32_t>(chosen), data<int32_t>(cu_q),
         data<int32_t>(cu_k), B, T, most, pools, layers, pages, heads, data<int32_t>(table),
         table ? table->size(1) : 0, data<int32_t>(tokens), data<int32_t>(accepted), data<int32_t>(path), nullptr,
         here.stream());
@@ -293,10 +314,10 @@ PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (tokens) logprob = here.empty({T}, at::kFloat), rank = here.empty({T}, at::kInt);
     const at::Tensor entropy = here.empty({T}, at::kFloat), best = here.empty({T, top}, at::kInt),
                      value = here.empty({T, top}, at::kFloat);
-    const int rc = calls.logprobs(logits->data_ptr(), logits->stride(0), type, data<int32_t>(tokens), T,
-                                  logits->size(1), top, tokens ? data<float>(logprob) : nullptr,
-                                  tokens ? data<int32_t>(rank) : nullptr, data<float>(entropy), data<int32_t>(best),
-                                  data<float>(value), here.stream());
+    const int rc = launch(calls.logprobs, logits->data_ptr(), logits->stride(0), type, data<int32_t>(tokens), T,
+                          logits->size(1), top, tokens ? data<float>(logprob) : nullptr,
+                          tokens ? data<int32_t>(rank) : nullptr, data<float>(entropy), data<int32_t>(best),
+                          data<float>(value), here.stream());
     return rc ? PyLong_FromLong(rc) : outputs({logprob, rank, entropy, best, value});
   });
 }
