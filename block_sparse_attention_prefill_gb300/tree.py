@@ -77,7 +77,9 @@ class MsaRope:
     them); interleaved: pair j is values 2j and 2j + 1 of a head, else j and
     j + len(inv_freq); axes: for positions of several axes, the axis of each
     pair; q_norm, k_norm: weights [128] of the heads' root-mean-square norms,
-    or None for none (their values are copied), with eps."""
+    or None for none (their values are copied, which waits for the current
+    stream), with eps.  It has to live as long as calls and graphs that use it
+    run."""
 
     def __init__(self, inv_freq, interleaved=False, axes=None, q_norm=None, k_norm=None, eps=1e-6):
         freq = inv_freq.tolist() if isinstance(inv_freq, torch.Tensor) else list(inv_freq)
@@ -101,6 +103,9 @@ class MsaRope:
         if len(set(weights)) > 1:
             _fail("q_norm and k_norm are on different devices")
         self._device = weights[0] if weights else -1
+        # the copies are there for calls on any stream (those of a capture on its own)
+        if weights and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self._device).synchronize()
 
 
 def _reach(t):
