@@ -119,7 +119,8 @@ tree_accept_kernel(const __grid_constant__ TreeAcceptArgs a) {
   uint32_t bad = ok ? 0 : (uint32_t)MSA_STATUS_BAD_SEQLENS;
   if (i > 0 && i < r.n) {
     if (up >= 0 && up < i) {
-      if (s_draft[i] == s_chosen[up]) atomicMin(&s_next[up], i);
+      // (-1, msa_logprobs' best of a row of NaN, is no token)
+      if (s_draft[i] >= 0 && s_draft[i] == s_chosen[up]) atomicMin(&s_next[up], i);
     } else if (up != -1) {
       bad |= MSA_STATUS_BAD_TREE;
     }

@@ -380,7 +380,7 @@ def msa_tree_accept(draft_tokens, parents, chosen, cu_seqlens_q, cu_seqlens_k, m
     the cache.  draft_tokens, parents, chosen int32 [T]: each node's token, its
     parent (as in msa_tree_mask) and the target's own token after it (the best,
     as msa_logprobs gives it, or a drawn one).  The path starts at a request's
-    first token and follows the target's choices.  kv: the pools of all layers,
+    first token and follows the target's choices; a negative draft stands never.  kv: the pools of all layers,
     a sequence of E4M3 pools [num_pages, Hkv, 128, 256] (at most 128, which
     share no memory), one pool, a tensor [layers, ...] of them, or None: the
     rows of the path are moved to follow the context directly, so that the

@@ -727,7 +727,8 @@ MSA_API int msa_tree_attention(const uint8_t *q, const uint8_t *kv, int64_t num_
  * tokens has them: row seq_len - q_len + path[j] becomes row seq_len - q_len +
  * j, in every layer's pool (K was rotated to the node's depth, which is j), so
  * that the sequence goes on at length seq_len - q_len + 1 + accepted.
- *   draft_tokens int32 [T]: the token of each node (node 0's is not looked at)
+ *   draft_tokens int32 [T]: the token of each node (node 0's is not looked at);
+ *                a negative one is no token and stands after no choice
  *   parents      as in msa_tree_mask; a node whose parent is no earlier node
  *                (other than -1) sets MSA_STATUS_BAD_TREE and is on no path
  *   chosen       int32 [T]
