@@ -19,6 +19,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -70,8 +71,17 @@ def binding_path() -> str:
                                                         sysconfig.get_config_var("EXT_SUFFIX")))
 
 
+_binding_lock = threading.Lock()
+
+
 def build_binding(force: bool = False) -> str:
-    """Compile the Python module if its source or the header is newer."""
+    """Compile the Python module if its source or the header is newer (threads
+    that ask at once: one compiles, the others wait for it)."""
+    with _binding_lock:
+        return _build_binding(force)
+
+
+def _build_binding(force: bool) -> str:
     os.makedirs(OUT, exist_ok=True)
     path, src = binding_path(), os.path.join(CSRC, "binding.cpp")
     if not force and not _stale(path, [src, os.path.join(INCLUDE, "msa.h"), __file__]):

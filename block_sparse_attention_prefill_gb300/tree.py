@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import importlib.machinery
 import importlib.util
+import threading
 
 import torch
 
@@ -31,12 +32,15 @@ LOGPROBS_MAX_TOP = 32
 
 
 _binding = None
+_binding_lock = threading.Lock()
 
 
 def load_binding():
     """The compiled module (building it first if it is missing)."""
     global _binding
-    if _binding is None:
+    with _binding_lock:
+        if _binding is not None:
+            return _binding
         lib, path = load(), _build.build_binding()
         loader = importlib.machinery.ExtensionFileLoader("msa_binding", path)
         module = importlib.util.module_from_spec(
@@ -47,7 +51,7 @@ def load_binding():
             lib.msa_tree_accept_nvfp4, lib.msa_logprobs, lib.msa_tree_attention,
             lib.msa_prefix_attention_workspace_bytes)])
         _binding = module
-    return _binding
+        return module
 
 
 def msa_rope_turns(inv_freq):
