@@ -17,6 +17,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import threading
+import warnings
 
 import torch
 
@@ -52,6 +53,30 @@ def load_binding():
             lib.msa_prefix_attention_workspace_bytes)])
         _binding = module
         return module
+
+
+class _Checked:
+    """In place of the compiled module where there is none: takes no call, so that
+    every one goes through the checks here and ctypes, to the same library."""
+
+    rope_write = tree_mask = tree_attention = tree_accept = logprobs = staticmethod(lambda *args: None)
+
+
+_way = None
+
+
+def _find_way():
+    """What the calls try first: the compiled module, or, where it cannot be built
+    (no C++ compiler, no headers), with a warning, none."""
+    global _way
+    load()
+    try:
+        _way = load_binding()
+    except (RuntimeError, OSError, ImportError) as e:
+        warnings.warn("the tree calls take 5-25 us more of the host's time each: their compiled module "
+                      "could not be built or loaded: %s" % e, RuntimeWarning, stacklevel=4)
+        _way = _Checked
+    return _way
 
 
 def msa_rope_turns(inv_freq):
@@ -180,7 +205,7 @@ def _check_rope(fp4, rope, q, k, v, kv, q_scale, block_table, cu_q, cu_k, positi
 def _rope_write(name, fp4, rope, q, k, v, kv, q_scale, k_scale, v_scale, block_table, cu_q, cu_k,
                 positions, q_out, status, stream):
     if type(rope) is MsaRope and q_out is status is stream is None:
-        r = (_binding or load_binding()).rope_write(
+        r = (_way or _find_way()).rope_write(
             rope._address, rope.axes, rope._device, fp4, q, k, v, kv, q_scale, k_scale, v_scale,
             block_table, cu_q, cu_k, positions)
         if r.__class__ is int:
@@ -263,7 +288,7 @@ def msa_tree_mask(parents, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, mask=None, 
     are OR-ed into; without it nothing tells of lengths that do not fit or of
     parents that are no earlier tokens (taken for -1)."""
     if mask is positions is status is stream is None:
-        r = (_binding or load_binding()).tree_mask(parents, cu_seqlens_q, cu_seqlens_k,
+        r = (_way or _find_way()).tree_mask(parents, cu_seqlens_q, cu_seqlens_k,
                                                    max_seqlen_q)
         if r.__class__ is int:
             _check(r, "msa_tree_mask")
@@ -298,7 +323,7 @@ def msa_tree_attention(q, kv, q_scale, k_scale, v_scale, softmax_scale, block_ta
     ceil(max_seqlen_q / 32)] (msa_tree_mask's, or any others); max_seqlen_q at
     most 256.  A token that sees no key gets zeros and lse -inf."""
     if workspace is out is lse is status is stream is None:
-        r = (_binding or load_binding()).tree_attention(
+        r = (_way or _find_way()).tree_attention(
             q, kv, q_scale, k_scale, v_scale, softmax_scale, block_table, cu_seqlens_q,
             cu_seqlens_k, mask, prefix_pages, max_seqlen_q, max_seqlen_k, want_lse)
         if r.__class__ is int:
@@ -353,7 +378,7 @@ def _check_accept(fp4, drafts, parents, chosen, cu_q, cu_k, n, pools, table, tok
 def _accept(name, fp4, drafts, parents, chosen, cu_q, cu_k, max_q, kv, table, tokens, accepted,
             path, status, stream):
     if tokens is accepted is path is status is stream is None:
-        r = (_binding or load_binding()).tree_accept(fp4, drafts, parents, chosen, cu_q, cu_k, max_q,
+        r = (_way or _find_way()).tree_accept(fp4, drafts, parents, chosen, cu_q, cu_k, max_q,
                                                      kv, table)
         if r.__class__ is int:
             _check(r, name)
@@ -438,7 +463,7 @@ def msa_logprobs(logits, tokens=None, top=0, logprobs=None, ranks=None, entropy=
     outside [0, V) has -inf and rank -1; a row with a NaN has NaN, but for the
     tokens and ranks."""
     if logprobs is ranks is entropy is top_tokens is top_logprobs is stream is None:
-        r = (_binding or load_binding()).logprobs(logits, tokens, top)
+        r = (_way or _find_way()).logprobs(logits, tokens, top)
         if r.__class__ is int:
             _check(r, "msa_logprobs")
         if r is not None:
