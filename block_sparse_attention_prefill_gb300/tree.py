@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import importlib.machinery
 import importlib.util
+import operator
 import threading
 import warnings
 
@@ -89,6 +90,14 @@ def msa_rope_turns(inv_freq):
     return list(turns)[:n]
 
 
+def _whole(x, name):
+    """A whole number of any type (no fraction cut off)."""
+    try:
+        return int(x) if isinstance(x, float) and x.is_integer() else operator.index(x)
+    except TypeError:
+        _fail("%s must be a whole number, got %r", name, x)
+
+
 def _weight(w, name):
     if w is None:
         return None
@@ -114,7 +123,7 @@ class MsaRope:
         freq = inv_freq.tolist() if isinstance(inv_freq, torch.Tensor) else list(inv_freq)
         if len(freq) > ROPE_MAX_PAIRS:
             _fail("at most %d frequencies, got %d", ROPE_MAX_PAIRS, len(freq))
-        axis = [0] * len(freq) if axes is None else [int(a) for a in axes]
+        axis = [0] * len(freq) if axes is None else [_whole(a, "an axis") for a in axes]
         if len(axis) != len(freq) or any(not 0 <= a < ROPE_MAX_AXES for a in axis):
             _fail("axes must be an axis below %d for each of the %d frequencies", ROPE_MAX_AXES,
                   len(freq))
@@ -271,9 +280,10 @@ def _check_tree(flat, cu_q, cu_k, outs, status):
 
 
 def _tree_limit(max_seqlen_q):
-    if not 0 <= max_seqlen_q <= TREE_MAX_TOKENS:
-        _fail("max_seqlen_q must be 0 .. %d, got %d", TREE_MAX_TOKENS, max_seqlen_q)
-    return int(max_seqlen_q)
+    n = _whole(max_seqlen_q, "max_seqlen_q")
+    if not 0 <= n <= TREE_MAX_TOKENS:
+        _fail("max_seqlen_q must be 0 .. %d, got %d", TREE_MAX_TOKENS, n)
+    return n
 
 
 def msa_tree_mask(parents, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, mask=None, positions=None,
@@ -468,9 +478,9 @@ def msa_logprobs(logits, tokens=None, top=0, logprobs=None, ranks=None, entropy=
             _check(r, "msa_logprobs")
         if r is not None:
             return r
+    top = _whole(top, "top")
     if not 0 <= top <= LOGPROBS_MAX_TOP:
         _fail("top must be 0 .. %d, got %d", LOGPROBS_MAX_TOP, top)
-    top = int(top)
     dev = _check_logprobs(logits, tokens, top,
                           {"logprobs": logprobs, "ranks": ranks, "entropy": entropy,
                            "top_tokens": top_tokens, "top_logprobs": top_logprobs})
