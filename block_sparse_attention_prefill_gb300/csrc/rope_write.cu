@@ -10,7 +10,8 @@
 // all in fp32, with one rounding at the end.  The angle: f_j is kept as a
 // fraction of a turn in steps of 2^-64, and its product with the whole number
 // pos, modulo 2^64, is the fraction of the turn at that position with an error
-// of pos 2^-65 turns.  So positions of any size cost no accuracy, no table of
+// of pos 2^-65 turns; its first 32 bits, from -1/2 to 1/2, become an fp32 number
+// (off by 2^-26 turns at most, by less near 0).  So positions of any size cost no accuracy, no table of
 // cosines is read (4 bytes a value and position, as many as a row of bf16 has)
 // and no fp64 arithmetic is needed.
 //

@@ -547,8 +547,10 @@ MSA_API int msa_kv_read_nvfp4(const uint8_t *kv4, int64_t num_pages, float k_sca
  *   y = x / sqrt(mean of the head's x^2 + eps) * norm
  *   pair j turned by positions[axis[j]][t] * inv_freq[j]:
  *     (a, b) -> (a cos - b sin, a sin + b cos)
- * in fp32 with one rounding at the end; the angle is exact to 2^-32 turns at
- * any position.  V is neither normalised nor rotated.
+ * in fp32 with one rounding at the end (squares that add up to more than fp32
+ * holds make y 0).  The angle, reduced to half a turn to either side, is within
+ * 2^-24 of itself and 2^-32 turns of the exact one at any position: 2^-26 turns
+ * at most.  V is neither normalised nor rotated.
  *
  * msa_rope_t (on the host, read during the call): how a model rotates.
  *   pairs        rotated pairs of a head, 0 .. 64; the other values of Q and K
