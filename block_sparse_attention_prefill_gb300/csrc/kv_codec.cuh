@@ -164,20 +164,19 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 // N pairs (a block of 16 values; or a half or a quarter of one, N = 4 or 2, with
 // the next lane's, or the next three's) -> words of eight E2M1 codes, the first
-// in the low nibble (N = 2: half a word), and the
-// block's E4M3 scale.  Called together by the lanes of the mask `lanes`.
+// in the low nibble (N = 2: half a word), and the block's E4M3 scale.  Called by
+// whole warps.
 template <int N>
 __device__ __forceinline__ void encode_nvfp4(const float2 (&x)[N], float g, float g6,
-                                             uint32_t (&w)[(N + 3) / 4], uint32_t* scale,
-                                             uint32_t lanes = 0xffffffffu) {
+                                             uint32_t (&w)[(N + 3) / 4], uint32_t* scale) {
   float amax = 0.f, sick = 0.f;  // sick: NaN if one of the values is
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     amax = fmaxf(amax, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));  // ignores NaN
     sick = max_nan(sick, max_nan(x[i].x, x[i].y));
   }
-  if constexpr (N <= 4) amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, 1));
-  if constexpr (N == 2) amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, 2));
+  if constexpr (N <= 4) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  if constexpr (N == 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
   const __nv_fp8_storage_t s8 =
       __nv_cvt_float_to_fp8(amax / g6, __NV_SATFINITE, __NV_E4M3);
   *scale = s8;
