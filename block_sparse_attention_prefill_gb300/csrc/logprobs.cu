@@ -182,7 +182,8 @@ struct Vec {
 // A reference m has sums in powers of 2 of one of two kinds.  Near 0, of x log2 e
 // - r with r = m log2 e rounded to fp32, whose rounding, at most 2^-4 here, is the
 // same in all terms.  Far from 0 that rounding would grow (to 64 at 1e9: powers
-// out of fp32's range), and they are of (x - m) log2 e.  (m = -FLT_MAX: no value yet.)
+// out of fp32's range), and they are of (x - m) log2 e, two operations.  (m =
+// -FLT_MAX: no value yet.)
 __device__ __forceinline__ bool is_far(float m) { return !(fabsf(m) < 1e6f); }
 enum { kPlain, kBounded, kFarM };
 // r of m: a rounded product, wherever it is used (never fused with a sum: the terms
@@ -282,8 +283,8 @@ __device__ __forceinline__ uint64_t pick(uint64_t lo, uint64_t hi, int n_lo, int
   return lo;
 }
 
-struct Part {  // of a warp
-  float m, r, l, s;
+struct Part {  // of a warp, its sums of 2^t with t = (x - m) log2 e
+  float m, l, s;
   int before;
 };
 
@@ -439,12 +440,17 @@ logprobs_kernel(const LogprobsArgs a, int cluster_size) {
     load(x[0], c + 2 * kStep);
     add(x[1], c + kStep);
   }
-  Part p = {sum.m, sum.r, sum.l.x + sum.l.y, sum.s.x + sum.s.y, sum.before};
+  Part p = {sum.m, sum.l.x + sum.l.y, sum.s.x + sum.s.y, sum.before};
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     p.l += __shfl_xor_sync(0xffffffffu, p.l, o);
     p.s += __shfl_xor_sync(0xffffffffu, p.s, o);
     p.before += __shfl_xor_sync(0xffffffffu, p.before, o);
+  }
+  if (!is_far(p.m)) {  // r's rounding out of the sums: from here on they are by m itself
+    const float o = fmaf(p.m, kLog2e, -ref_of(p.m)), f = ex2_approx(-o);
+    p.s = f * fmaf(p.l, -o, p.s);
+    p.l *= f;
   }
   if (lane == 0) s_top[warp] = sum.m;
   // 64 buckets of the CTA: its lanes by as many together as make 64
@@ -624,16 +630,15 @@ logprobs_kernel(const LogprobsArgs a, int cluster_size) {
   int before = 0;
 #pragma unroll
   for (int i = 0; i < kParts; ++i) {
-    part[i] = {kLowest, kLowest, 0.f, 0.f, 0};
+    part[i] = {kLowest, 0.f, 0.f, 0};
     if (lane + 32 * i < parts) part[i] = s_part[lane + 32 * i];
     m = largest(m, part[i].m);
     before += part[i].before;
   }
   m = warp_max(m);
-  const float ref = ref_of(m);
   float l = 0.f, s = 0.f;
   auto join = [&](const Part& q) {
-    const float d = shift_of(q.m, q.r, m, ref), f = ex2_approx(d);
+    const float d = max_or_nan((q.m - m) * kLog2e, kFar), f = ex2_approx(d);
     l += f * q.l;
     s += f * fmaf(q.l, d, q.s);
   };
@@ -646,11 +651,7 @@ logprobs_kernel(const LogprobsArgs a, int cluster_size) {
     before += __shfl_xor_sync(0xffffffffu, before, o);
   }
   const float norm = log2f(l);
-  auto logprob = [&](float value) {
-    if (l == 0.f) return -INFINITY;
-    // (beside a value whose product with log2 e is not finite ref's rounding vanishes)
-    return is_far(m) || !(fabsf(value) < 2e38f) ? (value - m) - kLn2 * norm : kLn2 * (fmaf(value, kLog2e, -ref) - norm);
-  };
+  auto logprob = [&](float value) { return l == 0.f ? -INFINITY : (value - m) - kLn2 * norm; };
   if (tid == 0) {
     if (a.logprobs) a.logprobs[t] = is_token ? logprob(mine) : -INFINITY;
     if (a.ranks) a.ranks[t] = mine == mine ? before : -1;
