@@ -126,7 +126,7 @@ PyObject* guarded(F body) {
 class Unlocked {
  public:
   Unlocked() : state_(PyEval_SaveThread()) {}
-  ~Unlocked() { PyEval_RestoreThread(state_); }
+  ~Unlocked() noexcept(false) { PyEval_RestoreThread(state_); }  // (ends the thread where the interpreter has ended)
   Unlocked(const Unlocked&) = delete;
   Unlocked& operator=(const Unlocked&) = delete;
 

@@ -16,7 +16,6 @@ from __future__ import annotations
 import ctypes
 import importlib.machinery
 import importlib.util
-import operator
 import threading
 import warnings
 
@@ -93,9 +92,12 @@ def msa_rope_turns(inv_freq):
 def _whole(x, name):
     """A whole number of any type (no fraction cut off)."""
     try:
-        return int(x) if isinstance(x, float) and x.is_integer() else operator.index(x)
-    except TypeError:
-        _fail("%s must be a whole number, got %r", name, x)
+        n = int(x)
+        if n == x:
+            return n
+    except (TypeError, ValueError, OverflowError):
+        pass
+    _fail("%s must be a whole number, got %r", name, x)
 
 
 def _weight(w, name):

@@ -20,7 +20,7 @@ def test_fractions_are_refused(bad):
 
 
 def test_other_whole_numbers_are_taken():
-    for n in (np.int64(6), np.int32(6), 6.0, torch.tensor(6)):
+    for n in (np.int64(6), np.int32(6), 6.0, np.float32(6), torch.tensor(6), torch.tensor(6.0)):
         assert "CUDA" in _err(msa.msa_tree_mask, i32(6), i32(3), i32(3), n)
         assert "CUDA" in _err(msa.msa_logprobs, torch.zeros((4, 50)), i32(4), top=n)
     assert msa.MsaRope([1.0, 2.0], axes=torch.tensor([0, 2])).axes == 3
